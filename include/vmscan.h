@@ -65,8 +65,8 @@ typedef enum {
   VMSCAN_OK = 0,
   VMSCAN_ERR_NULL = 1,        /* a required pointer is NULL                                  */
   VMSCAN_ERR_SHAPE = 2,       /* a size is < 1, or too large for the index types               */
-  VMSCAN_ERR_UNSUPPORTED = 3, /* d_state or dtype not supported                                */
-  VMSCAN_ERR_ALIGN = 4,       /* a pointer is not 16-byte aligned                              */
+  VMSCAN_ERR_UNSUPPORTED = 3, /* d_state, dtype or another option not supported                */
+  VMSCAN_ERR_ALIGN = 4,       /* a pointer (a stride, where one is taken) is not 16-byte aligned */
   VMSCAN_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than the queried size               */
   VMSCAN_ERR_HIP = 6,         /* a HIP call failed; see vmscan_last_hip_error()                */
   VMSCAN_ERR_SCRATCH = 7,     /* the call needs more than VMSCAN_SCRATCH_BYTES (no-alloc entry) */
@@ -374,6 +374,150 @@ vmscan_status vmscan_conv1d_silu_fwd(const void *x, const float *conv_w, const f
 vmscan_status ss2d_conv2d_silu_fwd(const void *x, const float *conv_w, const float *conv_b, int act,
                                    void *x_out, void *xT_out, int64_t batch, int64_t dim, int64_t H,
                                    int64_t W, int d_conv, vmscan_dtype dtype, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Operators of a linear-attention block over the same tokens: the residual addition with its norm,
+ * the rotary positions, and the attention whose state is a matrix per head.  Their activations are
+ * token-major.  Ownership, errors, streams and the workspace follow the conventions above (no wait
+ * status word: none of these kernels waits for another).
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition.  Per row, in float32:
+ *   r = x + residual;   rstd = 1 / sqrt(mean(r^2) + eps);   y = r * rstd * weight
+ *   x            : [rows, dim] with a row stride of x_stride >= dim elements, activation dtype
+ *   residual     : [rows, dim] residual_dtype, or NULL (r = x; then residual_out is NULL too)
+ *   weight       : [dim] float32
+ *   y            : [rows, dim] activation dtype, or with out_fp8 = 1 8-bit codes (OCP e4m3)
+ *   scale        : out_fp8 = 0: NULL.  out_fp8 = 1: float32, [rows] (group 0) or
+ *                  [rows, ceil(dim / 128)] (group 128, the last group may be short)
+ *   residual_out : [rows, dim] residual_dtype, r rounded once; NULL with residual.  May be residual.
+ *   rstd         : [rows] float32, for the gradient, or NULL
+ * y is computed from r before its rounding.  8 bits: y = code * scale, scale = max|y| / 448 over the
+ * row or group (1 where that maximum is 0; at least the smallest normal float32), the code the value
+ * nearest to y / scale.  A NaN in a row makes its rstd, scale and codes NaN.
+ * dtype F32 takes residual_dtype F32; BF16 takes F32 or BF16.  1 <= dim <= 32768, any value.
+ * No workspace.
+ */
+vmscan_status vmscan_rmsnorm_fwd(const void *x, int64_t x_stride, const void *residual,
+                                 const float *weight, void *y, float *scale, void *residual_out,
+                                 float *rstd, int64_t rows, int64_t dim, float eps,
+                                 vmscan_dtype dtype, vmscan_dtype residual_dtype, int out_fp8,
+                                 int group, hipStream_t stream);
+
+/*
+ * Gradient of vmscan_rmsnorm_fwd (activation output).  With n = r * rstd:
+ *   dr = rstd * (weight * dy - n * mean(weight * dy * n)) + dresidual_out;   dweight = sum_rows dy * n
+ *   dy             : [rows, dim] activation dtype
+ *   r              : [rows, dim] residual_dtype: the forward's residual_out (x when it had no residual)
+ *   rstd           : [rows] float32, the forward's
+ *   dresidual_out  : [rows, dim] residual_dtype, the gradient of residual_out, or NULL
+ *   dx             : [rows, dim] activation dtype: dr rounded
+ *   dresidual      : [rows, dim] residual_dtype: dr rounded to that type, or NULL; must be NULL when the
+ *                    two types are the same (dx is it)
+ *   dweight        : [dim] float32, summed in a fixed order
+ * Outputs must not alias inputs, except dx = dy and dresidual = dresidual_out.
+ */
+size_t vmscan_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+vmscan_status vmscan_rmsnorm_bwd(const void *dy, const void *r, const float *weight,
+                                 const float *rstd, const void *dresidual_out, void *dx,
+                                 void *dresidual, float *dweight, int64_t rows, int64_t dim,
+                                 vmscan_dtype dtype, vmscan_dtype residual_dtype, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Rotary positions with several axes (rows and columns of an image; time, rows and columns of a
+ * video).  Pair p of every head turns by the angle  positions[b, t, axis[p]] * inv_freq[p]:
+ *   y1 = x1 cos - x2 sin,   y2 = x1 sin + x2 cos        (inverse = 1: by the negative angle, which is
+ *                                                        also the gradient of the forward turn)
+ * Pair p of the rot/2 pairs is the channels (p, p + rot/2), or with interleaved = 1 (2p, 2p + 1);
+ * the channels from rot on pass through unchanged.
+ *   q, q_out   : [batch, seqlen, heads, dim]  activation dtype; *_strides: batch, token and head
+ *   k, k_out   : [batch, seqlen, kheads, dim]  stride in elements, channels contiguous.  kheads = 0:
+ *                no k (its four arguments are not looked at).  An output may be its own input (same
+ *                strides); otherwise they must not overlap.  Pointers: aligned to one element.
+ *   positions  : [seqlen, axes] float32 per batch, positions_stride elements apart (0: shared)
+ *   inv_freq   : [rot / 2] float32
+ *   axis       : [rot / 2] int32; a pair whose axis is not in 0 .. axes - 1 is not turned
+ * The angle is reduced from the exact product, so large positions lose nothing.  No workspace.
+ */
+vmscan_status vmscan_rope_axes(const void *q, const int64_t *q_strides, void *q_out,
+                               const int64_t *q_out_strides, const void *k,
+                               const int64_t *k_strides, void *k_out,
+                               const int64_t *k_out_strides, const float *positions,
+                               int64_t positions_stride, const float *inv_freq, const int32_t *axis,
+                               int64_t batch, int64_t seqlen, int heads, int kheads, int dim,
+                               int rot, int axes, int interleaved, int inverse,
+                               vmscan_dtype dtype, hipStream_t stream);
+
+/*
+ * Linear attention with a decay for each head.  Per (batch b, head h), with hk = h / (heads / kheads)
+ * and a float32 state S [dk, dv], S_{-1} = initial_state (NULL: 0):
+ *   S_t = exp(log_decay[b, t, h]) S_{t-1} + k[b, t, hk] v[b, t, h]^T;   out[b, t, h] = scale S_t^T q[b, t, hk]
+ *   q, k          : [batch, seqlen, kheads, dk]  activation dtype; *_strides: batch, token and head
+ *   v             : [batch, seqlen, heads, dv]   stride in elements, channels contiguous.  Pointers
+ *                   and strides must be multiples of 16 bytes (else VMSCAN_ERR_ALIGN).
+ *   log_decay     : float32; decay_strides (batch, token, head; 0 broadcasts) or NULL for one value
+ *                   per head, [heads].  -inf clears the state; values above 0 are taken as they are.
+ *   initial_state, final_state : [batch, heads, dk, dv] float32 or NULL
+ *   lengths       : [batch] int32 or NULL: row b has lengths[b] tokens (clamped to 0 .. seqlen).  What
+ *                   lies past them is never read (it may be NaN), `out` is 0 there and the
+ *                   final state is the one after the last token.
+ *   out           : [batch, seqlen, heads, dv]   activation dtype, dense
+ * heads must be a multiple of kheads; dk and dv multiples of 8 up to 128 (else
+ * VMSCAN_ERR_UNSUPPORTED).  A NaN or infinity in a token's v can reach earlier outputs of the same
+ * 64 tokens.
+ */
+size_t vmscan_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int dk, int dv,
+                                          vmscan_dtype dtype);
+vmscan_status vmscan_linattn_fwd(const void *q, const int64_t *q_strides, const void *k,
+                                 const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                                 const float *log_decay, const int64_t *decay_strides,
+                                 const float *initial_state, const int32_t *lengths, void *out,
+                                 float *final_state, int64_t batch, int64_t seqlen, int heads,
+                                 int kheads, int dk, int dv, float scale, vmscan_dtype dtype,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of vmscan_linattn_fwd.  Inputs as there, and
+ *   dout           : [batch, seqlen, heads, dv]  activation dtype, dout_strides as q's
+ *   dfinal_state   : [batch, heads, dk, dv] float32 or NULL (0)
+ * Outputs, dense: dq, dk_out [batch, seqlen, kheads, dk] (summed over the heads that share them) and
+ * dv_out [batch, seqlen, heads, dv], activation dtype; dlog_decay float32, [batch, seqlen, heads] or,
+ * when decay_strides is NULL, [heads]; dinitial_state [batch, heads, dk, dv] float32 or NULL.  Zero
+ * past a row's length.  No atomics: the same inputs give the same bits.
+ * per_head of the workspace query: 1 when decay_strides will be NULL.
+ */
+size_t vmscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int kheads,
+                                          int dk, int dv, int per_head, vmscan_dtype dtype);
+vmscan_status vmscan_linattn_bwd(const void *q, const int64_t *q_strides, const void *k,
+                                 const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                                 const float *log_decay, const int64_t *decay_strides,
+                                 const float *initial_state, const int32_t *lengths,
+                                 const void *dout, const int64_t *dout_strides,
+                                 const float *dfinal_state, void *dq, void *dk_out, void *dv_out,
+                                 float *dlog_decay, float *dinitial_state, int64_t batch,
+                                 int64_t seqlen, int heads, int kheads, int dk, int dv, float scale,
+                                 vmscan_dtype dtype, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * One token of each of `batch` sequences: the recurrence of vmscan_linattn_fwd once, the states
+ * updated in place.
+ *   q, k      : [batch, kheads, dk], v : [batch, heads, dv]  activation dtype; *_strides: batch, head
+ *   log_decay : float32, decay_strides (batch, head) or NULL for [heads]
+ *   state     : [pool, heads, dk, dv] float32
+ *   slots     : [batch] int32: the state of each sequence, all different; a row whose slot is not in
+ *               0 .. pool - 1 has no state: its out is 0.  NULL: row b has state b, pool = batch.
+ *   out       : [batch, heads, dv]  activation dtype, dense
+ * q, k and v may start at any element.  No workspace.
+ */
+vmscan_status vmscan_linattn_step(const void *q, const int64_t *q_strides, const void *k,
+                                  const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                                  const float *log_decay, const int64_t *decay_strides,
+                                  float *state, const int32_t *slots, void *out, int64_t batch,
+                                  int64_t pool, int heads, int kheads, int dk, int dv, float scale,
+                                  vmscan_dtype dtype, hipStream_t stream);
 
 #ifdef __cplusplus
 }

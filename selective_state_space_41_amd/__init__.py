@@ -80,6 +80,30 @@ def _load():
     lib.ss2d_conv2d_silu_fwd.restype = ctypes.c_int
     lib.ss2d_conv2d_silu_fwd.argtypes = ([_c_void_p] * 3 + [ctypes.c_int] + [_c_void_p] * 2 +
                                          [_i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p])
+    lib.vmscan_rmsnorm_fwd.restype = ctypes.c_int
+    lib.vmscan_rmsnorm_fwd.argtypes = ([_c_void_p, _i64] + [_c_void_p] * 6 + [_i64, _i64, ctypes.c_float] +
+                                       [ctypes.c_int] * 4 + [_c_void_p])
+    lib.vmscan_rmsnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_rmsnorm_bwd_workspace_bytes.argtypes = [_i64, _i64]
+    lib.vmscan_rmsnorm_bwd.restype = ctypes.c_int
+    lib.vmscan_rmsnorm_bwd.argtypes = ([_c_void_p] * 8 + [_i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p,
+                                                         ctypes.c_size_t, _c_void_p])
+    lib.vmscan_rope_axes.restype = ctypes.c_int
+    lib.vmscan_rope_axes.argtypes = ([_c_void_p] * 9 + [_i64, _c_void_p, _c_void_p, _i64, _i64] + [ctypes.c_int] * 8 +
+                                     [_c_void_p])
+    sizes = [_i64, _i64] + [ctypes.c_int] * 4
+    lib.vmscan_linattn_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_linattn_fwd_workspace_bytes.argtypes = [_i64, _i64] + [ctypes.c_int] * 4
+    lib.vmscan_linattn_fwd.restype = ctypes.c_int
+    lib.vmscan_linattn_fwd.argtypes = ([_c_void_p] * 12 + sizes + [ctypes.c_float, ctypes.c_int, _c_void_p,
+                                                                   ctypes.c_size_t, _c_void_p])
+    lib.vmscan_linattn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_linattn_bwd_workspace_bytes.argtypes = [_i64, _i64] + [ctypes.c_int] * 6
+    lib.vmscan_linattn_bwd.restype = ctypes.c_int
+    lib.vmscan_linattn_bwd.argtypes = ([_c_void_p] * 18 + sizes + [ctypes.c_float, ctypes.c_int, _c_void_p,
+                                                                   ctypes.c_size_t, _c_void_p])
+    lib.vmscan_linattn_step.restype = ctypes.c_int
+    lib.vmscan_linattn_step.argtypes = [_c_void_p] * 11 + sizes + [ctypes.c_float, ctypes.c_int, _c_void_p]
     return lib
 
 
@@ -474,3 +498,326 @@ def ss2d_conv2d_silu_fwd(x, conv_w, conv_b, act=True, transposed=True, x_out=Non
 
 def fwd_bidir_chunk_len(batch, dim, seqlen, d_state=D_STATE):
     return int(load().vmscan_fwd_bidir_chunk_len(batch, dim, seqlen, d_state))
+
+
+# ------------------------------------------------------------------------------------------------
+# Operators of a linear-attention block: norm with residual, rotary positions, decayed attention.
+
+_DTYPES = {torch.float32: VMSCAN_F32, torch.bfloat16: VMSCAN_BF16}
+_FP8 = torch.float8_e4m3fn
+
+
+def _is_act(t, name, ndim):
+    """The activation dtype code of a [..., channels] device tensor whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return dt
+
+
+def _strided(t, name, shape, dtype, device):
+    """A tensor of any strides but contiguous channels; its leading strides for the library (0 where
+    the dimension has one element, whose stride says nothing)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    n = len(st) - 1
+    return (_i64 * n)(*[s if d != 1 else 0 for s, d in zip(st[:n], shape)])
+
+
+def _made(stream, *tensors):
+    """Tensors that a call allocated itself and uses on ``stream``: if that is not the stream they
+    were allocated on, the allocator must not reuse them before that stream is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _enqueue(fn, args, dev, prepare=False, keep=None):
+    """The C call with the tensors' device current (a stream belongs to a device)."""
+    if prepare:
+        return _call(fn, args, True, keep)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+    return None
+
+
+def _on(stream, dev):
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+
+def _p(t):
+    return t.data_ptr() if t is not None else None
+
+
+def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=None, residual_out=None, stream=None):
+    """Residual addition and root-mean-square norm (vmscan_rmsnorm_fwd): r = x + residual, y = r *
+    rsqrt(mean(r^2) + eps) * weight.  Returns (y, scale, residual_out, rstd).
+
+    x: [..., dim] float32 or bfloat16 (rows may be apart: [rows, dim] with any row stride); weight: [dim]
+    float32; residual: like x, dtype x's or float32, or None (then residual_out is x itself).
+    out_dtype None: y in x's dtype, scale None; torch.float8_e4m3fn: y holds 8-bit codes and scale
+    [..., 1] float32 (group 0, one per row) or [..., ceil(dim / 128)] (group 128): y * scale is the
+    norm.  ``residual_out`` may be ``residual`` (in place).  rstd [...] float32 is for ``rmsnorm_bwd``."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with a channel dimension")
+    dt = _is_act(x, "x", x.dim())
+    dev, shape, dim = x.device, x.shape, x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    if x.is_contiguous():
+        row_stride = dim
+    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= dim:
+        row_stride = x.stride(0)
+    else:
+        raise ValueError("x must be contiguous, or [rows, dim] with contiguous channels and rows that do not overlap")
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    rdt = dt
+    if residual is not None:
+        rdt = _is_act(residual, "residual", x.dim())
+        _need(residual, "residual", shape, residual.dtype, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+            _made(stream, residual_out)
+        else:
+            _need(residual_out, "residual_out", shape, residual.dtype, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    fp8 = out_dtype == _FP8
+    if out_dtype is not None and not fp8 and out_dtype != x.dtype:
+        raise TypeError(f"out_dtype must be {x.dtype} or {_FP8}, got {out_dtype}")
+    ydt = _FP8 if fp8 else x.dtype
+    if y is None:
+        y = torch.empty(shape, dtype=ydt, device=dev)
+        _made(stream, y)
+    else:
+        _need(y, "y", shape, ydt, dev)
+    scale = None
+    if fp8:
+        scale = torch.empty(*shape[:-1], -(-dim // group) if group else 1, dtype=torch.float32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _made(stream, scale, rstd)
+    _enqueue(load().vmscan_rmsnorm_fwd,
+             (x.data_ptr(), row_stride, _p(residual), weight.data_ptr(), y.data_ptr(), _p(scale), _p(residual_out),
+              rstd.data_ptr(), rows, dim, eps, dt, rdt, int(fp8), int(group), _on(stream, dev)), dev)
+    return y, scale, residual_out if residual is not None else x, rstd
+
+
+def rmsnorm_bwd(dy, r, weight, rstd, dresidual_out=None, workspace=None, stream=None):
+    """Gradient of ``rmsnorm_fwd`` (vmscan_rmsnorm_bwd); returns a dict with dx (dy's dtype), dresidual
+    (r's dtype; dx itself when the two are the same) and dweight [dim] float32.
+
+    dy: [..., dim] gradient of y; r: the forward's residual_out; rstd: the forward's; dresidual_out: the
+    gradient that reaches residual_out on its other way, or None."""
+    dt = _is_act(dy, "dy", dy.dim() if isinstance(dy, torch.Tensor) else 0)
+    dev, shape, dim = dy.device, dy.shape, dy.shape[-1]
+    rdt = _is_act(r, "r", dy.dim())
+    _need(dy, "dy", shape, dy.dtype, dev)
+    _need(r, "r", shape, r.dtype, dev)
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    _need(rstd, "rstd", shape[:-1], torch.float32, dev)
+    if dresidual_out is not None:
+        _need(dresidual_out, "dresidual_out", shape, r.dtype, dev)
+    rows = dy.numel() // dim if dim else 0
+    lib = load()
+    given = workspace
+    workspace = _workspace(workspace, lib.vmscan_rmsnorm_bwd_workspace_bytes(rows, dim), dev)
+    dx, dw = torch.empty_like(dy), torch.empty(dim, dtype=torch.float32, device=dev)
+    dres = torch.empty_like(r) if r.dtype != dy.dtype else None
+    _made(stream, dx, dw, dres, workspace if given is None else None)
+    _enqueue(lib.vmscan_rmsnorm_bwd,
+             (dy.data_ptr(), r.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _p(dresidual_out), dx.data_ptr(),
+              _p(dres), dw.data_ptr(), rows, dim, dt, rdt, _p(workspace), _nbytes(workspace), _on(stream, dev)), dev)
+    return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
+
+
+def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions with several axes (vmscan_rope_axes); returns (q_out, k_out).
+
+    q: [batch, L, heads, dim], k: [batch, L, kheads, dim] or None, float32 or bfloat16, any strides with
+    contiguous channels; positions: [L, axes] or [batch, L, axes] float32; inv_freq: [pairs] float32 and
+    axis: [pairs] int32 give pair p the angle positions[..., axis[p]] * inv_freq[p].  The pairs are the
+    channels (p, p + pairs), or (2p, 2p + 1) when ``interleaved``; channels from 2 * pairs on pass
+    through.  ``inverse`` turns back: the gradient of the forward turn.  Outputs are contiguous unless
+    given; an output may be its own input."""
+    dt = _is_act(q, "q", 4)
+    dev, (nb, L, H, dim) = q.device, q.shape
+    qs = _strided(q, "q", q.shape, q.dtype, dev)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a [pairs] tensor")
+    pairs = inv_freq.shape[0]
+    _need(inv_freq, "inv_freq", (pairs,), torch.float32, dev)
+    _need(axis, "axis", (pairs,), torch.int32, dev)
+    if not isinstance(positions, torch.Tensor) or positions.dim() not in (2, 3):
+        raise ValueError("positions must be [L, axes] or [batch, L, axes]")
+    axes = positions.shape[-1]
+    _need(positions, "positions", (L, axes) if positions.dim() == 2 else (nb, L, axes), torch.float32, dev)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _made(stream, q_out)
+    qos = _strided(q_out, "q_out", q.shape, q.dtype, dev)
+    Hk, ks, kos = 0, None, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be [batch, L, kheads, dim]")
+        Hk = k.shape[2]
+        if Hk < 1:
+            raise ValueError("k has no heads")
+        ks = _strided(k, "k", (nb, L, Hk, dim), q.dtype, dev)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            _made(stream, k_out)
+        kos = _strided(k_out, "k_out", k.shape, q.dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out needs a k")
+    _enqueue(load().vmscan_rope_axes,
+             (q.data_ptr(), qs, q_out.data_ptr(), qos, _p(k), ks, _p(k_out), kos, positions.data_ptr(),
+              L * axes if positions.dim() == 3 else 0, inv_freq.data_ptr(), axis.data_ptr(), nb, L, H, Hk, dim,
+              2 * pairs, axes, int(bool(interleaved)), int(bool(inverse)), dt, _on(stream, dev)), dev)
+    return q_out, k_out
+
+
+def _linattn_args(q, k, v, log_decay, ndim):
+    """Checks what every linear-attention call takes; returns (dtype code, batch and token sizes, heads,
+    kheads, dk, dv, strides of q, k, v and of the decay, None for one decay per head)."""
+    dt = _is_act(q, "q", ndim)
+    dev, lead = q.device, q.shape[:-2]
+    Hk, dk = q.shape[-2:]
+    if not isinstance(v, torch.Tensor) or v.dim() != ndim:
+        raise ValueError(f"v must have {ndim} dimensions")
+    H, dv = v.shape[-2:]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} heads of v cannot share {Hk} heads of q and k")
+    qs = _strided(q, "q", q.shape, q.dtype, dev)
+    ks = _strided(k, "k", q.shape, q.dtype, dev)
+    vs = _strided(v, "v", lead + (H, dv), q.dtype, dev)
+    if not isinstance(log_decay, torch.Tensor):
+        raise TypeError("log_decay must be a torch.Tensor")
+    if log_decay.dtype != torch.float32 or log_decay.device != dev:
+        raise TypeError(f"log_decay must be float32 on {dev}, got {log_decay.dtype} on {log_decay.device}")
+    gs = None
+    if log_decay.dim() == 1:
+        _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    elif log_decay.shape == lead + (H,):
+        gs = (_i64 * (ndim - 1))(*log_decay.stride())
+    else:
+        raise ValueError(f"log_decay has shape {tuple(log_decay.shape)}, expected {(H,)} or {tuple(lead) + (H,)}")
+    return dt, lead, H, Hk, dk, dv, qs, ks, vs, gs
+
+
+def linattn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None, out=None, final_state=None,
+                workspace=None, stream=None, prepare=False):
+    """Linear attention with a decay for each head (vmscan_linattn_fwd); returns (out, final_state).
+
+    Per head S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T and out_t = scale * S_t^T q_t.  q, k: [batch, L,
+    kheads, dk]; v: [batch, L, heads, dv], heads a multiple of kheads (a q/k head serves neighbouring
+    heads); float32 or bfloat16, contiguous channels, other strides multiples of 16 bytes; dk and dv
+    multiples of 8 up to 128.  log_decay: float32 [batch, L, heads] (any strides) or [heads].  scale
+    defaults to dk ** -0.5.  initial_state / final_state: [batch, heads, dk, dv] float32.  lengths: [batch]
+    int32, the tokens of each row; out is 0 past them.  ``prepare`` as for ``vmscan_fwd_bidir`` (the
+    callable then rewrites the same out and final_state): returns (callable, out, final_state)."""
+    dt, (nb, L), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 4)
+    dev = q.device
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _need(t, name, (nb, H, dk, dv), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    if out is None:
+        out = torch.empty(nb, L, H, dv, dtype=q.dtype, device=dev)
+        _made(stream, out)
+    else:
+        _need(out, "out", (nb, L, H, dv), q.dtype, dev)
+    if final_state is None:
+        final_state = torch.empty(nb, H, dk, dv, dtype=torch.float32, device=dev)
+        _made(stream, final_state)
+    lib = load()
+    given = workspace
+    workspace = _workspace(workspace, lib.vmscan_linattn_fwd_workspace_bytes(nb, L, H, dk, dv, dt), dev)
+    if given is None:
+        _made(stream, workspace)
+    args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, _p(initial_state),
+            _p(lengths), out.data_ptr(), final_state.data_ptr(), nb, L, H, Hk, dk, dv,
+            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _on(stream, dev))
+    run = _enqueue(lib.vmscan_linattn_fwd, args, dev, prepare,
+                   (q, k, v, log_decay, initial_state, lengths, out, final_state, workspace))
+    return (run, out, final_state) if prepare else (out, final_state)
+
+
+def linattn_bwd(q, k, v, log_decay, dout, scale=None, initial_state=None, lengths=None, dfinal_state=None,
+                workspace=None, stream=None, prepare=False):
+    """Gradients of ``linattn_fwd`` for ``dout`` [batch, L, heads, dv] and, optionally, ``dfinal_state``
+    [batch, heads, dk, dv] (vmscan_linattn_bwd); returns a dict with dq, dk, dv, dlog_decay (of log_decay's
+    shape) and dinitial_state (None without an initial_state).  Deterministic.  ``prepare`` as for
+    ``vmscan_bwd_bidir_v2``."""
+    dt, (nb, L), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 4)
+    dev = q.device
+    os_ = _strided(dout, "dout", (nb, L, H, dv), q.dtype, dev)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _need(t, name, (nb, H, dk, dv), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=dev)
+    act = lambda *s: torch.empty(*s, dtype=q.dtype, device=dev)
+    g = dict(dq=act(nb, L, Hk, dk), dk=act(nb, L, Hk, dk), dv=act(nb, L, H, dv), dlog_decay=f32(*log_decay.shape),
+             dinitial_state=f32(nb, H, dk, dv) if initial_state is not None else None)
+    lib = load()
+    given = workspace
+    workspace = _workspace(workspace, lib.vmscan_linattn_bwd_workspace_bytes(nb, L, H, Hk, dk, dv, int(gs is None), dt),
+                           dev)
+    _made(stream, *g.values(), workspace if given is None else None)
+    args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, _p(initial_state),
+            _p(lengths), dout.data_ptr(), os_, _p(dfinal_state), g["dq"].data_ptr(), g["dk"].data_ptr(),
+            g["dv"].data_ptr(), g["dlog_decay"].data_ptr(), _p(g["dinitial_state"]), nb, L, H, Hk, dk, dv,
+            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _on(stream, dev))
+    run = _enqueue(lib.vmscan_linattn_bwd, args, dev, prepare,
+                   (q, k, v, log_decay, initial_state, lengths, dout, dfinal_state, g, workspace))
+    return (run, g) if prepare else g
+
+
+def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, stream=None, prepare=False):
+    """One token of each of ``batch`` sequences (vmscan_linattn_step): updates ``state`` in place and
+    returns out [batch, heads, dv].
+
+    q, k: [batch, kheads, dk]; v: [batch, heads, dv]; log_decay: float32 [batch, heads] or [heads]; state:
+    [pool, heads, dk, dv] float32; slots: [batch] int32, the state of each sequence (all different; one
+    outside 0 .. pool - 1 skips the row, whose out is 0), or None with pool = batch.  ``prepare`` as for
+    ``linattn_fwd``: returns (callable, out)."""
+    dt, (nb,), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 3)
+    dev = q.device
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be [pool, heads, dk, dv]")
+    pool = state.shape[0]
+    _need(state, "state", (pool, H, dk, dv), torch.float32, dev)
+    if slots is not None:
+        _need(slots, "slots", (nb,), torch.int32, dev)
+    elif pool != nb:
+        raise ValueError(f"without slots the pool holds one state per sequence: {pool} for {nb}")
+    if out is None:
+        out = torch.empty(nb, H, dv, dtype=q.dtype, device=dev)
+        _made(stream, out)
+    else:
+        _need(out, "out", (nb, H, dv), q.dtype, dev)
+    args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, state.data_ptr(),
+            _p(slots), out.data_ptr(), nb, pool, H, Hk, dk, dv, float(dk ** -0.5 if scale is None else scale), dt,
+            _on(stream, dev))
+    run = _enqueue(load().vmscan_linattn_step, args, dev, prepare, (q, k, v, log_decay, state, slots, out))
+    return (run, out) if prepare else out

@@ -1,7 +1,8 @@
 """Compile the HIP library in-tree for gfx950.
 
-``python -m selective_state_space_41_amd.build`` (or ``build()``) runs hipcc on
-``csrc/vmscan.hip`` and writes ``libvmscan.so`` next to this file; it always recompiles.
+``python -m selective_state_space_41_amd.build`` (or ``build()``) runs hipcc on the library's
+sources (``SOURCES``, side by side) and links ``libvmscan.so`` next to this file; it always
+recompiles.
 ``python -m selective_state_space_41_amd.build --probe`` builds only the issue-rate
 microbenchmark (``csrc/probe.hip`` -> ``vmscan_probe``), which is not part of the library.
 """
@@ -10,10 +11,12 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libvmscan.so")
+SOURCES = ("vmscan.hip", "linattn.hip", "norm.hip", "rope.hip")  # in csrc/
 PROBE = os.path.join(PKG, "vmscan_probe")
 
 # Packed fp32 VALU forms are kept out of every gfx950 code object.
@@ -88,8 +91,15 @@ def build(verbose=False):
     """Compile libvmscan.so and check the hot kernels' occupancy."""
     hipcc = _hipcc()
     tmp = LIB + ".tmp"
-    out = _run([hipcc, *HIP_FLAGS, "-Rpass-analysis=kernel-resource-usage", "-shared", "-I",
-                os.path.join(ROOT, "include"), "-o", tmp, os.path.join(PKG, "csrc", "vmscan.hip")])
+    objs = [os.path.join(PKG, "csrc", src[:-len(".hip")] + ".o") for src in SOURCES]
+
+    def compile_one(src, obj):
+        return _run([hipcc, *HIP_FLAGS, "-Rpass-analysis=kernel-resource-usage", "-I", os.path.join(ROOT, "include"),
+                     "-c", "-o", obj, os.path.join(PKG, "csrc", src)])
+
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
+        out = "\n".join(pool.map(compile_one, SOURCES, objs))
+    _run([hipcc, *HIP_FLAGS, "-shared", "-o", tmp, *objs])
     res = kernel_resources(out)
     if not any(frag in name for name in res for frag, _ in OCCUPANCY_FLOORS):
         raise RuntimeError("build: the compiler printed no kernel resource report")

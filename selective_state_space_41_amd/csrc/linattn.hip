@@ -1,0 +1,1355 @@
+// Linear attention with a decay for each head: forward over sequences, gradient, single tokens.
+// What is computed is stated in include/vmscan.h.
+//
+// Per head the state is a matrix S [dk, dv] and token t does S = e^{g_t} S + k_t v_t^T, o_t = scale
+// S^T q_t.  Over a block of C tokens with G_i = g_1 + .. + g_i and the state S entering it, that is
+//   o_i  = scale (e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j),
+//   S'   = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T:
+// four matrix products per block, on the matrix cores, with float32 accumulators.  Every exponent
+// is a sum of logarithms over the tokens between two positions, so nothing overflows for decays
+// however strong; the running sums are taken in float64 and kept as a head and a tail in float32,
+// because a difference of two of them is a small number between large ones.
+//
+// A workgroup walks the blocks of one sequence and head, or of a segment of it when there are too few
+// (sequence, head) pairs to fill the chip: then a first pass sums each segment's own state, a small
+// prefix kernel makes the state entering each, and the walk starts from there.
+//
+// Layouts.  All products use the 16 x 16 (x 32) matrix instructions, whose operands hold 8 elements
+// of the contracted index per lane and whose results hold 4 consecutive rows of one column.  The
+// contracted index may be taken in any order as long as both operands agree, so a result (a tile of
+// the masked scores) becomes an operand of the next product in the register it is in, in the order
+// 16 t + 4 (lane / 16) + r; the other operand, whose contracted index is the token, is read from
+// the row-major tile with the transposing LDS read, which gives that order.  Tiles: Q, K, V
+// [token][channel], the state [dk][dv].  The float32 path has the same structure with the
+// 16 x 16 x 4 float32 instruction, eight per product, and plain LDS reads.
+//
+// Rounding for bfloat16 activations: scores, their gradients and the state are rounded to bfloat16
+// where they enter a product whose result is rounded to bfloat16 anyway (o, dq, dk, dv).  What ends
+// in float32 (the states, their gradients, the decays' gradient) keeps 16 bits of mantissa: the
+// operand that would be rounded is split in two bfloat16 numbers and multiplied twice.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.h"
+#include "vmscan.h"
+
+namespace {
+
+using namespace vmscan_internal;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinLog = -1e4f;  // e^-1e4 is 0 in float32; keeps sums of -inf finite
+
+struct Frag32 {
+  float v[8];
+};
+template <typename T>
+struct FragOf {
+  using type = bf16x8;
+};
+template <>
+struct FragOf<float> {
+  using type = Frag32;
+};
+template <typename T>
+using Frag = typename FragOf<T>::type;
+
+__device__ __forceinline__ f32x4 mma(const bf16x8& a, const bf16x8& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag32& a, const Frag32& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+  return c;
+}
+
+// Operand whose contracted index runs along the LDS row: lane (i, g) holds row i, elements
+// 8 g .. 8 g + 7 of the 32.  `p`: the tile's row 0 at the first of the 32.
+template <int S>
+__device__ __forceinline__ bf16x8 frag_row(const uint16_t* p) {
+  const int l = threadIdx.x & 63;
+  return *reinterpret_cast<const bf16x8*>(p + (l & 15) * S + (l >> 4) * 8);
+}
+template <int S>
+__device__ __forceinline__ Frag32 frag_row(const float* p) {
+  const int l = threadIdx.x & 63;
+  Frag32 f;
+  __builtin_memcpy(f.v, __builtin_assume_aligned(p + (l & 15) * S + (l >> 4) * 8, 16), 32);
+  return f;
+}
+
+// The same with the elements in the order of frag_col: 16 t + 4 g + r.
+template <int S>
+__device__ __forceinline__ bf16x8 frag_row_perm(const uint16_t* p) {
+  const int l = threadIdx.x & 63;
+  const uint16_t* q = p + (l & 15) * S + (l >> 4) * 4;
+  const uint2 a = *reinterpret_cast<const uint2*>(q), b = *reinterpret_cast<const uint2*>(q + 16);
+  const uint4 w = make_uint4(a.x, a.y, b.x, b.y);
+  return __builtin_bit_cast(bf16x8, w);
+}
+template <int S>
+__device__ __forceinline__ Frag32 frag_row_perm(const float* p) {
+  const int l = threadIdx.x & 63;
+  const float* q = p + (l & 15) * S + (l >> 4) * 4;
+  Frag32 f;
+  __builtin_memcpy(f.v, __builtin_assume_aligned(q, 16), 16);
+  __builtin_memcpy(f.v + 4, __builtin_assume_aligned(q + 16, 16), 16);
+  return f;
+}
+
+// Operand whose contracted index runs down the LDS column: lane (i, g) holds column i, rows
+// 16 t + 4 g + r (t 0..1, r 0..3) of the 32.  `p`: row 0, first of the 16 columns.
+template <int S>
+__device__ __forceinline__ bf16x8 frag_col(const uint16_t* p) {
+  const int l = threadIdx.x & 63, i = l & 15;
+  const uint16_t* q = p + ((l >> 4) * 4 + (i >> 2)) * S + (i & 3) * 4;
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 16 * S));
+  union {
+    i16x4 h[2];
+    bf16x8 f;
+  } u;
+  u.h[0] = a;
+  u.h[1] = b;
+  return u.f;
+}
+template <int S>
+__device__ __forceinline__ Frag32 frag_col(const float* p) {
+  const int l = threadIdx.x & 63;
+  const float* q = p + (l >> 4) * 4 * S + (l & 15);
+  Frag32 f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f.v[r] = q[r * S];
+    f.v[4 + r] = q[(16 + r) * S];
+  }
+  return f;
+}
+
+// Two result tiles (rows 16 t + 4 g + r) as an operand in frag_col's order.
+__device__ __forceinline__ void pack(const float (&x)[8], bf16x8& f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = static_cast<__bf16>(x[e]);
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Frag32& f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.v[e] = x[e];
+}
+__device__ __forceinline__ float elem(const bf16x8& f, int e) { return static_cast<float>(f[e]); }
+__device__ __forceinline__ float elem(const Frag32& f, int e) { return f.v[e]; }
+
+// c += a * (f with its elements scaled by w), the scaled operand split in two where it is bfloat16.
+__device__ __forceinline__ void scale_split(const bf16x8& f, const float (&w)[8], bf16x8& hi, bf16x8& lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = static_cast<float>(f[e]) * w[e];
+    hi[e] = static_cast<__bf16>(x);
+    lo[e] = static_cast<__bf16>(x - static_cast<float>(hi[e]));
+  }
+}
+
+__device__ __forceinline__ float exp2_diff(float hi_a, float lo_a, float hi_b, float lo_b) {
+  return __builtin_amdgcn_exp2f((hi_a - hi_b) + (lo_a - lo_b));
+}
+
+// ---------------------------------------------------------------------------------------------
+// arguments
+
+struct View {  // [batch, seqlen, heads, dim], innermost contiguous; strides in elements
+  const void* p;
+  int64_t b, t, h;
+};
+
+struct LinArgs {
+  View q, k, v, dout;
+  const float* g;          // log decay
+  int64_t gb, gt, gh;      // its strides (0: broadcast)
+  const float *s0, *dsT;   // initial state; gradient of the final state
+  const int* lengths;
+  void* out;               // [batch, seqlen, heads, dv]
+  float* sT;               // final state
+  float *ds0;              // gradient of the initial state
+  void *dq, *dk_out;       // [batch, seqlen, heads, dk]: activations, or float32 where heads share q and k
+  void* dv_out;            // [batch, seqlen, heads, dv]
+  float* dg;               // [batch, seqlen, heads]
+  float *seg_s, *seg_ds;   // [batch * heads][segment][DK][DV]
+  float *seg_g;            // [batch * heads][segment]: the segment's log2 decay
+  float* states;           // [batch * heads][block][DK][DV]: the state entering each block
+  float* qa;               // [batch * heads][blocks * C]: e^{G_i} scale q_i . S do_i
+  int64_t batch;
+  int seqlen, heads, share, dk, dvd;  // share: heads per query/key head
+  int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
+  float scale;
+};
+
+template <typename T>
+struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
+  static constexpr int kWaves = std::is_same<T, float>::value ? 2 : 4;
+  static constexpr int kC = 16 * kWaves;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kPad = 16 / sizeof(T);  // LDS rows stay 16-byte aligned and rotate over the banks
+  static constexpr bool kSplit = sizeof(T) == 2;
+};
+
+// A tile of C tokens on its way from global memory to LDS.  Tokens from `live` on and channels from
+// `dim` on are not read: they enter as zeros, whatever the memory holds.
+template <typename T, int D>
+struct Tile {
+  using B = Block<T>;
+  static constexpr int kPer = 16 / sizeof(T);
+  static constexpr int kRow = D / kPer;
+  static constexpr int kN = B::kC * kRow / B::kThreads;
+  static constexpr int kStride = D + B::kPad;
+  uint4 r[kN];
+  __device__ __forceinline__ void load(const T* base, int64_t st, int t0, int live, int dim) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
+      r[i] = make_uint4(0, 0, 0, 0);
+      if (t0 + row < live && col < dim) r[i] = *reinterpret_cast<const uint4*>(base + (t0 + row) * st + col);
+    }
+  }
+  __device__ __forceinline__ void store(T* lds) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
+      *reinterpret_cast<uint4*>(lds + row * kStride + col) = r[i];
+    }
+  }
+};
+
+// The running log2 decays of a block as head and tail, by one wave: lane t takes token t0 + t.
+template <int C>
+__device__ __forceinline__ float load_g(const LinArgs& a, const float* g, int t0, int live) {
+  const int l = threadIdx.x & 63;
+  float x = 0.0f;
+  if (l < C && t0 + l < live) {
+    x = g[(t0 + l) * a.gt];
+    x = x < kMinLog ? kMinLog : x;  // NaN stays
+  }
+  return x;
+}
+template <int C>
+__device__ __forceinline__ void scan_g(float x, float* hi, float* lo) {
+  const int l = threadIdx.x & 63;
+  double s = static_cast<double>(x) * 1.4426950408889634;
+#pragma unroll
+  for (int m = 1; m < C; m <<= 1) {
+    const double up = __shfl_up(s, m);
+    if (l >= m) s += up;
+  }
+  if (l < C) {
+    const float h = static_cast<float>(s);
+    hi[l] = h;
+    lo[l] = static_cast<float>(s - static_cast<double>(h));
+  }
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+// The state, transposed in the accumulators: wave w holds columns d of its own tiles (tile index
+// w * DT + t), rows n = 16 nt + 4 g + r.
+template <typename T, int DK, int DV>
+struct State {
+  using B = Block<T>;
+  static constexpr int kDT = DK / 16 / B::kWaves;
+  static constexpr int kNT = DV / 16;
+  static constexpr int kStride = DV + B::kPad;
+  f32x4 s[kDT][kNT];
+
+  __device__ __forceinline__ static int d_of(int t) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    return (w * kDT + t) * 16 + (l & 15);
+  }
+  __device__ __forceinline__ static int n_of(int nt) { return nt * 16 + ((threadIdx.x & 63) >> 4) * 4; }
+
+  // rows of `ld` floats, of which d < dk and n < dv exist
+  __device__ __forceinline__ void load(const float* p, int dk, int dv, int ld) {
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        s[t][nt] = zero4();
+        if (p && d_of(t) < dk && n_of(nt) < dv)
+          s[t][nt] = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(d_of(t)) * ld + n_of(nt));
+      }
+  }
+  __device__ __forceinline__ void store(float* p, int dk, int dv, int ld) const {
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        if (d_of(t) < dk && n_of(nt) < dv)
+          *reinterpret_cast<f32x4*>(p + static_cast<int64_t>(d_of(t)) * ld + n_of(nt)) = s[t][nt];
+  }
+  // into LDS as an operand, [d][n]: rounded, and what the rounding left in `lo` if that is wanted
+  __device__ __forceinline__ void publish(T* hi, T* lo) const {
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const int at = d_of(t) * kStride + n_of(nt);
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<f32x4*>(hi + at) = s[t][nt];
+        } else {
+          uint32_t h[2], r[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint16_t h0 = f32_to_bf16(s[t][nt][2 * p]), h1 = f32_to_bf16(s[t][nt][2 * p + 1]);
+            h[p] = h0 | (static_cast<uint32_t>(h1) << 16);
+            if (lo) {
+              const uint16_t r0 = f32_to_bf16(s[t][nt][2 * p] - bf16_to_f32(h0));
+              const uint16_t r1 = f32_to_bf16(s[t][nt][2 * p + 1] - bf16_to_f32(h1));
+              r[p] = r0 | (static_cast<uint32_t>(r1) << 16);
+            }
+          }
+          *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
+          if (lo) *reinterpret_cast<uint2*>(lo + at) = make_uint2(r[0], r[1]);
+        }
+      }
+  }
+  // s = e^{G_C} s + sum_j w_j y_j x_j^T over the block, y [token][d], x [token][n]; forward: w_j =
+  // e^{G_C - G_j}; backward: w_j = e^{G_j} mul.
+  template <bool BACK>
+  __device__ __forceinline__ void update(const T* y, const T* x, const float* hi, const float* lo, float mul) {
+    constexpr int C = B::kC, SY = Tile<T, DK>::kStride, SX = Tile<T, DV>::kStride;
+    const int g4 = ((threadIdx.x & 63) >> 4) * 4;
+    const float eh = hi[C - 1], el = lo[C - 1];
+    const float decay = __builtin_amdgcn_exp2f(eh + el);
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) s[t][nt] *= decay;
+#pragma unroll
+    for (int kk = 0; kk < C / 32; ++kk) {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = kk * 32 + (e >> 2) * 16 + g4 + (e & 3);
+        w[e] = BACK ? mul * __builtin_amdgcn_exp2f(hi[j] + lo[j]) : exp2_diff(eh, el, hi[j], lo[j]);
+      }
+#pragma unroll
+      for (int t = 0; t < kDT; ++t) {
+        const int d0 = ((threadIdx.x >> 6) * kDT + t) * 16;
+        const Frag<T> f = frag_col<SY>(y + kk * 32 * SY + d0);
+        if constexpr (B::kSplit) {
+          Frag<T> fh, fl;
+          scale_split(f, w, fh, fl);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const Frag<T> xa = frag_col<SX>(x + kk * 32 * SX + nt * 16);
+            s[t][nt] = mma(xa, fh, s[t][nt]);
+            s[t][nt] = mma(xa, fl, s[t][nt]);
+          }
+        } else {
+          float m[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = elem(f, e) * w[e];
+          Frag<T> fm;
+          pack(m, fm);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) s[t][nt] = mma(frag_col<SX>(x + kk * 32 * SX + nt * 16), fm, s[t][nt]);
+        }
+      }
+    }
+  }
+};
+
+struct Where {  // this workgroup's place
+  int64_t bh;
+  int64_t b;
+  int h, seg, live, c0, c1;
+};
+__device__ __forceinline__ Where where(const LinArgs& a) {
+  Where w;
+  const int64_t id = blockIdx.x;
+  w.seg = static_cast<int>(id % a.segments);
+  w.bh = id / a.segments;
+  w.b = w.bh / a.heads;
+  w.h = static_cast<int>(w.bh - w.b * a.heads);
+  int n = a.seqlen;
+  if (a.lengths) {
+    n = a.lengths[w.b];
+    n = n < 0 ? 0 : n > a.seqlen ? a.seqlen : n;
+  }
+  w.live = n;
+  w.c0 = w.seg * a.per_segment;
+  const int end = w.c0 + a.per_segment;
+  w.c1 = end < a.blocks ? end : a.blocks;
+  return w;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* head(const View& v, int64_t b, int h) {
+  return static_cast<const T*>(v.p) + b * v.b + h * v.h;
+}
+
+// Results in the accumulators' layout (4 consecutive channels of one token per lane) to memory.
+__device__ __forceinline__ void store_acc(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store_acc(uint16_t* p, f32x4 v) {
+  const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+  const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+}
+
+// Zeros for the tokens [t0, t1) of a tensor with token stride `st`, `dim` (a multiple of 8) channels.
+template <int THREADS, typename O>
+__device__ __forceinline__ void zero_tokens(O* p, int64_t st, int dim, int t0, int t1) {
+  const int runs = dim / 4;
+  for (int64_t id = threadIdx.x; id < static_cast<int64_t>(t1 - t0) * runs; id += THREADS) {
+    const int64_t t = id / runs;
+    store_acc(p + (t0 + t) * st + (id - t * runs) * 4, zero4());
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// A segment's own state from a zero start: forward (k, v) or, BACK, the state's gradient (q, dout)
+// from a zero end.
+
+template <typename T, int DK, int DV, bool BACK>
+__global__ __launch_bounds__(Block<T>::kThreads) void linattn_segment_kernel(LinArgs a) {
+  using B = Block<T>;
+  constexpr int C = B::kC;
+  __shared__ __align__(16) T ys[C * Tile<T, DK>::kStride];
+  __shared__ __align__(16) T xs[C * Tile<T, DV>::kStride];
+  __shared__ float hi[C], lo[C];
+  const Where w = where(a);
+  const T* y = head<T>(BACK ? a.q : a.k, w.b, w.h / a.share);
+  const T* x = head<T>(BACK ? a.dout : a.v, w.b, w.h);
+  const int64_t yt = BACK ? a.q.t : a.k.t, xt = BACK ? a.dout.t : a.v.t;
+  const float* g = a.g + w.b * a.gb + w.h * a.gh;
+  const int wave = threadIdx.x >> 6;
+  State<T, DK, DV> st;
+  st.load(nullptr, 0, 0, 0);
+  float total = 0.0f;
+  const int live_blocks = (w.live + C - 1) / C;
+  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
+  const int n = c1 - w.c0;
+  Tile<T, DK> ty;
+  Tile<T, DV> tx;
+  float gx = 0.0f;
+  auto at = [&](int i) { return (BACK ? c1 - 1 - i : w.c0 + i) * C; };
+  if (n > 0) {
+    ty.load(y, yt, at(0), w.live, a.dk);
+    tx.load(x, xt, at(0), w.live, a.dvd);
+    gx = load_g<C>(a, g, at(0), w.live);
+  }
+  for (int i = 0; i < n; ++i) {
+    ty.store(ys);
+    tx.store(xs);
+    if (wave == i % B::kWaves) scan_g<C>(gx, hi, lo);
+    __syncthreads();
+    if (i + 1 < n) {
+      ty.load(y, yt, at(i + 1), w.live, a.dk);
+      tx.load(x, xt, at(i + 1), w.live, a.dvd);
+      gx = load_g<C>(a, g, at(i + 1), w.live);
+    }
+    total += hi[C - 1] + lo[C - 1];
+    st.template update<BACK>(ys, xs, hi, lo, a.scale);
+    __syncthreads();
+  }
+  st.store((BACK ? a.seg_ds : a.seg_s) + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+  if (!BACK && threadIdx.x == 0) a.seg_g[w.bh * a.segments + w.seg] = total;
+}
+
+// In place: each segment's own state becomes the state that enters it (BACK: the gradient at its
+// end).  A thread owns 4 elements of one (sequence, head).
+template <bool BACK>
+__global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK, int DV) {
+  const int per = DK * DV / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t bh = id / per;
+  if (bh >= a.batch * a.heads) return;
+  const int e = static_cast<int>(id - bh * per) * 4, d = e / DV, n = e % DV;
+  f32x4 run = zero4();
+  const float* first = BACK ? a.dsT : a.s0;
+  if (first && d < a.dk && n < a.dvd)
+    run = *reinterpret_cast<const f32x4*>(first + (bh * a.dk + d) * a.dvd + n);
+  float* p = (BACK ? a.seg_ds : a.seg_s) + bh * a.segments * static_cast<int64_t>(DK * DV) + e;
+  const float* g = a.seg_g + bh * a.segments;
+  for (int i = 0; i < a.segments; ++i) {
+    const int s = BACK ? a.segments - 1 - i : i;
+    f32x4* at = reinterpret_cast<f32x4*>(p + static_cast<int64_t>(s) * (DK * DV));
+    const f32x4 own = *at;
+    *at = run;
+    run = run * __builtin_amdgcn_exp2f(g[s]) + own;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// forward
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(Block<T>::kThreads) void linattn_fwd_kernel(LinArgs a) {
+  using B = Block<T>;
+  using S = State<T, DK, DV>;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  __shared__ __align__(16) T qs[C * SK];
+  __shared__ __align__(16) T ks[C * SK];
+  __shared__ __align__(16) T vs[C * SV];
+  __shared__ __align__(16) T ss[DK * SS];
+  __shared__ __align__(16) float hi[C], lo[C];
+  const Where w = where(a);
+  const T* q = head<T>(a.q, w.b, w.h / a.share);
+  const T* k = head<T>(a.k, w.b, w.h / a.share);
+  const T* v = head<T>(a.v, w.b, w.h);
+  const float* g = a.g + w.b * a.gb + w.h * a.gh;
+  T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd;
+  const int64_t ot = static_cast<int64_t>(a.heads) * a.dvd;
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+
+  S st;
+  if (a.segments > 1)
+    st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+  else
+    st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+
+  const int live_blocks = (w.live + C - 1) / C;
+  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
+  Tile<T, DK> tq, tk;
+  Tile<T, DV> tv;
+  float gx = 0.0f;
+  if (w.c0 < c1) {
+    tq.load(q, a.q.t, w.c0 * C, w.live, a.dk);
+    tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
+    tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
+    gx = load_g<C>(a, g, w.c0 * C, w.live);
+  }
+  for (int c = w.c0; c < c1; ++c) {
+    const int t0 = c * C;
+    tq.store(qs);
+    tk.store(ks);
+    tv.store(vs);
+    st.publish(ss, nullptr);
+    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
+    __syncthreads();
+    if (c + 1 < c1) {
+      tq.load(q, a.q.t, t0 + C, w.live, a.dk);
+      tk.load(k, a.k.t, t0 + C, w.live, a.dk);
+      tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
+      gx = load_g<C>(a, g, t0 + C, w.live);
+    }
+    // this wave's 16 queries: column i of every result tile
+    const int i0 = wave * 16, i = i0 + li;
+    const float gh = hi[i], gl = lo[i];
+    f32x4 acc[DV / 16];
+    {
+      // e^{G_i} S^T q_i
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = zero4();
+#pragma unroll
+      for (int kk = 0; kk < DK / 32; ++kk) {
+        const Frag<T> qp = frag_row_perm<SK>(qs + i0 * SK + kk * 32);
+#pragma unroll
+        for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), qp, acc[nt]);
+      }
+      const float e = __builtin_amdgcn_exp2f(gh + gl);
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] *= e;
+    }
+    Frag<T> qf[DK / 32];
+#pragma unroll
+    for (int kk = 0; kk < DK / 32; ++kk) qf[kk] = frag_row<SK>(qs + i0 * SK + kk * 32);
+    // the masked scores of 32 keys at a time, then their product with the values
+    for (int jj = 0; jj <= wave / 2; ++jj) {
+      float p[8];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j0 = jj * 32 + t * 16;
+        f32x4 sc = zero4();
+        if (j0 <= i0) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 32; ++kk) sc = mma(frag_row<SK>(ks + j0 * SK + kk * 32), qf[kk], sc);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + g4 + r;
+          const float e = exp2_diff(gh, gl, hi[j], lo[j]);
+          p[t * 4 + r] = j <= i ? sc[r] * e : 0.0f;
+        }
+      }
+      Frag<T> pf;
+      pack(p, pf);
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = mma(frag_col<SV>(vs + jj * 32 * SV + nt * 16), pf, acc[nt]);
+    }
+    if (t0 + i < w.live) {
+      T* o = out + (t0 + i) * ot;
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt)
+        if (nt * 16 + g4 < a.dvd) store_acc(o + nt * 16 + g4, acc[nt] * a.scale);
+    }
+    st.template update<false>(ks, vs, hi, lo, 1.0f);
+    __syncthreads();
+  }
+  // tokens past the row's length
+  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
+  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
+  zero_tokens<B::kThreads>(out, ot, a.dvd, t_dead, t_end);
+  if (a.sT && w.seg == a.segments - 1) st.store(a.sT + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
+}
+
+// ---------------------------------------------------------------------------------------------
+// gradient
+//
+// With R the gradient of the state leaving a block (it includes every later token) and X_ij =
+// scale e^{G_i - G_j} (do_i . v_j), P_ij = scale e^{G_i - G_j} (q_i . k_j) for j <= i:
+//   dq_i = e^{G_i} scale S do_i + sum_j X_ij k_j          (walk forwards, carrying S)
+//   dk_j = e^{G_C - G_j} R v_j  + sum_i X_ij q_i          (walk backwards, carrying R)
+//   dv_j = e^{G_C - G_j} R^T k_j + sum_i P_ij do_i
+//   R'   = e^{G_C} R + sum_i e^{G_i} scale q_i do_i^T.
+// The decay of token t multiplies every contribution from a token before t to one at or after it,
+// so its logarithm's gradient is the sum of those contributions, here split by where the two lie:
+// both in the block (M_ij = scale e^{G_i - G_j} (q_i . k_j)(do_i . v_j)), before and in it (a_i = q_i .
+// the first term of dq_i), in and after it (b_j = k_j . the first term of dk_j), before and after it
+// (Y = e^{G_C} <S, R>):
+//   dg_t = sum_{j < t <= i} M_ij + sum_{i >= t} a_i + sum_{j < t} b_j + Y.
+// Summing q . dq - k . dk over all later tokens would give the same with two dot products, but as a
+// small difference of sums over the whole sequence; here only terms that belong are added.
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs a) {
+  using B = Block<T>;
+  using S = State<T, DK, DV>;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  __shared__ __align__(16) T ks[C * SK];
+  __shared__ __align__(16) T vs[C * SV];
+  __shared__ __align__(16) T os[C * SV];
+  __shared__ __align__(16) T ss[(B::kSplit ? 2 : 1) * DK * SS];
+  __shared__ __align__(16) float hi[C], lo[C];
+  T* const sl = B::kSplit ? ss + DK * SS : nullptr;
+  const Where w = where(a);
+  const T* q = head<T>(a.q, w.b, w.h / a.share);
+  const T* k = head<T>(a.k, w.b, w.h / a.share);
+  const T* v = head<T>(a.v, w.b, w.h);
+  const T* o = head<T>(a.dout, w.b, w.h);
+  const float* g = a.g + w.b * a.gb + w.h * a.gh;
+  const int64_t ot = static_cast<int64_t>(a.heads) * a.dk, obase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+
+  S st;
+  if (a.segments > 1)
+    st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+  else
+    st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+
+  const int live_blocks = (w.live + C - 1) / C;
+  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
+  Tile<T, DK> tk;
+  Tile<T, DV> tv, to;
+  float gx = 0.0f;
+  if (w.c0 < c1) {
+    tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
+    tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
+    to.load(o, a.dout.t, w.c0 * C, w.live, a.dvd);
+    gx = load_g<C>(a, g, w.c0 * C, w.live);
+  }
+  for (int c = w.c0; c < c1; ++c) {
+    const int t0 = c * C;
+    tk.store(ks);
+    tv.store(vs);
+    to.store(os);
+    st.publish(ss, sl);
+    st.store(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
+    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
+    __syncthreads();
+    const int i0 = wave * 16, i = i0 + li;
+    const bool live = t0 + i < w.live;
+    // this lane's 4 channels of its query, for a_i
+    f32x4 qv[DK / 16];
+#pragma unroll
+    for (int dt = 0; dt < DK / 16; ++dt) {
+      qv[dt] = zero4();
+      if (live && dt * 16 + g4 < a.dk) {
+        const T* qp = q + (t0 + i) * a.q.t + dt * 16 + g4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) qv[dt][r] = load1(qp + r);
+      }
+    }
+    if (c + 1 < c1) {
+      tk.load(k, a.k.t, t0 + C, w.live, a.dk);
+      tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
+      to.load(o, a.dout.t, t0 + C, w.live, a.dvd);
+      gx = load_g<C>(a, g, t0 + C, w.live);
+    }
+    const float gh = hi[i], gl = lo[i];
+    Frag<T> of[DV / 32];
+#pragma unroll
+    for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<SV>(os + i0 * SV + kk * 32);
+    f32x4 acc[DK / 16];
+    float dot = 0.0f;
+    const float e0 = __builtin_amdgcn_exp2f(gh + gl) * a.scale;
+#pragma unroll
+    for (int dt = 0; dt < DK / 16; ++dt) {
+      acc[dt] = zero4();
+#pragma unroll
+      for (int kk = 0; kk < DV / 32; ++kk) {
+        acc[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+        if constexpr (B::kSplit) acc[dt] = mma(frag_row<SS>(sl + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+      }
+      acc[dt] *= e0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dot = __builtin_fmaf(acc[dt][r], qv[dt][r], dot);
+    }
+    dot += __shfl_xor(dot, 16);
+    dot += __shfl_xor(dot, 32);
+    if (l < 16) a.qa[w.bh * a.blocks * C + t0 + i] = dot;
+    for (int jj = 0; jj <= wave / 2; ++jj) {
+      float p[8];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j0 = jj * 32 + t * 16;
+        f32x4 dp = zero4();
+        if (j0 <= i0) {
+#pragma unroll
+          for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(vs + j0 * SV + kk * 32), of[kk], dp);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + g4 + r;
+          const float e = exp2_diff(gh, gl, hi[j], lo[j]) * a.scale;
+          p[t * 4 + r] = j <= i ? dp[r] * e : 0.0f;
+        }
+      }
+      Frag<T> pf;
+      pack(p, pf);
+#pragma unroll
+      for (int dt = 0; dt < DK / 16; ++dt) acc[dt] = mma(frag_col<SK>(ks + jj * 32 * SK + dt * 16), pf, acc[dt]);
+    }
+    if (live) {
+#pragma unroll
+      for (int dt = 0; dt < DK / 16; ++dt)
+        if (dt * 16 + g4 < a.dk) {
+          const int64_t at = obase + (t0 + i) * ot + dt * 16 + g4;
+          if (a.share == 1)
+            store_acc(static_cast<T*>(a.dq) + at, acc[dt]);
+          else
+            store_acc(static_cast<float*>(a.dq) + at, acc[dt]);
+        }
+    }
+    st.template update<false>(ks, vs, hi, lo, 1.0f);
+    __syncthreads();
+  }
+  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
+  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
+  if (a.share == 1)
+    zero_tokens<B::kThreads>(static_cast<T*>(a.dq) + obase, ot, a.dk, t_dead, t_end);
+  else
+    zero_tokens<B::kThreads>(static_cast<float*>(a.dq) + obase, ot, a.dk, t_dead, t_end);
+}
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs a) {
+  using B = Block<T>;
+  using S = State<T, DK, DV>;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  __shared__ __align__(16) T qs[C * SK];
+  __shared__ __align__(16) T ks[C * SK];
+  __shared__ __align__(16) T vs[C * SV];
+  __shared__ __align__(16) T os[C * SV];
+  __shared__ __align__(16) T ss[(B::kSplit ? 2 : 1) * DK * SS];
+  __shared__ __align__(16) float hi[C], lo[C];
+  __shared__ float rows[B::kWaves][C], after[C], across[B::kWaves];
+  T* const sl = B::kSplit ? ss + DK * SS : nullptr;
+  const Where w = where(a);
+  const T* q = head<T>(a.q, w.b, w.h / a.share);
+  const T* k = head<T>(a.k, w.b, w.h / a.share);
+  const T* v = head<T>(a.v, w.b, w.h);
+  const T* o = head<T>(a.dout, w.b, w.h);
+  const float* g = a.g + w.b * a.gb + w.h * a.gh;
+  const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
+  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+
+  S st;
+  if (a.segments > 1)
+    st.load(a.seg_ds + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+  else
+    st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+
+  const int live_blocks = (w.live + C - 1) / C;
+  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
+  Tile<T, DK> tq, tk;
+  Tile<T, DV> tv, to;
+  float gx = 0.0f;
+  auto load = [&](int t0) {
+    tq.load(q, a.q.t, t0, w.live, a.dk);
+    tk.load(k, a.k.t, t0, w.live, a.dk);
+    tv.load(v, a.v.t, t0, w.live, a.dvd);
+    to.load(o, a.dout.t, t0, w.live, a.dvd);
+    gx = load_g<C>(a, g, t0, w.live);
+  };
+  if (w.c0 < c1) load((c1 - 1) * C);
+  for (int c = c1 - 1; c >= w.c0; --c) {
+    const int t0 = c * C;
+    tq.store(qs);
+    tk.store(ks);
+    tv.store(vs);
+    to.store(os);
+    st.publish(ss, sl);
+    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
+    __syncthreads();
+    if (c > w.c0) load(t0 - C);
+    {
+      // Y: the state that entered the block against R, both in this wave's layout
+      const float* p = a.states + (w.bh * a.blocks + c) * (DK * DV);
+      float y = 0.0f;
+#pragma unroll
+      for (int t = 0; t < S::kDT; ++t)
+#pragma unroll
+        for (int nt = 0; nt < S::kNT; ++nt) {
+          const f32x4 s = *reinterpret_cast<const f32x4*>(p + S::d_of(t) * DV + S::n_of(nt));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(s[r], st.s[t][nt][r], y);
+        }
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) y += __shfl_xor(y, m);
+      if (l == 0) across[wave] = y * __builtin_amdgcn_exp2f(hi[C - 1] + lo[C - 1]);
+    }
+    // this wave's 16 keys: column j of every result tile
+    const int j0 = wave * 16, j = j0 + li;
+    const float gh = hi[j], gl = lo[j];
+    const float ec = exp2_diff(hi[C - 1], lo[C - 1], gh, gl);
+    Frag<T> kf[DK / 32], vf[DV / 32];
+#pragma unroll
+    for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<SK>(ks + j0 * SK + kk * 32);
+#pragma unroll
+    for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<SV>(vs + j0 * SV + kk * 32);
+    f32x4 ak[DK / 16], av[DV / 16];
+    float bj = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < DK / 16; ++dt) {
+      ak[dt] = zero4();
+#pragma unroll
+      for (int kk = 0; kk < DV / 32; ++kk) {
+        ak[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
+        if constexpr (B::kSplit) ak[dt] = mma(frag_row<SS>(sl + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
+      }
+      ak[dt] *= ec;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) bj = __builtin_fmaf(ak[dt][r], load1(ks + j * SK + dt * 16 + g4 + r), bj);
+    }
+#pragma unroll
+    for (int nt = 0; nt < DV / 16; ++nt) av[nt] = zero4();
+#pragma unroll
+    for (int kk = 0; kk < DK / 32; ++kk) {
+      const Frag<T> kp = frag_row_perm<SK>(ks + j0 * SK + kk * 32);
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt) av[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), kp, av[nt]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < DV / 16; ++nt) av[nt] *= ec;
+
+    // Queries from the last 32 down.  Beside the products, M_ij summed over the queries from t on (in
+    // this lane's column; `later`: the tiles done) and then over the keys before t.
+    float later = 0.0f;
+    for (int ii = C / 32 - 1; ii >= wave / 2; --ii) {
+      float p[8], x[8];
+#pragma unroll
+      for (int t = 1; t >= 0; --t) {
+        const int i0 = ii * 32 + t * 16;
+        f32x4 sc = zero4(), dp = zero4();
+        if (i0 >= j0) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 32; ++kk) sc = mma(frag_row<SK>(qs + i0 * SK + kk * 32), kf[kk], sc);
+#pragma unroll
+          for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(os + i0 * SV + kk * 32), vf[kk], dp);
+        }
+        float u[4];
+#pragma unroll
+        for (int r = 3; r >= 0; --r) {
+          const int i = i0 + g4 + r;
+          const float e = exp2_diff(hi[i], lo[i], gh, gl) * a.scale;
+          p[t * 4 + r] = i >= j ? sc[r] * e : 0.0f;
+          x[t * 4 + r] = i >= j ? dp[r] * e : 0.0f;
+          u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
+        }
+        float sum = u[0];  // of this lane's rows and those below them
+        float down = __shfl_down(sum, 16);
+        sum += g4 < 12 ? down : 0.0f;
+        down = __shfl_down(sum, 32);
+        sum += g4 < 8 ? down : 0.0f;
+        down = __shfl_down(sum, 16);
+        const float below = (g4 < 12 ? down : 0.0f) + later;
+        later += __shfl(sum, li);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = i0 + g4 + r;
+          float m = j < i ? u[r] + below : 0.0f;
+#pragma unroll
+          for (int s = 1; s < 16; s <<= 1) m += __shfl_xor(m, s);
+          if (li == 0) rows[wave][i] = m;
+        }
+      }
+      Frag<T> pf, xf;
+      pack(p, pf);
+      pack(x, xf);
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt) av[nt] = mma(frag_col<SV>(os + ii * 32 * SV + nt * 16), pf, av[nt]);
+#pragma unroll
+      for (int dt = 0; dt < DK / 16; ++dt) ak[dt] = mma(frag_col<SK>(qs + ii * 32 * SK + dt * 16), xf, ak[dt]);
+    }
+    bj += __shfl_xor(bj, 16);
+    bj += __shfl_xor(bj, 32);
+    if (l < 16) after[j] = bj;
+    if (t0 + j < w.live) {
+#pragma unroll
+      for (int dt = 0; dt < DK / 16; ++dt)
+        if (dt * 16 + g4 < a.dk) {
+          const int64_t at = kbase + (t0 + j) * kt + dt * 16 + g4;
+          if (a.share == 1)
+            store_acc(static_cast<T*>(a.dk_out) + at, ak[dt]);
+          else
+            store_acc(static_cast<float*>(a.dk_out) + at, ak[dt]);
+        }
+#pragma unroll
+      for (int nt = 0; nt < DV / 16; ++nt)
+        if (nt * 16 + g4 < a.dvd) store_acc(static_cast<T*>(a.dv_out) + vbase + (t0 + j) * vt + nt * 16 + g4, av[nt]);
+    }
+    st.template update<true>(qs, os, hi, lo, a.scale);
+    __syncthreads();
+    if (wave == c % B::kWaves) {
+      // lane t: token t0 + t.  The other waves write these arrays again only past the next barrier.
+      const bool mine = l < C && t0 + l < w.live;
+      float from = 0.0f, before = 0.0f, y = 0.0f;
+      if (mine) {
+        from = a.qa[w.bh * a.blocks * C + t0 + l];
+        before = after[l];
+        for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
+      }
+#pragma unroll
+      for (int i = 0; i < B::kWaves; ++i) y += across[i];
+#pragma unroll
+      for (int m = 1; m < C; m <<= 1) {
+        const float down = __shfl_down(from, m), up = __shfl_up(before, m);
+        if (l + m < C) from += down;
+        if (l >= m) before += up;
+      }
+      before = __shfl_up(before, 1);
+      if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + (l ? before : 0.0f) + y;
+    }
+  }
+  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
+  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
+  if (a.share == 1)
+    zero_tokens<B::kThreads>(static_cast<T*>(a.dk_out) + kbase, kt, a.dk, t_dead, t_end);
+  else
+    zero_tokens<B::kThreads>(static_cast<float*>(a.dk_out) + kbase, kt, a.dk, t_dead, t_end);
+  zero_tokens<B::kThreads>(static_cast<T*>(a.dv_out) + vbase, vt, a.dvd, t_dead, t_end);
+  for (int64_t t = t_dead + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads) dg[t * a.heads] = 0.0f;
+  if (a.ds0 && w.seg == 0) st.store(a.ds0 + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
+}
+
+// dq and dk of a shared head: the sum over the heads that read it, rounded once.  `in` is [tokens]
+// [heads][dim] float32, `out` [tokens][heads / share][dim]; a thread takes 4 channels.
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restrict__ in, T* __restrict__ out,
+                                                            int64_t tokens, int heads, int share, int dim) {
+  const int runs = dim / 4, per = heads / share * runs;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t t = id / per;
+  if (t >= tokens) return;
+  const int rest = static_cast<int>(id - t * per), hk = rest / runs, c = rest % runs * 4;
+  const float* p = in + (t * heads + static_cast<int64_t>(hk) * share) * dim + c;
+  f32x4 s = *reinterpret_cast<const f32x4*>(p);
+  for (int i = 1; i < share; ++i) s += *reinterpret_cast<const f32x4*>(p + i * dim);
+  store_acc(out + t * (heads / share) * dim + hk * dim + c, s);
+}
+
+// The gradient of a decay that all tokens of a head share: kDecayParts partial sums of dg, then
+// their sum, each in a fixed order.
+constexpr int kDecayParts = 64;
+__global__ __launch_bounds__(256) void linattn_decay_kernel(const float* __restrict__ in, float* __restrict__ out,
+                                                            int64_t n, int heads) {
+  __shared__ float s[256];
+  const int h = blockIdx.x, parts = gridDim.y;
+  float t = 0.0f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(parts) * 256)
+    t += in[i * heads + h];
+  s[threadIdx.x] = t;
+  __syncthreads();
+#pragma unroll
+  for (int m = 128; m >= 1; m >>= 1) {
+    if (threadIdx.x < m) s[threadIdx.x] += s[threadIdx.x + m];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) out[static_cast<int64_t>(blockIdx.y) * heads + h] = s[0];
+}
+
+// ---------------------------------------------------------------------------------------------
+// single tokens
+
+struct StepArgs {
+  View q, k, v;  // t stride unused
+  const float* g;
+  int64_t gb, gh;
+  float* state;
+  const int* slots;
+  void* out;
+  int64_t batch, pool;
+  int heads, share, dk, dv;
+  float scale;
+};
+
+// One workgroup per (sequence, head, 64 columns): 16 lanes hold 4 columns each, 16 rows at a time.
+// The state is read once and written once in 16-byte accesses, which is all the time there is to
+// it; the products are float32.
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
+  __shared__ float qs[128], ks[128];
+  __shared__ __align__(16) float red[4][64];
+  const int64_t bh = blockIdx.x;
+  const int64_t b = bh / a.heads;
+  const int h = static_cast<int>(bh - b * a.heads);
+  const int n = blockIdx.y * 64 + (threadIdx.x & 15) * 4, row = threadIdx.x >> 4;
+  const int64_t slot = a.slots ? a.slots[b] : b;
+  T* out = static_cast<T*>(a.out) + bh * a.dv;
+  if (slot < 0 || slot >= a.pool) {  // no state: the row is skipped
+    if (threadIdx.x < 16 && n < a.dv) store_acc(out + n, zero4());
+    return;
+  }
+  float* s = a.state + (slot * a.heads + h) * static_cast<int64_t>(a.dk) * a.dv + n;
+  const bool mine = n < a.dv;
+  f32x4 st[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = i * 16 + row;
+    st[i] = zero4();
+    if (mine && d < a.dk) st[i] = *reinterpret_cast<const f32x4*>(s + static_cast<int64_t>(d) * a.dv);
+  }
+  const int hk = h / a.share;
+  if (threadIdx.x < a.dk) {
+    qs[threadIdx.x] = load1(static_cast<const T*>(a.q.p) + b * a.q.b + hk * a.q.h + threadIdx.x);
+    ks[threadIdx.x] = load1(static_cast<const T*>(a.k.p) + b * a.k.b + hk * a.k.h + threadIdx.x);
+  }
+  f32x4 v = zero4();
+  if (mine) {
+    const T* vp = static_cast<const T*>(a.v.p) + b * a.v.b + h * a.v.h + n;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = load1(vp + r);
+  }
+  const float decay = __builtin_amdgcn_exp2f(a.g[b * a.gb + h * a.gh] * kLog2e);
+  __syncthreads();
+  f32x4 o = zero4();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = i * 16 + row;
+    if (mine && d < a.dk) {
+      const f32x4 u = st[i] * decay + v * ks[d];
+      *reinterpret_cast<f32x4*>(s + static_cast<int64_t>(d) * a.dv) = u;
+      o += u * qs[d];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    o[r] += __shfl_xor(o[r], 16);
+    o[r] += __shfl_xor(o[r], 32);
+  }
+  if ((threadIdx.x & 63) < 16) *reinterpret_cast<f32x4*>(&red[threadIdx.x >> 6][(threadIdx.x & 15) * 4]) = o;
+  __syncthreads();
+  if (threadIdx.x < 16 && mine) {
+    f32x4 t = zero4();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t += *reinterpret_cast<const f32x4*>(&red[i][threadIdx.x * 4]);
+    store_acc(out + n, t * a.scale);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+
+constexpr int kMaxHeadDim = 128;
+constexpr int64_t kFillBlocks = 1024;   // workgroups wanted before a sequence is walked whole
+constexpr int kMinSegment = 2;          // blocks
+
+int pad_dim(int d) { return d <= 64 ? 64 : 128; }
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct Plan {
+  int blocks, segments, per;
+};
+Plan plan(int64_t batch, int64_t seqlen, int heads, vmscan_dtype dtype) {
+  const int C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
+  Plan p;
+  p.blocks = static_cast<int>((seqlen + C - 1) / C);
+  const int64_t bh = batch * heads;
+  int64_t seg = (kFillBlocks + bh - 1) / bh;
+  if (seg > p.blocks / kMinSegment) seg = p.blocks / kMinSegment;
+  if (seg < 1 || 2 * bh > kFillBlocks) seg = 1;
+  p.per = static_cast<int>((p.blocks + seg - 1) / seg);
+  p.segments = (p.blocks + p.per - 1) / p.per;
+  return p;
+}
+
+bool sizes_ok(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv) {
+  if (batch < 1 || seqlen < 1 || heads < 1 || kheads < 1 || dk < 1 || dv < 1) return false;
+  if (batch >= (int64_t{1} << 31) || seqlen >= (int64_t{1} << 30) || heads > 65536 || kheads > heads) return false;
+  return batch * heads < (int64_t{1} << 31);
+}
+bool options_ok(int heads, int kheads, int dk, int dv, vmscan_dtype dtype) {
+  return heads % kheads == 0 && dk % 8 == 0 && dv % 8 == 0 && dk <= kMaxHeadDim && dv <= kMaxHeadDim &&
+         (dtype == VMSCAN_F32 || dtype == VMSCAN_BF16);
+}
+
+struct Layout {
+  Plan p;
+  size_t seg_s, seg_ds, seg_g, states, qa, dq, dk, dg, parts, total;
+};
+Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv, bool per_head, vmscan_dtype dtype,
+              bool back) {
+  Layout y{};
+  y.p = plan(batch, seqlen, heads, dtype);
+  const size_t bh = static_cast<size_t>(batch) * heads, state = static_cast<size_t>(pad_dim(dk)) * pad_dim(dv) * 4;
+  const size_t C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t was = at;
+    at += round256(n);
+    return was;
+  };
+  if (y.p.segments > 1) {
+    y.seg_s = take(bh * y.p.segments * state);
+    if (back) y.seg_ds = take(bh * y.p.segments * state);
+    y.seg_g = take(bh * y.p.segments * 4);
+  }
+  if (back) {
+    y.states = take(bh * y.p.blocks * state);
+    y.qa = take(bh * y.p.blocks * C * 4);
+    if (kheads != heads) {
+      y.dq = take(bh * seqlen * dk * 4);
+      y.dk = take(bh * seqlen * dk * 4);
+    }
+    if (per_head) {
+      y.dg = take(bh * seqlen * 4);
+      y.parts = take(static_cast<size_t>(kDecayParts) * heads * 4);
+    }
+  }
+  y.total = at;
+  return y;
+}
+
+// The pointers and strides of one [batch, seqlen, heads, dim] argument: 16-byte aligned.
+vmscan_status view(View& v, const void* p, const int64_t* strides, vmscan_dtype dtype) {
+  const int64_t run = dtype == VMSCAN_F32 ? 4 : 8;
+  if (!aligned_to(p, 16)) return VMSCAN_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0) return VMSCAN_ERR_SHAPE;
+    if (strides[i] % run) return VMSCAN_ERR_ALIGN;
+  }
+  v = View{p, strides[0], strides[1], strides[2]};
+  return VMSCAN_OK;
+}
+
+template <typename F>
+void with_dims(int dk, int dv, F&& f) {
+  using std::integral_constant;
+  integral_constant<int, 64> s;
+  integral_constant<int, 128> b;
+  if (dk <= 64 && dv <= 64) f(s, s);
+  else if (dk <= 64) f(s, b);
+  else if (dv <= 64) f(b, s);
+  else f(b, b);
+}
+
+template <typename T>
+void launch_segments(const LinArgs& a, bool back, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments));
+  with_dims(a.dk, a.dvd, [&](auto dk, auto dv) {
+    constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+    const int64_t n = a.batch * a.heads * (DK * DV / 4);
+    const dim3 pgrid(static_cast<unsigned>((n + 255) / 256));
+    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false>), grid, dim3(Block<T>::kThreads), 0, stream, a);
+    hipLaunchKernelGGL((linattn_prefix_kernel<false>), pgrid, dim3(256), 0, stream, a, DK, DV);
+    if (back) {
+      hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, true>), grid, dim3(Block<T>::kThreads), 0, stream, a);
+      hipLaunchKernelGGL((linattn_prefix_kernel<true>), pgrid, dim3(256), 0, stream, a, DK, DV);
+    }
+  });
+}
+
+template <typename T>
+vmscan_status run_fwd(const LinArgs& a, hipStream_t stream) {
+  if (a.segments > 1) launch_segments<T>(a, false, stream);
+  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments));
+  with_dims(a.dk, a.dvd, [&](auto dk, auto dv) {
+    hipLaunchKernelGGL((linattn_fwd_kernel<T, decltype(dk)::value, decltype(dv)::value>), grid,
+                       dim3(Block<T>::kThreads), 0, stream, a);
+  });
+  return launched();
+}
+
+template <typename T>
+vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, void* dk, float* dg, bool per_head,
+                      hipStream_t stream) {
+  const bool shared = a.share > 1;
+  a.dq = shared ? ws + y.dq : dq;
+  a.dk_out = shared ? ws + y.dk : dk;
+  a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
+  if (a.segments > 1) launch_segments<T>(a, true, stream);
+  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments)), block(Block<T>::kThreads);
+  with_dims(a.dk, a.dvd, [&](auto k, auto v) {
+    constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
+    hipLaunchKernelGGL((linattn_dq_kernel<T, DK, DV>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((linattn_dkv_kernel<T, DK, DV>), grid, block, 0, stream, a);
+  });
+  const int64_t tokens = a.batch * a.seqlen;
+  if (shared) {
+    const int64_t n = tokens * (a.heads / a.share) * (a.dk / 4);
+    const dim3 sgrid(static_cast<unsigned>((n + 255) / 256));
+    hipLaunchKernelGGL(linattn_share_kernel<T>, sgrid, dim3(256), 0, stream, static_cast<const float*>(a.dq),
+                       static_cast<T*>(dq), tokens, a.heads, a.share, a.dk);
+    hipLaunchKernelGGL(linattn_share_kernel<T>, sgrid, dim3(256), 0, stream, static_cast<const float*>(a.dk_out),
+                       static_cast<T*>(dk), tokens, a.heads, a.share, a.dk);
+  }
+  if (per_head) {
+    float* parts = reinterpret_cast<float*>(ws + y.parts);
+    hipLaunchKernelGGL(linattn_decay_kernel, dim3(a.heads, kDecayParts), dim3(256), 0, stream, a.dg, parts, tokens,
+                       a.heads);
+    hipLaunchKernelGGL(linattn_decay_kernel, dim3(a.heads, 1), dim3(256), 0, stream, parts, dg,
+                       static_cast<int64_t>(kDecayParts), a.heads);
+  }
+  return launched();
+}
+
+// What forward and gradient check alike; fills the shared arguments.
+vmscan_status common_args(LinArgs& a, const void* q, const int64_t* qs, const void* k, const int64_t* ks,
+                          const void* v, const int64_t* vs, const float* g, const int64_t* gs, const float* s0,
+                          const int32_t* lengths, int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv,
+                          float scale, vmscan_dtype dtype) {
+  if (!q || !qs || !k || !ks || !v || !vs || !g) return VMSCAN_ERR_NULL;
+  if (!sizes_ok(batch, seqlen, heads, kheads, dk, dv)) return VMSCAN_ERR_SHAPE;
+  if (!options_ok(heads, kheads, dk, dv, dtype)) return VMSCAN_ERR_UNSUPPORTED;
+  vmscan_status st = view(a.q, q, qs, dtype);
+  if (st == VMSCAN_OK) st = view(a.k, k, ks, dtype);
+  if (st == VMSCAN_OK) st = view(a.v, v, vs, dtype);
+  if (st != VMSCAN_OK) return st;
+  if (!aligned_to(g, 4) || !aligned_to(s0, 16) || !aligned_to(lengths, 4)) return VMSCAN_ERR_ALIGN;
+  a.g = g;
+  a.gb = gs ? gs[0] : 0, a.gt = gs ? gs[1] : 0, a.gh = gs ? gs[2] : 1;
+  if (a.gb < 0 || a.gt < 0 || a.gh < 0) return VMSCAN_ERR_SHAPE;
+  a.s0 = s0, a.lengths = lengths;
+  a.batch = batch, a.seqlen = static_cast<int>(seqlen), a.heads = heads, a.share = heads / kheads;
+  a.dk = dk, a.dvd = dv, a.scale = scale;
+  return VMSCAN_OK;
+}
+
+void place(LinArgs& a, const Layout& y, unsigned char* ws) {
+  a.blocks = y.p.blocks, a.segments = y.p.segments, a.per_segment = y.p.per;
+  a.seg_s = reinterpret_cast<float*>(ws + y.seg_s);
+  a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
+  a.seg_g = reinterpret_cast<float*>(ws + y.seg_g);
+  a.states = reinterpret_cast<float*>(ws + y.states);
+  a.qa = reinterpret_cast<float*>(ws + y.qa);
+}
+
+vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, int segments) {
+  if (a.batch * a.heads * segments >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+  if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
+  return need && (!ws || have < need) ? VMSCAN_ERR_WORKSPACE : VMSCAN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t vmscan_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int dk, int dv,
+                                          vmscan_dtype dtype) {
+  if (!sizes_ok(batch, seqlen, heads, heads, dk, dv) || !options_ok(heads, heads, dk, dv, dtype)) return 0;
+  return layout(batch, seqlen, heads, heads, dk, dv, false, dtype, false).total;
+}
+
+vmscan_status vmscan_linattn_fwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                 const void* v, const int64_t* v_strides, const float* log_decay,
+                                 const int64_t* decay_strides, const float* initial_state, const int32_t* lengths,
+                                 void* out, float* final_state, int64_t batch, int64_t seqlen, int heads, int kheads,
+                                 int dk, int dv, float scale, vmscan_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+  LinArgs a{};
+  if (!out) return VMSCAN_ERR_NULL;
+  vmscan_status st = common_args(a, q, q_strides, k, k_strides, v, v_strides, log_decay, decay_strides, initial_state,
+                                 lengths, batch, seqlen, heads, kheads, dk, dv, scale, dtype);
+  if (st != VMSCAN_OK) return st;
+  if (!aligned_to(out, 16) || !aligned_to(final_state, 16)) return VMSCAN_ERR_ALIGN;
+  const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, false, dtype, false);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p.segments);
+  if (st != VMSCAN_OK) return st;
+  place(a, y, static_cast<unsigned char*>(workspace));
+  a.out = out, a.sT = final_state;
+  return dtype == VMSCAN_F32 ? run_fwd<float>(a, stream) : run_fwd<uint16_t>(a, stream);
+}
+
+size_t vmscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv,
+                                          int per_head, vmscan_dtype dtype) {
+  if (!sizes_ok(batch, seqlen, heads, kheads, dk, dv) || !options_ok(heads, kheads, dk, dv, dtype)) return 0;
+  return layout(batch, seqlen, heads, kheads, dk, dv, per_head != 0, dtype, true).total;
+}
+
+vmscan_status vmscan_linattn_bwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                 const void* v, const int64_t* v_strides, const float* log_decay,
+                                 const int64_t* decay_strides, const float* initial_state, const int32_t* lengths,
+                                 const void* dout, const int64_t* dout_strides, const float* dfinal_state, void* dq,
+                                 void* dk_out, void* dv_out, float* dlog_decay, float* dinitial_state, int64_t batch,
+                                 int64_t seqlen, int heads, int kheads, int dk, int dv, float scale,
+                                 vmscan_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  LinArgs a{};
+  if (!dout || !dout_strides || !dq || !dk_out || !dv_out || !dlog_decay) return VMSCAN_ERR_NULL;
+  vmscan_status st = common_args(a, q, q_strides, k, k_strides, v, v_strides, log_decay, decay_strides, initial_state,
+                                 lengths, batch, seqlen, heads, kheads, dk, dv, scale, dtype);
+  if (st != VMSCAN_OK) return st;
+  st = view(a.dout, dout, dout_strides, dtype);
+  if (st != VMSCAN_OK) return st;
+  const void* ptrs[] = {dfinal_state, dq, dk_out, dv_out, dinitial_state};
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return VMSCAN_ERR_ALIGN;
+  if (!aligned_to(dlog_decay, 4)) return VMSCAN_ERR_ALIGN;
+  const bool per_head = decay_strides == nullptr;
+  const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, per_head, dtype, true);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p.segments);
+  if (st != VMSCAN_OK) return st;
+  if (kheads != heads && batch * seqlen * kheads * (dk / 4) / 256 >= (int64_t{1} << 31) - 1) return VMSCAN_ERR_SHAPE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  place(a, y, ws);
+  a.dsT = dfinal_state, a.ds0 = dinitial_state, a.dv_out = dv_out;
+  return dtype == VMSCAN_F32 ? run_bwd<float>(a, y, ws, dq, dk_out, dlog_decay, per_head, stream)
+                             : run_bwd<uint16_t>(a, y, ws, dq, dk_out, dlog_decay, per_head, stream);
+}
+
+vmscan_status vmscan_linattn_step(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                  const void* v, const int64_t* v_strides, const float* log_decay,
+                                  const int64_t* decay_strides, float* state, const int32_t* slots, void* out,
+                                  int64_t batch, int64_t pool, int heads, int kheads, int dk, int dv, float scale,
+                                  vmscan_dtype dtype, hipStream_t stream) {
+  if (!q || !q_strides || !k || !k_strides || !v || !v_strides || !log_decay || !state || !out) return VMSCAN_ERR_NULL;
+  if (!sizes_ok(batch, 1, heads, kheads, dk, dv) || pool < 1 || pool >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+  if (!slots && pool != batch) return VMSCAN_ERR_SHAPE;
+  if (!options_ok(heads, kheads, dk, dv, dtype)) return VMSCAN_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k, v};
+  for (const void* p : ptrs)
+    if (!aligned_to(p, dtype == VMSCAN_F32 ? 4 : 2)) return VMSCAN_ERR_ALIGN;
+  if (!aligned_to(state, 16) || !aligned_to(out, 16) || !aligned_to(log_decay, 4) || !aligned_to(slots, 4))
+    return VMSCAN_ERR_ALIGN;
+  StepArgs a{};
+  a.q = View{q, q_strides[0], 0, q_strides[1]};
+  a.k = View{k, k_strides[0], 0, k_strides[1]};
+  a.v = View{v, v_strides[0], 0, v_strides[1]};
+  a.g = log_decay;
+  a.gb = decay_strides ? decay_strides[0] : 0, a.gh = decay_strides ? decay_strides[1] : 1;
+  a.state = state, a.slots = slots, a.out = out, a.batch = batch, a.pool = pool;
+  a.heads = heads, a.share = heads / kheads, a.dk = dk, a.dv = dv, a.scale = scale;
+  const dim3 grid(static_cast<unsigned>(batch * heads), static_cast<unsigned>((dv + 63) / 64));
+  if (dtype == VMSCAN_F32)
+    hipLaunchKernelGGL(linattn_step_kernel<float>, grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL(linattn_step_kernel<uint16_t>, grid, dim3(256), 0, stream, a);
+  return launched();
+}
+
+}  // extern "C"

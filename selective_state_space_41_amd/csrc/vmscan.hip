@@ -64,6 +64,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "internal.h"
 #include "vmscan.h"
 
 namespace {
@@ -2172,10 +2173,16 @@ bool shape_ok(int64_t batch, int64_t dim, int64_t L) {
   return true;
 }
 
-vmscan_status launch_failed(hipError_t e) {
+}  // namespace
+
+vmscan_status vmscan_internal::launch_failed(hipError_t e) {
   g_last_hip_error = static_cast<int>(e);
   return VMSCAN_ERR_HIP;
 }
+
+namespace {
+
+using vmscan_internal::launch_failed;
 
 // The end of an entry point.  In a build with VMSCAN_CHECK_WAITS the call waits for its kernels and
 // reads the workspace's status word, so that a wait between state parts that gave up is reported
@@ -3750,8 +3757,9 @@ const char* vmscan_status_string(vmscan_status s) {
     case VMSCAN_ERR_NULL: return "VMSCAN_ERR_NULL: a required pointer is NULL";
     case VMSCAN_ERR_SHAPE: return "VMSCAN_ERR_SHAPE: a size is < 1 or too large";
     case VMSCAN_ERR_UNSUPPORTED:
-      return "VMSCAN_ERR_UNSUPPORTED: d_state must be 16 or 32 and dtype F32 or BF16";
-    case VMSCAN_ERR_ALIGN: return "VMSCAN_ERR_ALIGN: a pointer is not 16-byte aligned";
+      return "VMSCAN_ERR_UNSUPPORTED: d_state must be 16 or 32 and dtype F32 or BF16 (other entry points: an option "
+             "they do not take)";
+    case VMSCAN_ERR_ALIGN: return "VMSCAN_ERR_ALIGN: a pointer (or a stride, where one is taken) is not 16-byte aligned";
     case VMSCAN_ERR_WORKSPACE: return "VMSCAN_ERR_WORKSPACE: workspace missing or too small";
     case VMSCAN_ERR_HIP: return "VMSCAN_ERR_HIP: a HIP call failed (see vmscan_last_hip_error)";
     case VMSCAN_ERR_SCRATCH:

@@ -1,0 +1,149 @@
+"""C-ABI checks of the linear-attention block's entry points that need no GPU: every bad argument is
+refused with the documented status before HIP is touched.  No kernel is launched."""
+import ctypes
+import os
+
+import pytest
+
+import selective_state_space_41_amd as V
+
+ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_ALIGN, ERR_WORKSPACE = 1, 2, 3, 4, 5
+P = [0x10000 + 0x100 * i for i in range(24)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(V.LIB_PATH):
+        pytest.fail(f"{V.LIB_PATH} not built (run __graft_entry__.build())")
+    return V.load()
+
+
+def st(*s):
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+def norm(lib, **kw):
+    a = dict(x=P[0], xs=64, res=P[1], w=P[2], y=P[3], scale=None, ro=P[4], rstd=P[5], rows=0, dim=64, eps=1e-5, dt=1,
+             rdt=0, fp8=0, group=0)
+    a.update(kw)
+    return lib.vmscan_rmsnorm_fwd(*a.values(), None)
+
+
+def test_norm(lib):
+    for k in ("x", "w", "y"):
+        assert norm(lib, rows=4, **{k: None}) == ERR_NULL
+    assert norm(lib, rows=4, ro=None) == ERR_NULL and norm(lib, rows=4, res=None) == ERR_NULL
+    assert norm(lib, rows=4, fp8=1) == ERR_NULL and norm(lib, rows=4, scale=P[6]) == ERR_NULL
+    for kw in (dict(rows=0), dict(rows=-1), dict(rows=4, dim=0), dict(rows=4, dim=32769, xs=40000),
+               dict(rows=4, xs=63), dict(rows=4, eps=-1.0), dict(rows=4, eps=float("nan"))):
+        assert norm(lib, **kw) == ERR_SHAPE, kw
+    for kw in (dict(dt=0, rdt=1), dict(dt=2), dict(rdt=2), dict(fp8=2, scale=P[6]), dict(fp8=1, scale=P[6], group=64),
+               dict(group=128)):
+        assert norm(lib, rows=4, **kw) == ERR_UNSUPPORTED, kw
+    for k in ("x", "res", "w", "y", "ro", "rstd"):
+        assert norm(lib, rows=4, **{k: P[9] + 8}) == ERR_ALIGN, k
+
+
+def norm_bwd(lib, **kw):
+    a = dict(dy=P[0], r=P[1], w=P[2], rstd=P[3], dro=P[4], dx=P[5], dres=P[6], dw=P[7], rows=4, dim=64, dt=1, rdt=0,
+             ws=P[8], wsb=1 << 20)
+    a.update(kw)
+    return lib.vmscan_rmsnorm_bwd(*a.values(), None)
+
+
+def test_norm_bwd(lib):
+    for k in ("dy", "r", "w", "rstd", "dx", "dw"):
+        assert norm_bwd(lib, **{k: None}) == ERR_NULL
+    assert norm_bwd(lib, rows=0) == ERR_SHAPE and norm_bwd(lib, dim=40000) == ERR_SHAPE
+    assert norm_bwd(lib, dt=1, rdt=1) == ERR_UNSUPPORTED  # one type: dx is the residual's gradient
+    assert norm_bwd(lib, dt=0, rdt=1, dres=None) == ERR_UNSUPPORTED
+    assert norm_bwd(lib, dx=P[5] + 4) == ERR_ALIGN
+    need = lib.vmscan_rmsnorm_bwd_workspace_bytes(4, 64)
+    assert need > 0 and lib.vmscan_rmsnorm_bwd_workspace_bytes(0, 64) == 0
+    assert norm_bwd(lib, wsb=need - 1) == ERR_WORKSPACE and norm_bwd(lib, ws=None) == ERR_WORKSPACE
+
+
+def rope(lib, **kw):
+    s = st(4096, 128, 32)
+    a = dict(q=P[0], qs=s, qo=P[1], qos=s, k=P[2], ks=s, ko=P[3], kos=s, pos=P[4], ps=0, f=P[5], axis=P[6], nb=2, L=9,
+             H=4, Hk=4, dim=32, rot=32, axes=2, inter=0, inv=0, dt=1)
+    a.update(kw)
+    return lib.vmscan_rope_axes(*a.values(), None)
+
+
+def test_rope(lib):
+    for k in ("q", "qs", "qo", "qos", "k", "ks", "ko", "kos", "pos", "f", "axis"):
+        assert rope(lib, **{k: None}) == ERR_NULL, k
+    for kw in (dict(nb=0), dict(L=0), dict(H=0), dict(Hk=-1), dict(dim=0), dict(rot=0), dict(rot=31), dict(rot=34),
+               dict(axes=0), dict(ps=-1), dict(L=1 << 31)):
+        assert rope(lib, **kw) == ERR_SHAPE, kw
+    for kw in (dict(dt=2), dict(inter=2), dict(inv=-1)):
+        assert rope(lib, **kw) == ERR_UNSUPPORTED, kw
+    assert rope(lib, q=P[0] + 1) == ERR_ALIGN and rope(lib, f=P[5] + 2) == ERR_ALIGN
+
+
+def fwd(lib, **kw):
+    s = st(1024, 128, 32)
+    a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, s0=P[4], n=P[5], out=P[6], sT=P[7], nb=2, L=300,
+             H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1, ws=P[8], wsb=0)
+    a.update(kw)
+    return lib.vmscan_linattn_fwd(*a.values(), None)
+
+
+def bwd(lib, **kw):
+    s = st(1024, 128, 32)
+    a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, s0=P[4], n=P[5], do=P[6], dos=s, dsT=P[7],
+             dq=P[8], dk_=P[9], dv_=P[10], dg=P[11], ds0=P[12], nb=2, L=300, H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1,
+             ws=P[13], wsb=0)
+    a.update(kw)
+    return lib.vmscan_linattn_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd], ids=["fwd", "bwd"])
+def test_linattn(lib, call):
+    need = ["q", "qs", "k", "ks", "v", "vs", "g"] + (["out"] if call is fwd else ["do", "dos", "dq", "dk_", "dv_", "dg"])
+    for k in need:
+        assert call(lib, **{k: None}) == ERR_NULL, k
+    for kw in (dict(nb=0), dict(L=0), dict(L=1 << 30), dict(H=0), dict(Hk=0), dict(dk=0), dict(dv=0), dict(Hk=8),
+               dict(qs=st(-1024, 128, 32)), dict(gs=st(-1, 4, 1))):
+        assert call(lib, **kw) == ERR_SHAPE, kw
+    for kw in (dict(Hk=3), dict(dk=12), dict(dv=20), dict(dk=136), dict(dv=136), dict(dt=2)):
+        assert call(lib, **kw) == ERR_UNSUPPORTED, kw
+    for kw in (dict(q=P[0] + 8), dict(ks=st(1024, 132, 32)), dict(vs=st(1024, 128, 33)), dict(s0=P[4] + 4),
+               dict(n=P[5] + 1), dict(g=P[3] + 2), dict(ws=P[8] + 4, wsb=1 << 30)):
+        assert call(lib, **kw) == ERR_ALIGN, kw
+    assert call(lib) == ERR_WORKSPACE and call(lib, ws=None, wsb=1 << 30) == ERR_WORKSPACE
+
+
+def test_linattn_workspace(lib):
+    f, b = lib.vmscan_linattn_fwd_workspace_bytes, lib.vmscan_linattn_bwd_workspace_bytes
+    assert f(128, 197, 12, 64, 64, 1) == 0            # enough pairs: no segments
+    assert f(1, 6085, 6, 64, 64, 1) > 0
+    assert f(1, 64, 1, 64, 64, 1) == 0                # one block
+    for bad in ((0, 9, 4, 32, 32, 1), (1, 0, 4, 32, 32, 1), (1, 9, 4, 12, 32, 1), (1, 9, 4, 32, 136, 1),
+                (1, 9, 4, 32, 32, 2)):
+        assert f(*bad) == 0
+    assert b(2, 300, 4, 4, 32, 32, 0, 1) > 0
+    # shared heads keep dq and dk per head, one decay per head keeps the tokens' gradients
+    assert b(2, 300, 4, 2, 32, 32, 0, 1) - b(2, 300, 4, 4, 32, 32, 0, 1) >= 2 * 2 * 300 * 4 * 32 * 4
+    assert b(2, 300, 4, 4, 32, 32, 1, 1) - b(2, 300, 4, 4, 32, 32, 0, 1) >= 2 * 300 * 4 * 4
+    assert b(2, 300, 4, 3, 32, 32, 0, 1) == 0
+
+
+def step(lib, **kw):
+    s = st(128, 32)
+    a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, state=P[4], slots=P[5], out=P[6], nb=2, pool=3,
+             H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1)
+    a.update(kw)
+    return lib.vmscan_linattn_step(*a.values(), None)
+
+
+def test_step(lib):
+    for k in ("q", "qs", "k", "ks", "v", "vs", "g", "state", "out"):
+        assert step(lib, **{k: None}) == ERR_NULL, k
+    for kw in (dict(nb=0), dict(pool=0), dict(H=0), dict(dk=0), dict(slots=None)):
+        assert step(lib, **kw) == ERR_SHAPE, kw
+    for kw in (dict(Hk=3), dict(dk=12), dict(dv=136), dict(dt=5)):
+        assert step(lib, **kw) == ERR_UNSUPPORTED, kw
+    for kw in (dict(q=P[0] + 1), dict(state=P[4] + 4), dict(out=P[6] + 8), dict(slots=P[5] + 2)):
+        assert step(lib, **kw) == ERR_ALIGN, kw

@@ -1,0 +1,405 @@
+"""Linear attention with a decay for each head on the GPU against the fp64 oracle.
+
+Tolerance, element by element: |y - r| <= OUT |r| + SUM S, where S is the oracle's value on the
+absolute values of all inputs, i.e. the sum of the magnitudes of the terms that make up y.
+  * float32: every product and sum is float32; an output is a dot product over dk (or dv) inside one
+    over the tokens of a block, added to a carried state: at most 128 + 64 roundings of 2^-24 along a
+    path plus a few for the decays (each exp2 is within an ulp, its argument exact to 2^-24 of itself
+    with |argument| < 64 where the term matters): SUM = 256 * 2^-24.
+  * bfloat16 (8 significant bits: nearest rounding is off by up to 2^-8): an activation output is rounded
+    once (OUT = 2^-8), and in each of its terms one operand (the score, or the state) was rounded to
+    bfloat16 once: SUM = 2^-8.
+  * float32 results of bfloat16 inputs (states and their gradients, the decays' gradient): the rounded
+    operand is carried as two bfloat16 numbers, 2^-16 of each term, at most two such operands on a
+    path (the state that entered and the block's own part): SUM = 2^-15 + 256 * 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import block_oracle as BO
+
+pytestmark = pytest.mark.gpu
+
+F32_SUM = 256 * 2.0 ** -24
+WIDE = {"f32": (0.0, F32_SUM), "bf16": (0.0, 2.0 ** -15 + F32_SUM)}  # float32 results
+ACT = {"f32": (2.0 ** -23, F32_SUM), "bf16": (2.0 ** -8, 2.0 ** -8)}  # results in the activations' type
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+
+
+def check(name, y, r, s_abs, tol):
+    y = y.double().cpu().numpy() if isinstance(y, torch.Tensor) else y
+    assert y.shape == r.shape, (name, y.shape, r.shape)
+    assert np.all(np.isfinite(y)), f"{name}: not finite"
+    room = tol[0] * np.abs(r) + tol[1] * np.abs(s_abs) + 1e-35
+    used = float(np.max(np.abs(y - r) / room)) if y.size else 0.0
+    print(f"[linattn] {name}: {used:.3f} of the tolerance", flush=True)
+    assert used <= 1.0, f"{name}: {used:.2f} times the tolerance"
+
+
+def make(seed, B, T, H, Hk, dk, dv, dtype, decay="token", strong=False):
+    rng = np.random.default_rng(seed)
+    rnd = (lambda a: synth.round_bf16(a.astype(np.float32))) if dtype == "bf16" else (lambda a: a.astype(np.float32))
+    p = dict(q=rnd(rng.standard_normal((B, T, Hk, dk))), k=rnd(rng.standard_normal((B, T, Hk, dk))),
+             v=rnd(rng.standard_normal((B, T, H, dv))), dout=rnd(rng.standard_normal((B, T, H, dv))),
+             s0=rng.standard_normal((B, H, dk, dv)).astype(np.float32),
+             dsT=rng.standard_normal((B, H, dk, dv)).astype(np.float32), dtype=dtype, scale=float(dk) ** -0.5)
+    shape = (H,) if decay == "head" else (B, T, H)
+    g = -np.exp(rng.uniform(np.log(1e-3), np.log(3.0), shape)).astype(np.float32)
+    if strong:  # steps that clear the state, nearly clear it, and keep it whole
+        g.reshape(-1)[::5] = -np.inf
+        g.reshape(-1)[1::7] = -80.0
+        g.reshape(-1)[2::9] = 0.0
+    p["g"] = g
+    return p
+
+
+def dev(p, k):
+    t = torch.from_numpy(np.ascontiguousarray(p[k])).cuda()
+    return t.to(torch.bfloat16) if p["dtype"] == "bf16" and k in ("q", "k", "v", "dout") else t
+
+
+def oracle_fwd(p, s0, lengths):
+    a = np.abs
+    r = BO.linattn(p["q"], p["k"], p["v"], p["g"], p["scale"], s0, lengths)
+    m = BO.linattn(a(p["q"]), a(p["k"]), a(p["v"]), p["g"], p["scale"], None if s0 is None else a(s0), lengths)
+    return r, m
+
+
+def oracle_bwd(p, s0, lengths, dsT):
+    a = lambda x: None if x is None else np.abs(x)
+    r = BO.linattn_bwd(p["q"], p["k"], p["v"], p["g"], p["dout"], p["scale"], s0, lengths, dsT)
+    m = BO.linattn_bwd(a(p["q"]), a(p["k"]), a(p["v"]), p["g"], a(p["dout"]), p["scale"], a(s0), lengths, a(dsT))
+    return r, m
+
+
+def run_both(name, p, state=True, lengths=None, **dev_inputs):
+    """Forward and gradient of one case against the oracle; dev_inputs replace the device tensors."""
+    import selective_state_space_41_amd as V
+    s0 = p["s0"] if state else None
+    dsT = p["dsT"] if state else None
+    t = {k: dev_inputs.get(k, dev(p, k)) for k in ("q", "k", "v", "g", "dout")}
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    ts0, tdsT = (dev(p, "s0"), dev(p, "dsT")) if state else (None, None)
+    print(f"[linattn] {name}", flush=True)
+    out, sT = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=p["scale"], initial_state=ts0, lengths=n)
+    torch.cuda.synchronize()
+    (r_out, r_sT), (m_out, m_sT) = oracle_fwd(p, s0, lengths)
+    check(f"{name} out", out, r_out, m_out, ACT[p["dtype"]])
+    check(f"{name} final_state", sT, r_sT, m_sT, WIDE[p["dtype"]])
+    g = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], scale=p["scale"], initial_state=ts0, lengths=n,
+                      dfinal_state=tdsT)
+    torch.cuda.synchronize()
+    r, m = oracle_bwd(p, s0, lengths, dsT)
+    for key in ("dq", "dk", "dv"):
+        check(f"{name} {key}", g[key], r[key], m[key], ACT[p["dtype"]])
+    check(f"{name} dlog_decay", g["dlog_decay"], r["dg"], m["dg"], WIDE[p["dtype"]])
+    if state:
+        check(f"{name} dinitial_state", g["dinitial_state"], r["ds0"], m["ds0"], WIDE[p["dtype"]])
+    else:
+        assert g["dinitial_state"] is None
+    return out, sT, g
+
+
+# one token, odd ones, block boundaries (64 bfloat16, 32 float32) and their neighbours
+LENGTHS = [1, 2, 5, 31, 32, 33, 63, 64, 65, 127, 130]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", LENGTHS)
+def test_lengths(T, dtype):
+    run_both(f"T {T} {dtype}", make(T, 2, T, 2, 2, 64, 64, dtype), state=T % 2 == 1)
+
+
+# every pair of kernel widths (64, 128) and head sizes that fill neither
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(8, 8), (16, 64), (24, 40), (32, 128), (64, 72), (72, 64), (128, 64), (128, 128),
+                                   (96, 104)])
+def test_head_sizes(dk, dv, dtype):
+    run_both(f"dk {dk} dv {dv} {dtype}", make(dk + dv, 1, 75, 2, 1, dk, dv, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (3, 3), (6, 2), (4, 1)])
+@pytest.mark.parametrize("decay", ["token", "head"])
+def test_heads(H, Hk, decay, dtype):
+    run_both(f"H {H} Hk {Hk} {decay} {dtype}", make(10 * H + Hk, 2, 70, H, Hk, 32, 32, dtype, decay), state=Hk == 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [193, 700])
+def test_segments(T, dtype):
+    """Few (sequence, head) pairs: the sequence is split into segments whose states are joined."""
+    import selective_state_space_41_amd as V
+    p = make(T, 1, T, 2, 1, 64, 64, dtype)
+    assert V.load().vmscan_linattn_fwd_workspace_bytes(1, T, 2, 64, 64, int(dtype == "bf16")) > 0
+    run_both(f"segments T {T} {dtype}", p, lengths=[T - 3])
+    run_both(f"segments T {T} {dtype} short", p, lengths=[T // 3], state=False)
+
+
+def test_whole_walk():
+    """Enough pairs that every sequence is walked by one workgroup, over several blocks."""
+    import selective_state_space_41_amd as V
+    B, T, H = 130, 150, 8
+    assert V.load().vmscan_linattn_fwd_workspace_bytes(B, T, H, 16, 16, 1) == 0
+    run_both("whole walk", make(5, B, T, H, 8, 16, 16, "bf16"), lengths=[(37 * b) % (T + 1) for b in range(B)])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_row_lengths(dtype):
+    """Rows of 0, 1 and all tokens; lengths outside 0 .. T are clamped.  What lies past a row's length
+    is never read: it holds NaN and infinities."""
+    import selective_state_space_41_amd as V
+    B, T = 6, 97
+    p = make(7, B, T, 2, 1, 32, 40, dtype)
+    lengths = [0, 1, 64, 97, -5, 1000]
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "dout")}
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), T)
+        for i, k in enumerate(t):
+            t[k][b, n:] = (float("nan"), float("inf"), -float("inf"))[(b + i) % 3]
+    out, sT, g = run_both(f"row lengths {dtype}", p, lengths=lengths, **t)
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), T)
+        for x in (out, g["dq"], g["dk"], g["dv"], g["dlog_decay"]):
+            assert torch.all(x[b, n:] == 0)
+    assert torch.equal(sT[0], dev(p, "s0")[0])  # an empty row keeps its state
+    assert torch.equal(g["dinitial_state"][0], dev(p, "dsT")[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", ["token", "head"])
+def test_strong_decays(decay, dtype):
+    """Steps of -inf, -80 and 0 among ordinary ones: nothing overflows or turns into NaN."""
+    run_both(f"strong {decay} {dtype}", make(9, 2, 140, 3, 3, 32, 32, dtype, decay, strong=True))
+
+
+def test_long_weak_and_growing():
+    """A decay near 1 over many blocks, and one slightly above 1 (taken as it is)."""
+    p = make(11, 1, 1500, 1, 1, 16, 16, "f32")
+    p["g"] = np.full((1,), -1e-4, np.float32)
+    run_both("weak", p)
+    p["g"] = np.full((1,), 1e-3, np.float32)
+    run_both("growing", p)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strides(dtype):
+    """Views of wider projections, a broadcast batch and a transposed decay."""
+    import selective_state_space_41_amd as V
+    B, T, H, dk, dv = 2, 70, 4, 32, 32
+    p = make(13, B, T, H, H, dk, dv, dtype)
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "dout")}
+    wide = torch.full((B, T + 3, 3 * H * dk + 16), 7.0, dtype=t["q"].dtype, device="cuda")
+    for i, k in enumerate("qkv"):
+        view = wide[:, 1:T + 1, 8 + i * H * dk:8 + (i + 1) * H * dk].view(B, T, H, dk)
+        view.copy_(t[k])
+        t[k] = view
+    t["g"] = t["g"].permute(2, 1, 0).contiguous().permute(2, 1, 0)
+    t["dout"] = t["dout"].permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)  # heads first in memory
+    assert not any(t[k].is_contiguous() for k in t)
+    run_both(f"strides {dtype}", p, **t)
+    # one k for the whole batch (stride 0)
+    p["k"] = np.broadcast_to(p["k"][:1], p["k"].shape)
+    t["k"] = dev(p, "k")[:1].expand(B, T, H, dk)
+    run_both(f"broadcast k {dtype}", p, **t)
+    out = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"])[0]
+    assert torch.equal(out, V.linattn_fwd(*[t[k].contiguous() for k in "qkvg"])[0])
+
+
+def test_offsets_past_32_bits():
+    """Batch rows more than 2^32 bytes (2^31 elements) apart."""
+    import selective_state_space_41_amd as V
+    B, T, H, d = 2, 66, 1, 16
+    p = make(17, B, T, H, H, d, d, "bf16")
+    gap = 2 ** 31 + 64
+    pool = torch.empty(gap + T * 3 * d, dtype=torch.bfloat16, device="cuda")
+    t = {}
+    for i, k in enumerate("qkv"):
+        t[k] = pool.as_strided((B, T, H, d), (gap, 3 * d, d, 1), i * d)
+        t[k].copy_(dev(p, k))
+    run_both("far rows", p, **t)
+    del pool, t
+    # a pool of states past 2^31 elements: the last slots
+    slots = 2 ** 31 // (8 * 64 * 64) + 3
+    state = torch.empty(slots, 8, 64, 64, device="cuda")
+    q = make(18, 2, 1, 8, 8, 64, 64, "bf16")
+    state[-1], state[0] = dev(q, "s0")
+    at = torch.tensor([slots - 1, 0], dtype=torch.int32, device="cuda")
+    out = V.linattn_step(dev(q, "q")[:, 0], dev(q, "k")[:, 0], dev(q, "v")[:, 0], dev(q, "g")[:, 0], state, slots=at)
+    one = dev(q, "s0")
+    want = V.linattn_step(dev(q, "q")[:, 0], dev(q, "k")[:, 0], dev(q, "v")[:, 0], dev(q, "g")[:, 0], one)
+    assert torch.equal(out, want) and torch.equal(state[-1], one[0]) and torch.equal(state[0], one[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,Hk,dk,dv,decay", [(1, 1, 8, 8, "token"), (6, 2, 64, 64, "head"), (2, 1, 128, 128, "token"),
+                                              (3, 3, 24, 72, "token"), (4, 4, 16, 128, "head")])
+def test_step(H, Hk, dk, dv, decay, dtype):
+    """One token: against the oracle, with a pool whose rows lie in any order, a row without a state
+    and states that no row names."""
+    import selective_state_space_41_amd as V
+    B, pool = 5, 9
+    p = make(dk + dv, B, 1, H, Hk, dk, dv, dtype, decay)
+    state = np.random.default_rng(1).standard_normal((pool, H, dk, dv)).astype(np.float32)
+    slots = [7, -1, 0, 3, pool]
+    one = {k: p[k][:, 0] for k in "qkv"}
+    g = p["g"] if decay == "head" else p["g"][:, 0]
+    tq, tk, tv = (dev(p, k)[:, 0] for k in "qkv")
+    tg = torch.from_numpy(np.ascontiguousarray(g)).cuda()
+    ts = torch.from_numpy(state).cuda()
+    out = V.linattn_step(tq, tk, tv, tg, ts, scale=p["scale"], slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    r, rs = BO.linattn_step(one["q"], one["k"], one["v"], g, state, p["scale"], slots)
+    m, ms = BO.linattn_step(*(np.abs(one[k]) for k in "qkv"), g, np.abs(state), p["scale"], slots)
+    check("step out", out, r, m, (ACT[dtype][0], F32_SUM))
+    check("step state", ts, rs, ms, (0.0, F32_SUM))
+    assert torch.all(out[1] == 0) and torch.all(out[4] == 0)
+    for i in set(range(pool)) - {7, 0, 3}:
+        assert np.array_equal(ts[i].cpu().numpy(), state[i])
+
+
+def test_step_follows_forward():
+    """A prompt by blocks, then token by token, equals the whole sequence by blocks."""
+    import selective_state_space_41_amd as V
+    p = make(21, 2, 80, 4, 2, 64, 64, "f32")
+    t = {k: dev(p, k) for k in "qkvg"}
+    whole, last = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"])
+    _, state = V.linattn_fwd(*[t[k][:, :77] for k in "qkvg"])
+    for i in range(77, 80):
+        out = V.linattn_step(*[t[k][:, i] for k in "qkvg"], state)
+    assert torch.allclose(out, whole[:, 79], rtol=1e-4, atol=1e-5)
+    assert torch.allclose(state, last, rtol=1e-4, atol=1e-5)
+
+
+def test_gradient_by_differences():
+    """The kernels' own gradient against differences of the kernels' own loss along random directions,
+    in float32 inputs; the loss in float64.  Central differences with step h are off by h^2 times the
+    third derivative over 6 and by the forward's rounding over h: with h = 2^-6 and losses of about a
+    thousand unit terms both stay under 1 % of the directional derivative's scale."""
+    import selective_state_space_41_amd as V
+    p = make(23, 2, 90, 2, 2, 16, 16, "f32")
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "s0")}
+    dout, dsT = dev(p, "dout"), dev(p, "dsT")
+
+    def loss(x):
+        out, sT = V.linattn_fwd(x["q"], x["k"], x["v"], x["g"], scale=p["scale"], initial_state=x["s0"])
+        return (out.double() * dout.double()).sum() + (sT.double() * dsT.double()).sum()
+
+    g = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], dout, scale=p["scale"], initial_state=t["s0"], dfinal_state=dsT)
+    names = dict(q="dq", k="dk", v="dv", g="dlog_decay", s0="dinitial_state")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for k, name in names.items():
+        step = torch.randn(t[k].shape, generator=gen, device="cuda")
+        h = 2.0 ** -6
+        hi, lo = (dict(t, **{k: t[k] + s * h * step}) for s in (1, -1))
+        want = float((loss(hi) - loss(lo)) / (2 * h))
+        got = float((g[name].double() * step.double()).sum())
+        scale = float(g[name].double().norm())
+        print(f"[linattn] differences {k}: {got:.6f} {want:.6f} scale {scale:.3f}", flush=True)
+        assert abs(got - want) <= 0.01 * scale, k
+
+
+def test_same_bits():
+    """No atomics: the same call gives the same bits, on a dirty workspace and another stream."""
+    import selective_state_space_41_amd as V
+    p = make(25, 2, 400, 4, 2, 64, 64, "bf16")
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "dout", "s0", "dsT")}
+    fwd = lambda **kw: V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], initial_state=t["s0"], **kw)
+    bwd = lambda **kw: V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], initial_state=t["s0"],
+                                     dfinal_state=t["dsT"], **kw)
+    out, sT = fwd()
+    g = bwd()
+    torch.cuda.synchronize()
+    lib = V.load()
+    n = max(lib.vmscan_linattn_fwd_workspace_bytes(2, 400, 4, 64, 64, 1),
+            lib.vmscan_linattn_bwd_workspace_bytes(2, 400, 4, 2, 64, 64, 0, 1))
+    stream = torch.cuda.Stream()
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        o2, s2 = fwd(workspace=ws, stream=stream)
+        stream.synchronize()
+        g2 = bwd(workspace=ws, stream=stream)
+        stream.synchronize()
+        assert torch.equal(out, o2) and torch.equal(sT, s2)
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_captured_graph():
+    """Forward, step and gradient captured in a graph and replayed between eager work: every replay
+    gives the eager results."""
+    import selective_state_space_41_amd as V
+    p = make(27, 2, 130, 2, 1, 32, 32, "bf16")
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "dout", "s0")}
+    eager = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], initial_state=t["s0"])
+    eg = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], initial_state=t["s0"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], initial_state=t["s0"])
+        gg = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], initial_state=t["s0"])
+    for _ in range(3):
+        for x in list(got) + list(gg.values()):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, got))
+        assert all(torch.equal(eg[k], gg[k]) for k in eg)
+
+
+def test_prepared():
+    import selective_state_space_41_amd as V
+    p = make(29, 1, 40, 2, 2, 16, 16, "f32")
+    t = {k: dev(p, k) for k in ("q", "k", "v", "g", "dout")}
+    run, out, sT = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], prepare=True)
+    grun, g = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], prepare=True)
+    for _ in range(2):
+        out.zero_()
+        run()
+        grun()
+        want = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"])
+        assert torch.equal(out, want[0]) and torch.equal(sT, want[1])
+    assert torch.equal(g["dq"], V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"])["dq"])
+
+
+def test_refusals():
+    """Bad arguments raise before anything is enqueued."""
+    import selective_state_space_41_amd as V
+    q, v = (torch.zeros(2, 9, 4, 16, device="cuda") for _ in range(2))
+    g = torch.zeros(2, 9, 4, device="cuda")
+    state = torch.zeros(2, 4, 16, 16, device="cuda")
+    for bad, kind in (
+        (lambda: V.linattn_fwd(q, q, v, g.double()), TypeError),
+        (lambda: V.linattn_fwd(q, q, v, g[:, :8]), ValueError),
+        (lambda: V.linattn_fwd(q, q.bfloat16(), v, g), TypeError),
+        (lambda: V.linattn_fwd(q.half(), q.half(), v.half(), g), TypeError),
+        (lambda: V.linattn_fwd(q.cpu(), q.cpu(), v.cpu(), g.cpu()), ValueError),
+        (lambda: V.linattn_fwd(q[:, :, :3], q[:, :, :3], v, g), ValueError),           # 4 heads over 3
+        (lambda: V.linattn_fwd(q[..., :12], q[..., :12], v, g), RuntimeError),         # dk not a multiple of 8
+        (lambda: V.linattn_fwd(q[..., ::2], q[..., ::2], v, g), ValueError),           # channels apart
+        (lambda: V.linattn_fwd(q[:, :0], q[:, :0], v[:, :0], g[:, :0]), RuntimeError),  # no tokens
+        (lambda: V.linattn_fwd(q, q, v, g, initial_state=state[:1]), ValueError),
+        (lambda: V.linattn_fwd(q, q, v, g, lengths=torch.zeros(2, device="cuda")), TypeError),
+        (lambda: V.linattn_bwd(q, q, v, g, v[:, :8]), ValueError),
+        (lambda: V.linattn_step(q[:, 0], q[:, 0], v[:, 0], g[:, 0], state[:1]), ValueError),
+        (lambda: V.linattn_step(q[:, 0], q[:, 0], v[:, 0], g[:, 0], state.bfloat16()), TypeError),
+        (lambda: V.linattn_step(q[:, 0], q[:, 0], v[:, 0], g[:, 0], state, slots=torch.zeros(2, device="cuda")),
+         TypeError),
+    ):
+        with pytest.raises(kind):
+            bad()
+    big = torch.zeros(1, 4, 1, 136, device="cuda")
+    with pytest.raises(RuntimeError, match="UNSUPPORTED"):
+        V.linattn_fwd(big, big, big, torch.zeros(1, device="cuda"))
+    odd = torch.zeros(4, 2 * 16 + 2, device="cuda")[:, 2:].view(1, 4, 2, 16)  # rows off the 16-byte grid
+    with pytest.raises(RuntimeError, match="ALIGN"):
+        V.linattn_fwd(odd, odd, odd, torch.zeros(2, device="cuda"))
+    p = make(1, 1, 300, 1, 1, 16, 16, "bf16")
+    with pytest.raises(ValueError, match="workspace"):
+        V.linattn_fwd(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "g"),
+                      workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
