@@ -145,14 +145,71 @@ __device__ __forceinline__ void pack(const float (&x)[8], Frag32& f) {
 __device__ __forceinline__ float elem(const bf16x8& f, int e) { return static_cast<float>(f[e]); }
 __device__ __forceinline__ float elem(const Frag32& f, int e) { return f.v[e]; }
 
-// c += a * (f with its elements scaled by w), the scaled operand split in two where it is bfloat16.
-__device__ __forceinline__ void scale_split(const bf16x8& f, const float (&w)[8], bf16x8& hi, bf16x8& lo) {
+// x as a sum of three bfloat16 numbers: 24 bits, all that float32 has.
+__device__ __forceinline__ void split3(float x, bf16x8 (&f)[3], int e) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = static_cast<float>(f[e]) * w[e];
-    hi[e] = static_cast<__bf16>(x);
-    lo[e] = static_cast<__bf16>(x - static_cast<float>(hi[e]));
+  for (int i = 0; i < 3; ++i) {
+    f[i][e] = static_cast<__bf16>(x);
+    x -= static_cast<float>(f[i][e]);
   }
+}
+__device__ __forceinline__ void split3(float x, Frag32 (&f)[1], int e) { f[0].v[e] = x; }
+template <typename T>
+constexpr int kPieces = sizeof(T) == 2 ? 3 : 1;
+
+// Sums and scans over the 16 lanes of a row with lane-rotating adds, over the 4 rows (g) of a wave
+// with row swaps: no LDS round trips.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf, 0xf, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf, 0xf, true);
+  return __hiloint2double(hi, lo);
+}
+constexpr int kRor = 0x120, kShr = 0x110, kShl = 0x100;  // by n lanes of the row; shifts bring in 0
+__device__ __forceinline__ float row_sum(float v) {  // in every lane of the row
+  v += dpp<kRor + 8>(v);
+  v += dpp<kRor + 4>(v);
+  v += dpp<kRor + 2>(v);
+  return v + dpp<kRor + 1>(v);
+}
+template <typename F>
+__device__ __forceinline__ F row_prefix(F v) {  // inclusive
+  v += dpp<kShr + 1>(v);
+  v += dpp<kShr + 2>(v);
+  v += dpp<kShr + 4>(v);
+  return v + dpp<kShr + 8>(v);
+}
+__device__ __forceinline__ float row_suffix(float v) {
+  v += dpp<kShl + 1>(v);
+  v += dpp<kShl + 2>(v);
+  v += dpp<kShl + 4>(v);
+  return v + dpp<kShl + 8>(v);
+}
+// the four rows' values, each in every lane (of the same place in its row)
+__device__ __forceinline__ void rows_of(float v, float (&r)[4]) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const unsigned x = __float_as_uint(v);
+  const u32x2 half = __builtin_amdgcn_permlane32_swap(x, x, false, false);  // rows (0, 1), rows (2, 3)
+  const u32x2 lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+  const u32x2 hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+  r[0] = __uint_as_float(lo[0]), r[1] = __uint_as_float(lo[1]);
+  r[2] = __uint_as_float(hi[0]), r[3] = __uint_as_float(hi[1]);
+}
+__device__ __forceinline__ float sum_rows(float v) {
+  float r[4];
+  rows_of(v, r);
+  return (r[0] + r[1]) + (r[2] + r[3]);
+}
+// the sum over the rows after / before this one
+__device__ __forceinline__ float sum_after(const float (&r)[4], int g) {
+  return (g < 1 ? r[1] : 0.0f) + (g < 2 ? r[2] : 0.0f) + (g < 3 ? r[3] : 0.0f);
+}
+__device__ __forceinline__ float sum_before(const float (&r)[4], int g) {
+  return (g > 0 ? r[0] : 0.0f) + (g > 1 ? r[1] : 0.0f) + (g > 2 ? r[2] : 0.0f);
 }
 
 __device__ __forceinline__ float exp2_diff(float hi_a, float lo_a, float hi_b, float lo_b) {
@@ -195,7 +252,6 @@ struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
   static constexpr int kC = 16 * kWaves;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kPad = 16 / sizeof(T);  // LDS rows stay 16-byte aligned and rotate over the banks
-  static constexpr bool kSplit = sizeof(T) == 2;
 };
 
 // A tile of C tokens on its way from global memory to LDS.  Tokens from `live` on and channels from
@@ -236,15 +292,21 @@ __device__ __forceinline__ float load_g(const LinArgs& a, const float* g, int t0
   }
   return x;
 }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
 template <int C>
 __device__ __forceinline__ void scan_g(float x, float* hi, float* lo) {
   const int l = threadIdx.x & 63;
-  double s = static_cast<double>(x) * 1.4426950408889634;
+  double s = row_prefix(static_cast<double>(x) * 1.4426950408889634);
+  double rows = 0.0;  // the sum of the rows before
 #pragma unroll
-  for (int m = 1; m < C; m <<= 1) {
-    const double up = __shfl_up(s, m);
-    if (l >= m) s += up;
+  for (int g = 0; g + 1 < C / 16; ++g) {
+    const double t = lane_of(s, 16 * g + 15);
+    if ((l >> 4) > g) rows += t;
   }
+  s += rows;
   if (l < C) {
     const float h = static_cast<float>(s);
     hi[l] = h;
@@ -253,6 +315,21 @@ __device__ __forceinline__ void scan_g(float x, float* hi, float* lo) {
 }
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+// Results in the accumulators' layout (4 consecutive channels of one token per lane) to memory.
+__device__ __forceinline__ void store_acc(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store_acc(uint16_t* p, f32x4 v) {
+  const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+  const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+}
+
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+               __uint_as_float(w.y & 0xffff0000u)};
+}
 
 // The state, transposed in the accumulators: wave w holds columns d of its own tiles (tile index
 // w * DT + t), rows n = 16 nt + 4 g + r.
@@ -289,31 +366,51 @@ struct State {
         if (d_of(t) < dk && n_of(nt) < dv)
           *reinterpret_cast<f32x4*>(p + static_cast<int64_t>(d_of(t)) * ld + n_of(nt)) = s[t][nt];
   }
-  // into LDS as an operand, [d][n]: rounded, and what the rounding left in `lo` if that is wanted
-  __device__ __forceinline__ void publish(T* hi, T* lo) const {
+  // into LDS as an operand, [d][n], rounded
+  __device__ __forceinline__ void publish(T* p) const {
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int at = d_of(t) * kStride + n_of(nt);
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<f32x4*>(hi + at) = s[t][nt];
-        } else {
-          uint32_t h[2], r[2];
+      for (int nt = 0; nt < kNT; ++nt) store_acc(p + d_of(t) * kStride + n_of(nt), s[t][nt]);
+  }
+  // sum over this wave's d of y_j[d] (S x_j)[d], to float32's precision: the state goes into the product
+  // from its registers, in as many bfloat16 pieces as it has bits.  x: [token][n]; y4(t, jt): this lane's
+  // 4 channels 16 d_tile + 4 g .. of token 16 jt + (lane & 15).  out[j] for the block's tokens.
+  template <typename Y>
+  __device__ __forceinline__ void bilinear(const T* x, Y&& y4, float* out) const {
+    constexpr int SX = Tile<T, DV>::kStride;
+    float part[B::kC / 16];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint16_t h0 = f32_to_bf16(s[t][nt][2 * p]), h1 = f32_to_bf16(s[t][nt][2 * p + 1]);
-            h[p] = h0 | (static_cast<uint32_t>(h1) << 16);
-            if (lo) {
-              const uint16_t r0 = f32_to_bf16(s[t][nt][2 * p] - bf16_to_f32(h0));
-              const uint16_t r1 = f32_to_bf16(s[t][nt][2 * p + 1] - bf16_to_f32(h1));
-              r[p] = r0 | (static_cast<uint32_t>(r1) << 16);
-            }
-          }
-          *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
-          if (lo) *reinterpret_cast<uint2*>(lo + at) = make_uint2(r[0], r[1]);
+    for (int jt = 0; jt < B::kC / 16; ++jt) part[jt] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kDT; ++t) {
+      f32x4 acc[B::kC / 16];
+#pragma unroll
+      for (int jt = 0; jt < B::kC / 16; ++jt) acc[jt] = zero4();
+#pragma unroll
+      for (int kk = 0; kk < DV / 32; ++kk) {
+        Frag<T> f[kPieces<T>];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split3(s[t][2 * kk + (e >> 2)][e & 3], f, e);
+#pragma unroll
+        for (int jt = 0; jt < B::kC / 16; ++jt) {
+          const Frag<T> xb = frag_row_perm<SX>(x + jt * 16 * SX + kk * 32);
+#pragma unroll
+          for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(f[i], xb, acc[jt]);
         }
       }
+#pragma unroll
+      for (int jt = 0; jt < B::kC / 16; ++jt) {
+        const f32x4 y = y4(t, jt);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[jt] = __builtin_fmaf(acc[jt][r], y[r], part[jt]);
+      }
+    }
+#pragma unroll
+    for (int jt = 0; jt < B::kC / 16; ++jt) {
+      const float v = sum_rows(part[jt]);
+      if ((threadIdx.x & 63) < 16) out[jt * 16 + (threadIdx.x & 15)] = v;
+    }
   }
   // s = e^{G_C} s + sum_j w_j y_j x_j^T over the block, y [token][d], x [token][n]; forward: w_j =
   // e^{G_C - G_j}; backward: w_j = e^{G_j} mul.
@@ -339,23 +436,14 @@ struct State {
       for (int t = 0; t < kDT; ++t) {
         const int d0 = ((threadIdx.x >> 6) * kDT + t) * 16;
         const Frag<T> f = frag_col<SY>(y + kk * 32 * SY + d0);
-        if constexpr (B::kSplit) {
-          Frag<T> fh, fl;
-          scale_split(f, w, fh, fl);
+        Frag<T> m[kPieces<T>];
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            const Frag<T> xa = frag_col<SX>(x + kk * 32 * SX + nt * 16);
-            s[t][nt] = mma(xa, fh, s[t][nt]);
-            s[t][nt] = mma(xa, fl, s[t][nt]);
-          }
-        } else {
-          float m[8];
+        for (int e = 0; e < 8; ++e) split3(elem(f, e) * w[e], m, e);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m[e] = elem(f, e) * w[e];
-          Frag<T> fm;
-          pack(m, fm);
+        for (int nt = 0; nt < kNT; ++nt) {
+          const Frag<T> xa = frag_col<SX>(x + kk * 32 * SX + nt * 16);
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) s[t][nt] = mma(frag_col<SX>(x + kk * 32 * SX + nt * 16), fm, s[t][nt]);
+          for (int i = 0; i < kPieces<T>; ++i) s[t][nt] = mma(xa, m[i], s[t][nt]);
         }
       }
     }
@@ -391,14 +479,6 @@ __device__ __forceinline__ const T* head(const View& v, int64_t b, int h) {
   return static_cast<const T*>(v.p) + b * v.b + h * v.h;
 }
 
-// Results in the accumulators' layout (4 consecutive channels of one token per lane) to memory.
-__device__ __forceinline__ void store_acc(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-__device__ __forceinline__ void store_acc(uint16_t* p, f32x4 v) {
-  const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
-  const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
-  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
-}
-
 // Zeros for the tokens [t0, t1) of a tensor with token stride `st`, `dim` (a multiple of 8) channels.
 template <int THREADS, typename O>
 __device__ __forceinline__ void zero_tokens(O* p, int64_t st, int dim, int t0, int t1) {
@@ -419,7 +499,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_segment_kernel(Lin
   constexpr int C = B::kC;
   __shared__ __align__(16) T ys[C * Tile<T, DK>::kStride];
   __shared__ __align__(16) T xs[C * Tile<T, DV>::kStride];
-  __shared__ float hi[C], lo[C];
+  __shared__ __align__(16) float his[2][C], los[2][C];
   const Where w = where(a);
   const T* y = head<T>(BACK ? a.q : a.k, w.b, w.h / a.share);
   const T* x = head<T>(BACK ? a.dout : a.v, w.b, w.h);
@@ -439,17 +519,19 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_segment_kernel(Lin
   if (n > 0) {
     ty.load(y, yt, at(0), w.live, a.dk);
     tx.load(x, xt, at(0), w.live, a.dvd);
-    gx = load_g<C>(a, g, at(0), w.live);
+    if (wave == 0) scan_g<C>(load_g<C>(a, g, at(0), w.live), his[0], los[0]);
+    if (n > 1) gx = load_g<C>(a, g, at(1), w.live);
   }
   for (int i = 0; i < n; ++i) {
+    const float *hi = his[i & 1], *lo = los[i & 1];
     ty.store(ys);
     tx.store(xs);
-    if (wave == i % B::kWaves) scan_g<C>(gx, hi, lo);
     __syncthreads();
     if (i + 1 < n) {
       ty.load(y, yt, at(i + 1), w.live, a.dk);
       tx.load(x, xt, at(i + 1), w.live, a.dvd);
-      gx = load_g<C>(a, g, at(i + 1), w.live);
+      if (wave == i % B::kWaves) scan_g<C>(gx, his[(i + 1) & 1], los[(i + 1) & 1]);
+      if (i + 2 < n) gx = load_g<C>(a, g, at(i + 2), w.live);
     }
     total += hi[C - 1] + lo[C - 1];
     st.template update<BACK>(ys, xs, hi, lo, a.scale);
@@ -495,7 +577,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_fwd_kernel(LinArgs
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T ss[DK * SS];
-  __shared__ __align__(16) float hi[C], lo[C];
+  __shared__ __align__(16) float his[2][C], los[2][C];
   const Where w = where(a);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
@@ -520,21 +602,24 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_fwd_kernel(LinArgs
     tq.load(q, a.q.t, w.c0 * C, w.live, a.dk);
     tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
     tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
-    gx = load_g<C>(a, g, w.c0 * C, w.live);
+    if (wave == 0) scan_g<C>(load_g<C>(a, g, w.c0 * C, w.live), his[w.c0 & 1], los[w.c0 & 1]);
+    gx = load_g<C>(a, g, w.c0 * C + C, w.live);
   }
   for (int c = w.c0; c < c1; ++c) {
     const int t0 = c * C;
+    const float *hi = his[c & 1], *lo = los[c & 1];
     tq.store(qs);
     tk.store(ks);
     tv.store(vs);
-    st.publish(ss, nullptr);
-    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
+    st.publish(ss);
     __syncthreads();
     if (c + 1 < c1) {
       tq.load(q, a.q.t, t0 + C, w.live, a.dk);
       tk.load(k, a.k.t, t0 + C, w.live, a.dk);
       tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
-      gx = load_g<C>(a, g, t0 + C, w.live);
+      // the next block's decays, by one wave; the others' products run meanwhile
+      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c + 1) & 1], los[(c + 1) & 1]);
+      gx = load_g<C>(a, g, t0 + 2 * C, w.live);
     }
     // this wave's 16 queries: column i of every result tile
     const int i0 = wave * 16, i = i0 + li;
@@ -622,9 +707,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T os[C * SV];
-  __shared__ __align__(16) T ss[(B::kSplit ? 2 : 1) * DK * SS];
-  __shared__ __align__(16) float hi[C], lo[C];
-  T* const sl = B::kSplit ? ss + DK * SS : nullptr;
+  __shared__ __align__(16) T ss[DK * SS];
+  __shared__ __align__(16) float his[2][C], los[2][C];
+  __shared__ float part[B::kWaves][C];
   const Where w = where(a);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
@@ -649,42 +734,43 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
     tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
     tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
     to.load(o, a.dout.t, w.c0 * C, w.live, a.dvd);
-    gx = load_g<C>(a, g, w.c0 * C, w.live);
+    if (wave == 0) scan_g<C>(load_g<C>(a, g, w.c0 * C, w.live), his[w.c0 & 1], los[w.c0 & 1]);
+    gx = load_g<C>(a, g, w.c0 * C + C, w.live);
   }
   for (int c = w.c0; c < c1; ++c) {
     const int t0 = c * C;
+    const float *hi = his[c & 1], *lo = los[c & 1];
     tk.store(ks);
     tv.store(vs);
     to.store(os);
-    st.publish(ss, sl);
+    st.publish(ss);
     st.store(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
-    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
     __syncthreads();
-    const int i0 = wave * 16, i = i0 + li;
-    const bool live = t0 + i < w.live;
-    // this lane's 4 channels of its query, for a_i
-    f32x4 qv[DK / 16];
+    // channels 16 d_tile + 4 g .. of the queries 16 jt + li, for a_i
+    f32x4 q4[S::kDT][B::kWaves];
 #pragma unroll
-    for (int dt = 0; dt < DK / 16; ++dt) {
-      qv[dt] = zero4();
-      if (live && dt * 16 + g4 < a.dk) {
-        const T* qp = q + (t0 + i) * a.q.t + dt * 16 + g4;
+    for (int t = 0; t < S::kDT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) qv[dt][r] = load1(qp + r);
+      for (int jt = 0; jt < B::kWaves; ++jt) {
+        const int d = (wave * S::kDT + t) * 16 + g4, n = t0 + jt * 16 + li;
+        q4[t][jt] = zero4();
+        if (n < w.live && d < a.dk) q4[t][jt] = load4(q + n * a.q.t + d);
       }
-    }
     if (c + 1 < c1) {
       tk.load(k, a.k.t, t0 + C, w.live, a.dk);
       tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
       to.load(o, a.dout.t, t0 + C, w.live, a.dvd);
-      gx = load_g<C>(a, g, t0 + C, w.live);
+      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c + 1) & 1], los[(c + 1) & 1]);
+      gx = load_g<C>(a, g, t0 + 2 * C, w.live);
     }
+    st.bilinear(os, [&](int t, int jt) { return q4[t][jt]; }, part[wave]);
+    const int i0 = wave * 16, i = i0 + li;
+    const bool live = t0 + i < w.live;
     const float gh = hi[i], gl = lo[i];
     Frag<T> of[DV / 32];
 #pragma unroll
     for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<SV>(os + i0 * SV + kk * 32);
     f32x4 acc[DK / 16];
-    float dot = 0.0f;
     const float e0 = __builtin_amdgcn_exp2f(gh + gl) * a.scale;
 #pragma unroll
     for (int dt = 0; dt < DK / 16; ++dt) {
@@ -692,15 +778,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
 #pragma unroll
       for (int kk = 0; kk < DV / 32; ++kk) {
         acc[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
-        if constexpr (B::kSplit) acc[dt] = mma(frag_row<SS>(sl + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
       }
       acc[dt] *= e0;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dot = __builtin_fmaf(acc[dt][r], qv[dt][r], dot);
     }
-    dot += __shfl_xor(dot, 16);
-    dot += __shfl_xor(dot, 32);
-    if (l < 16) a.qa[w.bh * a.blocks * C + t0 + i] = dot;
     for (int jj = 0; jj <= wave / 2; ++jj) {
       float p[8];
 #pragma unroll
@@ -736,6 +816,12 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
     }
     st.template update<false>(ks, vs, hi, lo, 1.0f);
     __syncthreads();
+    if (wave == c % B::kWaves && l < C) {  // part is written again only past the next barrier
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < B::kWaves; ++n) sum += part[n][l];
+      a.qa[w.bh * a.blocks * C + t0 + l] = sum * a.scale * __builtin_amdgcn_exp2f(hi[l] + lo[l]);
+    }
   }
   const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
   const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
@@ -754,10 +840,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T os[C * SV];
-  __shared__ __align__(16) T ss[(B::kSplit ? 2 : 1) * DK * SS];
-  __shared__ __align__(16) float hi[C], lo[C];
-  __shared__ float rows[B::kWaves][C], after[C], across[B::kWaves];
-  T* const sl = B::kSplit ? ss + DK * SS : nullptr;
+  __shared__ __align__(16) T ss[DK * SS];
+  __shared__ __align__(16) float his[2][C], los[2][C];
+  __shared__ float rows[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
   const Where w = where(a);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
@@ -785,35 +870,44 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
     tk.load(k, a.k.t, t0, w.live, a.dk);
     tv.load(v, a.v.t, t0, w.live, a.dvd);
     to.load(o, a.dout.t, t0, w.live, a.dvd);
-    gx = load_g<C>(a, g, t0, w.live);
   };
-  if (w.c0 < c1) load((c1 - 1) * C);
+  if (w.c0 < c1) {
+    load((c1 - 1) * C);
+    if (wave == 0) scan_g<C>(load_g<C>(a, g, (c1 - 1) * C, w.live), his[(c1 - 1) & 1], los[(c1 - 1) & 1]);
+    if (c1 - 1 > w.c0) gx = load_g<C>(a, g, (c1 - 2) * C, w.live);
+  }
   for (int c = c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
+    const float *hi = his[c & 1], *lo = los[c & 1];
+    // the state that entered the block and the a_i, from the walk forwards
+    S old;
+    old.load(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
+    const float qa = l < C ? a.qa[w.bh * a.blocks * C + t0 + l] : 0.0f;
     tq.store(qs);
     tk.store(ks);
     tv.store(vs);
     to.store(os);
-    st.publish(ss, sl);
-    if (wave == c % B::kWaves) scan_g<C>(gx, hi, lo);
+    st.publish(ss);
     __syncthreads();
-    if (c > w.c0) load(t0 - C);
+    if (c > w.c0) {
+      load(t0 - C);
+      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c - 1) & 1], los[(c - 1) & 1]);
+      if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
+    }
     {
-      // Y: the state that entered the block against R, both in this wave's layout
-      const float* p = a.states + (w.bh * a.blocks + c) * (DK * DV);
+      // Y: that state against R, both in this wave's layout
       float y = 0.0f;
 #pragma unroll
       for (int t = 0; t < S::kDT; ++t)
 #pragma unroll
-        for (int nt = 0; nt < S::kNT; ++nt) {
-          const f32x4 s = *reinterpret_cast<const f32x4*>(p + S::d_of(t) * DV + S::n_of(nt));
+        for (int nt = 0; nt < S::kNT; ++nt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(s[r], st.s[t][nt][r], y);
-        }
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) y += __shfl_xor(y, m);
+          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
+      y = sum_rows(row_sum(y));
       if (l == 0) across[wave] = y * __builtin_amdgcn_exp2f(hi[C - 1] + lo[C - 1]);
     }
+    st.bilinear(vs, [&](int t, int jt) { return load4(ks + (jt * 16 + li) * SK + (wave * S::kDT + t) * 16 + g4); },
+                after[wave]);
     // this wave's 16 keys: column j of every result tile
     const int j0 = wave * 16, j = j0 + li;
     const float gh = hi[j], gl = lo[j];
@@ -824,18 +918,14 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
 #pragma unroll
     for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<SV>(vs + j0 * SV + kk * 32);
     f32x4 ak[DK / 16], av[DV / 16];
-    float bj = 0.0f;
 #pragma unroll
     for (int dt = 0; dt < DK / 16; ++dt) {
       ak[dt] = zero4();
 #pragma unroll
       for (int kk = 0; kk < DV / 32; ++kk) {
         ak[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
-        if constexpr (B::kSplit) ak[dt] = mma(frag_row<SS>(sl + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
       }
       ak[dt] *= ec;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) bj = __builtin_fmaf(ak[dt][r], load1(ks + j * SK + dt * 16 + g4 + r), bj);
     }
 #pragma unroll
     for (int nt = 0; nt < DV / 16; ++nt) av[nt] = zero4();
@@ -872,20 +962,14 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
           x[t * 4 + r] = i >= j ? dp[r] * e : 0.0f;
           u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
         }
-        float sum = u[0];  // of this lane's rows and those below them
-        float down = __shfl_down(sum, 16);
-        sum += g4 < 12 ? down : 0.0f;
-        down = __shfl_down(sum, 32);
-        sum += g4 < 8 ? down : 0.0f;
-        down = __shfl_down(sum, 16);
-        const float below = (g4 < 12 ? down : 0.0f) + later;
-        later += __shfl(sum, li);
+        float tiles[4];  // this lane's rows of the tile, and the other lanes' of the column
+        rows_of(u[0], tiles);
+        const float below = sum_after(tiles, g4 / 4) + later;
+        later += (tiles[0] + tiles[1]) + (tiles[2] + tiles[3]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = i0 + g4 + r;
-          float m = j < i ? u[r] + below : 0.0f;
-#pragma unroll
-          for (int s = 1; s < 16; s <<= 1) m += __shfl_xor(m, s);
+          const float m = row_sum(j < i ? u[r] + below : 0.0f);
           if (li == 0) rows[wave][i] = m;
         }
       }
@@ -897,9 +981,6 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
 #pragma unroll
       for (int dt = 0; dt < DK / 16; ++dt) ak[dt] = mma(frag_col<SK>(qs + ii * 32 * SK + dt * 16), xf, ak[dt]);
     }
-    bj += __shfl_xor(bj, 16);
-    bj += __shfl_xor(bj, 32);
-    if (l < 16) after[j] = bj;
     if (t0 + j < w.live) {
 #pragma unroll
       for (int dt = 0; dt < DK / 16; ++dt)
@@ -921,20 +1002,20 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
       const bool mine = l < C && t0 + l < w.live;
       float from = 0.0f, before = 0.0f, y = 0.0f;
       if (mine) {
-        from = a.qa[w.bh * a.blocks * C + t0 + l];
-        before = after[l];
+        from = qa;
+#pragma unroll
+        for (int i = 0; i < B::kWaves; ++i) before += after[i][l];
+        before *= exp2_diff(hi[C - 1], lo[C - 1], hi[l], lo[l]);
         for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
       }
 #pragma unroll
       for (int i = 0; i < B::kWaves; ++i) y += across[i];
-#pragma unroll
-      for (int m = 1; m < C; m <<= 1) {
-        const float down = __shfl_down(from, m), up = __shfl_up(before, m);
-        if (l + m < C) from += down;
-        if (l >= m) before += up;
-      }
-      before = __shfl_up(before, 1);
-      if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + (l ? before : 0.0f) + y;
+      float r[4];
+      rows_of(row_sum(from), r);
+      from = row_suffix(from) + sum_after(r, l >> 4);
+      rows_of(row_sum(before), r);
+      before = dpp<kShr + 1>(row_prefix(before)) + sum_before(r, l >> 4);
+      if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + before + y;
     }
   }
   const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
