@@ -456,7 +456,8 @@ vmscan_status vmscan_rope_axes(const void *q, const int64_t *q_strides, void *q_
  *   S_t = exp(log_decay[b, t, h]) S_{t-1} + k[b, t, hk] v[b, t, h]^T;   out[b, t, h] = scale S_t^T q[b, t, hk]
  *   q, k          : [batch, seqlen, kheads, dk]  activation dtype; *_strides: batch, token and head
  *   v             : [batch, seqlen, heads, dv]   stride in elements, channels contiguous.  Pointers
- *                   and strides must be multiples of 16 bytes (else VMSCAN_ERR_ALIGN).
+ *                   and strides must be multiples of 16 bytes (else VMSCAN_ERR_ALIGN),
+ *                   token strides below 2^24 elements.
  *   log_decay     : float32; decay_strides (batch, token, head; 0 broadcasts) or NULL for one value
  *                   per head, [heads].  -inf clears the state; values above 0 are taken as they are.
  *   initial_state, final_state : [batch, heads, dk, dv] float32 or NULL

@@ -8,6 +8,7 @@ cannot be loaded that raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -521,9 +522,20 @@ def _is_act(t, name, ndim):
     return dt
 
 
+_pack2, _pack3 = struct.Struct("=2q").pack, struct.Struct("=3q").pack
+
+
+def _strides(t, n):
+    """The first n (2 or 3) strides as the library's int64 array; 0 where the dimension has one
+    element, whose stride says nothing."""
+    st = t.stride()[:n]
+    if 1 in t.shape[:n]:
+        st = [s if d != 1 else 0 for s, d in zip(st, t.shape)]
+    return _pack3(*st) if n == 3 else _pack2(*st)
+
+
 def _strided(t, name, shape, dtype, device):
-    """A tensor of any strides but contiguous channels; its leading strides for the library (0 where
-    the dimension has one element, whose stride says nothing)."""
+    """A tensor of any strides but contiguous channels; its leading strides for the library."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -532,11 +544,9 @@ def _strided(t, name, shape, dtype, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
+    if t.stride(-1) != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous channels")
-    n = len(st) - 1
-    return (_i64 * n)(*[s if d != 1 else 0 for s, d in zip(st[:n], shape)])
+    return _strides(t, len(shape) - 1)
 
 
 def _made(stream, *tensors):
@@ -553,15 +563,24 @@ def _enqueue(fn, args, dev, prepare=False, keep=None):
     if prepare:
         return _call(fn, args, True, keep)
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args))
+        code = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args))
+            code = fn(*args)
+    if code:
+        _check(code)
     return None
 
 
+# The current stream's handle without making a Stream object (a tenth of the time, and these calls
+# may be as short as a few microseconds), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on(stream, dev):
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _p(t):
@@ -605,7 +624,7 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
         raise TypeError(f"out_dtype must be {x.dtype} or {_FP8}, got {out_dtype}")
     ydt = _FP8 if fp8 else x.dtype
     if y is None:
-        y = torch.empty(shape, dtype=ydt, device=dev)
+        y = torch.empty(shape, dtype=ydt, device=dev) if fp8 or row_stride != dim else torch.empty_like(x)
         _made(stream, y)
     else:
         _need(y, "y", shape, ydt, dev)
@@ -716,7 +735,7 @@ def _linattn_args(q, k, v, log_decay, ndim):
     if log_decay.dim() == 1:
         _need(log_decay, "log_decay", (H,), torch.float32, dev)
     elif log_decay.shape == lead + (H,):
-        gs = (_i64 * (ndim - 1))(*log_decay.stride())
+        gs = _strides(log_decay, ndim - 1)
     else:
         raise ValueError(f"log_decay has shape {tuple(log_decay.shape)}, expected {(H,)} or {tuple(lead) + (H,)}")
     return dt, lead, H, Hk, dk, dv, qs, ks, vs, gs

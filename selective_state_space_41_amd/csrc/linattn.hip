@@ -133,6 +133,24 @@ __device__ __forceinline__ Frag32 frag_col(const float* p) {
   return f;
 }
 
+// The column operands of N neighbouring tiles, for several products: bfloat16 ones (4 registers each)
+// are read once and kept, float32 ones (8) are read at each use.
+template <typename T, int S, int N>
+struct Cols {
+  const T* p;
+  Frag<T> f[sizeof(T) == 2 ? N : 1];
+  __device__ __forceinline__ explicit Cols(const T* at) : p(at) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) f[n] = frag_col<S>(p + n * 16);
+    }
+  }
+  __device__ __forceinline__ Frag<T> operator[](int n) const {
+    if constexpr (sizeof(T) == 2) return f[n];
+    else return frag_col<S>(p + n * 16);
+  }
+};
+
 // Two result tiles (rows 16 t + 4 g + r) as an operand in frag_col's order.
 __device__ __forceinline__ void pack(const float (&x)[8], bf16x8& f) {
 #pragma unroll
@@ -145,15 +163,26 @@ __device__ __forceinline__ void pack(const float (&x)[8], Frag32& f) {
 __device__ __forceinline__ float elem(const bf16x8& f, int e) { return static_cast<float>(f[e]); }
 __device__ __forceinline__ float elem(const Frag32& f, int e) { return f.v[e]; }
 
-// x as a sum of three bfloat16 numbers: 24 bits, all that float32 has.
-__device__ __forceinline__ void split3(float x, bf16x8 (&f)[3], int e) {
+// Eight float32 numbers as the sum of three operands of bfloat16 numbers: each piece is the leading 8
+// bits of what the ones before left, so the three hold all 24.
+__device__ __forceinline__ void split(const float (&x)[8], bf16x8 (&f)[3]) {
+  float rest[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rest[e] = x[e];
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    f[i][e] = static_cast<__bf16>(x);
-    x -= static_cast<float>(f[i][e]);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // the upper halves of two numbers
+      w[e] = __builtin_amdgcn_perm(__float_as_uint(rest[2 * e + 1]), __float_as_uint(rest[2 * e]), 0x07060302u);
+    f[i] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    if (i < 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rest[e] -= __uint_as_float(__float_as_uint(rest[e]) & 0xffff0000u);
+    }
   }
 }
-__device__ __forceinline__ void split3(float x, Frag32 (&f)[1], int e) { f[0].v[e] = x; }
+__device__ __forceinline__ void split(const float (&x)[8], Frag32 (&f)[1]) { pack(x, f[0]); }
 template <typename T>
 constexpr int kPieces = sizeof(T) == 2 ? 3 : 1;
 
@@ -212,10 +241,6 @@ __device__ __forceinline__ float sum_before(const float (&r)[4], int g) {
   return (g > 0 ? r[0] : 0.0f) + (g > 1 ? r[1] : 0.0f) + (g > 2 ? r[2] : 0.0f);
 }
 
-__device__ __forceinline__ float exp2_diff(float hi_a, float lo_a, float hi_b, float lo_b) {
-  return __builtin_amdgcn_exp2f((hi_a - hi_b) + (lo_a - lo_b));
-}
-
 // ---------------------------------------------------------------------------------------------
 // arguments
 
@@ -236,13 +261,14 @@ struct LinArgs {
   void *dq, *dk_out;       // [batch, seqlen, heads, dk]: activations, or float32 where heads share q and k
   void* dv_out;            // [batch, seqlen, heads, dv]
   float* dg;               // [batch, seqlen, heads]
-  float *seg_s, *seg_ds;   // [batch * heads][segment][DK][DV]
+  float *seg_s, *seg_ds;   // [batch * heads][segment][DK][ld]
   float *seg_g;            // [batch * heads][segment]: the segment's log2 decay
   float* states;           // [batch * heads][block][DK][DV]: the state entering each block
   float* qa;               // [batch * heads][blocks * C]: e^{G_i} scale q_i . S do_i
   int64_t batch;
   int seqlen, heads, share, dk, dvd;  // share: heads per query/key head
   int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
+  int slices, ld;                     // slices of the value channels; a segment state's row
   float scale;
 };
 
@@ -254,7 +280,14 @@ struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
   static constexpr int kPad = 16 / sizeof(T);  // LDS rows stay 16-byte aligned and rotate over the banks
 };
 
-// A tile of C tokens on its way from global memory to LDS.  Tokens from `live` on and channels from
+// Waves per SIMD that a kernel's registers must leave room for, where LDS does too: narrow bfloat16 heads
+// only; the others need their registers.
+constexpr int waves_for(size_t elem, int dk, int dv, int narrow) { return elem == 2 && dk <= 64 && dv <= 64 ? narrow : 1; }
+#define VMSCAN_WAVES(N) __attribute__((amdgpu_waves_per_eu(waves_for(sizeof(T), DK, DV, N))))
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// A tile of C tokens on its way from global memory to LDS.  Tokens from `rows` on and channels from
 // `dim` on are not read: they enter as zeros, whatever the memory holds.
 template <typename T, int D>
 struct Tile {
@@ -264,12 +297,23 @@ struct Tile {
   static constexpr int kN = B::kC * kRow / B::kThreads;
   static constexpr int kStride = D + B::kPad;
   uint4 r[kN];
-  __device__ __forceinline__ void load(const T* base, int64_t st, int t0, int live, int dim) {
+  // base: the block's first token; offsets in it fit 32 bits (the caller checked the stride)
+  __device__ __forceinline__ void load(const T* base, uint32_t st, int rows, int dim) {
+    const char* p = reinterpret_cast<const char*>(base);
+    if (rows >= B::kC && dim >= D) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
-      r[i] = make_uint4(0, 0, 0, 0);
-      if (t0 + row < live && col < dim) r[i] = *reinterpret_cast<const uint4*>(base + (t0 + row) * st + col);
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
+        r[i] = *reinterpret_cast<const uint4*>(p + static_cast<uint32_t>((row * st + col) * sizeof(T)));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (static_cast<int>(row) < rows && static_cast<int>(col) < dim)
+          r[i] = *reinterpret_cast<const uint4*>(p + static_cast<uint32_t>((row * st + col) * sizeof(T)));
+      }
     }
   }
   __device__ __forceinline__ void store(T* lds) const {
@@ -281,7 +325,21 @@ struct Tile {
   }
 };
 
-// The running log2 decays of a block as head and tail, by one wave: lane t takes token t0 + t.
+// A block's decays.  With G the running log2 decay, E(t) the last token of t's 16 and F(t) the last one
+// before t's 16 (G = 0 before the block):
+template <int C>
+struct Decays {
+  float hi[C], lo[C];  // G, head and tail
+  float from0[C];      // 2^G_t
+  float toC[C];        // 2^(G_C - G_t)
+  float toE[C];        // 2^(G_E(t) - G_t)
+  float fromF[C];      // 2^(G_t - G_F(t))
+  // 2^(G_i - G_j) for j <= i
+  __device__ __forceinline__ float between(float hi_i, float lo_i, int j) const {
+    return __builtin_amdgcn_exp2f((hi_i - hi[j]) + (lo_i - lo[j]));
+  }
+};
+// By one wave, lane t for token t0 + t: load, then scan.
 template <int C>
 __device__ __forceinline__ float load_g(const LinArgs& a, const float* g, int t0, int live) {
   const int l = threadIdx.x & 63;
@@ -297,20 +355,27 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
                           __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
 template <int C>
-__device__ __forceinline__ void scan_g(float x, float* hi, float* lo) {
+__device__ __forceinline__ void scan_g(float x, Decays<C>& d) {
   const int l = threadIdx.x & 63;
   double s = row_prefix(static_cast<double>(x) * 1.4426950408889634);
-  double rows = 0.0;  // the sum of the rows before
+  double before = 0.0;  // at the end of the rows of 16 before this one
+  double end = 0.0, all = 0.0;
 #pragma unroll
-  for (int g = 0; g + 1 < C / 16; ++g) {
-    const double t = lane_of(s, 16 * g + 15);
-    if ((l >> 4) > g) rows += t;
+  for (int g = 0; g < C / 16; ++g) {
+    if ((l >> 4) == g) before = all;
+    all += lane_of(s, 16 * g + 15);
+    if ((l >> 4) == g) end = all;
   }
-  s += rows;
+  const double own = s;
+  s += before;
   if (l < C) {
     const float h = static_cast<float>(s);
-    hi[l] = h;
-    lo[l] = static_cast<float>(s - static_cast<double>(h));
+    d.hi[l] = h;
+    d.lo[l] = static_cast<float>(s - static_cast<double>(h));
+    d.from0[l] = __builtin_amdgcn_exp2f(h);
+    d.toC[l] = __builtin_amdgcn_exp2f(static_cast<float>(all - s));
+    d.toE[l] = __builtin_amdgcn_exp2f(static_cast<float>(end - s));
+    d.fromF[l] = __builtin_amdgcn_exp2f(static_cast<float>(own));
   }
 }
 
@@ -341,10 +406,7 @@ struct State {
   static constexpr int kStride = DV + B::kPad;
   f32x4 s[kDT][kNT];
 
-  __device__ __forceinline__ static int d_of(int t) {
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
-    return (w * kDT + t) * 16 + (l & 15);
-  }
+  __device__ __forceinline__ static int d_of(int t) { return (wave_id() * kDT + t) * 16 + (threadIdx.x & 15); }
   __device__ __forceinline__ static int n_of(int nt) { return nt * 16 + ((threadIdx.x & 63) >> 4) * 4; }
 
   // rows of `ld` floats, of which d < dk and n < dv exist
@@ -354,8 +416,7 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         s[t][nt] = zero4();
-        if (p && d_of(t) < dk && n_of(nt) < dv)
-          s[t][nt] = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(d_of(t)) * ld + n_of(nt));
+        if (p && d_of(t) < dk && n_of(nt) < dv) s[t][nt] = load4(p + (d_of(t) * ld + n_of(nt)));
       }
   }
   __device__ __forceinline__ void store(float* p, int dk, int dv, int ld) const {
@@ -363,8 +424,7 @@ struct State {
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
-        if (d_of(t) < dk && n_of(nt) < dv)
-          *reinterpret_cast<f32x4*>(p + static_cast<int64_t>(d_of(t)) * ld + n_of(nt)) = s[t][nt];
+        if (d_of(t) < dk && n_of(nt) < dv) store_acc(p + (d_of(t) * ld + n_of(nt)), s[t][nt]);
   }
   // into LDS as an operand, [d][n], rounded
   __device__ __forceinline__ void publish(T* p) const {
@@ -373,104 +433,115 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) store_acc(p + d_of(t) * kStride + n_of(nt), s[t][nt]);
   }
+  __device__ __forceinline__ void decay(float e) {
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) s[t][nt] *= e;
+  }
+  // s += sum_j w_j y_j x_j^T over the 32 tokens from y (the tile [token][d]); xa: the operand of x, w: the
+  // weights, both in frag_col's order.
+  __device__ __forceinline__ void add(const T* y, const Cols<T, kStride, kNT>& xa, const float (&w)[8]) {
+    constexpr int SY = Tile<T, DK>::kStride;
+#pragma unroll
+    for (int t = 0; t < kDT; ++t) {
+      const Frag<T> f = frag_col<SY>(y + (wave_id() * kDT + t) * 16);
+      float m[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[e] = elem(f, e) * w[e];
+      Frag<T> piece[kPieces<T>];
+      split(m, piece);
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const Frag<T> x = xa[nt];
+#pragma unroll
+        for (int i = 0; i < kPieces<T>; ++i) s[t][nt] = mma(x, piece[i], s[t][nt]);
+      }
+    }
+  }
   // sum over this wave's d of y_j[d] (S x_j)[d], to float32's precision: the state goes into the product
   // from its registers, in as many bfloat16 pieces as it has bits.  x: [token][n]; y4(t, jt): this lane's
   // 4 channels 16 d_tile + 4 g .. of token 16 jt + (lane & 15).  out[j] for the block's tokens.
   template <typename Y>
   __device__ __forceinline__ void bilinear(const T* x, Y&& y4, float* out) const {
     constexpr int SX = Tile<T, DV>::kStride;
-    float part[B::kC / 16];
+    float part[B::kWaves];
 #pragma unroll
-    for (int jt = 0; jt < B::kC / 16; ++jt) part[jt] = 0.0f;
+    for (int jt = 0; jt < B::kWaves; ++jt) part[jt] = 0.0f;
 #pragma unroll
     for (int t = 0; t < kDT; ++t) {
-      f32x4 acc[B::kC / 16];
+      f32x4 acc[B::kWaves];
 #pragma unroll
-      for (int jt = 0; jt < B::kC / 16; ++jt) acc[jt] = zero4();
+      for (int jt = 0; jt < B::kWaves; ++jt) acc[jt] = zero4();
 #pragma unroll
       for (int kk = 0; kk < DV / 32; ++kk) {
-        Frag<T> f[kPieces<T>];
+        float m[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split3(s[t][2 * kk + (e >> 2)][e & 3], f, e);
+        for (int e = 0; e < 8; ++e) m[e] = s[t][2 * kk + (e >> 2)][e & 3];
+        Frag<T> piece[kPieces<T>];
+        split(m, piece);
 #pragma unroll
-        for (int jt = 0; jt < B::kC / 16; ++jt) {
+        for (int jt = 0; jt < B::kWaves; ++jt) {
           const Frag<T> xb = frag_row_perm<SX>(x + jt * 16 * SX + kk * 32);
 #pragma unroll
-          for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(f[i], xb, acc[jt]);
+          for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(piece[i], xb, acc[jt]);
         }
       }
 #pragma unroll
-      for (int jt = 0; jt < B::kC / 16; ++jt) {
+      for (int jt = 0; jt < B::kWaves; ++jt) {
         const f32x4 y = y4(t, jt);
 #pragma unroll
         for (int r = 0; r < 4; ++r) part[jt] = __builtin_fmaf(acc[jt][r], y[r], part[jt]);
       }
     }
 #pragma unroll
-    for (int jt = 0; jt < B::kC / 16; ++jt) {
+    for (int jt = 0; jt < B::kWaves; ++jt) {
       const float v = sum_rows(part[jt]);
       if ((threadIdx.x & 63) < 16) out[jt * 16 + (threadIdx.x & 15)] = v;
     }
   }
-  // s = e^{G_C} s + sum_j w_j y_j x_j^T over the block, y [token][d], x [token][n]; forward: w_j =
-  // e^{G_C - G_j}; backward: w_j = e^{G_j} mul.
-  template <bool BACK>
-  __device__ __forceinline__ void update(const T* y, const T* x, const float* hi, const float* lo, float mul) {
-    constexpr int C = B::kC, SY = Tile<T, DK>::kStride, SX = Tile<T, DV>::kStride;
-    const int g4 = ((threadIdx.x & 63) >> 4) * 4;
-    const float eh = hi[C - 1], el = lo[C - 1];
-    const float decay = __builtin_amdgcn_exp2f(eh + el);
-#pragma unroll
-    for (int t = 0; t < kDT; ++t)
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) s[t][nt] *= decay;
-#pragma unroll
-    for (int kk = 0; kk < C / 32; ++kk) {
-      float w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = kk * 32 + (e >> 2) * 16 + g4 + (e & 3);
-        w[e] = BACK ? mul * __builtin_amdgcn_exp2f(hi[j] + lo[j]) : exp2_diff(eh, el, hi[j], lo[j]);
-      }
-#pragma unroll
-      for (int t = 0; t < kDT; ++t) {
-        const int d0 = ((threadIdx.x >> 6) * kDT + t) * 16;
-        const Frag<T> f = frag_col<SY>(y + kk * 32 * SY + d0);
-        Frag<T> m[kPieces<T>];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split3(elem(f, e) * w[e], m, e);
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const Frag<T> xa = frag_col<SX>(x + kk * 32 * SX + nt * 16);
-#pragma unroll
-          for (int i = 0; i < kPieces<T>; ++i) s[t][nt] = mma(xa, m[i], s[t][nt]);
-        }
-      }
-    }
-  }
 };
 
+// Eight values of a table in frag_col's order, for the 32 tokens from p.
+__device__ __forceinline__ void eight(const float* p, float (&w)[8]) {
+  const int g4 = ((threadIdx.x & 63) >> 4) * 4;
+  const f32x4 a = load4(p + g4), b = load4(p + 16 + g4);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) w[r] = a[r], w[4 + r] = b[r];
+}
+
 struct Where {  // this workgroup's place
-  int64_t bh;
-  int64_t b;
-  int h, seg, live, c0, c1;
+  int64_t bh, b;
+  int h, seg, n0, live, c0, c1, end;  // n0: first value channel; c0 .. c1: blocks with tokens, .. end: all
 };
-__device__ __forceinline__ Where where(const LinArgs& a) {
+// Workgroup i runs on XCD i % 8.  An XCD takes consecutive places: the slices of the value channels and the
+// heads that share q and k, which then find them in its L2, then a sequence's segments.
+template <typename T>
+__device__ __forceinline__ Where where(const LinArgs& a, int width) {
+  constexpr int C = Block<T>::kC;
+  const uint32_t n = gridDim.x, q = n >> 3, r = n & 7, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  uint32_t id = (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + local;
   Where w;
-  const int64_t id = blockIdx.x;
+  w.n0 = static_cast<int>(id % a.slices) * width;
+  id /= a.slices;
+  const int in = static_cast<int>(id % a.share);
+  id /= a.share;
   w.seg = static_cast<int>(id % a.segments);
-  w.bh = id / a.segments;
-  w.b = w.bh / a.heads;
-  w.h = static_cast<int>(w.bh - w.b * a.heads);
-  int n = a.seqlen;
+  id /= a.segments;
+  const int kheads = a.heads / a.share;
+  w.b = id / kheads;
+  w.h = static_cast<int>(id % kheads) * a.share + in;
+  w.bh = w.b * a.heads + w.h;
+  int len = a.seqlen;
   if (a.lengths) {
-    n = a.lengths[w.b];
-    n = n < 0 ? 0 : n > a.seqlen ? a.seqlen : n;
+    len = a.lengths[w.b];
+    len = len < 0 ? 0 : len > a.seqlen ? a.seqlen : len;
   }
-  w.live = n;
+  w.live = __builtin_amdgcn_readfirstlane(len);
   w.c0 = w.seg * a.per_segment;
-  const int end = w.c0 + a.per_segment;
-  w.c1 = end < a.blocks ? end : a.blocks;
+  w.end = w.c0 + a.per_segment < a.blocks ? w.c0 + a.per_segment : a.blocks;
+  const int live_blocks = (w.live + C - 1) / C;
+  w.c1 = w.end < live_blocks ? w.end : live_blocks;
   return w;
 }
 
@@ -479,11 +550,15 @@ __device__ __forceinline__ const T* head(const View& v, int64_t b, int h) {
   return static_cast<const T*>(v.p) + b * v.b + h * v.h;
 }
 
-// Zeros for the tokens [t0, t1) of a tensor with token stride `st`, `dim` (a multiple of 8) channels.
-template <int THREADS, typename O>
-__device__ __forceinline__ void zero_tokens(O* p, int64_t st, int dim, int t0, int t1) {
+// Zeros for this place's tokens past the row's length, in a tensor with token stride `st`, `dim` (a multiple
+// of 4) channels.
+template <typename T, typename O>
+__device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p, int64_t st, int dim) {
+  constexpr int C = Block<T>::kC;
+  const int t1 = w.end * C < a.seqlen ? w.end * C : a.seqlen;
+  const int t0 = w.live > w.c0 * C ? w.live : w.c0 * C;
   const int runs = dim / 4;
-  for (int64_t id = threadIdx.x; id < static_cast<int64_t>(t1 - t0) * runs; id += THREADS) {
+  for (int64_t id = threadIdx.x; id < static_cast<int64_t>(t1 - t0) * runs; id += Block<T>::kThreads) {
     const int64_t t = id / runs;
     store_acc(p + (t0 + t) * st + (id - t * runs) * 4, zero4());
   }
@@ -494,74 +569,99 @@ __device__ __forceinline__ void zero_tokens(O* p, int64_t st, int dim, int t0, i
 // from a zero end.
 
 template <typename T, int DK, int DV, bool BACK>
-__global__ __launch_bounds__(Block<T>::kThreads) void linattn_segment_kernel(LinArgs a) {
+__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
   using B = Block<T>;
-  constexpr int C = B::kC;
-  __shared__ __align__(16) T ys[C * Tile<T, DK>::kStride];
-  __shared__ __align__(16) T xs[C * Tile<T, DV>::kStride];
-  __shared__ __align__(16) float his[2][C], los[2][C];
-  const Where w = where(a);
+  using S = State<T, DK, DV>;
+  constexpr int C = B::kC, SX = Tile<T, DV>::kStride, SY = Tile<T, DK>::kStride;
+  __shared__ __align__(16) T ys[C * SY];
+  __shared__ __align__(16) T xs[C * SX];
+  __shared__ __align__(16) Decays<C> decays[2];
+  const Where w = where<T>(a, DV);
   const T* y = head<T>(BACK ? a.q : a.k, w.b, w.h / a.share);
-  const T* x = head<T>(BACK ? a.dout : a.v, w.b, w.h);
+  const T* x = head<T>(BACK ? a.dout : a.v, w.b, w.h) + w.n0;
   const int64_t yt = BACK ? a.q.t : a.k.t, xt = BACK ? a.dout.t : a.v.t;
+  const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
-  const int wave = threadIdx.x >> 6;
-  State<T, DK, DV> st;
+  const int wave = wave_id();
+  S st;
   st.load(nullptr, 0, 0, 0);
   float total = 0.0f;
-  const int live_blocks = (w.live + C - 1) / C;
-  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
-  const int n = c1 - w.c0;
+  const int n = w.c1 - w.c0;
   Tile<T, DK> ty;
   Tile<T, DV> tx;
   float gx = 0.0f;
-  auto at = [&](int i) { return (BACK ? c1 - 1 - i : w.c0 + i) * C; };
+  auto at = [&](int i) { return (BACK ? w.c1 - 1 - i : w.c0 + i) * C; };
+  auto load = [&](int t0) {
+    ty.load(y + t0 * yt, yt, w.live - t0, a.dk);
+    tx.load(x + t0 * xt, xt, w.live - t0, dv);
+  };
   if (n > 0) {
-    ty.load(y, yt, at(0), w.live, a.dk);
-    tx.load(x, xt, at(0), w.live, a.dvd);
-    if (wave == 0) scan_g<C>(load_g<C>(a, g, at(0), w.live), his[0], los[0]);
+    load(at(0));
+    if (wave == 0) scan_g(load_g<C>(a, g, at(0), w.live), decays[0]);
     if (n > 1) gx = load_g<C>(a, g, at(1), w.live);
   }
   for (int i = 0; i < n; ++i) {
-    const float *hi = his[i & 1], *lo = los[i & 1];
+    const Decays<C>& d = decays[i & 1];
     ty.store(ys);
     tx.store(xs);
     __syncthreads();
     if (i + 1 < n) {
-      ty.load(y, yt, at(i + 1), w.live, a.dk);
-      tx.load(x, xt, at(i + 1), w.live, a.dvd);
-      if (wave == i % B::kWaves) scan_g<C>(gx, his[(i + 1) & 1], los[(i + 1) & 1]);
+      load(at(i + 1));
+      if (wave == i % B::kWaves) scan_g(gx, decays[(i + 1) & 1]);
       if (i + 2 < n) gx = load_g<C>(a, g, at(i + 2), w.live);
     }
-    total += hi[C - 1] + lo[C - 1];
-    st.template update<BACK>(ys, xs, hi, lo, a.scale);
+    total += d.hi[C - 1] + d.lo[C - 1];
+    st.decay(d.from0[C - 1]);
+#pragma unroll
+    for (int kk = 0; kk < C / 32; ++kk) {
+      float m[8];
+      eight((BACK ? d.from0 : d.toC) + kk * 32, m);
+      if (BACK) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] *= a.scale;
+      }
+      const Cols<T, SX, S::kNT> xa(xs + kk * 32 * SX);
+      st.add(ys + kk * 32 * SY, xa, m);
+    }
     __syncthreads();
   }
-  st.store((BACK ? a.seg_ds : a.seg_s) + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
-  if (!BACK && threadIdx.x == 0) a.seg_g[w.bh * a.segments + w.seg] = total;
+  st.store((BACK ? a.seg_ds : a.seg_s) + (w.bh * a.segments + w.seg) * (DK * a.ld) + w.n0, DK, DV, a.ld);
+  if (!BACK && w.n0 == 0 && threadIdx.x == 0) a.seg_g[w.bh * a.segments + w.seg] = total;
 }
 
 // In place: each segment's own state becomes the state that enters it (BACK: the gradient at its
-// end).  A thread owns 4 elements of one (sequence, head).
+// end).  A thread owns 4 elements of one (sequence, head) and has 8 segments on their way at a time.
 template <bool BACK>
-__global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK, int DV) {
-  const int per = DK * DV / 4;
+__global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) {
+  const int per = DK * a.ld / 4;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t bh = id / per;
   if (bh >= a.batch * a.heads) return;
-  const int e = static_cast<int>(id - bh * per) * 4, d = e / DV, n = e % DV;
+  const int e = static_cast<int>(id - bh * per) * 4, d = e / a.ld, n = e % a.ld;
   f32x4 run = zero4();
   const float* first = BACK ? a.dsT : a.s0;
-  if (first && d < a.dk && n < a.dvd)
-    run = *reinterpret_cast<const f32x4*>(first + (bh * a.dk + d) * a.dvd + n);
-  float* p = (BACK ? a.seg_ds : a.seg_s) + bh * a.segments * static_cast<int64_t>(DK * DV) + e;
+  if (first && d < a.dk && n < a.dvd) run = load4(first + (bh * a.dk + d) * a.dvd + n);
+  const int64_t step = static_cast<int64_t>(DK) * a.ld;
+  float* p = (BACK ? a.seg_ds : a.seg_s) + bh * a.segments * step + e;
   const float* g = a.seg_g + bh * a.segments;
-  for (int i = 0; i < a.segments; ++i) {
-    const int s = BACK ? a.segments - 1 - i : i;
-    f32x4* at = reinterpret_cast<f32x4*>(p + static_cast<int64_t>(s) * (DK * DV));
-    const f32x4 own = *at;
-    *at = run;
-    run = run * __builtin_amdgcn_exp2f(g[s]) + own;
+  constexpr int kAhead = 8;
+  for (int i0 = 0; i0 < a.segments; i0 += kAhead) {
+    f32x4 own[kAhead];
+    float m[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < a.segments) {
+        const int s = BACK ? a.segments - 1 - i0 - i : i0 + i;
+        own[i] = load4(p + s * step);
+        m[i] = __builtin_amdgcn_exp2f(g[s]);
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < a.segments) {
+        const int s = BACK ? a.segments - 1 - i0 - i : i0 + i;
+        store_acc(p + s * step, run);
+        run = run * m[i] + own[i];
+      }
   }
 }
 
@@ -569,116 +669,128 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK, 
 // forward
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) void linattn_fwd_kernel(LinArgs a) {
+__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride, NT = DV / 16;
   __shared__ __align__(16) T qs[C * SK];
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T ss[DK * SS];
-  __shared__ __align__(16) float his[2][C], los[2][C];
-  const Where w = where(a);
+  __shared__ __align__(16) Decays<C> decays[2];
+  const Where w = where<T>(a, DV);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
-  const T* v = head<T>(a.v, w.b, w.h);
+  const T* v = head<T>(a.v, w.b, w.h) + w.n0;
+  const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
-  T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd;
+  T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd + w.n0;
   const int64_t ot = static_cast<int64_t>(a.heads) * a.dvd;
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+  const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
 
   S st;
   if (a.segments > 1)
-    st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+    st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * a.ld) + w.n0, DK, DV, a.ld);
   else
-    st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+    st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd + w.n0 : nullptr, a.dk, dv, a.dvd);
 
-  const int live_blocks = (w.live + C - 1) / C;
-  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
   Tile<T, DK> tq, tk;
   Tile<T, DV> tv;
+  auto load = [&](int t0) {
+    tq.load(q + t0 * a.q.t, a.q.t, w.live - t0, a.dk);
+    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
+    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, dv);
+  };
   float gx = 0.0f;
-  if (w.c0 < c1) {
-    tq.load(q, a.q.t, w.c0 * C, w.live, a.dk);
-    tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
-    tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
-    if (wave == 0) scan_g<C>(load_g<C>(a, g, w.c0 * C, w.live), his[w.c0 & 1], los[w.c0 & 1]);
+  if (w.c0 < w.c1) {
+    load(w.c0 * C);
+    if (wave == 0) scan_g(load_g<C>(a, g, w.c0 * C, w.live), decays[w.c0 & 1]);
     gx = load_g<C>(a, g, w.c0 * C + C, w.live);
   }
-  for (int c = w.c0; c < c1; ++c) {
+  for (int c = w.c0; c < w.c1; ++c) {
     const int t0 = c * C;
-    const float *hi = his[c & 1], *lo = los[c & 1];
+    const Decays<C>& d = decays[c & 1];
     tq.store(qs);
     tk.store(ks);
     tv.store(vs);
     st.publish(ss);
     __syncthreads();
-    if (c + 1 < c1) {
-      tq.load(q, a.q.t, t0 + C, w.live, a.dk);
-      tk.load(k, a.k.t, t0 + C, w.live, a.dk);
-      tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
+    if (c + 1 < w.c1) {
+      load(t0 + C);
       // the next block's decays, by one wave; the others' products run meanwhile
-      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c + 1) & 1], los[(c + 1) & 1]);
+      if (wave == c % B::kWaves) scan_g(gx, decays[(c + 1) & 1]);
       gx = load_g<C>(a, g, t0 + 2 * C, w.live);
     }
     // this wave's 16 queries: column i of every result tile
     const int i0 = wave * 16, i = i0 + li;
-    const float gh = hi[i], gl = lo[i];
-    f32x4 acc[DV / 16];
-    {
+    const bool own = t0 + i0 < w.live;
+    const float gh = d.hi[i], gl = d.lo[i];
+    f32x4 acc[NT];
+    Frag<T> qf[DK / 32];
+    if (own) {
       // e^{G_i} S^T q_i
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = zero4();
+      for (int nt = 0; nt < NT; ++nt) acc[nt] = zero4();
 #pragma unroll
       for (int kk = 0; kk < DK / 32; ++kk) {
         const Frag<T> qp = frag_row_perm<SK>(qs + i0 * SK + kk * 32);
+        qf[kk] = frag_row<SK>(qs + i0 * SK + kk * 32);
 #pragma unroll
-        for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), qp, acc[nt]);
+        for (int nt = 0; nt < NT; ++nt) acc[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), qp, acc[nt]);
       }
-      const float e = __builtin_amdgcn_exp2f(gh + gl);
+      const float e = d.from0[i];
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] *= e;
+      for (int nt = 0; nt < NT; ++nt) acc[nt] *= e;
     }
-    Frag<T> qf[DK / 32];
+    st.decay(d.from0[C - 1]);
 #pragma unroll
-    for (int kk = 0; kk < DK / 32; ++kk) qf[kk] = frag_row<SK>(qs + i0 * SK + kk * 32);
-    // the masked scores of 32 keys at a time, then their product with the values
-    for (int jj = 0; jj <= wave / 2; ++jj) {
-      float p[8];
+    for (int kk = 0; kk < C / 32; ++kk) {
+      if (t0 + kk * 32 >= w.live) break;
+      const Cols<T, SV, NT> xa(vs + kk * 32 * SV);
+      if (own && kk <= wave / 2) {
+        // the masked scores of 32 keys, then their product with the values
+        float p[8];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int j0 = jj * 32 + t * 16;
-        f32x4 sc = zero4();
-        if (j0 <= i0) {
+        for (int t = 0; t < 2; ++t) {
+          const int j0 = kk * 32 + t * 16;
+          if (j0 <= i0) {
+            f32x4 sc = zero4();
 #pragma unroll
-          for (int kk = 0; kk < DK / 32; ++kk) sc = mma(frag_row<SK>(ks + j0 * SK + kk * 32), qf[kk], sc);
+            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(ks + j0 * SK + n * 32), qf[n], sc);
+            if (j0 < i0) {  // through the last of the 16 keys: both factors are powers of the decays between
+              const f32x4 e = load4(d.toE + j0 + g4);
+              const float from = d.between(gh, gl, j0 + 15);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) p[t * 4 + r] = sc[r] * (e[r] * from);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                p[t * 4 + r] = g4 + r <= li ? sc[r] * d.between(gh, gl, j0 + g4 + r) : 0.0f;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
+          }
         }
+        Frag<T> pf;
+        pack(p, pf);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = j0 + g4 + r;
-          const float e = exp2_diff(gh, gl, hi[j], lo[j]);
-          p[t * 4 + r] = j <= i ? sc[r] * e : 0.0f;
-        }
+        for (int nt = 0; nt < NT; ++nt) acc[nt] = mma(xa[nt], pf, acc[nt]);
       }
-      Frag<T> pf;
-      pack(p, pf);
-#pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt) acc[nt] = mma(frag_col<SV>(vs + jj * 32 * SV + nt * 16), pf, acc[nt]);
+      float m[8];
+      eight(d.toC + kk * 32, m);
+      st.add(ks + kk * 32 * SK, xa, m);
     }
     if (t0 + i < w.live) {
-      T* o = out + (t0 + i) * ot;
+      T* o = out + t0 * ot;
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt)
-        if (nt * 16 + g4 < a.dvd) store_acc(o + nt * 16 + g4, acc[nt] * a.scale);
+      for (int nt = 0; nt < NT; ++nt)
+        if (nt * 16 + g4 < dv) store_acc(o + static_cast<uint32_t>(i * ot + nt * 16 + g4), acc[nt] * a.scale);
     }
-    st.template update<false>(ks, vs, hi, lo, 1.0f);
     __syncthreads();
   }
-  // tokens past the row's length
-  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
-  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
-  zero_tokens<B::kThreads>(out, ot, a.dvd, t_dead, t_end);
-  if (a.sT && w.seg == a.segments - 1) st.store(a.sT + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
+  zero_rest<T>(a, w, out, ot, dv < DV ? dv : DV);
+  if (a.sT && w.seg == a.segments - 1) st.store(a.sT + w.bh * a.dk * a.dvd + w.n0, a.dk, dv, a.dvd);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -700,24 +812,24 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_fwd_kernel(LinArgs
 // small difference of sums over the whole sequence; here only terms that belong are added.
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs a) {
+__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_dq_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride, DT = DK / 16;
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T os[C * SV];
   __shared__ __align__(16) T ss[DK * SS];
-  __shared__ __align__(16) float his[2][C], los[2][C];
+  __shared__ __align__(16) Decays<C> decays[2];
   __shared__ float part[B::kWaves][C];
-  const Where w = where(a);
+  const Where w = where<T>(a, DV);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
   const T* v = head<T>(a.v, w.b, w.h);
   const T* o = head<T>(a.dout, w.b, w.h);
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int64_t ot = static_cast<int64_t>(a.heads) * a.dk, obase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+  const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
 
   S st;
   if (a.segments > 1)
@@ -725,21 +837,22 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
   else
     st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
 
-  const int live_blocks = (w.live + C - 1) / C;
-  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
   Tile<T, DK> tk;
   Tile<T, DV> tv, to;
+  auto load = [&](int t0) {
+    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
+    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, a.dvd);
+    to.load(o + t0 * a.dout.t, a.dout.t, w.live - t0, a.dvd);
+  };
   float gx = 0.0f;
-  if (w.c0 < c1) {
-    tk.load(k, a.k.t, w.c0 * C, w.live, a.dk);
-    tv.load(v, a.v.t, w.c0 * C, w.live, a.dvd);
-    to.load(o, a.dout.t, w.c0 * C, w.live, a.dvd);
-    if (wave == 0) scan_g<C>(load_g<C>(a, g, w.c0 * C, w.live), his[w.c0 & 1], los[w.c0 & 1]);
+  if (w.c0 < w.c1) {
+    load(w.c0 * C);
+    if (wave == 0) scan_g(load_g<C>(a, g, w.c0 * C, w.live), decays[w.c0 & 1]);
     gx = load_g<C>(a, g, w.c0 * C + C, w.live);
   }
-  for (int c = w.c0; c < c1; ++c) {
+  for (int c = w.c0; c < w.c1; ++c) {
     const int t0 = c * C;
-    const float *hi = his[c & 1], *lo = los[c & 1];
+    const Decays<C>& d = decays[c & 1];
     tk.store(ks);
     tv.store(vs);
     to.store(os);
@@ -748,102 +861,115 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dq_kernel(LinArgs 
     __syncthreads();
     // channels 16 d_tile + 4 g .. of the queries 16 jt + li, for a_i
     f32x4 q4[S::kDT][B::kWaves];
+    const T* qt = q + t0 * a.q.t;
 #pragma unroll
     for (int t = 0; t < S::kDT; ++t)
 #pragma unroll
       for (int jt = 0; jt < B::kWaves; ++jt) {
-        const int d = (wave * S::kDT + t) * 16 + g4, n = t0 + jt * 16 + li;
+        const int dd = (wave * S::kDT + t) * 16 + g4, n = jt * 16 + li;
         q4[t][jt] = zero4();
-        if (n < w.live && d < a.dk) q4[t][jt] = load4(q + n * a.q.t + d);
+        if (t0 + n < w.live && dd < a.dk)
+          q4[t][jt] = load4(qt + static_cast<uint32_t>(n * static_cast<uint32_t>(a.q.t) + dd));
       }
-    if (c + 1 < c1) {
-      tk.load(k, a.k.t, t0 + C, w.live, a.dk);
-      tv.load(v, a.v.t, t0 + C, w.live, a.dvd);
-      to.load(o, a.dout.t, t0 + C, w.live, a.dvd);
-      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c + 1) & 1], los[(c + 1) & 1]);
+    if (c + 1 < w.c1) {
+      load(t0 + C);
+      if (wave == c % B::kWaves) scan_g(gx, decays[(c + 1) & 1]);
       gx = load_g<C>(a, g, t0 + 2 * C, w.live);
     }
-    st.bilinear(os, [&](int t, int jt) { return q4[t][jt]; }, part[wave]);
     const int i0 = wave * 16, i = i0 + li;
-    const bool live = t0 + i < w.live;
-    const float gh = hi[i], gl = lo[i];
-    Frag<T> of[DV / 32];
+    if (t0 + i0 < w.live) {
+      const float gh = d.hi[i], gl = d.lo[i];
+      Frag<T> of[DV / 32];
 #pragma unroll
-    for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<SV>(os + i0 * SV + kk * 32);
-    f32x4 acc[DK / 16];
-    const float e0 = __builtin_amdgcn_exp2f(gh + gl) * a.scale;
+      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<SV>(os + i0 * SV + kk * 32);
+      f32x4 acc[DT];
+      const float e0 = d.from0[i] * a.scale;
 #pragma unroll
-    for (int dt = 0; dt < DK / 16; ++dt) {
-      acc[dt] = zero4();
+      for (int dt = 0; dt < DT; ++dt) {
+        acc[dt] = zero4();
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) {
-        acc[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+        for (int kk = 0; kk < DV / 32; ++kk) acc[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+        acc[dt] *= e0;
       }
-      acc[dt] *= e0;
-    }
-    for (int jj = 0; jj <= wave / 2; ++jj) {
-      float p[8];
+      for (int jj = 0; jj <= wave / 2; ++jj) {
+        float p[8];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int j0 = jj * 32 + t * 16;
-        f32x4 dp = zero4();
-        if (j0 <= i0) {
+        for (int t = 0; t < 2; ++t) {
+          const int j0 = jj * 32 + t * 16;
+          if (j0 <= i0) {
+            f32x4 dp = zero4();
 #pragma unroll
-          for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(vs + j0 * SV + kk * 32), of[kk], dp);
+            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(vs + j0 * SV + kk * 32), of[kk], dp);
+            if (j0 < i0) {
+              const f32x4 e = load4(d.toE + j0 + g4);
+              const float from = d.between(gh, gl, j0 + 15) * a.scale;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) p[t * 4 + r] = dp[r] * (e[r] * from);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                p[t * 4 + r] = g4 + r <= li ? dp[r] * (d.between(gh, gl, j0 + g4 + r) * a.scale) : 0.0f;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
+          }
         }
+        Frag<T> pf;
+        pack(p, pf);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = j0 + g4 + r;
-          const float e = exp2_diff(gh, gl, hi[j], lo[j]) * a.scale;
-          p[t * 4 + r] = j <= i ? dp[r] * e : 0.0f;
-        }
+        for (int dt = 0; dt < DT; ++dt) acc[dt] = mma(frag_col<SK>(ks + jj * 32 * SK + dt * 16), pf, acc[dt]);
       }
-      Frag<T> pf;
-      pack(p, pf);
+      if (t0 + i < w.live) {
 #pragma unroll
-      for (int dt = 0; dt < DK / 16; ++dt) acc[dt] = mma(frag_col<SK>(ks + jj * 32 * SK + dt * 16), pf, acc[dt]);
+        for (int dt = 0; dt < DT; ++dt)
+          if (dt * 16 + g4 < a.dk) {
+            const uint32_t at = static_cast<uint32_t>(i * ot + dt * 16 + g4);
+            if (a.share == 1)
+              store_acc(static_cast<T*>(a.dq) + (obase + t0 * ot) + at, acc[dt]);
+            else
+              store_acc(static_cast<float*>(a.dq) + (obase + t0 * ot) + at, acc[dt]);
+          }
+      }
     }
-    if (live) {
+    st.bilinear(os, [&](int t, int jt) { return q4[t][jt]; }, part[wave]);
+    st.decay(d.from0[C - 1]);
 #pragma unroll
-      for (int dt = 0; dt < DK / 16; ++dt)
-        if (dt * 16 + g4 < a.dk) {
-          const int64_t at = obase + (t0 + i) * ot + dt * 16 + g4;
-          if (a.share == 1)
-            store_acc(static_cast<T*>(a.dq) + at, acc[dt]);
-          else
-            store_acc(static_cast<float*>(a.dq) + at, acc[dt]);
-        }
+    for (int kk = 0; kk < C / 32; ++kk) {
+      if (t0 + kk * 32 >= w.live) break;
+      const Cols<T, SV, S::kNT> xa(vs + kk * 32 * SV);
+      float m[8];
+      eight(d.toC + kk * 32, m);
+      st.add(ks + kk * 32 * SK, xa, m);
     }
-    st.template update<false>(ks, vs, hi, lo, 1.0f);
     __syncthreads();
     if (wave == c % B::kWaves && l < C) {  // part is written again only past the next barrier
       float sum = 0.0f;
 #pragma unroll
       for (int n = 0; n < B::kWaves; ++n) sum += part[n][l];
-      a.qa[w.bh * a.blocks * C + t0 + l] = sum * a.scale * __builtin_amdgcn_exp2f(hi[l] + lo[l]);
+      a.qa[w.bh * a.blocks * C + t0 + l] = sum * a.scale * d.from0[l];
     }
   }
-  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
-  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
   if (a.share == 1)
-    zero_tokens<B::kThreads>(static_cast<T*>(a.dq) + obase, ot, a.dk, t_dead, t_end);
+    zero_rest<T>(a, w, static_cast<T*>(a.dq) + obase, ot, a.dk);
   else
-    zero_tokens<B::kThreads>(static_cast<float*>(a.dq) + obase, ot, a.dk, t_dead, t_end);
+    zero_rest<T>(a, w, static_cast<float*>(a.dq) + obase, ot, a.dk);
 }
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs a) {
+__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dkv_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  constexpr int DT = DK / 16, NT = DV / 16;
   __shared__ __align__(16) T qs[C * SK];
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T os[C * SV];
   __shared__ __align__(16) T ss[DK * SS];
-  __shared__ __align__(16) float his[2][C], los[2][C];
+  __shared__ __align__(16) Decays<C> decays[2];
   __shared__ float rows[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
-  const Where w = where(a);
+  const Where w = where<T>(a, DV);
   const T* q = head<T>(a.q, w.b, w.h / a.share);
   const T* k = head<T>(a.k, w.b, w.h / a.share);
   const T* v = head<T>(a.v, w.b, w.h);
@@ -852,7 +978,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
   const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
   const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
   float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+  const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
 
   S st;
   if (a.segments > 1)
@@ -860,25 +986,23 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
   else
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
 
-  const int live_blocks = (w.live + C - 1) / C;
-  const int c1 = w.c1 < live_blocks ? w.c1 : live_blocks;
   Tile<T, DK> tq, tk;
   Tile<T, DV> tv, to;
   float gx = 0.0f;
   auto load = [&](int t0) {
-    tq.load(q, a.q.t, t0, w.live, a.dk);
-    tk.load(k, a.k.t, t0, w.live, a.dk);
-    tv.load(v, a.v.t, t0, w.live, a.dvd);
-    to.load(o, a.dout.t, t0, w.live, a.dvd);
+    tq.load(q + t0 * a.q.t, a.q.t, w.live - t0, a.dk);
+    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
+    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, a.dvd);
+    to.load(o + t0 * a.dout.t, a.dout.t, w.live - t0, a.dvd);
   };
-  if (w.c0 < c1) {
-    load((c1 - 1) * C);
-    if (wave == 0) scan_g<C>(load_g<C>(a, g, (c1 - 1) * C, w.live), his[(c1 - 1) & 1], los[(c1 - 1) & 1]);
-    if (c1 - 1 > w.c0) gx = load_g<C>(a, g, (c1 - 2) * C, w.live);
+  if (w.c0 < w.c1) {
+    load((w.c1 - 1) * C);
+    if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), decays[(w.c1 - 1) & 1]);
+    if (w.c1 - 1 > w.c0) gx = load_g<C>(a, g, (w.c1 - 2) * C, w.live);
   }
-  for (int c = c1 - 1; c >= w.c0; --c) {
+  for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
-    const float *hi = his[c & 1], *lo = los[c & 1];
+    const Decays<C>& d = decays[c & 1];
     // the state that entered the block and the a_i, from the walk forwards
     S old;
     old.load(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
@@ -891,111 +1015,132 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
     __syncthreads();
     if (c > w.c0) {
       load(t0 - C);
-      if (wave == c % B::kWaves) scan_g<C>(gx, his[(c - 1) & 1], los[(c - 1) & 1]);
+      if (wave == c % B::kWaves) scan_g(gx, decays[(c - 1) & 1]);
       if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
-    }
-    {
-      // Y: that state against R, both in this wave's layout
-      float y = 0.0f;
-#pragma unroll
-      for (int t = 0; t < S::kDT; ++t)
-#pragma unroll
-        for (int nt = 0; nt < S::kNT; ++nt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
-      y = sum_rows(row_sum(y));
-      if (l == 0) across[wave] = y * __builtin_amdgcn_exp2f(hi[C - 1] + lo[C - 1]);
     }
     st.bilinear(vs, [&](int t, int jt) { return load4(ks + (jt * 16 + li) * SK + (wave * S::kDT + t) * 16 + g4); },
                 after[wave]);
     // this wave's 16 keys: column j of every result tile
     const int j0 = wave * 16, j = j0 + li;
-    const float gh = hi[j], gl = lo[j];
-    const float ec = exp2_diff(hi[C - 1], lo[C - 1], gh, gl);
+    const float gh = d.hi[j], gl = d.lo[j], toC = d.toC[j], toE = d.toE[j] * a.scale;
     Frag<T> kf[DK / 32], vf[DV / 32];
 #pragma unroll
     for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<SK>(ks + j0 * SK + kk * 32);
 #pragma unroll
     for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<SV>(vs + j0 * SV + kk * 32);
-    f32x4 ak[DK / 16], av[DV / 16];
+    f32x4 ak[DT], av[NT];
 #pragma unroll
-    for (int dt = 0; dt < DK / 16; ++dt) {
+    for (int dt = 0; dt < DT; ++dt) {
       ak[dt] = zero4();
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) {
-        ak[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
-      }
-      ak[dt] *= ec;
+      for (int kk = 0; kk < DV / 32; ++kk) ak[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
+      ak[dt] *= toC;
     }
 #pragma unroll
-    for (int nt = 0; nt < DV / 16; ++nt) av[nt] = zero4();
+    for (int nt = 0; nt < NT; ++nt) av[nt] = zero4();
 #pragma unroll
     for (int kk = 0; kk < DK / 32; ++kk) {
       const Frag<T> kp = frag_row_perm<SK>(ks + j0 * SK + kk * 32);
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt) av[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), kp, av[nt]);
+      for (int nt = 0; nt < NT; ++nt) av[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), kp, av[nt]);
     }
 #pragma unroll
-    for (int nt = 0; nt < DV / 16; ++nt) av[nt] *= ec;
-
+    for (int nt = 0; nt < NT; ++nt) av[nt] *= toC;
+    {
+      // Y: the state before the block against R, both in this wave's layout
+      float y = 0.0f;
+#pragma unroll
+      for (int t = 0; t < S::kDT; ++t)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
+      y = sum_rows(row_sum(y));
+      if (l == 0) across[wave] = y * d.from0[C - 1];
+    }
+    st.decay(d.from0[C - 1]);
     // Queries from the last 32 down.  Beside the products, M_ij summed over the queries from t on (in
     // this lane's column; `later`: the tiles done) and then over the keys before t.
     float later = 0.0f;
-    for (int ii = C / 32 - 1; ii >= wave / 2; --ii) {
-      float p[8], x[8];
 #pragma unroll
-      for (int t = 1; t >= 0; --t) {
-        const int i0 = ii * 32 + t * 16;
-        f32x4 sc = zero4(), dp = zero4();
-        if (i0 >= j0) {
+    for (int kk = C / 32 - 1; kk >= 0; --kk) {
+      const Cols<T, SV, NT> xa(os + kk * 32 * SV);
+      if (kk >= wave / 2) {
+        float p[8], x[8];
 #pragma unroll
-          for (int kk = 0; kk < DK / 32; ++kk) sc = mma(frag_row<SK>(qs + i0 * SK + kk * 32), kf[kk], sc);
+        for (int t = 1; t >= 0; --t) {
+          const int i0 = kk * 32 + t * 16;
+          if (i0 >= j0) {
+            f32x4 sc = zero4(), dp = zero4();
 #pragma unroll
-          for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(os + i0 * SV + kk * 32), vf[kk], dp);
+            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(qs + i0 * SK + n * 32), kf[n], sc);
+#pragma unroll
+            for (int n = 0; n < DV / 32; ++n) dp = mma(frag_row<SV>(os + i0 * SV + n * 32), vf[n], dp);
+            float u[4];
+            if (i0 > j0) {  // through the last token before the 16 queries
+              const f32x4 e = load4(d.fromF + i0 + g4);
+              const float to_ = __builtin_amdgcn_exp2f((d.hi[i0 - 1] - gh) + (d.lo[i0 - 1] - gl)) * a.scale;
+#pragma unroll
+              for (int r = 3; r >= 0; --r) {
+                const float f = e[r] * to_;
+                p[t * 4 + r] = sc[r] * f;
+                x[t * 4 + r] = dp[r] * f;
+                u[r] = sc[r] * x[t * 4 + r] + (r < 3 ? u[r + 1] : 0.0f);
+              }
+            } else {
+#pragma unroll
+              for (int r = 3; r >= 0; --r) {
+                const int i = i0 + g4 + r;
+                const float f = __builtin_amdgcn_exp2f((d.hi[i] - gh) + (d.lo[i] - gl)) * a.scale;
+                p[t * 4 + r] = i >= j ? sc[r] * f : 0.0f;
+                x[t * 4 + r] = i >= j ? dp[r] * f : 0.0f;
+                u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
+              }
+            }
+            float tiles[4];  // this lane's rows of the tile, and the other lanes' of the column
+            rows_of(u[0], tiles);
+            const float below = sum_after(tiles, g4 / 4) + later;
+            later += (tiles[0] + tiles[1]) + (tiles[2] + tiles[3]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = i0 + g4 + r;
+              const float m = row_sum(j < i ? u[r] + below : 0.0f);
+              if (li == 0) rows[wave][i] = m;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[t * 4 + r] = x[t * 4 + r] = 0.0f;
+          }
         }
-        float u[4];
+        Frag<T> pf, xf;
+        pack(p, pf);
+        pack(x, xf);
 #pragma unroll
-        for (int r = 3; r >= 0; --r) {
-          const int i = i0 + g4 + r;
-          const float e = exp2_diff(hi[i], lo[i], gh, gl) * a.scale;
-          p[t * 4 + r] = i >= j ? sc[r] * e : 0.0f;
-          x[t * 4 + r] = i >= j ? dp[r] * e : 0.0f;
-          u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
-        }
-        float tiles[4];  // this lane's rows of the tile, and the other lanes' of the column
-        rows_of(u[0], tiles);
-        const float below = sum_after(tiles, g4 / 4) + later;
-        later += (tiles[0] + tiles[1]) + (tiles[2] + tiles[3]);
+        for (int nt = 0; nt < NT; ++nt) av[nt] = mma(xa[nt], pf, av[nt]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = i0 + g4 + r;
-          const float m = row_sum(j < i ? u[r] + below : 0.0f);
-          if (li == 0) rows[wave][i] = m;
-        }
+        for (int dt = 0; dt < DT; ++dt) ak[dt] = mma(frag_col<SK>(qs + kk * 32 * SK + dt * 16), xf, ak[dt]);
       }
-      Frag<T> pf, xf;
-      pack(p, pf);
-      pack(x, xf);
+      float m[8];
+      eight(d.from0 + kk * 32, m);
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt) av[nt] = mma(frag_col<SV>(os + ii * 32 * SV + nt * 16), pf, av[nt]);
-#pragma unroll
-      for (int dt = 0; dt < DK / 16; ++dt) ak[dt] = mma(frag_col<SK>(qs + ii * 32 * SK + dt * 16), xf, ak[dt]);
+      for (int e = 0; e < 8; ++e) m[e] *= a.scale;
+      st.add(qs + kk * 32 * SK, xa, m);
     }
     if (t0 + j < w.live) {
 #pragma unroll
-      for (int dt = 0; dt < DK / 16; ++dt)
+      for (int dt = 0; dt < DT; ++dt)
         if (dt * 16 + g4 < a.dk) {
-          const int64_t at = kbase + (t0 + j) * kt + dt * 16 + g4;
+          const uint32_t at = static_cast<uint32_t>(j * kt + dt * 16 + g4);
           if (a.share == 1)
-            store_acc(static_cast<T*>(a.dk_out) + at, ak[dt]);
+            store_acc(static_cast<T*>(a.dk_out) + (kbase + t0 * kt) + at, ak[dt]);
           else
-            store_acc(static_cast<float*>(a.dk_out) + at, ak[dt]);
+            store_acc(static_cast<float*>(a.dk_out) + (kbase + t0 * kt) + at, ak[dt]);
         }
 #pragma unroll
-      for (int nt = 0; nt < DV / 16; ++nt)
-        if (nt * 16 + g4 < a.dvd) store_acc(static_cast<T*>(a.dv_out) + vbase + (t0 + j) * vt + nt * 16 + g4, av[nt]);
+      for (int nt = 0; nt < NT; ++nt)
+        if (nt * 16 + g4 < a.dvd)
+          store_acc(static_cast<T*>(a.dv_out) + (vbase + t0 * vt) + static_cast<uint32_t>(j * vt + nt * 16 + g4), av[nt]);
     }
-    st.template update<true>(qs, os, hi, lo, a.scale);
     __syncthreads();
     if (wave == c % B::kWaves) {
       // lane t: token t0 + t.  The other waves write these arrays again only past the next barrier.
@@ -1005,7 +1150,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
         from = qa;
 #pragma unroll
         for (int i = 0; i < B::kWaves; ++i) before += after[i][l];
-        before *= exp2_diff(hi[C - 1], lo[C - 1], hi[l], lo[l]);
+        before *= d.toC[l];
         for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
       }
 #pragma unroll
@@ -1018,14 +1163,14 @@ __global__ __launch_bounds__(Block<T>::kThreads) void linattn_dkv_kernel(LinArgs
       if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + before + y;
     }
   }
-  const int t_end = w.c1 * C < a.seqlen ? w.c1 * C : a.seqlen;
-  const int t_dead = w.live > w.c0 * C ? w.live : w.c0 * C;
   if (a.share == 1)
-    zero_tokens<B::kThreads>(static_cast<T*>(a.dk_out) + kbase, kt, a.dk, t_dead, t_end);
+    zero_rest<T>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
   else
-    zero_tokens<B::kThreads>(static_cast<float*>(a.dk_out) + kbase, kt, a.dk, t_dead, t_end);
-  zero_tokens<B::kThreads>(static_cast<T*>(a.dv_out) + vbase, vt, a.dvd, t_dead, t_end);
-  for (int64_t t = t_dead + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads) dg[t * a.heads] = 0.0f;
+    zero_rest<T>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
+  zero_rest<T>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
+  const int t_end = w.end * C < a.seqlen ? w.end * C : a.seqlen;
+  for (int64_t t = (w.live > w.c0 * C ? w.live : w.c0 * C) + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads)
+    dg[t * a.heads] = 0.0f;
   if (a.ds0 && w.seg == 0) st.store(a.ds0 + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
 }
 
@@ -1148,26 +1293,52 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
 // host side
 
 constexpr int kMaxHeadDim = 128;
-constexpr int64_t kFillBlocks = 1024;   // workgroups wanted before a sequence is walked whole
-constexpr int kMinSegment = 2;          // blocks
+constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // a block's offsets fit 32 bits in bytes
+constexpr double kBlockTime[3] = {0.7, 1.0, 1.7};
+constexpr double kStartTime = 1.0;      // a walk's start and end, in blocks
+constexpr double kSegmentTime = 0.4;    // the segments' pass against the walk
+constexpr double kPrefixTime = 4.0;     // two more launches and the prefix
+constexpr int kMaxSegments = 64;
+constexpr int kSlice = 32;              // value channels of the narrowest workgroup
 
 int pad_dim(int d) { return d <= 64 ? 64 : 128; }
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Plan {
-  int blocks, segments, per;
+  int blocks, segments, per, width, slices;
 };
-Plan plan(int64_t batch, int64_t seqlen, int heads, vmscan_dtype dtype) {
+// Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
+int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
+  const int wide = (pad_dim(dk) == 128) + (width == 128);
+  const int per_cu = dtype == VMSCAN_F32 ? (wide == 0 ? 4 : 2) : (wide == 0 ? 3 : wide == 1 && !back ? 2 : 1);
+  return 256 * per_cu;
+}
+// How a call is cut up.  The forward's value channels are independent, so several workgroups can share them (each
+// repeats the scores), and a sequence can be cut into segments (a pass over the keys and values more, and
+// a prefix over the segments).  Of all cuts the one whose rounds of workgroups take the fewest block times
+// is taken, a block of 32, 64 or 128 value channels counted as kBlockTime.  The gradient needs all channels
+// of a token together and is only cut into segments.
+Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
   const int C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
-  Plan p;
-  p.blocks = static_cast<int>((seqlen + C - 1) / C);
-  const int64_t bh = batch * heads;
-  int64_t seg = (kFillBlocks + bh - 1) / bh;
-  if (seg > p.blocks / kMinSegment) seg = p.blocks / kMinSegment;
-  if (seg < 1 || 2 * bh > kFillBlocks) seg = 1;
-  p.per = static_cast<int>((p.blocks + seg - 1) / seg);
-  p.segments = (p.blocks + p.per - 1) / p.per;
-  return p;
+  Plan best{};
+  double least = 0.0;
+  const int blocks = static_cast<int>((seqlen + C - 1) / C);
+  for (int width = pad_dim(dv); width >= (back ? pad_dim(dv) : kSlice); width /= 2) {
+    const int slices = (dv + width - 1) / width;
+    const int64_t walks = batch * heads * slices, slots = slots_for(dtype, dk, width, back);
+    const double block = width == 32 ? kBlockTime[0] : width == 64 ? kBlockTime[1] : kBlockTime[2];
+    for (int seg = 1; seg <= blocks && seg <= kMaxSegments; ++seg) {
+      const int per = (blocks + seg - 1) / seg;
+      if ((blocks + per - 1) / per != seg) continue;
+      const double rounds = static_cast<double>((walks * seg + slots - 1) / slots);
+      const double time = rounds * (per + kStartTime) * block + (seg > 1 ? kSegmentTime * rounds * (per + kStartTime) * block + kPrefixTime : 0.0);
+      if (best.blocks == 0 || time < least) {
+        least = time;
+        best = Plan{blocks, seg, per, width, slices};
+      }
+    }
+  }
+  return best;
 }
 
 bool sizes_ok(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv) {
@@ -1187,8 +1358,9 @@ struct Layout {
 Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv, bool per_head, vmscan_dtype dtype,
               bool back) {
   Layout y{};
-  y.p = plan(batch, seqlen, heads, dtype);
-  const size_t bh = static_cast<size_t>(batch) * heads, state = static_cast<size_t>(pad_dim(dk)) * pad_dim(dv) * 4;
+  y.p = plan(batch, seqlen, heads, dk, dv, dtype, back);
+  const size_t bh = static_cast<size_t>(batch) * heads;
+  const size_t state = static_cast<size_t>(pad_dim(dk)) * y.p.slices * y.p.width * 4;
   const size_t C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -1222,46 +1394,42 @@ vmscan_status view(View& v, const void* p, const int64_t* strides, vmscan_dtype 
   const int64_t run = dtype == VMSCAN_F32 ? 4 : 8;
   if (!aligned_to(p, 16)) return VMSCAN_ERR_ALIGN;
   for (int i = 0; i < 3; ++i) {
-    if (strides[i] < 0) return VMSCAN_ERR_SHAPE;
+    if (strides[i] < 0 || (i == 1 && strides[i] >= kMaxTokenStride)) return VMSCAN_ERR_SHAPE;
     if (strides[i] % run) return VMSCAN_ERR_ALIGN;
   }
   v = View{p, strides[0], strides[1], strides[2]};
   return VMSCAN_OK;
 }
 
+// Calls f with the padded dk and the width of a workgroup's value channels.
 template <typename F>
-void with_dims(int dk, int dv, F&& f) {
+void with_dims(int dk, int width, F&& f) {
   using std::integral_constant;
+  integral_constant<int, 32> t;
   integral_constant<int, 64> s;
   integral_constant<int, 128> b;
-  if (dk <= 64 && dv <= 64) f(s, s);
-  else if (dk <= 64) f(s, b);
-  else if (dv <= 64) f(b, s);
-  else f(b, b);
+  if (dk <= 64) width == 32 ? f(s, t) : width == 64 ? f(s, s) : f(s, b);
+  else width == 32 ? f(b, t) : width == 64 ? f(b, s) : f(b, b);
 }
 
-template <typename T>
-void launch_segments(const LinArgs& a, bool back, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments));
-  with_dims(a.dk, a.dvd, [&](auto dk, auto dv) {
+dim3 walks(const LinArgs& a) { return dim3(static_cast<unsigned>(a.batch * a.heads * a.segments * a.slices)); }
+
+template <typename T, bool BACK>
+void launch_segments(const LinArgs& a, int width, hipStream_t stream) {
+  with_dims(a.dk, width, [&](auto dk, auto dv) {
     constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-    const int64_t n = a.batch * a.heads * (DK * DV / 4);
-    const dim3 pgrid(static_cast<unsigned>((n + 255) / 256));
-    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false>), grid, dim3(Block<T>::kThreads), 0, stream, a);
-    hipLaunchKernelGGL((linattn_prefix_kernel<false>), pgrid, dim3(256), 0, stream, a, DK, DV);
-    if (back) {
-      hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, true>), grid, dim3(Block<T>::kThreads), 0, stream, a);
-      hipLaunchKernelGGL((linattn_prefix_kernel<true>), pgrid, dim3(256), 0, stream, a, DK, DV);
-    }
+    const int64_t n = a.batch * a.heads * (DK * a.ld / 4);
+    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK>), walks(a), dim3(Block<T>::kThreads), 0, stream, a);
+    hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
+                       stream, a, DK);
   });
 }
 
 template <typename T>
-vmscan_status run_fwd(const LinArgs& a, hipStream_t stream) {
-  if (a.segments > 1) launch_segments<T>(a, false, stream);
-  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments));
-  with_dims(a.dk, a.dvd, [&](auto dk, auto dv) {
-    hipLaunchKernelGGL((linattn_fwd_kernel<T, decltype(dk)::value, decltype(dv)::value>), grid,
+vmscan_status run_fwd(const LinArgs& a, int width, hipStream_t stream) {
+  if (a.segments > 1) launch_segments<T, false>(a, width, stream);
+  with_dims(a.dk, width, [&](auto dk, auto dv) {
+    hipLaunchKernelGGL((linattn_fwd_kernel<T, decltype(dk)::value, decltype(dv)::value>), walks(a),
                        dim3(Block<T>::kThreads), 0, stream, a);
   });
   return launched();
@@ -1274,12 +1442,17 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   a.dq = shared ? ws + y.dq : dq;
   a.dk_out = shared ? ws + y.dk : dk;
   a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
-  if (a.segments > 1) launch_segments<T>(a, true, stream);
-  const dim3 grid(static_cast<unsigned>(a.batch * a.heads * a.segments)), block(Block<T>::kThreads);
-  with_dims(a.dk, a.dvd, [&](auto k, auto v) {
+  if (a.segments > 1) {
+    launch_segments<T, false>(a, y.p.width, stream);
+    launch_segments<T, true>(a, y.p.width, stream);
+  }
+  const dim3 grid = walks(a), block(Block<T>::kThreads);
+  with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
-    hipLaunchKernelGGL((linattn_dq_kernel<T, DK, DV>), grid, block, 0, stream, a);
-    hipLaunchKernelGGL((linattn_dkv_kernel<T, DK, DV>), grid, block, 0, stream, a);
+    if constexpr (DV >= 64) {
+      hipLaunchKernelGGL((linattn_dq_kernel<T, DK, DV>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((linattn_dkv_kernel<T, DK, DV>), grid, block, 0, stream, a);
+    }
   });
   const int64_t tokens = a.batch * a.seqlen;
   if (shared) {
@@ -1324,6 +1497,7 @@ vmscan_status common_args(LinArgs& a, const void* q, const int64_t* qs, const vo
 
 void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.blocks = y.p.blocks, a.segments = y.p.segments, a.per_segment = y.p.per;
+  a.slices = y.p.slices, a.ld = y.p.slices * y.p.width;
   a.seg_s = reinterpret_cast<float*>(ws + y.seg_s);
   a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
   a.seg_g = reinterpret_cast<float*>(ws + y.seg_g);
@@ -1331,8 +1505,8 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.qa = reinterpret_cast<float*>(ws + y.qa);
 }
 
-vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, int segments) {
-  if (a.batch * a.heads * segments >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
+  if (a.batch * a.heads * p.segments * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
   if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
   return need && (!ws || have < need) ? VMSCAN_ERR_WORKSPACE : VMSCAN_OK;
 }
@@ -1360,11 +1534,12 @@ vmscan_status vmscan_linattn_fwd(const void* q, const int64_t* q_strides, const 
   if (st != VMSCAN_OK) return st;
   if (!aligned_to(out, 16) || !aligned_to(final_state, 16)) return VMSCAN_ERR_ALIGN;
   const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, false, dtype, false);
-  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p.segments);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
   if (st != VMSCAN_OK) return st;
   place(a, y, static_cast<unsigned char*>(workspace));
   a.out = out, a.sT = final_state;
-  return dtype == VMSCAN_F32 ? run_fwd<float>(a, stream) : run_fwd<uint16_t>(a, stream);
+  return dtype == VMSCAN_F32 ? run_fwd<float>(a, y.p.width, stream)
+                            : run_fwd<uint16_t>(a, y.p.width, stream);
 }
 
 size_t vmscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv,
@@ -1393,7 +1568,7 @@ vmscan_status vmscan_linattn_bwd(const void* q, const int64_t* q_strides, const 
   if (!aligned_to(dlog_decay, 4)) return VMSCAN_ERR_ALIGN;
   const bool per_head = decay_strides == nullptr;
   const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, per_head, dtype, true);
-  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p.segments);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
   if (st != VMSCAN_OK) return st;
   if (kheads != heads && batch * seqlen * kheads * (dk / 4) / 256 >= (int64_t{1} << 31) - 1) return VMSCAN_ERR_SHAPE;
   unsigned char* ws = static_cast<unsigned char*>(workspace);

@@ -84,7 +84,7 @@ def test_rope(lib):
 
 def fwd(lib, **kw):
     s = st(1024, 128, 32)
-    a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, s0=P[4], n=P[5], out=P[6], sT=P[7], nb=2, L=300,
+    a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, s0=P[4], n=P[5], out=P[6], sT=P[7], nb=2, L=6000,
              H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1, ws=P[8], wsb=0)
     a.update(kw)
     return lib.vmscan_linattn_fwd(*a.values(), None)
@@ -93,7 +93,7 @@ def fwd(lib, **kw):
 def bwd(lib, **kw):
     s = st(1024, 128, 32)
     a = dict(q=P[0], qs=s, k=P[1], ks=s, v=P[2], vs=s, g=P[3], gs=None, s0=P[4], n=P[5], do=P[6], dos=s, dsT=P[7],
-             dq=P[8], dk_=P[9], dv_=P[10], dg=P[11], ds0=P[12], nb=2, L=300, H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1,
+             dq=P[8], dk_=P[9], dv_=P[10], dg=P[11], ds0=P[12], nb=2, L=6000, H=4, Hk=2, dk=32, dv=32, scale=1.0, dt=1,
              ws=P[13], wsb=0)
     a.update(kw)
     return lib.vmscan_linattn_bwd(*a.values(), None)

@@ -134,10 +134,11 @@ def test_heads(H, Hk, decay, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [193, 700])
 def test_segments(T, dtype):
-    """Few (sequence, head) pairs: the sequence is split into segments whose states are joined."""
+    """Few (sequence, head) pairs: a long sequence is split into segments whose states are joined."""
     import selective_state_space_41_amd as V
     p = make(T, 1, T, 2, 1, 64, 64, dtype)
-    assert V.load().vmscan_linattn_fwd_workspace_bytes(1, T, 2, 64, 64, int(dtype == "bf16")) > 0
+    if T == 700:
+        assert V.load().vmscan_linattn_fwd_workspace_bytes(1, T, 2, 64, 64, int(dtype == "bf16")) > 0
     run_both(f"segments T {T} {dtype}", p, lengths=[T - 3])
     run_both(f"segments T {T} {dtype} short", p, lengths=[T // 3], state=False)
 
@@ -399,7 +400,7 @@ def test_refusals():
     odd = torch.zeros(4, 2 * 16 + 2, device="cuda")[:, 2:].view(1, 4, 2, 16)  # rows off the 16-byte grid
     with pytest.raises(RuntimeError, match="ALIGN"):
         V.linattn_fwd(odd, odd, odd, torch.zeros(2, device="cuda"))
-    p = make(1, 1, 300, 1, 1, 16, 16, "bf16")
+    p = make(1, 1, 3000, 1, 1, 16, 16, "bf16")
     with pytest.raises(ValueError, match="workspace"):
         V.linattn_fwd(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "g"),
                       workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
