@@ -133,6 +133,29 @@ __device__ __forceinline__ Frag32 frag_col(const float* p) {
   return f;
 }
 
+// The same in frag_row's order, rows 8 g .. 8 g + 7.
+template <int S>
+__device__ __forceinline__ bf16x8 frag_col_row(const uint16_t* p) {
+  const int l = threadIdx.x & 63, i = l & 15;
+  const uint16_t* q = p + ((l >> 4) * 8 + (i >> 2)) * S + (i & 3) * 4;
+  union {
+    i16x4 h[2];
+    bf16x8 f;
+  } u;
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q));
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 4 * S));
+  return u.f;
+}
+template <int S>
+__device__ __forceinline__ Frag32 frag_col_row(const float* p) {
+  const int l = threadIdx.x & 63;
+  const float* q = p + (l >> 4) * 8 * S + (l & 15);
+  Frag32 f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) f.v[r] = q[r * S];
+  return f;
+}
+
 // The column operands of N neighbouring tiles, for several products: bfloat16 ones (4 registers each)
 // are read once and kept, float32 ones (8) are read at each use.
 template <typename T, int S, int N>
@@ -152,9 +175,14 @@ struct Cols {
 };
 
 // Two result tiles (rows 16 t + 4 g + r) as an operand in frag_col's order.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {  // two roundings to nearest, one instruction
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
 __device__ __forceinline__ void pack(const float (&x)[8], bf16x8& f) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = static_cast<__bf16>(x[e]);
+  const uint4 w = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+  f = __builtin_bit_cast(bf16x8, w);
 }
 __device__ __forceinline__ void pack(const float (&x)[8], Frag32& f) {
 #pragma unroll
@@ -262,9 +290,9 @@ struct LinArgs {
   void* dv_out;            // [batch, seqlen, heads, dv]
   float* dg;               // [batch, seqlen, heads]
   float *seg_s, *seg_ds;   // [batch * heads][segment][DK][ld]
-  float *seg_g;            // [batch * heads][segment]: the segment's log2 decay
-  float* states;           // [batch * heads][block][DK][DV]: the state entering each block
-  float* qa;               // [batch * heads][blocks * C]: e^{G_i} scale q_i . S do_i
+  float *seg_g, *seg_dg;   // [batch * heads][segment]: the segment's log2 decay, as each walk found it
+  float* states;           // [batch * heads][block][DK][DV]: a segment's own state before each block
+  float* block_g;          // [batch * heads][block]: the segment's log2 decay before each block
   int64_t batch;
   int seqlen, heads, share, dk, dvd;  // share: heads per query/key head
   int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
@@ -280,9 +308,11 @@ struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
   static constexpr int kPad = 16 / sizeof(T);  // LDS rows stay 16-byte aligned and rotate over the banks
 };
 
-// Waves per SIMD that a kernel's registers must leave room for, where LDS does too: narrow bfloat16 heads
-// only; the others need their registers.
-constexpr int waves_for(size_t elem, int dk, int dv, int narrow) { return elem == 2 && dk <= 64 && dv <= 64 ? narrow : 1; }
+// Waves per SIMD that a kernel's registers must leave room for, where LDS does too: bfloat16 heads; the others need
+// their registers.
+constexpr int waves_for(size_t elem, int dk, int dv, int narrow) {
+  return elem != 2 || dk + dv > 192 ? 1 : dk + dv > 128 ? (narrow > 2 ? 2 : 1) : narrow;
+}
 #define VMSCAN_WAVES(N) __attribute__((amdgpu_waves_per_eu(waves_for(sizeof(T), DK, DV, N))))
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -323,6 +353,38 @@ struct Tile {
       *reinterpret_cast<uint4*>(lds + row * kStride + col) = r[i];
     }
   }
+};
+
+// A wave's 16 rows of a block straight from global memory as row operands, for a tensor no other wave reads.
+template <typename T, int D>
+struct OwnRows {
+  Frag<T> f[D / 32];
+  __device__ __forceinline__ void load(const T* base, uint32_t st, int row0, int rows, int dim) {
+    const int l = threadIdx.x & 63, row = row0 + (l & 15), col = (l >> 4) * 8;
+    const T* p = base + static_cast<uint32_t>(row * st + col);
+#pragma unroll
+    for (int kk = 0; kk < D / 32; ++kk) {
+      uint4 w[sizeof(T) / 2];
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (row < rows && col + kk * 32 < dim) w[i] = *reinterpret_cast<const uint4*>(p + kk * 32 + i * 4);
+      }
+      __builtin_memcpy(&f[kk], w, sizeof(w));
+    }
+  }
+};
+
+// A tensor of one (sequence, head), block by block.
+template <typename T, int D>
+struct Stream {
+  const T* p;  // the block's first token
+  int st;      // token stride
+  Tile<T, D> tile;
+  __device__ __forceinline__ Stream(const View& v, int64_t b, int h, int n0)
+      : p(static_cast<const T*>(v.p) + b * v.b + h * v.h + n0), st(static_cast<int>(v.t)) {}
+  __device__ __forceinline__ void skip(int blocks) { p += static_cast<int64_t>(blocks) * (Block<T>::kC * st); }
+  __device__ __forceinline__ void load(int rows, int dim) { tile.load(p, st, rows, dim); }
 };
 
 // A block's decays.  With G the running log2 decay, E(t) the last token of t's 16 and F(t) the last one
@@ -384,9 +446,7 @@ __device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 // Results in the accumulators' layout (4 consecutive channels of one token per lane) to memory.
 __device__ __forceinline__ void store_acc(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store_acc(uint16_t* p, f32x4 v) {
-  const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
-  const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
-  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -426,12 +486,27 @@ struct State {
       for (int nt = 0; nt < kNT; ++nt)
         if (d_of(t) < dk && n_of(nt) < dv) store_acc(p + (d_of(t) * ld + n_of(nt)), s[t][nt]);
   }
-  // into LDS as an operand, [d][n], rounded
+  // into LDS as an operand, [d][n]; bfloat16 with what the rounding left in a second plane
+  static constexpr int kPlane = DK * kStride;
+  static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
   __device__ __forceinline__ void publish(T* p) const {
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) store_acc(p + d_of(t) * kStride + n_of(nt), s[t][nt]);
+      for (int nt = 0; nt < kNT; ++nt) {
+        T* at = p + d_of(t) * kStride + n_of(nt);
+        store_acc(at, s[t][nt]);
+        if constexpr (kPlanes == 2) {
+          f32x4 rest;
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const uint32_t h = pack2(s[t][nt][r], s[t][nt][r + 1]);
+            rest[r] = s[t][nt][r] - __uint_as_float(h << 16);
+            rest[r + 1] = s[t][nt][r + 1] - __uint_as_float(h & 0xffff0000u);
+          }
+          store_acc(at + kPlane, rest);
+        }
+      }
   }
   __device__ __forceinline__ void decay(float e) {
 #pragma unroll
@@ -566,9 +641,9 @@ __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p
 
 // ---------------------------------------------------------------------------------------------
 // A segment's own state from a zero start: forward (k, v) or, BACK, the state's gradient (q, dout)
-// from a zero end.
+// from a zero end.  KEEP also writes the state before each block.
 
-template <typename T, int DK, int DV, bool BACK>
+template <typename T, int DK, int DV, bool BACK, bool KEEP>
 __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
@@ -577,9 +652,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
   __shared__ __align__(16) T xs[C * SX];
   __shared__ __align__(16) Decays<C> decays[2];
   const Where w = where<T>(a, DV);
-  const T* y = head<T>(BACK ? a.q : a.k, w.b, w.h / a.share);
-  const T* x = head<T>(BACK ? a.dout : a.v, w.b, w.h) + w.n0;
-  const int64_t yt = BACK ? a.q.t : a.k.t, xt = BACK ? a.dout.t : a.v.t;
+  if (!KEEP && w.seg == (BACK ? 0 : a.segments - 1)) return;  // nothing comes after (before) it
+  Stream<T, DK> y(BACK ? a.q : a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV> x(BACK ? a.dout : a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int wave = wave_id();
@@ -587,26 +662,31 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
   st.load(nullptr, 0, 0, 0);
   float total = 0.0f;
   const int n = w.c1 - w.c0;
-  Tile<T, DK> ty;
-  Tile<T, DV> tx;
   float gx = 0.0f;
   auto at = [&](int i) { return (BACK ? w.c1 - 1 - i : w.c0 + i) * C; };
-  auto load = [&](int t0) {
-    ty.load(y + t0 * yt, yt, w.live - t0, a.dk);
-    tx.load(x + t0 * xt, xt, w.live - t0, dv);
-  };
   if (n > 0) {
-    load(at(0));
+    y.skip(BACK ? w.c1 - 1 : w.c0);
+    x.skip(BACK ? w.c1 - 1 : w.c0);
+    y.load(w.live - at(0), a.dk);
+    x.load(w.live - at(0), dv);
     if (wave == 0) scan_g(load_g<C>(a, g, at(0), w.live), decays[0]);
     if (n > 1) gx = load_g<C>(a, g, at(1), w.live);
   }
   for (int i = 0; i < n; ++i) {
     const Decays<C>& d = decays[i & 1];
-    ty.store(ys);
-    tx.store(xs);
+    y.tile.store(ys);
+    x.tile.store(xs);
+    if constexpr (KEEP) {
+      const int64_t block = w.bh * a.blocks + (w.c0 + i);
+      st.store(a.states + block * (DK * DV), DK, DV, DV);
+      if (threadIdx.x == 0) a.block_g[block] = total;
+    }
     __syncthreads();
     if (i + 1 < n) {
-      load(at(i + 1));
+      y.skip(BACK ? -1 : 1);
+      x.skip(BACK ? -1 : 1);
+      y.load(w.live - at(i + 1), a.dk);
+      x.load(w.live - at(i + 1), dv);
       if (wave == i % B::kWaves) scan_g(gx, decays[(i + 1) & 1]);
       if (i + 2 < n) gx = load_g<C>(a, g, at(i + 2), w.live);
     }
@@ -625,8 +705,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
     }
     __syncthreads();
   }
+  if (a.segments == 1) return;
   st.store((BACK ? a.seg_ds : a.seg_s) + (w.bh * a.segments + w.seg) * (DK * a.ld) + w.n0, DK, DV, a.ld);
-  if (!BACK && w.n0 == 0 && threadIdx.x == 0) a.seg_g[w.bh * a.segments + w.seg] = total;
+  if (w.n0 == 0 && threadIdx.x == 0) (BACK ? a.seg_dg : a.seg_g)[w.bh * a.segments + w.seg] = total;
 }
 
 // In place: each segment's own state becomes the state that enters it (BACK: the gradient at its
@@ -643,7 +724,7 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
   if (first && d < a.dk && n < a.dvd) run = load4(first + (bh * a.dk + d) * a.dvd + n);
   const int64_t step = static_cast<int64_t>(DK) * a.ld;
   float* p = (BACK ? a.seg_ds : a.seg_s) + bh * a.segments * step + e;
-  const float* g = a.seg_g + bh * a.segments;
+  const float* g = (BACK ? a.seg_dg : a.seg_g) + bh * a.segments;
   constexpr int kAhead = 8;
   for (int i0 = 0; i0 < a.segments; i0 += kAhead) {
     f32x4 own[kAhead];
@@ -652,8 +733,12 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
     for (int i = 0; i < kAhead; ++i)
       if (i0 + i < a.segments) {
         const int s = BACK ? a.segments - 1 - i0 - i : i0 + i;
-        own[i] = load4(p + s * step);
-        m[i] = __builtin_amdgcn_exp2f(g[s]);
+        own[i] = zero4();
+        m[i] = 0.0f;
+        if (i0 + i + 1 < a.segments) {  // what the last one adds enters nothing
+          own[i] = load4(p + s * step);
+          m[i] = __builtin_amdgcn_exp2f(g[s]);
+        }
       }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
@@ -673,20 +758,21 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
   using B = Block<T>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride, NT = DV / 16;
-  __shared__ __align__(16) T qs[C * SK];
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
-  __shared__ __align__(16) T ss[DK * SS];
+  __shared__ __align__(16) T ss[S::kPlanes * S::kPlane];
   __shared__ __align__(16) Decays<C> decays[2];
   const Where w = where<T>(a, DV);
-  const T* q = head<T>(a.q, w.b, w.h / a.share);
-  const T* k = head<T>(a.k, w.b, w.h / a.share);
-  const T* v = head<T>(a.v, w.b, w.h) + w.n0;
+  Stream<T, DK> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV> v(a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd + w.n0;
   const int64_t ot = static_cast<int64_t>(a.heads) * a.dvd;
   const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+  // The last 16 queries of a block have four times the first ones' scores.  Workgroups that share a CU give
+  // them to different waves, so that no SIMD gets all of them.
+  const int qt = (blockIdx.x >> 8) & 1 ? B::kWaves - 1 - wave : wave;
 
   S st;
   if (a.segments > 1)
@@ -694,15 +780,17 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
   else
     st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd + w.n0 : nullptr, a.dk, dv, a.dvd);
 
-  Tile<T, DK> tq, tk;
-  Tile<T, DV> tv;
+  OwnRows<T, DK> qn;  // the next block's queries
   auto load = [&](int t0) {
-    tq.load(q + t0 * a.q.t, a.q.t, w.live - t0, a.dk);
-    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
-    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, dv);
+    qn.load(q.p, q.st, qt * 16, w.live - t0, a.dk);
+    k.load(w.live - t0, a.dk);
+    v.load(w.live - t0, dv);
   };
   float gx = 0.0f;
   if (w.c0 < w.c1) {
+    q.skip(w.c0);
+    k.skip(w.c0);
+    v.skip(w.c0);
     load(w.c0 * C);
     if (wave == 0) scan_g(load_g<C>(a, g, w.c0 * C, w.live), decays[w.c0 & 1]);
     gx = load_g<C>(a, g, w.c0 * C + C, w.live);
@@ -710,33 +798,36 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
   for (int c = w.c0; c < w.c1; ++c) {
     const int t0 = c * C;
     const Decays<C>& d = decays[c & 1];
-    tq.store(qs);
-    tk.store(ks);
-    tv.store(vs);
+    const OwnRows<T, DK> qf = qn;
+    k.tile.store(ks);
+    v.tile.store(vs);
     st.publish(ss);
     __syncthreads();
     if (c + 1 < w.c1) {
+      q.skip(1);
+      k.skip(1);
+      v.skip(1);
       load(t0 + C);
       // the next block's decays, by one wave; the others' products run meanwhile
       if (wave == c % B::kWaves) scan_g(gx, decays[(c + 1) & 1]);
       gx = load_g<C>(a, g, t0 + 2 * C, w.live);
     }
     // this wave's 16 queries: column i of every result tile
-    const int i0 = wave * 16, i = i0 + li;
+    const int i0 = qt * 16, i = i0 + li;
     const bool own = t0 + i0 < w.live;
     const float gh = d.hi[i], gl = d.lo[i];
     f32x4 acc[NT];
-    Frag<T> qf[DK / 32];
     if (own) {
       // e^{G_i} S^T q_i
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[nt] = zero4();
 #pragma unroll
       for (int kk = 0; kk < DK / 32; ++kk) {
-        const Frag<T> qp = frag_row_perm<SK>(qs + i0 * SK + kk * 32);
-        qf[kk] = frag_row<SK>(qs + i0 * SK + kk * 32);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), qp, acc[nt]);
+        for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            acc[nt] = mma(frag_col_row<SS>(ss + pl * S::kPlane + kk * 32 * SS + nt * 16), qf.f[kk], acc[nt]);
       }
       const float e = d.from0[i];
 #pragma unroll
@@ -747,7 +838,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
     for (int kk = 0; kk < C / 32; ++kk) {
       if (t0 + kk * 32 >= w.live) break;
       const Cols<T, SV, NT> xa(vs + kk * 32 * SV);
-      if (own && kk <= wave / 2) {
+      if (own && kk <= qt / 2) {
         // the masked scores of 32 keys, then their product with the values
         float p[8];
 #pragma unroll
@@ -756,7 +847,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
           if (j0 <= i0) {
             f32x4 sc = zero4();
 #pragma unroll
-            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(ks + j0 * SK + n * 32), qf[n], sc);
+            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(ks + j0 * SK + n * 32), qf.f[n], sc);
             if (j0 < i0) {  // through the last of the 16 keys: both factors are powers of the decays between
               const f32x4 e = load4(d.toE + j0 + g4);
               const float from = d.between(gh, gl, j0 + 15);
@@ -798,8 +889,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
 //
 // With R the gradient of the state leaving a block (it includes every later token) and X_ij =
 // scale e^{G_i - G_j} (do_i . v_j), P_ij = scale e^{G_i - G_j} (q_i . k_j) for j <= i:
-//   dq_i = e^{G_i} scale S do_i + sum_j X_ij k_j          (walk forwards, carrying S)
-//   dk_j = e^{G_C - G_j} R v_j  + sum_i X_ij q_i          (walk backwards, carrying R)
+//   dq_i = e^{G_i} scale S do_i + sum_j X_ij k_j
+//   dk_j = e^{G_C - G_j} R v_j  + sum_i X_ij q_i
 //   dv_j = e^{G_C - G_j} R^T k_j + sum_i P_ij do_i
 //   R'   = e^{G_C} R + sum_i e^{G_i} scale q_i do_i^T.
 // The decay of token t multiplies every contribution from a token before t to one at or after it,
@@ -811,73 +902,103 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
 // Summing q . dq - k . dk over all later tokens would give the same with two dot products, but as a
 // small difference of sums over the whole sequence; here only terms that belong are added.
 
+//
+// A first walk forwards (the segment kernel) leaves each block's entering state, counted from its segment's
+// start; this kernel walks backwards and does the rest, reading q, k, v and dout once.
+
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_dq_kernel(LinArgs a) {
+__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_grad_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride, DT = DK / 16;
+  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  constexpr int DT = DK / 16, NT = DV / 16;
+  // S and R as operands: side by side where LDS has room for both, else one after the other
+  constexpr int kStateLds = S::kPlanes * S::kPlane;
+  constexpr bool kBoth = (2 * C * (SK + SV) + 2 * kStateLds) * sizeof(T) + 8192 <= 160 * 1024;
+  __shared__ __align__(16) T qs[C * SK];
   __shared__ __align__(16) T ks[C * SK];
   __shared__ __align__(16) T vs[C * SV];
   __shared__ __align__(16) T os[C * SV];
-  __shared__ __align__(16) T ss[DK * SS];
+  __shared__ __align__(16) T ss[(kBoth ? 2 : 1) * kStateLds];
   __shared__ __align__(16) Decays<C> decays[2];
-  __shared__ float part[B::kWaves][C];
+  __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
+  T* const rs = kBoth ? ss + kStateLds : ss;
   const Where w = where<T>(a, DV);
-  const T* q = head<T>(a.q, w.b, w.h / a.share);
-  const T* k = head<T>(a.k, w.b, w.h / a.share);
-  const T* v = head<T>(a.v, w.b, w.h);
-  const T* o = head<T>(a.dout, w.b, w.h);
+  Stream<T, DK> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV> v(a.v, w.b, w.h, 0), o(a.dout, w.b, w.h, 0);
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
-  const int64_t ot = static_cast<int64_t>(a.heads) * a.dk, obase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
+  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
   const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
 
-  S st;
-  if (a.segments > 1)
-    st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
-  else
-    st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-
-  Tile<T, DK> tk;
-  Tile<T, DV> tv, to;
-  auto load = [&](int t0) {
-    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
-    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, a.dvd);
-    to.load(o + t0 * a.dout.t, a.dout.t, w.live - t0, a.dvd);
-  };
-  float gx = 0.0f;
-  if (w.c0 < w.c1) {
-    load(w.c0 * C);
-    if (wave == 0) scan_g(load_g<C>(a, g, w.c0 * C, w.live), decays[w.c0 & 1]);
-    gx = load_g<C>(a, g, w.c0 * C + C, w.live);
+  S st, first;  // R; the state that enters the segment
+  if (a.segments > 1) {
+    const int64_t at = (w.bh * a.segments + w.seg) * (DK * DV);
+    st.load(a.seg_ds + at, DK, DV, DV);
+    first.load(a.seg_s + at, DK, DV, DV);
+  } else {
+    st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+    first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
   }
-  for (int c = w.c0; c < w.c1; ++c) {
+  float gx = 0.0f;
+  auto skip = [&](int blocks) {
+    q.skip(blocks);
+    k.skip(blocks);
+    v.skip(blocks);
+    o.skip(blocks);
+  };
+  auto load = [&](int t0) {
+    q.load(w.live - t0, a.dk);
+    k.load(w.live - t0, a.dk);
+    v.load(w.live - t0, a.dvd);
+    o.load(w.live - t0, a.dvd);
+  };
+  if (w.c0 < w.c1) {
+    skip(w.c1 - 1);
+    load((w.c1 - 1) * C);
+    if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), decays[(w.c1 - 1) & 1]);
+    if (w.c1 - 1 > w.c0) gx = load_g<C>(a, g, (w.c1 - 2) * C, w.live);
+  }
+  for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
     const Decays<C>& d = decays[c & 1];
-    tk.store(ks);
-    tv.store(vs);
-    to.store(os);
-    st.publish(ss);
-    st.store(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
-    __syncthreads();
-    // channels 16 d_tile + 4 g .. of the queries 16 jt + li, for a_i
-    f32x4 q4[S::kDT][B::kWaves];
-    const T* qt = q + t0 * a.q.t;
+    const int64_t block = w.bh * a.blocks + c;
+    S old;  // the state that enters the block
+    old.load(a.states + block * (DK * DV), DK, DV, DV);
+    const float since = __builtin_amdgcn_exp2f(a.block_g[block]);
+    q.tile.store(qs);
+    k.tile.store(ks);
+    v.tile.store(vs);
+    o.tile.store(os);
+    {
+      float y = 0.0f;  // <S, R>, both in this wave's layout
 #pragma unroll
-    for (int t = 0; t < S::kDT; ++t)
+      for (int t = 0; t < S::kDT; ++t)
 #pragma unroll
-      for (int jt = 0; jt < B::kWaves; ++jt) {
-        const int dd = (wave * S::kDT + t) * 16 + g4, n = jt * 16 + li;
-        q4[t][jt] = zero4();
-        if (t0 + n < w.live && dd < a.dk)
-          q4[t][jt] = load4(qt + static_cast<uint32_t>(n * static_cast<uint32_t>(a.q.t) + dd));
-      }
-    if (c + 1 < w.c1) {
-      load(t0 + C);
-      if (wave == c % B::kWaves) scan_g(gx, decays[(c + 1) & 1]);
-      gx = load_g<C>(a, g, t0 + 2 * C, w.live);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            old.s[t][nt][r] = __builtin_fmaf(first.s[t][nt][r], since, old.s[t][nt][r]);
+            y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
+          }
+      y = sum_rows(row_sum(y));
+      if (l == 0) across[wave] = y;
     }
-    const int i0 = wave * 16, i = i0 + li;
-    if (t0 + i0 < w.live) {
+    old.publish(ss);
+    if constexpr (kBoth) st.publish(rs);
+    __syncthreads();
+    if (c > w.c0) {
+      skip(-1);
+      load(t0 - C);
+      if (wave == c % B::kWaves) scan_g(gx, decays[(c - 1) & 1]);
+      if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
+    }
+    const int d0 = wave * S::kDT * 16 + g4;
+    old.bilinear(os, [&](int t, int jt) { return load4(qs + (jt * 16 + li) * SK + d0 + t * 16); }, into[wave]);
+    // dq of this wave's 16 queries: column i of every result tile
+    if (t0 + wave * 16 < w.live) {
+      const int i0 = wave * 16, i = i0 + li;
       const float gh = d.hi[i], gl = d.lo[i];
       Frag<T> of[DV / 32];
 #pragma unroll
@@ -888,10 +1009,15 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_dq
       for (int dt = 0; dt < DT; ++dt) {
         acc[dt] = zero4();
 #pragma unroll
-        for (int kk = 0; kk < DV / 32; ++kk) acc[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+        for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+          for (int kk = 0; kk < DV / 32; ++kk)
+            acc[dt] = mma(frag_row<SS>(ss + pl * S::kPlane + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
         acc[dt] *= e0;
       }
-      for (int jj = 0; jj <= wave / 2; ++jj) {
+#pragma unroll
+      for (int jj = 0; jj < C / 32; ++jj) {
+        if (jj > wave / 2) break;
         float p[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -924,105 +1050,23 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_dq
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
           if (dt * 16 + g4 < a.dk) {
-            const uint32_t at = static_cast<uint32_t>(i * ot + dt * 16 + g4);
+            const uint32_t at = static_cast<uint32_t>(i * kt + dt * 16 + g4);
             if (a.share == 1)
-              store_acc(static_cast<T*>(a.dq) + (obase + t0 * ot) + at, acc[dt]);
+              store_acc(static_cast<T*>(a.dq) + (kbase + t0 * kt) + at, acc[dt]);
             else
-              store_acc(static_cast<float*>(a.dq) + (obase + t0 * ot) + at, acc[dt]);
+              store_acc(static_cast<float*>(a.dq) + (kbase + t0 * kt) + at, acc[dt]);
           }
       }
     }
-    st.bilinear(os, [&](int t, int jt) { return q4[t][jt]; }, part[wave]);
-    st.decay(d.from0[C - 1]);
-#pragma unroll
-    for (int kk = 0; kk < C / 32; ++kk) {
-      if (t0 + kk * 32 >= w.live) break;
-      const Cols<T, SV, S::kNT> xa(vs + kk * 32 * SV);
-      float m[8];
-      eight(d.toC + kk * 32, m);
-      st.add(ks + kk * 32 * SK, xa, m);
+    if constexpr (!kBoth) {
+      __syncthreads();
+      st.publish(rs);
+      __syncthreads();
     }
-    __syncthreads();
-    if (wave == c % B::kWaves && l < C) {  // part is written again only past the next barrier
-      float sum = 0.0f;
-#pragma unroll
-      for (int n = 0; n < B::kWaves; ++n) sum += part[n][l];
-      a.qa[w.bh * a.blocks * C + t0 + l] = sum * a.scale * d.from0[l];
-    }
-  }
-  if (a.share == 1)
-    zero_rest<T>(a, w, static_cast<T*>(a.dq) + obase, ot, a.dk);
-  else
-    zero_rest<T>(a, w, static_cast<float*>(a.dq) + obase, ot, a.dk);
-}
-
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dkv_kernel(LinArgs a) {
-  using B = Block<T>;
-  using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
-  constexpr int DT = DK / 16, NT = DV / 16;
-  __shared__ __align__(16) T qs[C * SK];
-  __shared__ __align__(16) T ks[C * SK];
-  __shared__ __align__(16) T vs[C * SV];
-  __shared__ __align__(16) T os[C * SV];
-  __shared__ __align__(16) T ss[DK * SS];
-  __shared__ __align__(16) Decays<C> decays[2];
-  __shared__ float rows[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
-  const Where w = where<T>(a, DV);
-  const T* q = head<T>(a.q, w.b, w.h / a.share);
-  const T* k = head<T>(a.k, w.b, w.h / a.share);
-  const T* v = head<T>(a.v, w.b, w.h);
-  const T* o = head<T>(a.dout, w.b, w.h);
-  const float* g = a.g + w.b * a.gb + w.h * a.gh;
-  const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
-  const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
-  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
-  const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
-
-  S st;
-  if (a.segments > 1)
-    st.load(a.seg_ds + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
-  else
-    st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-
-  Tile<T, DK> tq, tk;
-  Tile<T, DV> tv, to;
-  float gx = 0.0f;
-  auto load = [&](int t0) {
-    tq.load(q + t0 * a.q.t, a.q.t, w.live - t0, a.dk);
-    tk.load(k + t0 * a.k.t, a.k.t, w.live - t0, a.dk);
-    tv.load(v + t0 * a.v.t, a.v.t, w.live - t0, a.dvd);
-    to.load(o + t0 * a.dout.t, a.dout.t, w.live - t0, a.dvd);
-  };
-  if (w.c0 < w.c1) {
-    load((w.c1 - 1) * C);
-    if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), decays[(w.c1 - 1) & 1]);
-    if (w.c1 - 1 > w.c0) gx = load_g<C>(a, g, (w.c1 - 2) * C, w.live);
-  }
-  for (int c = w.c1 - 1; c >= w.c0; --c) {
-    const int t0 = c * C;
-    const Decays<C>& d = decays[c & 1];
-    // the state that entered the block and the a_i, from the walk forwards
-    S old;
-    old.load(a.states + (w.bh * a.blocks + c) * (DK * DV), DK, DV, DV);
-    const float qa = l < C ? a.qa[w.bh * a.blocks * C + t0 + l] : 0.0f;
-    tq.store(qs);
-    tk.store(ks);
-    tv.store(vs);
-    to.store(os);
-    st.publish(ss);
-    __syncthreads();
-    if (c > w.c0) {
-      load(t0 - C);
-      if (wave == c % B::kWaves) scan_g(gx, decays[(c - 1) & 1]);
-      if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
-    }
-    st.bilinear(vs, [&](int t, int jt) { return load4(ks + (jt * 16 + li) * SK + (wave * S::kDT + t) * 16 + g4); },
-                after[wave]);
-    // this wave's 16 keys: column j of every result tile
+    st.bilinear(vs, [&](int t, int jt) { return load4(ks + (jt * 16 + li) * SK + d0 + t * 16); }, after[wave]);
+    // dk and dv of this wave's 16 keys: column j of every result tile
     const int j0 = wave * 16, j = j0 + li;
-    const float gh = d.hi[j], gl = d.lo[j], toC = d.toC[j], toE = d.toE[j] * a.scale;
+    const float gh = d.hi[j], gl = d.lo[j], toC = d.toC[j];
     Frag<T> kf[DK / 32], vf[DV / 32];
 #pragma unroll
     for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<SK>(ks + j0 * SK + kk * 32);
@@ -1033,37 +1077,34 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dk
     for (int dt = 0; dt < DT; ++dt) {
       ak[dt] = zero4();
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) ak[dt] = mma(frag_row<SS>(ss + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
+      for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+        for (int kk = 0; kk < DV / 32; ++kk)
+          ak[dt] = mma(frag_row<SS>(rs + pl * S::kPlane + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
       ak[dt] *= toC;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) av[nt] = zero4();
 #pragma unroll
     for (int kk = 0; kk < DK / 32; ++kk) {
-      const Frag<T> kp = frag_row_perm<SK>(ks + j0 * SK + kk * 32);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) av[nt] = mma(frag_col<SS>(ss + kk * 32 * SS + nt * 16), kp, av[nt]);
+      for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          av[nt] = mma(frag_col_row<SS>(rs + pl * S::kPlane + kk * 32 * SS + nt * 16), kf[kk], av[nt]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) av[nt] *= toC;
-    {
-      // Y: the state before the block against R, both in this wave's layout
-      float y = 0.0f;
-#pragma unroll
-      for (int t = 0; t < S::kDT; ++t)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
-      y = sum_rows(row_sum(y));
-      if (l == 0) across[wave] = y * d.from0[C - 1];
-    }
     st.decay(d.from0[C - 1]);
     // Queries from the last 32 down.  Beside the products, M_ij summed over the queries from t on (in
     // this lane's column; `later`: the tiles done) and then over the keys before t.
     float later = 0.0f;
 #pragma unroll
     for (int kk = C / 32 - 1; kk >= 0; --kk) {
+      if (t0 + kk * 32 >= w.live) {  // no tokens; the table of rows has to be whole
+        if (kk >= wave / 2 && l < 32 && kk * 32 + l >= j0) rows[wave][kk * 32 + l] = 0.0f;
+        continue;
+      }
       const Cols<T, SV, NT> xa(os + kk * 32 * SV);
       if (kk >= wave / 2) {
         float p[8], x[8];
@@ -1079,10 +1120,10 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dk
             float u[4];
             if (i0 > j0) {  // through the last token before the 16 queries
               const f32x4 e = load4(d.fromF + i0 + g4);
-              const float to_ = __builtin_amdgcn_exp2f((d.hi[i0 - 1] - gh) + (d.lo[i0 - 1] - gl)) * a.scale;
+              const float to = __builtin_amdgcn_exp2f((d.hi[i0 - 1] - gh) + (d.lo[i0 - 1] - gl)) * a.scale;
 #pragma unroll
               for (int r = 3; r >= 0; --r) {
-                const float f = e[r] * to_;
+                const float f = e[r] * to;
                 p[t * 4 + r] = sc[r] * f;
                 x[t * 4 + r] = dp[r] * f;
                 u[r] = sc[r] * x[t * 4 + r] + (r < 3 ? u[r + 1] : 0.0f);
@@ -1147,14 +1188,18 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dk
       const bool mine = l < C && t0 + l < w.live;
       float from = 0.0f, before = 0.0f, y = 0.0f;
       if (mine) {
-        from = qa;
 #pragma unroll
-        for (int i = 0; i < B::kWaves; ++i) before += after[i][l];
+        for (int i = 0; i < B::kWaves; ++i) {
+          from += into[i][l];
+          before += after[i][l];
+        }
+        from *= a.scale * d.from0[l];
         before *= d.toC[l];
+#pragma unroll
+        for (int i = 0; i < B::kWaves; ++i) y += across[i];
+        y *= d.from0[C - 1];
         for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
       }
-#pragma unroll
-      for (int i = 0; i < B::kWaves; ++i) y += across[i];
       float r[4];
       rows_of(row_sum(from), r);
       from = row_suffix(from) + sum_after(r, l >> 4);
@@ -1163,10 +1208,13 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_dk
       if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + before + y;
     }
   }
-  if (a.share == 1)
+  if (a.share == 1) {
+    zero_rest<T>(a, w, static_cast<T*>(a.dq) + kbase, kt, a.dk);
     zero_rest<T>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
-  else
+  } else {
+    zero_rest<T>(a, w, static_cast<float*>(a.dq) + kbase, kt, a.dk);
     zero_rest<T>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
+  }
   zero_rest<T>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
   const int t_end = w.end * C < a.seqlen ? w.end * C : a.seqlen;
   for (int64_t t = (w.live > w.c0 * C ? w.live : w.c0 * C) + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads)
@@ -1310,7 +1358,13 @@ struct Plan {
 // Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
 int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
   const int wide = (pad_dim(dk) == 128) + (width == 128);
-  const int per_cu = dtype == VMSCAN_F32 ? (wide == 0 ? 4 : 2) : (wide == 0 ? 3 : wide == 1 && !back ? 2 : 1);
+  int per_cu;
+  if (back)
+    per_cu = wide == 0 ? 2 : 1;
+  else if (dtype == VMSCAN_F32)
+    per_cu = wide == 0 ? 4 : 2;
+  else
+    per_cu = wide == 0 ? 3 : wide == 1 ? 2 : 1;
   return 256 * per_cu;
 }
 // How a call is cut up.  The forward's value channels are independent, so several workgroups can share them (each
@@ -1353,7 +1407,7 @@ bool options_ok(int heads, int kheads, int dk, int dv, vmscan_dtype dtype) {
 
 struct Layout {
   Plan p;
-  size_t seg_s, seg_ds, seg_g, states, qa, dq, dk, dg, parts, total;
+  size_t seg_s, seg_ds, seg_g, seg_dg, states, block_g, dq, dk, dg, parts, total;
 };
 Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int dv, bool per_head, vmscan_dtype dtype,
               bool back) {
@@ -1361,7 +1415,6 @@ Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int 
   y.p = plan(batch, seqlen, heads, dk, dv, dtype, back);
   const size_t bh = static_cast<size_t>(batch) * heads;
   const size_t state = static_cast<size_t>(pad_dim(dk)) * y.p.slices * y.p.width * 4;
-  const size_t C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t was = at;
@@ -1370,12 +1423,15 @@ Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int 
   };
   if (y.p.segments > 1) {
     y.seg_s = take(bh * y.p.segments * state);
-    if (back) y.seg_ds = take(bh * y.p.segments * state);
     y.seg_g = take(bh * y.p.segments * 4);
+    if (back) {
+      y.seg_ds = take(bh * y.p.segments * state);
+      y.seg_dg = take(bh * y.p.segments * 4);
+    }
   }
   if (back) {
     y.states = take(bh * y.p.blocks * state);
-    y.qa = take(bh * y.p.blocks * C * 4);
+    y.block_g = take(bh * y.p.blocks * 4);
     if (kheads != heads) {
       y.dq = take(bh * seqlen * dk * 4);
       y.dk = take(bh * seqlen * dk * 4);
@@ -1414,20 +1470,22 @@ void with_dims(int dk, int width, F&& f) {
 
 dim3 walks(const LinArgs& a) { return dim3(static_cast<unsigned>(a.batch * a.heads * a.segments * a.slices)); }
 
-template <typename T, bool BACK>
+template <typename T, bool BACK, bool KEEP>
 void launch_segments(const LinArgs& a, int width, hipStream_t stream) {
   with_dims(a.dk, width, [&](auto dk, auto dv) {
     constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK, KEEP>), walks(a), dim3(Block<T>::kThreads), 0, stream,
+                       a);
     const int64_t n = a.batch * a.heads * (DK * a.ld / 4);
-    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK>), walks(a), dim3(Block<T>::kThreads), 0, stream, a);
-    hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
-                       stream, a, DK);
+    if (a.segments > 1)
+      hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
+                         stream, a, DK);
   });
 }
 
 template <typename T>
 vmscan_status run_fwd(const LinArgs& a, int width, hipStream_t stream) {
-  if (a.segments > 1) launch_segments<T, false>(a, width, stream);
+  if (a.segments > 1) launch_segments<T, false, false>(a, width, stream);
   with_dims(a.dk, width, [&](auto dk, auto dv) {
     hipLaunchKernelGGL((linattn_fwd_kernel<T, decltype(dk)::value, decltype(dv)::value>), walks(a),
                        dim3(Block<T>::kThreads), 0, stream, a);
@@ -1442,16 +1500,13 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   a.dq = shared ? ws + y.dq : dq;
   a.dk_out = shared ? ws + y.dk : dk;
   a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
-  if (a.segments > 1) {
-    launch_segments<T, false>(a, y.p.width, stream);
-    launch_segments<T, true>(a, y.p.width, stream);
-  }
+  launch_segments<T, false, true>(a, y.p.width, stream);
+  if (a.segments > 1) launch_segments<T, true, false>(a, y.p.width, stream);
   const dim3 grid = walks(a), block(Block<T>::kThreads);
   with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
     if constexpr (DV >= 64) {
-      hipLaunchKernelGGL((linattn_dq_kernel<T, DK, DV>), grid, block, 0, stream, a);
-      hipLaunchKernelGGL((linattn_dkv_kernel<T, DK, DV>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), grid, block, 0, stream, a);
     }
   });
   const int64_t tokens = a.batch * a.seqlen;
@@ -1502,7 +1557,8 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
   a.seg_g = reinterpret_cast<float*>(ws + y.seg_g);
   a.states = reinterpret_cast<float*>(ws + y.states);
-  a.qa = reinterpret_cast<float*>(ws + y.qa);
+  a.block_g = reinterpret_cast<float*>(ws + y.block_g);
+  a.seg_dg = reinterpret_cast<float*>(ws + y.seg_dg);
 }
 
 vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
