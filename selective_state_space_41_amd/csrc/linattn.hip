@@ -70,107 +70,151 @@ __device__ __forceinline__ f32x4 mma(const Frag32& a, const Frag32& b, f32x4 c) 
   return c;
 }
 
-// Operand whose contracted index runs along the LDS row: lane (i, g) holds row i, elements
-// 8 g .. 8 g + 7 of the 32.  `p`: the tile's row 0 at the first of the 32.
-template <int S>
-__device__ __forceinline__ bf16x8 frag_row(const uint16_t* p) {
-  const int l = threadIdx.x & 63;
-  return *reinterpret_cast<const bf16x8*>(p + (l & 15) * S + (l >> 4) * 8);
+// LDS tiles are [rows][D] without padding; the 16-byte runs of a row lie in an order that depends on the
+// row, so that the products' accesses meet no bank twice (the padded tiles that this replaced lost 40 % of
+// their LDS cycles to conflicts).  256 bytes are served at a time, one word from each of 64 banks: 16 rows of
+// one run (row operands), and 8 rows of two neighbouring runs, rows 0 .. 7 or 0 .. 3 and 8 .. 11 (column
+// operands).  256 / row bytes rows (at least 1) lie side by side; row r's run c is at place c ^ m, m from the
+// bits k of r above those: all k differ in m, and the k of such 8 rows differ in m / 2.  (Float32 columns are
+// read word by word, rows r, 4 + r, 8 + r, 12 + r of four runs: there m = k.)
+template <typename T, int D>
+__device__ __forceinline__ int run_mask(int r) {
+  constexpr int kRuns = D * static_cast<int>(sizeof(T)) / 16;  // 4 .. 32
+  constexpr int kSide = kRuns < 16 ? 16 / kRuns : 1;
+  constexpr int kBits = kRuns == 4 ? 2 : kRuns == 8 ? 3 : 4;
+  constexpr int kTop = kBits - 1;
+  const int k = (r / kSide) & ((1 << kBits) - 1);
+  if constexpr (sizeof(T) == 4) return k;
+  else return (((k & ((1 << kTop) - 1)) ^ ((k >> kTop) << (kTop - 1))) << 1) | (k >> kTop);
 }
-template <int S>
-__device__ __forceinline__ Frag32 frag_row(const float* p) {
-  const int l = threadIdx.x & 63;
+template <typename T, int D>
+__device__ __forceinline__ int place(int r, int col) {  // in bytes, r < 32
+  constexpr int kPer = 16 / sizeof(T);
+  return r * D * static_cast<int>(sizeof(T)) + ((col / kPer) ^ run_mask<T, D>(r)) * 16 + col % kPer * static_cast<int>(sizeof(T));
+}
+// A lane's places in a tile of rows of D.  The mask is linear in the bits of the row (over exclusive or), and what
+// a product adds to the lane's row and column has other bits than those, so any place is one of these four with
+// constants taken in by one exclusive or and the instruction's offset.
+template <typename T, int D>
+struct Places {
+  int row;      // row i, elements 8 g ..
+  int perm;     // row i, elements 4 g ..
+  int col;      // row 4 g + .., the column operands' first rows
+  int col_row;  // row 8 g + ..
+  __device__ __forceinline__ Places() {
+    const int l = threadIdx.x & 63, i = l & 15, g = l >> 4;
+    row = place<T, D>(i, 8 * g);
+    perm = place<T, D>(i, 4 * g);
+    if constexpr (sizeof(T) == 2) {  // the transposing read: 4 rows of 16 lanes, 4 elements each
+      col = place<T, D>(4 * g + (i >> 2), (l & 3) * 4);
+      col_row = place<T, D>(8 * g + (i >> 2), (l & 3) * 4);
+    } else {
+      col = place<T, D>(4 * g, i);
+      col_row = place<T, D>(8 * g, i);
+    }
+  }
+  // Called at the top of a loop: the places with their constants are then made in the loop, where they are
+  // used, and do not take its registers (the constants' many combinations would).
+  __device__ __forceinline__ void here() { asm volatile("" : "+v"(row), "+v"(perm), "+v"(col), "+v"(col_row)); }
+};
+// base with `r` more rows and `col` more elements; the tile's rows start at row0, a multiple of 16.
+template <typename T, int D>
+__device__ __forceinline__ T* at(T* tile, int row0, int base, int r, int col) {
+  using E = typename std::remove_const<T>::type;
+  constexpr int kRow = D * static_cast<int>(sizeof(T));
+  const int off = (base ^ (run_mask<E, D>(r) * 16) ^ (col * static_cast<int>(sizeof(T)))) + r * kRow;
+  using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(tile + row0 * D) + off);
+}
+
+// Operand whose contracted index runs along the LDS row: lane (i, g) holds row row0 + i, elements
+// col + 8 g .. + 7 of the 32.
+template <int D>
+__device__ __forceinline__ bf16x8 frag_row(const Places<uint16_t, D>& w, const uint16_t* tile, int row0, int col) {
+  return *reinterpret_cast<const bf16x8*>(at<const uint16_t, D>(tile, row0, w.row, 0, col));
+}
+template <int D>
+__device__ __forceinline__ Frag32 frag_row(const Places<float, D>& w, const float* tile, int row0, int col) {
   Frag32 f;
-  __builtin_memcpy(f.v, __builtin_assume_aligned(p + (l & 15) * S + (l >> 4) * 8, 16), 32);
+  __builtin_memcpy(f.v, __builtin_assume_aligned(at<const float, D>(tile, row0, w.row, 0, col), 16), 16);
+  __builtin_memcpy(f.v + 4, __builtin_assume_aligned(at<const float, D>(tile, row0, w.row, 0, col + 4), 16), 16);
   return f;
 }
 
 // The same with the elements in the order of frag_col: 16 t + 4 g + r.
-template <int S>
-__device__ __forceinline__ bf16x8 frag_row_perm(const uint16_t* p) {
-  const int l = threadIdx.x & 63;
-  const uint16_t* q = p + (l & 15) * S + (l >> 4) * 4;
-  const uint2 a = *reinterpret_cast<const uint2*>(q), b = *reinterpret_cast<const uint2*>(q + 16);
-  const uint4 w = make_uint4(a.x, a.y, b.x, b.y);
-  return __builtin_bit_cast(bf16x8, w);
+template <int D>
+__device__ __forceinline__ bf16x8 frag_row_perm(const Places<uint16_t, D>& w, const uint16_t* tile, int row0, int col) {
+  const uint2 a = *reinterpret_cast<const uint2*>(at<const uint16_t, D>(tile, row0, w.perm, 0, col));
+  const uint2 b = *reinterpret_cast<const uint2*>(at<const uint16_t, D>(tile, row0, w.perm, 0, col + 16));
+  return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
 }
-template <int S>
-__device__ __forceinline__ Frag32 frag_row_perm(const float* p) {
-  const int l = threadIdx.x & 63;
-  const float* q = p + (l & 15) * S + (l >> 4) * 4;
+template <int D>
+__device__ __forceinline__ Frag32 frag_row_perm(const Places<float, D>& w, const float* tile, int row0, int col) {
   Frag32 f;
-  __builtin_memcpy(f.v, __builtin_assume_aligned(q, 16), 16);
-  __builtin_memcpy(f.v + 4, __builtin_assume_aligned(q + 16, 16), 16);
+  __builtin_memcpy(f.v, __builtin_assume_aligned(at<const float, D>(tile, row0, w.perm, 0, col), 16), 16);
+  __builtin_memcpy(f.v + 4, __builtin_assume_aligned(at<const float, D>(tile, row0, w.perm, 0, col + 16), 16), 16);
   return f;
 }
 
-// Operand whose contracted index runs down the LDS column: lane (i, g) holds column i, rows
-// 16 t + 4 g + r (t 0..1, r 0..3) of the 32.  `p`: row 0, first of the 16 columns.
-template <int S>
-__device__ __forceinline__ bf16x8 frag_col(const uint16_t* p) {
-  const int l = threadIdx.x & 63, i = l & 15;
-  const uint16_t* q = p + ((l >> 4) * 4 + (i >> 2)) * S + (i & 3) * 4;
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q));
-  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 16 * S));
+// Operand whose contracted index runs down the LDS column: lane (i, g) holds column col + i, rows
+// row0 + 16 t + 4 g + r (t 0..1, r 0..3) of the 32.
+__device__ __forceinline__ bf16x8 read_transposed(const uint16_t* a, const uint16_t* b) {
   union {
     i16x4 h[2];
     bf16x8 f;
   } u;
-  u.h[0] = a;
-  u.h[1] = b;
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(a));
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(b));
   return u.f;
 }
-template <int S>
-__device__ __forceinline__ Frag32 frag_col(const float* p) {
-  const int l = threadIdx.x & 63;
-  const float* q = p + (l >> 4) * 4 * S + (l & 15);
+template <int D>
+__device__ __forceinline__ bf16x8 frag_col(const Places<uint16_t, D>& w, const uint16_t* tile, int row0, int col) {
+  const uint16_t* p = at<const uint16_t, D>(tile, row0, w.col, 0, col);
+  return read_transposed(p, p + 16 * D);
+}
+template <int D>
+__device__ __forceinline__ Frag32 frag_col(const Places<float, D>& w, const float* tile, int row0, int col) {
   Frag32 f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    f.v[r] = q[r * S];
-    f.v[4 + r] = q[(16 + r) * S];
+    const float* p = at<const float, D>(tile, row0, w.col, r, col);
+    f.v[r] = p[0];
+    f.v[4 + r] = p[16 * D];
   }
   return f;
 }
 
 // The same in frag_row's order, rows 8 g .. 8 g + 7.
-template <int S>
-__device__ __forceinline__ bf16x8 frag_col_row(const uint16_t* p) {
-  const int l = threadIdx.x & 63, i = l & 15;
-  const uint16_t* q = p + ((l >> 4) * 8 + (i >> 2)) * S + (i & 3) * 4;
-  union {
-    i16x4 h[2];
-    bf16x8 f;
-  } u;
-  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q));
-  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(q + 4 * S));
-  return u.f;
+template <int D>
+__device__ __forceinline__ bf16x8 frag_col_row(const Places<uint16_t, D>& w, const uint16_t* tile, int row0, int col) {
+  return read_transposed(at<const uint16_t, D>(tile, row0, w.col_row, 0, col),
+                         at<const uint16_t, D>(tile, row0, w.col_row, 4, col));
 }
-template <int S>
-__device__ __forceinline__ Frag32 frag_col_row(const float* p) {
-  const int l = threadIdx.x & 63;
-  const float* q = p + (l >> 4) * 8 * S + (l & 15);
+template <int D>
+__device__ __forceinline__ Frag32 frag_col_row(const Places<float, D>& w, const float* tile, int row0, int col) {
   Frag32 f;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) f.v[r] = q[r * S];
+  for (int r = 0; r < 8; ++r) f.v[r] = *at<const float, D>(tile, row0, w.col_row, r, col);
   return f;
 }
 
-// The column operands of N neighbouring tiles, for several products: bfloat16 ones (4 registers each)
+// The column operands of all of a row's tiles, for several products: bfloat16 ones (4 registers each)
 // are read once and kept, float32 ones (8) are read at each use.
-template <typename T, int S, int N>
+template <typename T, int D>
 struct Cols {
+  const Places<T, D>& w;
   const T* p;
-  Frag<T> f[sizeof(T) == 2 ? N : 1];
-  __device__ __forceinline__ explicit Cols(const T* at) : p(at) {
+  int row0;
+  Frag<T> f[sizeof(T) == 2 ? D / 16 : 1];
+  __device__ __forceinline__ Cols(const Places<T, D>& places, const T* tile, int row) : w(places), p(tile), row0(row) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) f[n] = frag_col<S>(p + n * 16);
+      for (int n = 0; n < D / 16; ++n) f[n] = frag_col<D>(w, p, row0, n * 16);
     }
   }
   __device__ __forceinline__ Frag<T> operator[](int n) const {
     if constexpr (sizeof(T) == 2) return f[n];
-    else return frag_col<S>(p + n * 16);
+    else return frag_col<D>(w, p, row0, n * 16);
   }
 };
 
@@ -305,7 +349,6 @@ struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
   static constexpr int kWaves = std::is_same<T, float>::value ? 2 : 4;
   static constexpr int kC = 16 * kWaves;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kPad = 16 / sizeof(T);  // LDS rows stay 16-byte aligned and rotate over the banks
 };
 
 // Waves per SIMD that a kernel's registers must leave room for, where LDS does too: bfloat16 heads; the others need
@@ -325,7 +368,7 @@ struct Tile {
   static constexpr int kPer = 16 / sizeof(T);
   static constexpr int kRow = D / kPer;
   static constexpr int kN = B::kC * kRow / B::kThreads;
-  static constexpr int kStride = D + B::kPad;
+  static constexpr int kSize = B::kC * D;
   uint4 r[kN];
   // base: the block's first token; offsets in it fit 32 bits (the caller checked the stride)
   __device__ __forceinline__ void load(const T* base, uint32_t st, int rows, int dim) {
@@ -350,7 +393,7 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
-      *reinterpret_cast<uint4*>(lds + row * kStride + col) = r[i];
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(lds + (row & ~15) * D) + place<T, D>(row & 15, col)) = r[i];
     }
   }
 };
@@ -463,7 +506,6 @@ struct State {
   using B = Block<T>;
   static constexpr int kDT = DK / 16 / B::kWaves;
   static constexpr int kNT = DV / 16;
-  static constexpr int kStride = DV + B::kPad;
   f32x4 s[kDT][kNT];
 
   __device__ __forceinline__ static int d_of(int t) { return (wave_id() * kDT + t) * 16 + (threadIdx.x & 15); }
@@ -487,15 +529,15 @@ struct State {
         if (d_of(t) < dk && n_of(nt) < dv) store_acc(p + (d_of(t) * ld + n_of(nt)), s[t][nt]);
   }
   // into LDS as an operand, [d][n]; bfloat16 with what the rounding left in a second plane
-  static constexpr int kPlane = DK * kStride;
+  static constexpr int kPlane = DK * DV;
   static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
-  __device__ __forceinline__ void publish(T* p) const {
+  __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p) const {
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        T* at = p + d_of(t) * kStride + n_of(nt);
-        store_acc(at, s[t][nt]);
+        T* to = at<T, DV>(p, (wave_id() * kDT + t) * 16, wv.perm, 0, nt * 16);
+        store_acc(to, s[t][nt]);
         if constexpr (kPlanes == 2) {
           f32x4 rest;
 #pragma unroll
@@ -504,7 +546,7 @@ struct State {
             rest[r] = s[t][nt][r] - __uint_as_float(h << 16);
             rest[r + 1] = s[t][nt][r + 1] - __uint_as_float(h & 0xffff0000u);
           }
-          store_acc(at + kPlane, rest);
+          store_acc(to + kPlane, rest);
         }
       }
   }
@@ -514,13 +556,13 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) s[t][nt] *= e;
   }
-  // s += sum_j w_j y_j x_j^T over the 32 tokens from y (the tile [token][d]); xa: the operand of x, w: the
-  // weights, both in frag_col's order.
-  __device__ __forceinline__ void add(const T* y, const Cols<T, kStride, kNT>& xa, const float (&w)[8]) {
-    constexpr int SY = Tile<T, DK>::kStride;
+  // s += sum_j w_j y_j x_j^T over the 32 tokens from row0 of y (the tile [token][d]); xa: the operand of x,
+  // w: the weights, both in frag_col's order.
+  __device__ __forceinline__ void add(const Places<T, DK>& wk, const T* y, int row0, const Cols<T, DV>& xa,
+                                      const float (&w)[8]) {
 #pragma unroll
     for (int t = 0; t < kDT; ++t) {
-      const Frag<T> f = frag_col<SY>(y + (wave_id() * kDT + t) * 16);
+      const Frag<T> f = frag_col<DK>(wk, y, row0, (wave_id() * kDT + t) * 16);
       float m[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) m[e] = elem(f, e) * w[e];
@@ -538,8 +580,7 @@ struct State {
   // from its registers, in as many bfloat16 pieces as it has bits.  x: [token][n]; y4(t, jt): this lane's
   // 4 channels 16 d_tile + 4 g .. of token 16 jt + (lane & 15).  out[j] for the block's tokens.
   template <typename Y>
-  __device__ __forceinline__ void bilinear(const T* x, Y&& y4, float* out) const {
-    constexpr int SX = Tile<T, DV>::kStride;
+  __device__ __forceinline__ void bilinear(const Places<T, DV>& wv, const T* x, Y&& y4, float* out) const {
     float part[B::kWaves];
 #pragma unroll
     for (int jt = 0; jt < B::kWaves; ++jt) part[jt] = 0.0f;
@@ -557,7 +598,7 @@ struct State {
         split(m, piece);
 #pragma unroll
         for (int jt = 0; jt < B::kWaves; ++jt) {
-          const Frag<T> xb = frag_row_perm<SX>(x + jt * 16 * SX + kk * 32);
+          const Frag<T> xb = frag_row_perm<DV>(wv, x, jt * 16, kk * 32);
 #pragma unroll
           for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(piece[i], xb, acc[jt]);
         }
@@ -647,9 +688,9 @@ template <typename T, int DK, int DV, bool BACK, bool KEEP>
 __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SX = Tile<T, DV>::kStride, SY = Tile<T, DK>::kStride;
-  __shared__ __align__(16) T ys[C * SY];
-  __shared__ __align__(16) T xs[C * SX];
+  constexpr int C = B::kC;
+  __shared__ __align__(16) T ys[C * DK];
+  __shared__ __align__(16) T xs[C * DV];
   __shared__ __align__(16) Decays<C> decays[2];
   const Where w = where<T>(a, DV);
   if (!KEEP && w.seg == (BACK ? 0 : a.segments - 1)) return;  // nothing comes after (before) it
@@ -658,6 +699,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
   const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int wave = wave_id();
+  Places<T, DK> wk;
+  Places<T, DV> wv;
   S st;
   st.load(nullptr, 0, 0, 0);
   float total = 0.0f;
@@ -674,6 +717,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
   }
   for (int i = 0; i < n; ++i) {
     const Decays<C>& d = decays[i & 1];
+    wk.here();
+    wv.here();
     y.tile.store(ys);
     x.tile.store(xs);
     if constexpr (KEEP) {
@@ -700,8 +745,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_se
 #pragma unroll
         for (int e = 0; e < 8; ++e) m[e] *= a.scale;
       }
-      const Cols<T, SX, S::kNT> xa(xs + kk * 32 * SX);
-      st.add(ys + kk * 32 * SY, xa, m);
+      const Cols<T, DV> xa(wv, xs, kk * 32);
+      st.add(wk, ys, kk * 32, xa, m);
     }
     __syncthreads();
   }
@@ -757,9 +802,9 @@ template <typename T, int DK, int DV>
 __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride, NT = DV / 16;
-  __shared__ __align__(16) T ks[C * SK];
-  __shared__ __align__(16) T vs[C * SV];
+  constexpr int C = B::kC, NT = DV / 16;
+  __shared__ __align__(16) T ks[C * DK];
+  __shared__ __align__(16) T vs[C * DV];
   __shared__ __align__(16) T ss[S::kPlanes * S::kPlane];
   __shared__ __align__(16) Decays<C> decays[2];
   const Where w = where<T>(a, DV);
@@ -770,6 +815,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
   T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd + w.n0;
   const int64_t ot = static_cast<int64_t>(a.heads) * a.dvd;
   const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
+  Places<T, DK> wk;
+  Places<T, DV> wv;
   // The last 16 queries of a block have four times the first ones' scores.  Workgroups that share a CU give
   // them to different waves, so that no SIMD gets all of them.
   const int qt = (blockIdx.x >> 8) & 1 ? B::kWaves - 1 - wave : wave;
@@ -798,10 +845,12 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
   for (int c = w.c0; c < w.c1; ++c) {
     const int t0 = c * C;
     const Decays<C>& d = decays[c & 1];
+    wk.here();
+    wv.here();
     const OwnRows<T, DK> qf = qn;
     k.tile.store(ks);
     v.tile.store(vs);
-    st.publish(ss);
+    st.publish(wv, ss);
     __syncthreads();
     if (c + 1 < w.c1) {
       q.skip(1);
@@ -827,7 +876,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
         for (int pl = 0; pl < S::kPlanes; ++pl)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            acc[nt] = mma(frag_col_row<SS>(ss + pl * S::kPlane + kk * 32 * SS + nt * 16), qf.f[kk], acc[nt]);
+            acc[nt] = mma(frag_col_row<DV>(wv, ss + pl * S::kPlane, kk * 32, nt * 16), qf.f[kk], acc[nt]);
       }
       const float e = d.from0[i];
 #pragma unroll
@@ -837,7 +886,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk) {
       if (t0 + kk * 32 >= w.live) break;
-      const Cols<T, SV, NT> xa(vs + kk * 32 * SV);
+      const Cols<T, DV> xa(wv, vs, kk * 32);
       if (own && kk <= qt / 2) {
         // the masked scores of 32 keys, then their product with the values
         float p[8];
@@ -847,7 +896,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
           if (j0 <= i0) {
             f32x4 sc = zero4();
 #pragma unroll
-            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(ks + j0 * SK + n * 32), qf.f[n], sc);
+            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<DK>(wk, ks, j0, n * 32), qf.f[n], sc);
             if (j0 < i0) {  // through the last of the 16 keys: both factors are powers of the decays between
               const f32x4 e = load4(d.toE + j0 + g4);
               const float from = d.between(gh, gl, j0 + 15);
@@ -870,7 +919,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
       }
       float m[8];
       eight(d.toC + kk * 32, m);
-      st.add(ks + kk * 32 * SK, xa, m);
+      st.add(wk, ks, kk * 32, xa, m);
     }
     if (t0 + i < w.live) {
       T* o = out + t0 * ot;
@@ -910,15 +959,15 @@ template <typename T, int DK, int DV>
 __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_grad_kernel(LinArgs a) {
   using B = Block<T>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC, SK = Tile<T, DK>::kStride, SV = Tile<T, DV>::kStride, SS = S::kStride;
+  constexpr int C = B::kC;
   constexpr int DT = DK / 16, NT = DV / 16;
   // S and R as operands: side by side where LDS has room for both, else one after the other
   constexpr int kStateLds = S::kPlanes * S::kPlane;
-  constexpr bool kBoth = (2 * C * (SK + SV) + 2 * kStateLds) * sizeof(T) + 8192 <= 160 * 1024;
-  __shared__ __align__(16) T qs[C * SK];
-  __shared__ __align__(16) T ks[C * SK];
-  __shared__ __align__(16) T vs[C * SV];
-  __shared__ __align__(16) T os[C * SV];
+  constexpr bool kBoth = (2 * C * (DK + DV) + 2 * kStateLds) * sizeof(T) + 8192 <= 160 * 1024;
+  __shared__ __align__(16) T qs[C * DK];
+  __shared__ __align__(16) T ks[C * DK];
+  __shared__ __align__(16) T vs[C * DV];
+  __shared__ __align__(16) T os[C * DV];
   __shared__ __align__(16) T ss[(kBoth ? 2 : 1) * kStateLds];
   __shared__ __align__(16) Decays<C> decays[2];
   __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
@@ -932,6 +981,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
   float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
   const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
 
+  Places<T, DK> wk;
+  Places<T, DV> wv;
   S st, first;  // R; the state that enters the segment
   if (a.segments > 1) {
     const int64_t at = (w.bh * a.segments + w.seg) * (DK * DV);
@@ -963,6 +1014,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
   for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
     const Decays<C>& d = decays[c & 1];
+    wk.here();
+    wv.here();
     const int64_t block = w.bh * a.blocks + c;
     S old;  // the state that enters the block
     old.load(a.states + block * (DK * DV), DK, DV, DV);
@@ -983,10 +1036,10 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
             y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
           }
       y = sum_rows(row_sum(y));
-      if (l == 0) across[wave] = y;
+      if ((threadIdx.x & 63) == 0) across[wave] = y;
     }
-    old.publish(ss);
-    if constexpr (kBoth) st.publish(rs);
+    old.publish(wv, ss);
+    if constexpr (kBoth) st.publish(wv, rs);
     __syncthreads();
     if (c > w.c0) {
       skip(-1);
@@ -994,15 +1047,16 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
       if (wave == c % B::kWaves) scan_g(gx, decays[(c - 1) & 1]);
       if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
     }
-    const int d0 = wave * S::kDT * 16 + g4;
-    old.bilinear(os, [&](int t, int jt) { return load4(qs + (jt * 16 + li) * SK + d0 + t * 16); }, into[wave]);
+    const int d0 = wave * S::kDT * 16;
+    old.bilinear(wv, os, [&](int t, int jt) { return load4(at<T, DK>(qs, jt * 16, wk.perm, 0, d0 + t * 16)); },
+                 into[wave]);
     // dq of this wave's 16 queries: column i of every result tile
     if (t0 + wave * 16 < w.live) {
       const int i0 = wave * 16, i = i0 + li;
       const float gh = d.hi[i], gl = d.lo[i];
       Frag<T> of[DV / 32];
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<SV>(os + i0 * SV + kk * 32);
+      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<DV>(wv, os, i0, kk * 32);
       f32x4 acc[DT];
       const float e0 = d.from0[i] * a.scale;
 #pragma unroll
@@ -1012,7 +1066,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
         for (int pl = 0; pl < S::kPlanes; ++pl)
 #pragma unroll
           for (int kk = 0; kk < DV / 32; ++kk)
-            acc[dt] = mma(frag_row<SS>(ss + pl * S::kPlane + dt * 16 * SS + kk * 32), of[kk], acc[dt]);
+            acc[dt] = mma(frag_row<DV>(wv, ss + pl * S::kPlane, dt * 16, kk * 32), of[kk], acc[dt]);
         acc[dt] *= e0;
       }
 #pragma unroll
@@ -1025,7 +1079,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
           if (j0 <= i0) {
             f32x4 dp = zero4();
 #pragma unroll
-            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<SV>(vs + j0 * SV + kk * 32), of[kk], dp);
+            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<DV>(wv, vs, j0, kk * 32), of[kk], dp);
             if (j0 < i0) {
               const f32x4 e = load4(d.toE + j0 + g4);
               const float from = d.between(gh, gl, j0 + 15) * a.scale;
@@ -1044,7 +1098,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
         Frag<T> pf;
         pack(p, pf);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc[dt] = mma(frag_col<SK>(ks + jj * 32 * SK + dt * 16), pf, acc[dt]);
+        for (int dt = 0; dt < DT; ++dt) acc[dt] = mma(frag_col<DK>(wk, ks, jj * 32, dt * 16), pf, acc[dt]);
       }
       if (t0 + i < w.live) {
 #pragma unroll
@@ -1060,18 +1114,19 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
     }
     if constexpr (!kBoth) {
       __syncthreads();
-      st.publish(rs);
+      st.publish(wv, rs);
       __syncthreads();
     }
-    st.bilinear(vs, [&](int t, int jt) { return load4(ks + (jt * 16 + li) * SK + d0 + t * 16); }, after[wave]);
+    st.bilinear(wv, vs, [&](int t, int jt) { return load4(at<T, DK>(ks, jt * 16, wk.perm, 0, d0 + t * 16)); },
+                after[wave]);
     // dk and dv of this wave's 16 keys: column j of every result tile
     const int j0 = wave * 16, j = j0 + li;
     const float gh = d.hi[j], gl = d.lo[j], toC = d.toC[j];
     Frag<T> kf[DK / 32], vf[DV / 32];
 #pragma unroll
-    for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<SK>(ks + j0 * SK + kk * 32);
+    for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<DK>(wk, ks, j0, kk * 32);
 #pragma unroll
-    for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<SV>(vs + j0 * SV + kk * 32);
+    for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<DV>(wv, vs, j0, kk * 32);
     f32x4 ak[DT], av[NT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
@@ -1080,7 +1135,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
       for (int pl = 0; pl < S::kPlanes; ++pl)
 #pragma unroll
         for (int kk = 0; kk < DV / 32; ++kk)
-          ak[dt] = mma(frag_row<SS>(rs + pl * S::kPlane + dt * 16 * SS + kk * 32), vf[kk], ak[dt]);
+          ak[dt] = mma(frag_row<DV>(wv, rs + pl * S::kPlane, dt * 16, kk * 32), vf[kk], ak[dt]);
       ak[dt] *= toC;
     }
 #pragma unroll
@@ -1091,7 +1146,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
       for (int pl = 0; pl < S::kPlanes; ++pl)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          av[nt] = mma(frag_col_row<SS>(rs + pl * S::kPlane + kk * 32 * SS + nt * 16), kf[kk], av[nt]);
+          av[nt] = mma(frag_col_row<DV>(wv, rs + pl * S::kPlane, kk * 32, nt * 16), kf[kk], av[nt]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) av[nt] *= toC;
@@ -1105,7 +1160,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
         if (kk >= wave / 2 && l < 32 && kk * 32 + l >= j0) rows[wave][kk * 32 + l] = 0.0f;
         continue;
       }
-      const Cols<T, SV, NT> xa(os + kk * 32 * SV);
+      const Cols<T, DV> xa(wv, os, kk * 32);
       if (kk >= wave / 2) {
         float p[8], x[8];
 #pragma unroll
@@ -1114,9 +1169,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
           if (i0 >= j0) {
             f32x4 sc = zero4(), dp = zero4();
 #pragma unroll
-            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<SK>(qs + i0 * SK + n * 32), kf[n], sc);
+            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<DK>(wk, qs, i0, n * 32), kf[n], sc);
 #pragma unroll
-            for (int n = 0; n < DV / 32; ++n) dp = mma(frag_row<SV>(os + i0 * SV + n * 32), vf[n], dp);
+            for (int n = 0; n < DV / 32; ++n) dp = mma(frag_row<DV>(wv, os, i0, n * 32), vf[n], dp);
             float u[4];
             if (i0 > j0) {  // through the last token before the 16 queries
               const f32x4 e = load4(d.fromF + i0 + g4);
@@ -1159,13 +1214,13 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) av[nt] = mma(xa[nt], pf, av[nt]);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) ak[dt] = mma(frag_col<SK>(qs + kk * 32 * SK + dt * 16), xf, ak[dt]);
+        for (int dt = 0; dt < DT; ++dt) ak[dt] = mma(frag_col<DK>(wk, qs, kk * 32, dt * 16), xf, ak[dt]);
       }
       float m[8];
       eight(d.from0 + kk * 32, m);
 #pragma unroll
       for (int e = 0; e < 8; ++e) m[e] *= a.scale;
-      st.add(qs + kk * 32 * SK, xa, m);
+      st.add(wk, qs, kk * 32, xa, m);
     }
     if (t0 + j < w.live) {
 #pragma unroll
