@@ -344,12 +344,17 @@ struct LinArgs {
   float scale;
 };
 
-template <typename T>
-struct Block {  // tokens per block and waves: a wave owns 16 tokens of a block
-  static constexpr int kWaves = std::is_same<T, float>::value ? 2 : 4;
+// Tokens per block and waves: a wave owns 16 tokens of a block.  64 tokens, but 32 where the gradient's float32
+// tiles of 128 channels would not fit LDS (all kernels of a call use the same blocks).
+constexpr int waves_of(size_t elem, int dk, int dv) { return elem == 4 && dk == 128 && dv == 128 ? 2 : 4; }
+template <int W>
+struct Block {
+  static constexpr int kWaves = W;
   static constexpr int kC = 16 * kWaves;
   static constexpr int kThreads = 64 * kWaves;
 };
+template <typename T, int DK, int DV>
+using BlockOf = Block<waves_of(sizeof(T), DK, DV)>;
 
 // Waves per SIMD that a kernel's registers must leave room for, where LDS does too: bfloat16 heads; the others need
 // their registers.
@@ -362,9 +367,8 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 
 // A tile of C tokens on its way from global memory to LDS.  Tokens from `rows` on and channels from
 // `dim` on are not read: they enter as zeros, whatever the memory holds.
-template <typename T, int D>
+template <typename T, int D, typename B>
 struct Tile {
-  using B = Block<T>;
   static constexpr int kPer = 16 / sizeof(T);
   static constexpr int kRow = D / kPer;
   static constexpr int kN = B::kC * kRow / B::kThreads;
@@ -419,14 +423,14 @@ struct OwnRows {
 };
 
 // A tensor of one (sequence, head), block by block.
-template <typename T, int D>
+template <typename T, int D, typename B>
 struct Stream {
   const T* p;  // the block's first token
   int st;      // token stride
-  Tile<T, D> tile;
+  Tile<T, D, B> tile;
   __device__ __forceinline__ Stream(const View& v, int64_t b, int h, int n0)
       : p(static_cast<const T*>(v.p) + b * v.b + h * v.h + n0), st(static_cast<int>(v.t)) {}
-  __device__ __forceinline__ void skip(int blocks) { p += static_cast<int64_t>(blocks) * (Block<T>::kC * st); }
+  __device__ __forceinline__ void skip(int blocks) { p += static_cast<int64_t>(blocks) * (B::kC * st); }
   __device__ __forceinline__ void load(int rows, int dim) { tile.load(p, st, rows, dim); }
 };
 
@@ -503,7 +507,7 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
 // w * DT + t), rows n = 16 nt + 4 g + r.
 template <typename T, int DK, int DV>
 struct State {
-  using B = Block<T>;
+  using B = BlockOf<T, DK, DV>;
   static constexpr int kDT = DK / 16 / B::kWaves;
   static constexpr int kNT = DV / 16;
   f32x4 s[kDT][kNT];
@@ -632,9 +636,9 @@ struct Where {  // this workgroup's place
 };
 // Workgroup i runs on XCD i % 8.  An XCD takes consecutive places: the slices of the value channels and the
 // heads that share q and k, which then find them in its L2, then a sequence's segments.
-template <typename T>
+template <typename B>
 __device__ __forceinline__ Where where(const LinArgs& a, int width) {
-  constexpr int C = Block<T>::kC;
+  constexpr int C = B::kC;
   const uint32_t n = gridDim.x, q = n >> 3, r = n & 7, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
   uint32_t id = (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + local;
   Where w;
@@ -668,13 +672,13 @@ __device__ __forceinline__ const T* head(const View& v, int64_t b, int h) {
 
 // Zeros for this place's tokens past the row's length, in a tensor with token stride `st`, `dim` (a multiple
 // of 4) channels.
-template <typename T, typename O>
+template <typename B, typename O>
 __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p, int64_t st, int dim) {
-  constexpr int C = Block<T>::kC;
+  constexpr int C = B::kC;
   const int t1 = w.end * C < a.seqlen ? w.end * C : a.seqlen;
   const int t0 = w.live > w.c0 * C ? w.live : w.c0 * C;
   const int runs = dim / 4;
-  for (int64_t id = threadIdx.x; id < static_cast<int64_t>(t1 - t0) * runs; id += Block<T>::kThreads) {
+  for (int64_t id = threadIdx.x; id < static_cast<int64_t>(t1 - t0) * runs; id += B::kThreads) {
     const int64_t t = id / runs;
     store_acc(p + (t0 + t) * st + (id - t * runs) * 4, zero4());
   }
@@ -685,17 +689,17 @@ __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p
 // from a zero end.  KEEP also writes the state before each block.
 
 template <typename T, int DK, int DV, bool BACK, bool KEEP>
-__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
-  using B = Block<T>;
+__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
+  using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC;
   __shared__ __align__(16) T ys[C * DK];
   __shared__ __align__(16) T xs[C * DV];
   __shared__ __align__(16) Decays<C> decays[2];
-  const Where w = where<T>(a, DV);
+  const Where w = where<B>(a, DV);
   if (!KEEP && w.seg == (BACK ? 0 : a.segments - 1)) return;  // nothing comes after (before) it
-  Stream<T, DK> y(BACK ? a.q : a.k, w.b, w.h / a.share, 0);
-  Stream<T, DV> x(BACK ? a.dout : a.v, w.b, w.h, w.n0);
+  Stream<T, DK, B> y(BACK ? a.q : a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV, B> x(BACK ? a.dout : a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int wave = wave_id();
@@ -799,17 +803,17 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
 // forward
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
-  using B = Block<T>;
+__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
+  using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC, NT = DV / 16;
   __shared__ __align__(16) T ks[C * DK];
   __shared__ __align__(16) T vs[C * DV];
   __shared__ __align__(16) T ss[S::kPlanes * S::kPlane];
   __shared__ __align__(16) Decays<C> decays[2];
-  const Where w = where<T>(a, DV);
-  Stream<T, DK> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
-  Stream<T, DV> v(a.v, w.b, w.h, w.n0);
+  const Where w = where<B>(a, DV);
+  Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV, B> v(a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   T* out = static_cast<T*>(a.out) + (w.b * a.seqlen * a.heads + w.h) * a.dvd + w.n0;
@@ -929,7 +933,7 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
     }
     __syncthreads();
   }
-  zero_rest<T>(a, w, out, ot, dv < DV ? dv : DV);
+  zero_rest<B>(a, w, out, ot, dv < DV ? dv : DV);
   if (a.sT && w.seg == a.segments - 1) st.store(a.sT + w.bh * a.dk * a.dvd + w.n0, a.dk, dv, a.dvd);
 }
 
@@ -956,8 +960,8 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(3) void linattn_fw
 // start; this kernel walks backwards and does the rest, reading q, k, v and dout once.
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_grad_kernel(LinArgs a) {
-  using B = Block<T>;
+__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) void linattn_grad_kernel(LinArgs a) {
+  using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC;
   constexpr int DT = DK / 16, NT = DV / 16;
@@ -972,9 +976,9 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
   __shared__ __align__(16) Decays<C> decays[2];
   __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
   T* const rs = kBoth ? ss + kStateLds : ss;
-  const Where w = where<T>(a, DV);
-  Stream<T, DK> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
-  Stream<T, DV> v(a.v, w.b, w.h, 0), o(a.dout, w.b, w.h, 0);
+  const Where w = where<B>(a, DV);
+  Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
+  Stream<T, DV, B> v(a.v, w.b, w.h, 0), o(a.dout, w.b, w.h, 0);
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
   const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
@@ -1264,13 +1268,13 @@ __global__ __launch_bounds__(Block<T>::kThreads) VMSCAN_WAVES(2) void linattn_gr
     }
   }
   if (a.share == 1) {
-    zero_rest<T>(a, w, static_cast<T*>(a.dq) + kbase, kt, a.dk);
-    zero_rest<T>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
+    zero_rest<B>(a, w, static_cast<T*>(a.dq) + kbase, kt, a.dk);
+    zero_rest<B>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
   } else {
-    zero_rest<T>(a, w, static_cast<float*>(a.dq) + kbase, kt, a.dk);
-    zero_rest<T>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
+    zero_rest<B>(a, w, static_cast<float*>(a.dq) + kbase, kt, a.dk);
+    zero_rest<B>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
   }
-  zero_rest<T>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
+  zero_rest<B>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
   const int t_end = w.end * C < a.seqlen ? w.end * C : a.seqlen;
   for (int64_t t = (w.live > w.c0 * C ? w.live : w.c0 * C) + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads)
     dg[t * a.heads] = 0.0f;
@@ -1428,11 +1432,11 @@ int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
 // is taken, a block of 32, 64 or 128 value channels counted as kBlockTime.  The gradient needs all channels
 // of a token together and is only cut into segments.
 Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
-  const int C = dtype == VMSCAN_F32 ? Block<float>::kC : Block<uint16_t>::kC;
   Plan best{};
   double least = 0.0;
-  const int blocks = static_cast<int>((seqlen + C - 1) / C);
   for (int width = pad_dim(dv); width >= (back ? pad_dim(dv) : kSlice); width /= 2) {
+    const int C = 16 * waves_of(dtype == VMSCAN_F32 ? 4 : 2, pad_dim(dk), width);
+    const int blocks = static_cast<int>((seqlen + C - 1) / C);
     const int slices = (dv + width - 1) / width;
     const int64_t walks = batch * heads * slices, slots = slots_for(dtype, dk, width, back);
     const double block = width == 32 ? kBlockTime[0] : width == 64 ? kBlockTime[1] : kBlockTime[2];
@@ -1529,7 +1533,7 @@ template <typename T, bool BACK, bool KEEP>
 void launch_segments(const LinArgs& a, int width, hipStream_t stream) {
   with_dims(a.dk, width, [&](auto dk, auto dv) {
     constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK, KEEP>), walks(a), dim3(Block<T>::kThreads), 0, stream,
+    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK, KEEP>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream,
                        a);
     const int64_t n = a.batch * a.heads * (DK * a.ld / 4);
     if (a.segments > 1)
@@ -1542,8 +1546,8 @@ template <typename T>
 vmscan_status run_fwd(const LinArgs& a, int width, hipStream_t stream) {
   if (a.segments > 1) launch_segments<T, false, false>(a, width, stream);
   with_dims(a.dk, width, [&](auto dk, auto dv) {
-    hipLaunchKernelGGL((linattn_fwd_kernel<T, decltype(dk)::value, decltype(dv)::value>), walks(a),
-                       dim3(Block<T>::kThreads), 0, stream, a);
+    constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+    hipLaunchKernelGGL((linattn_fwd_kernel<T, DK, DV>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream, a);
   });
   return launched();
 }
@@ -1557,11 +1561,10 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
   launch_segments<T, false, true>(a, y.p.width, stream);
   if (a.segments > 1) launch_segments<T, true, false>(a, y.p.width, stream);
-  const dim3 grid = walks(a), block(Block<T>::kThreads);
   with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
     if constexpr (DV >= 64) {
-      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream, a);
     }
   });
   const int64_t tokens = a.batch * a.seqlen;
