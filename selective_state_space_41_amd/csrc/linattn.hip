@@ -341,6 +341,7 @@ struct LinArgs {
   int seqlen, heads, share, dk, dvd;  // share: heads per query/key head
   int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
   int slices, ld;                     // slices of the value channels; a segment state's row
+  int subs, back_segments;            // the pass from the end: segments it cuts one into, and all of them
   float scale;
 };
 
@@ -697,7 +698,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) voi
   __shared__ __align__(16) T xs[C * DV];
   __shared__ __align__(16) Decays<C> decays[2];
   const Where w = where<B>(a, DV);
-  if (!KEEP && w.seg == (BACK ? 0 : a.segments - 1)) return;  // nothing comes after (before) it
+  if (!KEEP && (BACK ? w.seg < a.subs : w.seg == a.segments - 1)) return;  // no segment lies past it
   Stream<T, DK, B> y(BACK ? a.q : a.k, w.b, w.h / a.share, 0);
   Stream<T, DV, B> x(BACK ? a.dout : a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
@@ -784,7 +785,7 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
         const int s = BACK ? a.segments - 1 - i0 - i : i0 + i;
         own[i] = zero4();
         m[i] = 0.0f;
-        if (i0 + i + 1 < a.segments) {  // what the last one adds enters nothing
+        if (BACK ? s >= a.subs : s + 1 < a.segments) {  // what the last one adds enters nothing
           own[i] = load4(p + s * step);
           m[i] = __builtin_amdgcn_exp2f(g[s]);
         }
@@ -989,9 +990,9 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
   Places<T, DV> wv;
   S st, first;  // R; the state that enters the segment
   if (a.segments > 1) {
-    const int64_t at = (w.bh * a.segments + w.seg) * (DK * DV);
-    st.load(a.seg_ds + at, DK, DV, DV);
-    first.load(a.seg_s + at, DK, DV, DV);
+    const int end = (w.seg + 1) * a.subs < a.back_segments ? (w.seg + 1) * a.subs : a.back_segments;
+    st.load(a.seg_ds + (w.bh * a.back_segments + end - 1) * (DK * DV), DK, DV, DV);
+    first.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
   } else {
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
     first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
@@ -1401,10 +1402,11 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
 
 constexpr int kMaxHeadDim = 128;
 constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // a block's offsets fit 32 bits in bytes
-constexpr double kBlockTime[3] = {0.7, 1.0, 1.7};
-constexpr double kStartTime = 1.0;      // a walk's start and end, in blocks
-constexpr double kSegmentTime = 0.4;    // the segments' pass against the walk
-constexpr double kPrefixTime = 4.0;     // two more launches and the prefix
+// Estimates of plan(), us: a block by [gradient][float32][channels 32, 64, 128]; the segments' pass as a share
+// of the walk, its launches, and the prefix per segment, each by [gradient].
+constexpr double kBlockUs[2][2][3] = {{{2.2, 2.9, 4.6}, {4.2, 5.5, 9.0}}, {{0.0, 8.0, 13.0}, {0.0, 14.0, 24.0}}};
+constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {6.0, 8.0}, kSegmentUs[2] = {0.2, 0.4};
+constexpr int64_t kBackWalks = 512;     // workgroups wanted in the gradient's pass from the end
 constexpr int kMaxSegments = 64;
 constexpr int kSlice = 32;              // value channels of the narrowest workgroup
 
@@ -1413,6 +1415,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Plan {
   int blocks, segments, per, width, slices;
+  int subs, back_segments;
 };
 // Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
 int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
@@ -1428,28 +1431,47 @@ int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
 }
 // How a call is cut up.  The forward's value channels are independent, so several workgroups can share them (each
 // repeats the scores), and a sequence can be cut into segments (a pass over the keys and values more, and
-// a prefix over the segments).  Of all cuts the one whose rounds of workgroups take the fewest block times
-// is taken, a block of 32, 64 or 128 value channels counted as kBlockTime.  The gradient needs all channels
-// of a token together and is only cut into segments.
+// a prefix over the segments).  Of all cuts the one with the least estimated time is taken: rounds of workgroups
+// times blocks, a block's time as measured where one workgroup has a CU for itself.  Measured, us, cut as taken
+// / whole: 8 x 6085 tokens, 6 heads of 128 x 64, bfloat16: 101 (10 segments) / over 500; 1 x 6085, 6 of 64 x 64:
+// 32 (32 segments, halves of the channels) / 282; 1 x 197, 6 of 64 x 64: bfloat16 11.4 (halves) / 14.2, float32 16.1
+// (halves, 4 segments) / 26.8; 128 x 197, 6 of 64 x 64: 24.6 (whole) / 50 in 2 segments, 30 in halves.
+// The gradient needs all channels of a token together and is only cut into segments: 32 x 3136, 8 of 64 x 64:
+// 481 (2 segments) / 649; 1 x 197, 6 of 64 x 64: 29 (4 segments) / 43.
 Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
   Plan best{};
   double least = 0.0;
+  const bool f32 = dtype == VMSCAN_F32;
   for (int width = pad_dim(dv); width >= (back ? pad_dim(dv) : kSlice); width /= 2) {
-    const int C = 16 * waves_of(dtype == VMSCAN_F32 ? 4 : 2, pad_dim(dk), width);
+    const int C = 16 * waves_of(f32 ? 4 : 2, pad_dim(dk), width);
     const int blocks = static_cast<int>((seqlen + C - 1) / C);
     const int slices = (dv + width - 1) / width;
     const int64_t walks = batch * heads * slices, slots = slots_for(dtype, dk, width, back);
-    const double block = width == 32 ? kBlockTime[0] : width == 64 ? kBlockTime[1] : kBlockTime[2];
+    const double block = kBlockUs[back][f32][width == 32 ? 0 : width == 64 ? 1 : 2];
     for (int seg = 1; seg <= blocks && seg <= kMaxSegments; ++seg) {
       const int per = (blocks + seg - 1) / seg;
       if ((blocks + per - 1) / per != seg) continue;
       const double rounds = static_cast<double>((walks * seg + slots - 1) / slots);
-      const double time = rounds * (per + kStartTime) * block + (seg > 1 ? kSegmentTime * rounds * (per + kStartTime) * block + kPrefixTime : 0.0);
+      double time = rounds * (per + 1) * block;  // a block's time to start and end
+      if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + kSegmentUs[back] * seg;
       if (best.blocks == 0 || time < least) {
         least = time;
-        best = Plan{blocks, seg, per, width, slices};
+        best = Plan{blocks, seg, per, width, slices, 1, seg};
       }
     }
+  }
+  // The pass from the end leaves out the first segment, so with few segments it has few workgroups: it cuts
+  // each further.
+  if (back && best.segments > 1) {
+    const int64_t walks = batch * heads * (best.segments - 1);
+    int64_t subs = (kBackWalks + walks - 1) / walks;
+    if (subs > best.per) subs = best.per;
+    const int part = static_cast<int>((best.per + subs - 1) / subs);
+    best.subs = (best.per + part - 1) / part;
+    best.per = best.subs * part;
+    best.segments = (best.blocks + best.per - 1) / best.per;
+    best.back_segments = (best.blocks + part - 1) / part;
+    if (best.segments == 1) best.subs = best.back_segments = 1;
   }
   return best;
 }
@@ -1484,8 +1506,8 @@ Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int 
     y.seg_s = take(bh * y.p.segments * state);
     y.seg_g = take(bh * y.p.segments * 4);
     if (back) {
-      y.seg_ds = take(bh * y.p.segments * state);
-      y.seg_dg = take(bh * y.p.segments * 4);
+      y.seg_ds = take(bh * y.p.back_segments * state);
+      y.seg_dg = take(bh * y.p.back_segments * 4);
     }
   }
   if (back) {
@@ -1560,7 +1582,11 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   a.dk_out = shared ? ws + y.dk : dk;
   a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
   launch_segments<T, false, true>(a, y.p.width, stream);
-  if (a.segments > 1) launch_segments<T, true, false>(a, y.p.width, stream);
+  if (a.segments > 1) {
+    LinArgs b = a;
+    b.segments = a.back_segments, b.per_segment = a.per_segment / a.subs;
+    launch_segments<T, true, false>(b, y.p.width, stream);
+  }
   with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
     if constexpr (DV >= 64) {
@@ -1611,6 +1637,7 @@ vmscan_status common_args(LinArgs& a, const void* q, const int64_t* qs, const vo
 void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.blocks = y.p.blocks, a.segments = y.p.segments, a.per_segment = y.p.per;
   a.slices = y.p.slices, a.ld = y.p.slices * y.p.width;
+  a.subs = y.p.subs, a.back_segments = y.p.back_segments;
   a.seg_s = reinterpret_cast<float*>(ws + y.seg_s);
   a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
   a.seg_g = reinterpret_cast<float*>(ws + y.seg_g);
@@ -1620,7 +1647,7 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
 }
 
 vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
-  if (a.batch * a.heads * p.segments * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+  if (a.batch * a.heads * p.back_segments * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
   if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
   return need && (!ws || have < need) ? VMSCAN_ERR_WORKSPACE : VMSCAN_OK;
 }
