@@ -52,10 +52,13 @@ __device__ __forceinline__ void cos_sin(float p, float f, float& c, float& s) {
   sincospif(2.0f * part, &s, &c);
 }
 
+// V consecutive channels: one 16-byte access, or one by one.
 template <typename T, int V>
 __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-  if constexpr (V == 8) {
+  if constexpr (V * sizeof(T) == 16 && V == 8) {
     load8(p, v);
+  } else if constexpr (V * sizeof(T) == 16) {
+    __builtin_memcpy(v, p, 16);
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = load1(p + k);
@@ -63,8 +66,10 @@ __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
-  if constexpr (V == 8) {
+  if constexpr (V * sizeof(T) == 16 && V == 8) {
     store8(p, v);
+  } else if constexpr (V * sizeof(T) == 16) {
+    __builtin_memcpy(p, v, 16);
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) store1(p + k, v[k]);
@@ -170,15 +175,15 @@ bool runs_aligned(const RopeTensor& x, int64_t n) {
   return aligned_to(x.in, 16) && aligned_to(x.out, 16) && x.ib % n == 0 && x.it % n == 0 && x.ih % n == 0 && x.ob % n == 0 && x.ot % n == 0 && x.oh % n == 0;
 }
 
-// The unit of channels: 8 at a time when every run of 8 of a head starts on a 16-byte boundary (two
-// for float32) and the rotated channels and the rest are whole runs, else one pair.
+// The unit of channels: 16 bytes when every run of that size starts on a 16-byte boundary and the rotated
+// channels and the rest are whole runs, else one pair.
 template <typename T>
 vmscan_status run_rope(const RopeArgs& a, int interleaved, hipStream_t stream) {
-  constexpr int64_t kRun = 16 / sizeof(T);
-  const bool wide = runs_aligned(a.q, kRun) && (!a.k.heads || runs_aligned(a.k, kRun)) && a.dim % 8 == 0 &&
-                    (interleaved ? a.rot % 8 == 0 : (a.rot / 2) % 8 == 0);
-  if (interleaved) return wide ? launch_rope<T, 8, true>(a, stream) : launch_rope<T, 2, true>(a, stream);
-  return wide ? launch_rope<T, 8, false>(a, stream) : launch_rope<T, 1, false>(a, stream);
+  constexpr int kRun = 16 / sizeof(T);
+  const bool wide = runs_aligned(a.q, kRun) && (!a.k.heads || runs_aligned(a.k, kRun)) && a.dim % kRun == 0 &&
+                    (interleaved ? a.rot % kRun == 0 : (a.rot / 2) % kRun == 0);
+  if (interleaved) return wide ? launch_rope<T, kRun, true>(a, stream) : launch_rope<T, 2, true>(a, stream);
+  return wide ? launch_rope<T, kRun, false>(a, stream) : launch_rope<T, 1, false>(a, stream);
 }
 
 }  // namespace
