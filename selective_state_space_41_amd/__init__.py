@@ -164,7 +164,7 @@ def _ptr(t):
 def _need(t, name, shape, dtype, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -525,17 +525,10 @@ def _is_act(t, name, ndim):
 _pack2, _pack3 = struct.Struct("=2q").pack, struct.Struct("=3q").pack
 
 
-def _strides(t, n):
-    """The first n (2 or 3) strides as the library's int64 array; 0 where the dimension has one
-    element, whose stride says nothing."""
-    st = t.stride()[:n]
-    if 1 in t.shape[:n]:
-        st = [s if d != 1 else 0 for s, d in zip(st, t.shape)]
-    return _pack3(*st) if n == 3 else _pack2(*st)
-
-
 def _strided(t, name, shape, dtype, device):
-    """A tensor of any strides but contiguous channels; its leading strides for the library."""
+    """A tensor [batch, (token,) head, channel] of any strides but contiguous channels; its leading
+    strides as the library's int64 array, 0 where the dimension has one element (whose stride says
+    nothing)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -544,9 +537,16 @@ def _strided(t, name, shape, dtype, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.stride(-1) != 1 and shape[-1] != 1:
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous channels")
-    return _strides(t, len(shape) - 1)
+    if len(st) == 4:
+        a, b, c, _ = st
+        n, m, k, _ = shape
+        return _pack3(a if n != 1 else 0, b if m != 1 else 0, c if k != 1 else 0)
+    a, b, _ = st
+    n, m, _ = shape
+    return _pack2(a if n != 1 else 0, b if m != 1 else 0)
 
 
 def _made(stream, *tensors):
@@ -599,7 +599,8 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor with a channel dimension")
     dt = _is_act(x, "x", x.dim())
-    dev, shape, dim = x.device, x.shape, x.shape[-1]
+    dev, shape = x.device, tuple(x.shape)
+    dim, lead = shape[-1], shape[:-1]
     rows = x.numel() // dim if dim else 0
     if x.is_contiguous():
         row_stride = dim
@@ -630,8 +631,8 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
         _need(y, "y", shape, ydt, dev)
     scale = None
     if fp8:
-        scale = torch.empty(*shape[:-1], -(-dim // group) if group else 1, dtype=torch.float32, device=dev)
-    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        scale = torch.empty(lead + (-(-dim // group) if group else 1,), dtype=torch.float32, device=dev)
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev)
     _made(stream, scale, rstd)
     _enqueue(load().vmscan_rmsnorm_fwd,
              (x.data_ptr(), row_stride, _p(residual), weight.data_ptr(), y.data_ptr(), _p(scale), _p(residual_out),
@@ -717,16 +718,17 @@ def _linattn_args(q, k, v, log_decay, ndim):
     """Checks what every linear-attention call takes; returns (dtype code, batch and token sizes, heads,
     kheads, dk, dv, strides of q, k, v and of the decay, None for one decay per head)."""
     dt = _is_act(q, "q", ndim)
-    dev, lead = q.device, q.shape[:-2]
-    Hk, dk = q.shape[-2:]
+    dev, adt, shape = q.device, q.dtype, tuple(q.shape)
+    lead, Hk, dk = shape[:-2], shape[-2], shape[-1]
     if not isinstance(v, torch.Tensor) or v.dim() != ndim:
         raise ValueError(f"v must have {ndim} dimensions")
-    H, dv = v.shape[-2:]
+    vshape = tuple(v.shape)
+    H, dv = vshape[-2], vshape[-1]
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} heads of v cannot share {Hk} heads of q and k")
-    qs = _strided(q, "q", q.shape, q.dtype, dev)
-    ks = _strided(k, "k", q.shape, q.dtype, dev)
-    vs = _strided(v, "v", lead + (H, dv), q.dtype, dev)
+    qs = _strided(q, "q", shape, adt, dev)
+    ks = _strided(k, "k", shape, adt, dev)
+    vs = _strided(v, "v", lead + (H, dv), adt, dev)
     if not isinstance(log_decay, torch.Tensor):
         raise TypeError("log_decay must be a torch.Tensor")
     if log_decay.dtype != torch.float32 or log_decay.device != dev:
@@ -735,9 +737,9 @@ def _linattn_args(q, k, v, log_decay, ndim):
     if log_decay.dim() == 1:
         _need(log_decay, "log_decay", (H,), torch.float32, dev)
     elif log_decay.shape == lead + (H,):
-        gs = _strides(log_decay, ndim - 1)
+        gs = (_pack3 if ndim == 4 else _pack2)(*[s if d != 1 else 0 for s, d in zip(log_decay.stride(), log_decay.shape)])
     else:
-        raise ValueError(f"log_decay has shape {tuple(log_decay.shape)}, expected {(H,)} or {tuple(lead) + (H,)}")
+        raise ValueError(f"log_decay has shape {tuple(log_decay.shape)}, expected {(H,)} or {lead + (H,)}")
     return dt, lead, H, Hk, dk, dv, qs, ks, vs, gs
 
 

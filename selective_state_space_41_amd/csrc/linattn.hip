@@ -1333,12 +1333,13 @@ struct StepArgs {
   float scale;
 };
 
-// One workgroup per (sequence, head, 64 columns): 16 lanes hold 4 columns each, 16 rows at a time.
-// The state is read once and written once in 16-byte accesses, which is all the time there is to
-// it; the products are float32.
-template <typename T>
-__global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
-  __shared__ float qs[128], ks[128];
+// One workgroup per (sequence, head, 64 columns): 16 lanes hold 4 columns each, 16 rows at a time, all ROWS /
+// 16 of them on their way at once.  The state is read once and written once in 16-byte accesses, which is all
+// the time there is to it; the products are float32.
+template <typename T, int ROWS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6))) void linattn_step_kernel(StepArgs a) {
+  constexpr int kN = ROWS / 16;
+  __shared__ float qs[ROWS], ks[ROWS];
   __shared__ __align__(16) float red[4][64];
   const int64_t bh = blockIdx.x;
   const int64_t b = bh / a.heads;
@@ -1350,14 +1351,14 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
     if (threadIdx.x < 16 && n < a.dv) store_acc(out + n, zero4());
     return;
   }
-  float* s = a.state + (slot * a.heads + h) * static_cast<int64_t>(a.dk) * a.dv + n;
+  float* s = a.state + (slot * a.heads + h) * static_cast<int64_t>(a.dk) * a.dv;
   const bool mine = n < a.dv;
-  f32x4 st[8];
+  const uint32_t off = row * a.dv + n, step = 16 * a.dv;
+  f32x4 st[kN];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = i * 16 + row;
+  for (int i = 0; i < kN; ++i) {
     st[i] = zero4();
-    if (mine && d < a.dk) st[i] = *reinterpret_cast<const f32x4*>(s + static_cast<int64_t>(d) * a.dv);
+    if (mine && i * 16 + row < a.dk) st[i] = load4(s + (off + i * step));
   }
   const int hk = h / a.share;
   if (threadIdx.x < a.dk) {
@@ -1374,25 +1375,22 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepArgs a) {
   __syncthreads();
   f32x4 o = zero4();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const int d = i * 16 + row;
     if (mine && d < a.dk) {
       const f32x4 u = st[i] * decay + v * ks[d];
-      *reinterpret_cast<f32x4*>(s + static_cast<int64_t>(d) * a.dv) = u;
+      store_acc(s + (off + i * step), u);
       o += u * qs[d];
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    o[r] += __shfl_xor(o[r], 16);
-    o[r] += __shfl_xor(o[r], 32);
-  }
-  if ((threadIdx.x & 63) < 16) *reinterpret_cast<f32x4*>(&red[threadIdx.x >> 6][(threadIdx.x & 15) * 4]) = o;
+  for (int r = 0; r < 4; ++r) o[r] = sum_rows(o[r]);
+  if ((threadIdx.x & 63) < 16) store_acc(&red[threadIdx.x >> 6][(threadIdx.x & 15) * 4], o);
   __syncthreads();
   if (threadIdx.x < 16 && mine) {
     f32x4 t = zero4();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t += *reinterpret_cast<const f32x4*>(&red[i][threadIdx.x * 4]);
+    for (int i = 0; i < 4; ++i) t += load4(&red[i][threadIdx.x * 4]);
     store_acc(out + n, t * a.scale);
   }
 }
@@ -1742,10 +1740,15 @@ vmscan_status vmscan_linattn_step(const void* q, const int64_t* q_strides, const
   a.state = state, a.slots = slots, a.out = out, a.batch = batch, a.pool = pool;
   a.heads = heads, a.share = heads / kheads, a.dk = dk, a.dv = dv, a.scale = scale;
   const dim3 grid(static_cast<unsigned>(batch * heads), static_cast<unsigned>((dv + 63) / 64));
-  if (dtype == VMSCAN_F32)
-    hipLaunchKernelGGL(linattn_step_kernel<float>, grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(linattn_step_kernel<uint16_t>, grid, dim3(256), 0, stream, a);
+  auto launch = [&](auto rows) {
+    constexpr int ROWS = decltype(rows)::value;
+    if (dtype == VMSCAN_F32)
+      hipLaunchKernelGGL((linattn_step_kernel<float, ROWS>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((linattn_step_kernel<uint16_t, ROWS>), grid, dim3(256), 0, stream, a);
+  };
+  if (dk <= 64) launch(std::integral_constant<int, 64>{});
+  else launch(std::integral_constant<int, 128>{});
   return launched();
 }
 
