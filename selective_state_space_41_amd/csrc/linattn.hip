@@ -342,6 +342,7 @@ struct LinArgs {
   int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
   int slices, ld;                     // slices of the value channels; a segment state's row
   int subs, back_segments;            // the pass from the end: segments it cuts one into, and all of them
+  bool chain;                         // few segments: each walk joins the states before it itself
   float scale;
 };
 
@@ -532,6 +533,31 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
         if (d_of(t) < dk && n_of(nt) < dv) store_acc(p + (d_of(t) * ld + n_of(nt)), s[t][nt]);
+  }
+  // What enters after segments from, from + dir, .. (n of them) that each add their own state, on top of what is
+  // here: s = s 2^g + own, four segments on their way at a time.
+  __device__ __forceinline__ void join(const float* own, const float* g, int from, int dir, int n, int ld) {
+    const int64_t step = static_cast<int64_t>(DK) * ld;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      State x[4];
+      float m[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < n) {
+          const int at = from + dir * (i0 + i);
+          x[i].load(own + at * step, DK, DV, ld);
+          m[i] = g[at];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < n) {
+          const float e = __builtin_amdgcn_exp2f(m[i]);
+#pragma unroll
+          for (int t = 0; t < kDT; ++t)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) s[t][nt] = s[t][nt] * e + x[i].s[t][nt];
+        }
+    }
   }
   // into LDS as an operand, [d][n]; bfloat16 with what the rounding left in a second plane
   static constexpr int kPlane = DK * DV;
@@ -827,10 +853,13 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
   const int qt = (blockIdx.x >> 8) & 1 ? B::kWaves - 1 - wave : wave;
 
   S st;
-  if (a.segments > 1)
+  if (a.segments > 1 && !a.chain) {
     st.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * a.ld) + w.n0, DK, DV, a.ld);
-  else
+  } else {
     st.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd + w.n0 : nullptr, a.dk, dv, a.dvd);
+    if (w.seg > 0)
+      st.join(a.seg_s + w.bh * a.segments * (DK * a.ld) + w.n0, a.seg_g + w.bh * a.segments, 0, 1, w.seg, a.ld);
+  }
 
   OwnRows<T, DK> qn;  // the next block's queries
   auto load = [&](int t0) {
@@ -989,13 +1018,18 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
   Places<T, DK> wk;
   Places<T, DV> wv;
   S st, first;  // R; the state that enters the segment
-  if (a.segments > 1) {
-    const int end = (w.seg + 1) * a.subs < a.back_segments ? (w.seg + 1) * a.subs : a.back_segments;
+  const int end = (w.seg + 1) * a.subs < a.back_segments ? (w.seg + 1) * a.subs : a.back_segments;
+  if (a.segments > 1 && !a.chain) {
     st.load(a.seg_ds + (w.bh * a.back_segments + end - 1) * (DK * DV), DK, DV, DV);
     first.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
   } else {
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
     first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+    if (end < a.back_segments)
+      st.join(a.seg_ds + w.bh * a.back_segments * (DK * DV), a.seg_dg + w.bh * a.back_segments, a.back_segments - 1, -1,
+              a.back_segments - end, DV);
+    if (w.seg > 0)
+      first.join(a.seg_s + w.bh * a.segments * (DK * DV), a.seg_g + w.bh * a.segments, 0, 1, w.seg, DV);
   }
   float gx = 0.0f;
   auto skip = [&](int blocks) {
@@ -1401,10 +1435,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6))) void l
 constexpr int kMaxHeadDim = 128;
 constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // a block's offsets fit 32 bits in bytes
 // Estimates of plan(), us: a block by [gradient][float32][channels 32, 64, 128]; the segments' pass as a share
-// of the walk, its launches, and the prefix per segment, each by [gradient].
+// of the walk and its launches by [gradient]; the join, by a launch and per segment, or per MB read.
 constexpr double kBlockUs[2][2][3] = {{{2.2, 2.9, 4.6}, {4.2, 5.5, 9.0}}, {{0.0, 8.0, 13.0}, {0.0, 14.0, 24.0}}};
-constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {6.0, 8.0}, kSegmentUs[2] = {0.2, 0.4};
-constexpr int64_t kBackWalks = 512;     // workgroups wanted in the gradient's pass from the end
+constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {3.0, 5.0}, kJoinUs = 3.0, kSegmentUs = 0.2, kMbUs = 0.1;
+// Measured, us, joined by the walks / by a launch: 12 MB 14.2 / 18.0 (1 x 1000 tokens, 6 heads of 64 x 64, 16
+// segments), 49 MB 29.1 / 31.9 (1 x 6085, 32 segments), 77 MB 106 / 101 (8 x 6085, 6 of 128 x 64, 10 segments).
+constexpr double kChainMb = 64.0;
+constexpr int64_t kBackWalks = 512;     // workgroups wanted in the gradient's pass from the end ..
+constexpr int kBackSegments = 12;       // .. as long as no more than so many segments have to be joined
 constexpr int kMaxSegments = 64;
 constexpr int kSlice = 32;              // value channels of the narrowest workgroup
 
@@ -1414,6 +1452,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct Plan {
   int blocks, segments, per, width, slices;
   int subs, back_segments;
+  bool chain;
 };
 // Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
 int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
@@ -1432,10 +1471,10 @@ int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
 // a prefix over the segments).  Of all cuts the one with the least estimated time is taken: rounds of workgroups
 // times blocks, a block's time as measured where one workgroup has a CU for itself.  Measured, us, cut as taken
 // / whole: 8 x 6085 tokens, 6 heads of 128 x 64, bfloat16: 101 (10 segments) / over 500; 1 x 6085, 6 of 64 x 64:
-// 32 (32 segments, halves of the channels) / 282; 1 x 197, 6 of 64 x 64: bfloat16 11.4 (halves) / 14.2, float32 16.1
+// 32 (32 segments, halves of the channels) / 282; 1 x 197, 6 of 64 x 64: bfloat16 11.4 (halves) / 14.2, float32 13.0
 // (halves, 4 segments) / 26.8; 128 x 197, 6 of 64 x 64: 24.6 (whole) / 50 in 2 segments, 30 in halves.
 // The gradient needs all channels of a token together and is only cut into segments: 32 x 3136, 8 of 64 x 64:
-// 481 (2 segments) / 649; 1 x 197, 6 of 64 x 64: 29 (4 segments) / 43.
+// 475 (2 segments) / 649; 1 x 197, 6 of 64 x 64: 24 (4 segments) / 43.
 Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
   Plan best{};
   double least = 0.0;
@@ -1451,10 +1490,13 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
       if ((blocks + per - 1) / per != seg) continue;
       const double rounds = static_cast<double>((walks * seg + slots - 1) / slots);
       double time = rounds * (per + 1) * block;  // a block's time to start and end
-      if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + kSegmentUs[back] * seg;
+      // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
+      const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_dim(dk) * width * 4 * (back ? 2 : 1);
+      const bool chain = seg > 1 && mb < kChainMb;
+      if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + (chain ? kMbUs * mb : (kJoinUs + kSegmentUs * seg) * (back ? 2 : 1));
       if (best.blocks == 0 || time < least) {
         least = time;
-        best = Plan{blocks, seg, per, width, slices, 1, seg};
+        best = Plan{blocks, seg, per, width, slices, 1, seg, chain};
       }
     }
   }
@@ -1463,7 +1505,9 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
   if (back && best.segments > 1) {
     const int64_t walks = batch * heads * (best.segments - 1);
     int64_t subs = (kBackWalks + walks - 1) / walks;
+    if (subs > kBackSegments / best.segments) subs = kBackSegments / best.segments;
     if (subs > best.per) subs = best.per;
+    if (subs < 1) subs = 1;
     const int part = static_cast<int>((best.per + subs - 1) / subs);
     best.subs = (best.per + part - 1) / part;
     best.per = best.subs * part;
@@ -1556,7 +1600,7 @@ void launch_segments(const LinArgs& a, int width, hipStream_t stream) {
     hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK, KEEP>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream,
                        a);
     const int64_t n = a.batch * a.heads * (DK * a.ld / 4);
-    if (a.segments > 1)
+    if (a.segments > 1 && !a.chain)
       hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
                          stream, a, DK);
   });
@@ -1636,6 +1680,7 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.blocks = y.p.blocks, a.segments = y.p.segments, a.per_segment = y.p.per;
   a.slices = y.p.slices, a.ld = y.p.slices * y.p.width;
   a.subs = y.p.subs, a.back_segments = y.p.back_segments;
+  a.chain = y.p.chain;
   a.seg_s = reinterpret_cast<float*>(ws + y.seg_s);
   a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
   a.seg_g = reinterpret_cast<float*>(ws + y.seg_g);
