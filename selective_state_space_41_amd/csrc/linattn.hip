@@ -258,6 +258,23 @@ __device__ __forceinline__ void split(const float (&x)[8], Frag32 (&f)[1]) { pac
 template <typename T>
 constexpr int kPieces = sizeof(T) == 2 ? 3 : 1;
 
+// Eight scores as an operand in two parts, the rounded ones and what the rounding left: one part alone would
+// add as much error to a bfloat16 output as its own rounding does, and all of a token's channels would have the
+// same one.
+__device__ __forceinline__ void pack_parts(const float (&x)[8], bf16x8 (&f)[2]) {
+  uint32_t h[4], r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = pack2(x[2 * e], x[2 * e + 1]);
+    r[e] = pack2(x[2 * e] - __uint_as_float(h[e] << 16), x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+  }
+  f[0] = __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
+  f[1] = __builtin_bit_cast(bf16x8, make_uint4(r[0], r[1], r[2], r[3]));
+}
+__device__ __forceinline__ void pack_parts(const float (&x)[8], Frag32 (&f)[1]) { pack(x, f[0]); }
+template <typename T>
+constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
+
 // Sums and scans over the 16 lanes of a row with lane-rotating adds, over the 4 rows (g) of a wave
 // with row swaps: no LDS round trips.
 template <int CTRL>
@@ -946,10 +963,14 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
             for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
           }
         }
-        Frag<T> pf;
-        pack(p, pf);
+        Frag<T> pf[kParts<T>];
+        pack_parts(p, pf);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt] = mma(xa[nt], pf, acc[nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const Frag<T> x = xa[nt];
+#pragma unroll
+          for (int i = 0; i < kParts<T>; ++i) acc[nt] = mma(x, pf[i], acc[nt]);
+        }
       }
       float m[8];
       eight(d.toC + kk * 32, m);
@@ -1134,10 +1155,14 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
             for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
           }
         }
-        Frag<T> pf;
-        pack(p, pf);
+        Frag<T> pf[kParts<T>];
+        pack_parts(p, pf);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc[dt] = mma(frag_col<DK>(wk, ks, jj * 32, dt * 16), pf, acc[dt]);
+        for (int dt = 0; dt < DT; ++dt) {
+          const Frag<T> x = frag_col<DK>(wk, ks, jj * 32, dt * 16);
+#pragma unroll
+          for (int i = 0; i < kParts<T>; ++i) acc[dt] = mma(x, pf[i], acc[dt]);
+        }
       }
       if (t0 + i < w.live) {
 #pragma unroll
@@ -1247,13 +1272,21 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
             for (int r = 0; r < 4; ++r) p[t * 4 + r] = x[t * 4 + r] = 0.0f;
           }
         }
-        Frag<T> pf, xf;
-        pack(p, pf);
-        pack(x, xf);
+        Frag<T> pf[kParts<T>], xf[kParts<T>];
+        pack_parts(p, pf);
+        pack_parts(x, xf);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) av[nt] = mma(xa[nt], pf, av[nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const Frag<T> f = xa[nt];
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) ak[dt] = mma(frag_col<DK>(wk, qs, kk * 32, dt * 16), xf, ak[dt]);
+          for (int i = 0; i < kParts<T>; ++i) av[nt] = mma(f, pf[i], av[nt]);
+        }
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const Frag<T> f = frag_col<DK>(wk, qs, kk * 32, dt * 16);
+#pragma unroll
+          for (int i = 0; i < kParts<T>; ++i) ak[dt] = mma(f, xf[i], ak[dt]);
+        }
       }
       float m[8];
       eight(d.from0 + kk * 32, m);
