@@ -358,7 +358,7 @@ struct LinArgs {
   int seqlen, heads, share, dk, dvd;  // share: heads per query/key head
   int blocks, segments, per_segment;  // blocks of C tokens; segments; blocks per segment
   int slices, ld;                     // slices of the value channels; a segment state's row
-  int subs, back_segments;            // the pass from the end: segments it cuts one into, and all of them
+  int subs, parts, per_part;          // the gradient's passes: parts of a segment, all of them, blocks of one
   bool chain;                         // few segments: each walk joins the states before it itself
   float scale;
 };
@@ -681,9 +681,9 @@ struct Where {  // this workgroup's place
 // Workgroup i runs on XCD i % 8.  An XCD takes consecutive places: the slices of the value channels and the
 // heads that share q and k, which then find them in its L2, then a sequence's segments.
 template <typename B>
-__device__ __forceinline__ Where where(const LinArgs& a, int width) {
+__device__ __forceinline__ Where where(const LinArgs& a, int width, uint32_t id0, uint32_t n) {
   constexpr int C = B::kC;
-  const uint32_t n = gridDim.x, q = n >> 3, r = n & 7, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  const uint32_t q = n >> 3, r = n & 7, xcd = id0 & 7, local = id0 >> 3;
   uint32_t id = (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + local;
   Where w;
   w.n0 = static_cast<int>(id % a.slices) * width;
@@ -732,16 +732,13 @@ __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p
 // A segment's own state from a zero start: forward (k, v) or, BACK, the state's gradient (q, dout)
 // from a zero end.  KEEP also writes the state before each block.
 
-template <typename T, int DK, int DV, bool BACK, bool KEEP>
-__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
+template <typename T, int DK, int DV, bool BACK, bool KEEP, int C = BlockOf<T, DK, DV>::kC>
+__device__ __forceinline__ void segment_walk(const LinArgs& a, uint32_t id, uint32_t n_ids, T* ys, T* xs,
+                                             Decays<C>* decays) {
   using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
-  constexpr int C = B::kC;
-  __shared__ __align__(16) T ys[C * DK];
-  __shared__ __align__(16) T xs[C * DV];
-  __shared__ __align__(16) Decays<C> decays[2];
-  const Where w = where<B>(a, DV);
-  if (!KEEP && (BACK ? w.seg < a.subs : w.seg == a.segments - 1)) return;  // no segment lies past it
+  const Where w = where<B>(a, DV, id, n_ids);
+  if (BACK ? w.seg < a.subs : !KEEP && w.seg == a.segments - 1) return;  // no segment lies past it
   Stream<T, DK, B> y(BACK ? a.q : a.k, w.b, w.h / a.share, 0);
   Stream<T, DV, B> x(BACK ? a.dout : a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
@@ -803,6 +800,30 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) voi
   if (w.n0 == 0 && threadIdx.x == 0) (BACK ? a.seg_dg : a.seg_g)[w.bh * a.segments + w.seg] = total;
 }
 
+template <typename T, int DK, int DV, bool BACK, bool KEEP>
+__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_segment_kernel(LinArgs a) {
+  constexpr int C = BlockOf<T, DK, DV>::kC;
+  __shared__ __align__(16) T ys[C * DK];
+  __shared__ __align__(16) T xs[C * DV];
+  __shared__ __align__(16) Decays<C> decays[2];
+  segment_walk<T, DK, DV, BACK, KEEP>(a, blockIdx.x, gridDim.x, ys, xs, decays);
+}
+
+// The gradient's two passes, which do not depend on each other, in one launch: the first half of the
+// workgroups walks from the end.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_passes_kernel(LinArgs a) {
+  constexpr int C = BlockOf<T, DK, DV>::kC;
+  __shared__ __align__(16) T ys[C * DK];
+  __shared__ __align__(16) T xs[C * DV];
+  __shared__ __align__(16) Decays<C> decays[2];
+  const uint32_t half = gridDim.x / 2;
+  if (blockIdx.x < half)
+    segment_walk<T, DK, DV, true, false>(a, blockIdx.x, half, ys, xs, decays);
+  else
+    segment_walk<T, DK, DV, false, true>(a, blockIdx.x - half, half, ys, xs, decays);
+}
+
 // In place: each segment's own state becomes the state that enters it (BACK: the gradient at its
 // end).  A thread owns 4 elements of one (sequence, head) and has 8 segments on their way at a time.
 template <bool BACK>
@@ -855,7 +876,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
   __shared__ __align__(16) T vs[C * DV];
   __shared__ __align__(16) T ss[S::kPlanes * S::kPlane];
   __shared__ __align__(16) Decays<C> decays[2];
-  const Where w = where<B>(a, DV);
+  const Where w = where<B>(a, DV, blockIdx.x, gridDim.x);
   Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
   Stream<T, DV, B> v(a.v, w.b, w.h, w.n0);
   const int dv = a.dvd - w.n0;
@@ -1027,7 +1048,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
   __shared__ __align__(16) Decays<C> decays[2];
   __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
   T* const rs = kBoth ? ss + kStateLds : ss;
-  const Where w = where<B>(a, DV);
+  const Where w = where<B>(a, DV, blockIdx.x, gridDim.x);
   Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
   Stream<T, DV, B> v(a.v, w.b, w.h, 0), o(a.dout, w.b, w.h, 0);
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
@@ -1038,20 +1059,23 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
 
   Places<T, DK> wk;
   Places<T, DV> wv;
-  S st, first;  // R; the state that enters the segment
-  const int end = (w.seg + 1) * a.subs < a.back_segments ? (w.seg + 1) * a.subs : a.back_segments;
-  if (a.segments > 1 && !a.chain) {
-    st.load(a.seg_ds + (w.bh * a.back_segments + end - 1) * (DK * DV), DK, DV, DV);
-    first.load(a.seg_s + (w.bh * a.segments + w.seg) * (DK * DV), DK, DV, DV);
+  S st, first;  // R; the state that enters the part of the segment
+  const int end = (w.seg + 1) * a.subs < a.parts ? (w.seg + 1) * a.subs : a.parts;
+  const int64_t part0 = w.bh * a.parts;
+  if (a.parts > 1 && !a.chain) {
+    st.load(a.seg_ds + (part0 + end - 1) * (DK * DV), DK, DV, DV);
   } else {
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-    first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-    if (end < a.back_segments)
-      st.join(a.seg_ds + w.bh * a.back_segments * (DK * DV), a.seg_dg + w.bh * a.back_segments, a.back_segments - 1, -1,
-              a.back_segments - end, DV);
-    if (w.seg > 0)
-      first.join(a.seg_s + w.bh * a.segments * (DK * DV), a.seg_g + w.bh * a.segments, 0, 1, w.seg, DV);
+    if (end < a.parts) st.join(a.seg_ds + part0 * (DK * DV), a.seg_dg + part0, a.parts - 1, -1, a.parts - end, DV);
   }
+  auto enter = [&](int part) {  // first: the state that enters a part
+    if (a.parts > 1 && !a.chain) {
+      first.load(a.seg_s + (part0 + part) * (DK * DV), DK, DV, DV);
+    } else {
+      first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
+      if (part > 0) first.join(a.seg_s + part0 * (DK * DV), a.seg_g + part0, 0, 1, part, DV);
+    }
+  };
   float gx = 0.0f;
   auto skip = [&](int blocks) {
     q.skip(blocks);
@@ -1066,6 +1090,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
     o.load(w.live - t0, a.dvd);
   };
   if (w.c0 < w.c1) {
+    enter((w.c1 - 1) / a.per_part);
     skip(w.c1 - 1);
     load((w.c1 - 1) * C);
     if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), decays[(w.c1 - 1) & 1]);
@@ -1077,6 +1102,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
     wk.here();
     wv.here();
     const int64_t block = w.bh * a.blocks + c;
+    if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1) enter(c / a.per_part);
     S old;  // the state that enters the block
     old.load(a.states + block * (DK * DV), DK, DV, DV);
     const float since = __builtin_amdgcn_exp2f(a.block_g[block]);
@@ -1474,8 +1500,8 @@ constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {3.0, 5.0}, kJoinUs =
 // Measured, us, joined by the walks / by a launch: 12 MB 14.2 / 18.0 (1 x 1000 tokens, 6 heads of 64 x 64, 16
 // segments), 49 MB 29.1 / 31.9 (1 x 6085, 32 segments), 77 MB 106 / 101 (8 x 6085, 6 of 128 x 64, 10 segments).
 constexpr double kChainMb = 64.0;
-constexpr int64_t kBackWalks = 512;     // workgroups wanted in the gradient's pass from the end ..
-constexpr int kBackSegments = 12;       // .. as long as no more than so many segments have to be joined
+constexpr int64_t kPassWalks = 1024;    // workgroups wanted in each of the gradient's passes ..
+constexpr int kMaxParts = 12;           // .. as long as no more than so many parts have to be joined
 constexpr int kMaxSegments = 64;
 constexpr int kSlice = 32;              // value channels of the narrowest workgroup
 
@@ -1484,7 +1510,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Plan {
   int blocks, segments, per, width, slices;
-  int subs, back_segments;
+  int subs, parts;
   bool chain;
 };
 // Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
@@ -1533,20 +1559,20 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
       }
     }
   }
-  // The pass from the end leaves out the first segment, so with few segments it has few workgroups: it cuts
-  // each further.
+  // The gradient's passes are light and need more workgroups than its walk to fill the chip: they cut each
+  // segment into parts.
   if (back && best.segments > 1) {
-    const int64_t walks = batch * heads * (best.segments - 1);
-    int64_t subs = (kBackWalks + walks - 1) / walks;
-    if (subs > kBackSegments / best.segments) subs = kBackSegments / best.segments;
+    const int64_t walks = batch * heads * best.segments;
+    int64_t subs = (kPassWalks + walks - 1) / walks;
+    if (subs > kMaxParts / best.segments) subs = kMaxParts / best.segments;
     if (subs > best.per) subs = best.per;
     if (subs < 1) subs = 1;
     const int part = static_cast<int>((best.per + subs - 1) / subs);
     best.subs = (best.per + part - 1) / part;
     best.per = best.subs * part;
     best.segments = (best.blocks + best.per - 1) / best.per;
-    best.back_segments = (best.blocks + part - 1) / part;
-    if (best.segments == 1) best.subs = best.back_segments = 1;
+    best.parts = (best.blocks + part - 1) / part;
+    if (best.segments == 1) best.subs = best.parts = 1;
   }
   return best;
 }
@@ -1578,11 +1604,11 @@ Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int 
     return was;
   };
   if (y.p.segments > 1) {
-    y.seg_s = take(bh * y.p.segments * state);
-    y.seg_g = take(bh * y.p.segments * 4);
+    y.seg_s = take(bh * y.p.parts * state);
+    y.seg_g = take(bh * y.p.parts * 4);
     if (back) {
-      y.seg_ds = take(bh * y.p.back_segments * state);
-      y.seg_dg = take(bh * y.p.back_segments * 4);
+      y.seg_ds = take(bh * y.p.parts * state);
+      y.seg_dg = take(bh * y.p.parts * 4);
     }
   }
   if (back) {
@@ -1626,24 +1652,23 @@ void with_dims(int dk, int width, F&& f) {
 
 dim3 walks(const LinArgs& a) { return dim3(static_cast<unsigned>(a.batch * a.heads * a.segments * a.slices)); }
 
-template <typename T, bool BACK, bool KEEP>
-void launch_segments(const LinArgs& a, int width, hipStream_t stream) {
-  with_dims(a.dk, width, [&](auto dk, auto dv) {
-    constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-    hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, BACK, KEEP>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream,
-                       a);
-    const int64_t n = a.batch * a.heads * (DK * a.ld / 4);
-    if (a.segments > 1 && !a.chain)
-      hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
-                         stream, a, DK);
-  });
+// The sums over the segments, where the walks do not make them themselves.
+template <bool BACK>
+void launch_prefix(const LinArgs& a, int dk, hipStream_t stream) {
+  if (a.segments == 1 || a.chain) return;
+  const int64_t n = a.batch * a.heads * (dk * a.ld / 4);
+  hipLaunchKernelGGL((linattn_prefix_kernel<BACK>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a,
+                     dk);
 }
 
 template <typename T>
 vmscan_status run_fwd(const LinArgs& a, int width, hipStream_t stream) {
-  if (a.segments > 1) launch_segments<T, false, false>(a, width, stream);
   with_dims(a.dk, width, [&](auto dk, auto dv) {
     constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+    if (a.segments > 1)
+      hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false, false>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads),
+                         0, stream, a);
+    launch_prefix<false>(a, DK, stream);
     hipLaunchKernelGGL((linattn_fwd_kernel<T, DK, DV>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream, a);
   });
   return launched();
@@ -1656,16 +1681,20 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   a.dq = shared ? ws + y.dq : dq;
   a.dk_out = shared ? ws + y.dk : dk;
   a.dg = per_head ? reinterpret_cast<float*>(ws + y.dg) : dg;
-  launch_segments<T, false, true>(a, y.p.width, stream);
-  if (a.segments > 1) {
-    LinArgs b = a;
-    b.segments = a.back_segments, b.per_segment = a.per_segment / a.subs;
-    launch_segments<T, true, false>(b, y.p.width, stream);
-  }
+  LinArgs b = a;  // the passes, whose segments are the parts
+  b.segments = a.parts, b.per_segment = a.per_part;
   with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
     if constexpr (DV >= 64) {
-      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream, a);
+      const dim3 block(BlockOf<T, DK, DV>::kThreads);
+      if (a.segments > 1) {
+        hipLaunchKernelGGL((linattn_passes_kernel<T, DK, DV>), dim3(2 * walks(b).x), block, 0, stream, b);
+        launch_prefix<false>(b, DK, stream);
+        launch_prefix<true>(b, DK, stream);
+      } else {
+        hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false, true>), walks(a), block, 0, stream, a);
+      }
+      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), walks(a), block, 0, stream, a);
     }
   });
   const int64_t tokens = a.batch * a.seqlen;
@@ -1712,7 +1741,7 @@ vmscan_status common_args(LinArgs& a, const void* q, const int64_t* qs, const vo
 void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.blocks = y.p.blocks, a.segments = y.p.segments, a.per_segment = y.p.per;
   a.slices = y.p.slices, a.ld = y.p.slices * y.p.width;
-  a.subs = y.p.subs, a.back_segments = y.p.back_segments;
+  a.subs = y.p.subs, a.parts = y.p.parts, a.per_part = a.per_segment / a.subs;
   a.chain = y.p.chain;
   a.seg_s = reinterpret_cast<float*>(ws + y.seg_s);
   a.seg_ds = reinterpret_cast<float*>(ws + y.seg_ds);
@@ -1723,7 +1752,7 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
 }
 
 vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
-  if (a.batch * a.heads * p.back_segments * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+  if (a.batch * a.heads * 2 * p.parts * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
   if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
   return need && (!ws || have < need) ? VMSCAN_ERR_WORKSPACE : VMSCAN_OK;
 }
