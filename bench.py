@@ -681,6 +681,31 @@ def bench_ss2d_bwd(cfg_id, steps, warmup, torch, V, with_cpu=False, d_state=None
     return rec
 
 
+def bench_operators(names, steps, warmup, torch):
+    """One line per case of the linear-attention block's operators (perf/operators.py): a user's call of
+    the library, inputs rotated over three sets, with the bytes and operations the case cannot do without."""
+    import perf.operators as P
+    P.own = True
+    for case in P.listed():
+        if names and case["name"] not in names:
+            continue
+        sets = [P.prepare(case, seed) for seed in range(3)]
+        for i in range(max(3, warmup)):
+            P.run(sets[i % 3])
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for i in range(steps):
+            P.run(sets[i % 3])
+        torch.cuda.synchronize()
+        s = (time.perf_counter() - t0) / steps
+        w = P.work(case)
+        print(json.dumps({"metric": "operator pass", "value": s * 1e6, "unit": "us", "n_gpus": 1, "steps": steps,
+                          "warmup": warmup, "higher_is_better": False, "dtype": case["x"], "data": "synthetic",
+                          "config": case, "hbm_gbs": w["bytes"] / s / 1e9, "tflops": w["flops"] / s / 1e12}), flush=True)
+        del sets
+        torch.cuda.empty_cache()
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -695,6 +720,8 @@ def main():
                     help="time the front convolution (conv1d / conv2d + SiLU) followed by the scan")
     ap.add_argument("--lane-scan", action="store_true",
                     help="Vim workloads through the lane-scan path (associative scan over positions, no chunk pass)")
+    ap.add_argument("--operators", nargs="?", const="all", metavar="NAME[,NAME]",
+                    help="time the linear-attention block's operators, all cases or the named ones")
     ap.add_argument("--d-state", type=int, default=None, choices=(16, 32),
                     help="state size of the workloads, forward or backward (default: the workload's own, 16)")
     ap.add_argument("--calibrate-copy", action="store_true",
@@ -738,6 +765,9 @@ def main():
         torch.cuda.synchronize()
         print(json.dumps({"calibration": "copy", "bytes_read_per_dispatch": n * 4, "bytes_written_per_dispatch": n * 4,
                           "dispatches": max(1, args.steps)}), flush=True)
+        return
+    if args.operators:
+        bench_operators(None if args.operators == "all" else args.operators.split(","), args.steps, args.warmup, torch)
         return
     import selective_state_space_41_amd as V
     cfgs = [0, 1, 2, 3, 4] if args.all else [args.config]

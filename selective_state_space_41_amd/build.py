@@ -54,6 +54,13 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("bwd_ckpt_kernel", 6),
     ("adj_state_kernel", 6),
     ("lane_scan_kernel", 2),
+    # linear attention, bfloat16 heads up to 64 x 64: what LDS leaves room for (planning counts on it)
+    ("linattn_fwd_kernelItLi64ELi64E", 3),
+    ("linattn_fwd_kernelItLi128ELi64E", 2),
+    ("linattn_segment_kernelItLi64ELi64E", 4),
+    ("linattn_passes_kernelItLi64ELi64E", 4),
+    ("linattn_grad_kernelItLi64ELi64E", 2),
+    ("linattn_step_kernel", 6),
 ]
 SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64)]  # bytes per lane
 
