@@ -527,8 +527,10 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
 template <typename T, int DK, int DV>
 struct State {
   using B = BlockOf<T, DK, DV>;
-  static constexpr int kDT = DK / 16 / B::kWaves;
+  static constexpr int kDT = DK / 16 < B::kWaves ? 1 : DK / 16 / B::kWaves;
   static constexpr int kNT = DV / 16;
+  // DK 32: two waves hold the state, the others have none of it
+  __device__ __forceinline__ static bool mine() { return DK / 16 >= B::kWaves || wave_id() < DK / 16; }
   f32x4 s[kDT][kNT];
 
   __device__ __forceinline__ static int d_of(int t) { return (wave_id() * kDT + t) * 16 + (threadIdx.x & 15); }
@@ -580,6 +582,7 @@ struct State {
   static constexpr int kPlane = DK * DV;
   static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
   __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p) const {
+    if (!mine()) return;
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
@@ -608,6 +611,7 @@ struct State {
   // w: the weights, both in frag_col's order.
   __device__ __forceinline__ void add(const Places<T, DK>& wk, const T* y, int row0, const Cols<T, DV>& xa,
                                       const float (&w)[8]) {
+    if (!mine()) return;
 #pragma unroll
     for (int t = 0; t < kDT; ++t) {
       const Frag<T> f = frag_col<DK>(wk, y, row0, (wave_id() * kDT + t) * 16);
@@ -632,30 +636,32 @@ struct State {
     float part[B::kWaves];
 #pragma unroll
     for (int jt = 0; jt < B::kWaves; ++jt) part[jt] = 0.0f;
+    if (mine()) {
 #pragma unroll
-    for (int t = 0; t < kDT; ++t) {
-      f32x4 acc[B::kWaves];
+      for (int t = 0; t < kDT; ++t) {
+        f32x4 acc[B::kWaves];
 #pragma unroll
-      for (int jt = 0; jt < B::kWaves; ++jt) acc[jt] = zero4();
+        for (int jt = 0; jt < B::kWaves; ++jt) acc[jt] = zero4();
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) {
-        float m[8];
+        for (int kk = 0; kk < DV / 32; ++kk) {
+          float m[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = s[t][2 * kk + (e >> 2)][e & 3];
-        Frag<T> piece[kPieces<T>];
-        split(m, piece);
+          for (int e = 0; e < 8; ++e) m[e] = s[t][2 * kk + (e >> 2)][e & 3];
+          Frag<T> piece[kPieces<T>];
+          split(m, piece);
+#pragma unroll
+          for (int jt = 0; jt < B::kWaves; ++jt) {
+            const Frag<T> xb = frag_row_perm<DV>(wv, x, jt * 16, kk * 32);
+#pragma unroll
+            for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(piece[i], xb, acc[jt]);
+          }
+        }
 #pragma unroll
         for (int jt = 0; jt < B::kWaves; ++jt) {
-          const Frag<T> xb = frag_row_perm<DV>(wv, x, jt * 16, kk * 32);
+          const f32x4 y = y4(t, jt);
 #pragma unroll
-          for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(piece[i], xb, acc[jt]);
+          for (int r = 0; r < 4; ++r) part[jt] = __builtin_fmaf(acc[jt][r], y[r], part[jt]);
         }
-      }
-#pragma unroll
-      for (int jt = 0; jt < B::kWaves; ++jt) {
-        const f32x4 y = y4(t, jt);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) part[jt] = __builtin_fmaf(acc[jt][r], y[r], part[jt]);
       }
     }
 #pragma unroll
@@ -1378,8 +1384,11 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
 // dq and dk of a shared head: the sum over the heads that read it, rounded once.  `in` is [tokens]
 // [heads][dim] float32, `out` [tokens][heads / share][dim]; a thread takes 4 channels.
 template <typename T>
-__global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restrict__ in, T* __restrict__ out,
+__global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restrict__ in_q, T* __restrict__ out_q,
+                                                            const float* __restrict__ in_k, T* __restrict__ out_k,
                                                             int64_t tokens, int heads, int share, int dim) {
+  const float* in = blockIdx.y ? in_k : in_q;
+  T* out = blockIdx.y ? out_k : out_q;
   const int runs = dim / 4, per = heads / share * runs;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t t = id / per;
@@ -1392,8 +1401,9 @@ __global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restr
 }
 
 // The gradient of a decay that all tokens of a head share: kDecayParts partial sums of dg, then
-// their sum, each in a fixed order.
+// their sum, each in a fixed order; few tokens in one go.
 constexpr int kDecayParts = 64;
+constexpr int64_t kDecayTokens = 4096;  // up to here one launch sums them
 __global__ __launch_bounds__(256) void linattn_decay_kernel(const float* __restrict__ in, float* __restrict__ out,
                                                             int64_t n, int heads) {
   __shared__ float s[256];
@@ -1505,7 +1515,8 @@ constexpr int kMaxParts = 12;           // .. as long as no more than so many pa
 constexpr int kMaxSegments = 64;
 constexpr int kSlice = 32;              // value channels of the narrowest workgroup
 
-int pad_dim(int d) { return d <= 64 ? 64 : 128; }
+int pad_key(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+int pad_value(int d) { return d <= 64 ? 64 : 128; }
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct Plan {
@@ -1515,7 +1526,7 @@ struct Plan {
 };
 // Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
 int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
-  const int wide = (pad_dim(dk) == 128) + (width == 128);
+  const int wide = (pad_key(dk) == 128) + (width == 128);
   int per_cu;
   if (back)
     per_cu = wide == 0 ? 2 : 1;
@@ -1538,8 +1549,8 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
   Plan best{};
   double least = 0.0;
   const bool f32 = dtype == VMSCAN_F32;
-  for (int width = pad_dim(dv); width >= (back ? pad_dim(dv) : kSlice); width /= 2) {
-    const int C = 16 * waves_of(f32 ? 4 : 2, pad_dim(dk), width);
+  for (int width = pad_value(dv); width >= (back ? pad_value(dv) : kSlice); width /= 2) {
+    const int C = 16 * waves_of(f32 ? 4 : 2, pad_key(dk), width);
     const int blocks = static_cast<int>((seqlen + C - 1) / C);
     const int slices = (dv + width - 1) / width;
     const int64_t walks = batch * heads * slices, slots = slots_for(dtype, dk, width, back);
@@ -1550,9 +1561,9 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
       const double rounds = static_cast<double>((walks * seg + slots - 1) / slots);
       double time = rounds * (per + 1) * block;  // a block's time to start and end
       // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
-      const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_dim(dk) * width * 4 * (back ? 2 : 1);
+      const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_key(dk) * width * 4;
       const bool chain = seg > 1 && mb < kChainMb;
-      if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + (chain ? kMbUs * mb : (kJoinUs + kSegmentUs * seg) * (back ? 2 : 1));
+      if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + (back ? 2 : 1) * (chain ? kMbUs * mb : kJoinUs + kSegmentUs * seg);
       if (best.blocks == 0 || time < least) {
         least = time;
         best = Plan{blocks, seg, per, width, slices, 1, seg, chain};
@@ -1596,7 +1607,7 @@ Layout layout(int64_t batch, int64_t seqlen, int heads, int kheads, int dk, int 
   Layout y{};
   y.p = plan(batch, seqlen, heads, dk, dv, dtype, back);
   const size_t bh = static_cast<size_t>(batch) * heads;
-  const size_t state = static_cast<size_t>(pad_dim(dk)) * y.p.slices * y.p.width * 4;
+  const size_t state = static_cast<size_t>(pad_key(dk)) * y.p.slices * y.p.width * 4;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t was = at;
@@ -1646,7 +1657,8 @@ void with_dims(int dk, int width, F&& f) {
   integral_constant<int, 32> t;
   integral_constant<int, 64> s;
   integral_constant<int, 128> b;
-  if (dk <= 64) width == 32 ? f(s, t) : width == 64 ? f(s, s) : f(s, b);
+  if (dk <= 32) width == 32 ? f(t, t) : width == 64 ? f(t, s) : f(t, b);
+  else if (dk <= 64) width == 32 ? f(s, t) : width == 64 ? f(s, s) : f(s, b);
   else width == 32 ? f(b, t) : width == 64 ? f(b, s) : f(b, b);
 }
 
@@ -1700,13 +1712,13 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   const int64_t tokens = a.batch * a.seqlen;
   if (shared) {
     const int64_t n = tokens * (a.heads / a.share) * (a.dk / 4);
-    const dim3 sgrid(static_cast<unsigned>((n + 255) / 256));
-    hipLaunchKernelGGL(linattn_share_kernel<T>, sgrid, dim3(256), 0, stream, static_cast<const float*>(a.dq),
-                       static_cast<T*>(dq), tokens, a.heads, a.share, a.dk);
-    hipLaunchKernelGGL(linattn_share_kernel<T>, sgrid, dim3(256), 0, stream, static_cast<const float*>(a.dk_out),
+    hipLaunchKernelGGL(linattn_share_kernel<T>, dim3(static_cast<unsigned>((n + 255) / 256), 2), dim3(256), 0, stream,
+                       static_cast<const float*>(a.dq), static_cast<T*>(dq), static_cast<const float*>(a.dk_out),
                        static_cast<T*>(dk), tokens, a.heads, a.share, a.dk);
   }
-  if (per_head) {
+  if (per_head && tokens <= kDecayTokens) {
+    hipLaunchKernelGGL(linattn_decay_kernel, dim3(a.heads, 1), dim3(256), 0, stream, a.dg, dg, tokens, a.heads);
+  } else if (per_head) {
     float* parts = reinterpret_cast<float*>(ws + y.parts);
     hipLaunchKernelGGL(linattn_decay_kernel, dim3(a.heads, kDecayParts), dim3(256), 0, stream, a.dg, parts, tokens,
                        a.heads);
