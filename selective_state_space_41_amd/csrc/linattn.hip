@@ -19,14 +19,18 @@
 // contracted index may be taken in any order as long as both operands agree, so a result (a tile of
 // the masked scores) becomes an operand of the next product in the register it is in, in the order
 // 16 t + 4 (lane / 16) + r; the other operand, whose contracted index is the token, is read from
-// the row-major tile with the transposing LDS read, which gives that order.  Tiles: Q, K, V
-// [token][channel], the state [dk][dv].  The float32 path has the same structure with the
-// 16 x 16 x 4 float32 instruction, eight per product, and plain LDS reads.
+// the row-major tile with the transposing LDS read, which gives that order.  Tiles in LDS: K, V (in
+// the gradient also Q, dO) [token][channel], the state [dk][dv]; the forward's queries, which only one
+// wave reads, go from global memory straight to operands.  The float32 path has the same structure with
+// the 16 x 16 x 4 float32 instruction, eight per product, and plain LDS reads.
 //
-// Rounding for bfloat16 activations: scores, their gradients and the state are rounded to bfloat16
-// where they enter a product whose result is rounded to bfloat16 anyway (o, dq, dk, dv).  What ends
-// in float32 (the states, their gradients, the decays' gradient) keeps 16 bits of mantissa: the
-// operand that would be rounded is split in two bfloat16 numbers and multiplied twice.
+// Rounding for bfloat16 activations.  Accumulators and carried states are float32.  Where the state, the
+// scores or their gradients enter a product whose result is rounded to bfloat16 (o, dq, dk, dv), they
+// are two bfloat16 numbers, the rounded value and what the rounding left (16 bits): with one alone o's
+// error was 1.5 times its own rounding's.  Where the result stays float32 (the states, their gradients,
+// the decays' gradient), the operand that is not a plain activation is three bfloat16 numbers, which
+// hold all of its 24 bits: with two the decays' gradient was off by 2.6e-6 of its largest value, with
+// three by under 5e-7.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -218,19 +222,11 @@ struct Cols {
   }
 };
 
-// Two result tiles (rows 16 t + 4 g + r) as an operand in frag_col's order.
-__device__ __forceinline__ uint32_t pack2(float a, float b) {  // two roundings to nearest, one instruction
+// two roundings to nearest, one instruction
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-}
-__device__ __forceinline__ void pack(const float (&x)[8], bf16x8& f) {
-  const uint4 w = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-  f = __builtin_bit_cast(bf16x8, w);
-}
-__device__ __forceinline__ void pack(const float (&x)[8], Frag32& f) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = x[e];
 }
 __device__ __forceinline__ float elem(const bf16x8& f, int e) { return static_cast<float>(f[e]); }
 __device__ __forceinline__ float elem(const Frag32& f, int e) { return f.v[e]; }
@@ -254,13 +250,13 @@ __device__ __forceinline__ void split(const float (&x)[8], bf16x8 (&f)[3]) {
     }
   }
 }
-__device__ __forceinline__ void split(const float (&x)[8], Frag32 (&f)[1]) { pack(x, f[0]); }
+__device__ __forceinline__ void split(const float (&x)[8], Frag32 (&f)[1]) { __builtin_memcpy(f[0].v, x, sizeof(x)); }
 template <typename T>
 constexpr int kPieces = sizeof(T) == 2 ? 3 : 1;
 
-// Eight scores as an operand in two parts, the rounded ones and what the rounding left: one part alone would
-// add as much error to a bfloat16 output as its own rounding does, and all of a token's channels would have the
-// same one.
+// Eight scores (two result tiles, rows 16 t + 4 g + r) as an operand in frag_col's order, in two parts: the
+// rounded ones and what the rounding left.  One part alone would add as much error to a bfloat16 output as its
+// own rounding does, and all of a token's channels would have the same one.
 __device__ __forceinline__ void pack_parts(const float (&x)[8], bf16x8 (&f)[2]) {
   uint32_t h[4], r[4];
 #pragma unroll
@@ -271,7 +267,7 @@ __device__ __forceinline__ void pack_parts(const float (&x)[8], bf16x8 (&f)[2]) 
   f[0] = __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
   f[1] = __builtin_bit_cast(bf16x8, make_uint4(r[0], r[1], r[2], r[3]));
 }
-__device__ __forceinline__ void pack_parts(const float (&x)[8], Frag32 (&f)[1]) { pack(x, f[0]); }
+__device__ __forceinline__ void pack_parts(const float (&x)[8], Frag32 (&f)[1]) { split(x, f); }
 template <typename T>
 constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
 
@@ -391,7 +387,6 @@ struct Tile {
   static constexpr int kPer = 16 / sizeof(T);
   static constexpr int kRow = D / kPer;
   static constexpr int kN = B::kC * kRow / B::kThreads;
-  static constexpr int kSize = B::kC * D;
   uint4 r[kN];
   // base: the block's first token; offsets in it fit 32 bits (the caller checked the stride)
   __device__ __forceinline__ void load(const T* base, uint32_t st, int rows, int dim) {
@@ -713,11 +708,6 @@ __device__ __forceinline__ Where where(const LinArgs& a, int width, uint32_t id0
   const int live_blocks = (w.live + C - 1) / C;
   w.c1 = w.end < live_blocks ? w.end : live_blocks;
   return w;
-}
-
-template <typename T>
-__device__ __forceinline__ const T* head(const View& v, int64_t b, int h) {
-  return static_cast<const T*>(v.p) + b * v.b + h * v.h;
 }
 
 // Zeros for this place's tokens past the row's length, in a tensor with token stride `st`, `dim` (a multiple
@@ -1052,7 +1042,8 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
   __shared__ __align__(16) T os[C * DV];
   __shared__ __align__(16) T ss[(kBoth ? 2 : 1) * kStateLds];
   __shared__ __align__(16) Decays<C> decays[2];
-  __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C], across[B::kWaves];
+  __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C];
+  __shared__ float across[2][B::kWaves];  // written before the barrier that the wave with the last block's has to pass
   T* const rs = kBoth ? ss + kStateLds : ss;
   const Where w = where<B>(a, DV, blockIdx.x, gridDim.x);
   Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
@@ -1128,7 +1119,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
             y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
           }
       y = sum_rows(row_sum(y));
-      if ((threadIdx.x & 63) == 0) across[wave] = y;
+      if ((threadIdx.x & 63) == 0) across[c & 1][wave] = y;
     }
     old.publish(wv, ss);
     if constexpr (kBoth) st.publish(wv, rs);
@@ -1355,7 +1346,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
         from *= a.scale * d.from0[l];
         before *= d.toC[l];
 #pragma unroll
-        for (int i = 0; i < B::kWaves; ++i) y += across[i];
+        for (int i = 0; i < B::kWaves; ++i) y += across[c & 1][i];
         y *= d.from0[C - 1];
         for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
       }
