@@ -59,7 +59,7 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("linattn_fwd_kernelItLi128ELi64E", 2),
     ("linattn_segment_kernelItLi64ELi64E", 4),
     ("linattn_passes_kernelItLi64ELi64E", 4),
-    ("linattn_grad_kernelItLi64ELi64E", 2),
+    ("linattn_grad_kernelItLi64ELi64E", 4),
     ("linattn_step_kernel", 6),
 ]
 SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64)]  # bytes per lane

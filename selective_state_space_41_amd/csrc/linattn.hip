@@ -202,22 +202,22 @@ __device__ __forceinline__ Frag32 frag_col_row(const Places<float, D>& w, const 
   return f;
 }
 
-// The column operands of all of a row's tiles, for several products: bfloat16 ones (4 registers each)
-// are read once and kept, float32 ones (8) are read at each use.
-template <typename T, int D>
+// The column operands of all of a row's tiles: read once and kept (for several products, where registers allow: 4
+// for one bfloat16 operand, 8 for a float32 one) or read at each use.
+template <typename T, int D, bool KEEP = sizeof(T) == 2>
 struct Cols {
   const Places<T, D>& w;
   const T* p;
   int row0;
-  Frag<T> f[sizeof(T) == 2 ? D / 16 : 1];
+  Frag<T> f[KEEP ? D / 16 : 1];
   __device__ __forceinline__ Cols(const Places<T, D>& places, const T* tile, int row) : w(places), p(tile), row0(row) {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (KEEP) {
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) f[n] = frag_col<D>(w, p, row0, n * 16);
     }
   }
   __device__ __forceinline__ Frag<T> operator[](int n) const {
-    if constexpr (sizeof(T) == 2) return f[n];
+    if constexpr (KEEP) return f[n];
     else return frag_col<D>(w, p, row0, n * 16);
   }
 };
@@ -376,9 +376,41 @@ using BlockOf = Block<waves_of(sizeof(T), DK, DV)>;
 constexpr int waves_for(size_t elem, int dk, int dv, int narrow) {
   return elem != 2 || dk + dv > 192 ? 1 : dk + dv > 128 ? (narrow > 2 ? 2 : 1) : narrow;
 }
+// The gradient's walk: two workgroups of 8 waves on a CU where LDS holds both, else one.
+constexpr int grad_waves_for(size_t elem, int dk, int dv) { return elem == 2 && dk + dv <= 128 ? 4 : waves_of(elem, dk, dv) / 2; }
 #define VMSCAN_WAVES(N) __attribute__((amdgpu_waves_per_eu(waves_for(sizeof(T), DK, DV, N))))
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// The lane, in a loop that shall make what depends on it where it is used, as Places::here().
+__device__ __forceinline__ int lane_here() {
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
+// Accesses off a base that all lanes share, at 32-bit byte offsets: one register per address, and no branch where
+// something is left out, which an offset of kNowhere, past the buffer's end, says (a load then gives zeros, a store
+// does nothing).  The forward of 128 x 197 tokens and the gradient's passes measured 5 % less time than with branches.
+constexpr uint32_t kNowhere = 0xffff0000u;  // more than 63 tokens of the largest stride
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+constexpr int kRaw = 0x00027000;  // the resource's last word: plain 32-bit data
+struct Buffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ explicit Buffer(const void* base)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(kNowhere), kRaw)) {}
+  // at + more, of which kNowhere looks at the first
+  __device__ __forceinline__ u32x4 load16(uint32_t at, int more = 0) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), more, 0);
+  }
+  __device__ __forceinline__ void store(const float*, f32x4 v, uint32_t at, int more) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, static_cast<int>(at), more, 0);
+  }
+  __device__ __forceinline__ void store(const uint16_t*, f32x4 v, uint32_t at, int more) const {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, r, static_cast<int>(at), more, 0);
+  }
+};
 
 // A tile of C tokens on its way from global memory to LDS.  Tokens from `rows` on and channels from
 // `dim` on are not read: they enter as zeros, whatever the memory holds.
@@ -386,32 +418,27 @@ template <typename T, int D, typename B>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);
   static constexpr int kRow = D / kPer;
-  static constexpr int kN = B::kC * kRow / B::kThreads;
-  uint4 r[kN];
+  static constexpr int kRuns = B::kC * kRow;
+  static constexpr int kN = (kRuns + B::kThreads - 1) / B::kThreads;
+  // fewer runs than threads: the last waves have none
+  __device__ __forceinline__ static bool mine() { return kRuns >= B::kThreads || threadIdx.x < kRuns; }
+  u32x4 r[kN];
   // base: the block's first token; offsets in it fit 32 bits (the caller checked the stride)
   __device__ __forceinline__ void load(const T* base, uint32_t st, int rows, int dim) {
-    const char* p = reinterpret_cast<const char*>(base);
-    if (rows >= B::kC && dim >= D) {
+    const Buffer p(base);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
-        r[i] = *reinterpret_cast<const uint4*>(p + static_cast<uint32_t>((row * st + col) * sizeof(T)));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
-        r[i] = make_uint4(0, 0, 0, 0);
-        if (static_cast<int>(row) < rows && static_cast<int>(col) < dim)
-          r[i] = *reinterpret_cast<const uint4*>(p + static_cast<uint32_t>((row * st + col) * sizeof(T)));
-      }
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
+      const bool in = mine() && static_cast<int>(row) < rows && static_cast<int>(col) < dim;
+      r[i] = p.load16(in ? (row * st + col) * static_cast<uint32_t>(sizeof(T)) : kNowhere);
     }
   }
   __device__ __forceinline__ void store(T* lds) const {
+    if (!mine()) return;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int id = i * B::kThreads + threadIdx.x, row = id / kRow, col = (id % kRow) * kPer;
-      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(lds + (row & ~15) * D) + place<T, D>(row & 15, col)) = r[i];
+      *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(lds + (row & ~15) * D) + place<T, D>(row & 15, col)) = r[i];
     }
   }
 };
@@ -422,15 +449,14 @@ struct OwnRows {
   Frag<T> f[D / 32];
   __device__ __forceinline__ void load(const T* base, uint32_t st, int row0, int rows, int dim) {
     const int l = threadIdx.x & 63, row = row0 + (l & 15), col = (l >> 4) * 8;
-    const T* p = base + static_cast<uint32_t>(row * st + col);
+    const Buffer p(base);
+    const uint32_t at = (row * st + col) * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
     for (int kk = 0; kk < D / 32; ++kk) {
-      uint4 w[sizeof(T) / 2];
+      u32x4 w[sizeof(T) / 2];
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (row < rows && col + kk * 32 < dim) w[i] = *reinterpret_cast<const uint4*>(p + kk * 32 + i * 4);
-      }
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+        w[i] = p.load16(row < rows && col + kk * 32 < dim ? at : kNowhere, (kk * 32 + i * 4) * static_cast<int>(sizeof(T)));
       __builtin_memcpy(&f[kk], w, sizeof(w));
     }
   }
@@ -510,6 +536,18 @@ __device__ __forceinline__ void store_acc(uint16_t* p, f32x4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 
+// N tiles of 16 channels of one token, of which `dim` exist, if it is there at all.  block: the block's place in the
+// tensor, the same for all lanes; at: the lane's offset in it.
+template <typename O, int N>
+__device__ __forceinline__ void store_tiles(O* block, uint32_t at, int dim, bool there, const f32x4 (&acc)[N]) {
+  const int g4 = ((threadIdx.x & 63) >> 4) * 4;
+  const Buffer p(block);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    p.store(block, acc[n], there && n * 16 + g4 < dim ? at * static_cast<uint32_t>(sizeof(O)) : kNowhere,
+            n * 16 * static_cast<int>(sizeof(O)));
+}
+
 __device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
   const uint2 w = *reinterpret_cast<const uint2*>(p);
@@ -532,38 +570,43 @@ struct State {
   __device__ __forceinline__ static int n_of(int nt) { return nt * 16 + ((threadIdx.x & 63) >> 4) * 4; }
 
   // rows of `ld` floats, of which d < dk and n < dv exist
-  __device__ __forceinline__ void load(const float* p, int dk, int dv, int ld) {
-#pragma unroll
-    for (int t = 0; t < kDT; ++t)
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        s[t][nt] = zero4();
-        if (p && d_of(t) < dk && n_of(nt) < dv) s[t][nt] = load4(p + (d_of(t) * ld + n_of(nt)));
-      }
+  __device__ __forceinline__ static uint32_t place_of(int ld) {  // of [0][0], in bytes
+    return (static_cast<uint32_t>(d_of(0)) * ld + n_of(0)) * 4;
   }
-  __device__ __forceinline__ void store(float* p, int dk, int dv, int ld) const {
+  __device__ __forceinline__ void load(const float* p, int dk, int dv, int ld) {
+    const Buffer from(p);
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
-        if (d_of(t) < dk && n_of(nt) < dv) store_acc(p + (d_of(t) * ld + n_of(nt)), s[t][nt]);
+        s[t][nt] = __builtin_bit_cast(
+            f32x4, from.load16(p && d_of(t) < dk && n_of(nt) < dv ? place_of(ld) : kNowhere, (t * 16 * ld + nt * 16) * 4));
+  }
+  __device__ __forceinline__ void store(float* p, int dk, int dv, int ld) const {
+    const Buffer to(p);
+#pragma unroll
+    for (int t = 0; t < kDT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        to.store(p, s[t][nt], d_of(t) < dk && n_of(nt) < dv ? place_of(ld) : kNowhere, (t * 16 * ld + nt * 16) * 4);
   }
   // What enters after segments from, from + dir, .. (n of them) that each add their own state, on top of what is
-  // here: s = s 2^g + own, four segments on their way at a time.
+  // here: s = s 2^g + own, AHEAD segments on their way at a time.
+  template <int AHEAD = 4>
   __device__ __forceinline__ void join(const float* own, const float* g, int from, int dir, int n, int ld) {
     const int64_t step = static_cast<int64_t>(DK) * ld;
-    for (int i0 = 0; i0 < n; i0 += 4) {
-      State x[4];
-      float m[4];
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+      State x[AHEAD];
+      float m[AHEAD];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < AHEAD; ++i)
         if (i0 + i < n) {
           const int at = from + dir * (i0 + i);
           x[i].load(own + at * step, DK, DV, ld);
           m[i] = g[at];
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < AHEAD; ++i)
         if (i0 + i < n) {
           const float e = __builtin_amdgcn_exp2f(m[i]);
 #pragma unroll
@@ -604,7 +647,8 @@ struct State {
   }
   // s += sum_j w_j y_j x_j^T over the 32 tokens from row0 of y (the tile [token][d]); xa: the operand of x,
   // w: the weights, both in frag_col's order.
-  __device__ __forceinline__ void add(const Places<T, DK>& wk, const T* y, int row0, const Cols<T, DV>& xa,
+  template <bool KEEP>
+  __device__ __forceinline__ void add(const Places<T, DK>& wk, const T* y, int row0, const Cols<T, DV, KEEP>& xa,
                                       const float (&w)[8]) {
     if (!mine()) return;
 #pragma unroll
@@ -615,6 +659,7 @@ struct State {
       for (int e = 0; e < 8; ++e) m[e] = elem(f, e) * w[e];
       Frag<T> piece[kPieces<T>];
       split(m, piece);
+      if constexpr (!KEEP) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         const Frag<T> x = xa[nt];
@@ -993,11 +1038,10 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
       eight(d.toC + kk * 32, m);
       st.add(wk, ks, kk * 32, xa, m);
     }
-    if (t0 + i < w.live) {
-      T* o = out + t0 * ot;
+    if (own) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (nt * 16 + g4 < dv) store_acc(o + static_cast<uint32_t>(i * ot + nt * 16 + g4), acc[nt] * a.scale);
+      for (int nt = 0; nt < NT; ++nt) acc[nt] *= a.scale;
+      store_tiles(out + t0 * ot, static_cast<uint32_t>(i * ot) + g4, dv, t0 + i < w.live, acc);
     }
     __syncthreads();
   }
@@ -1027,33 +1071,82 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
 // A first walk forwards (the segment kernel) leaves each block's entering state, counted from its segment's
 // start; this kernel walks backwards and does the rest, reading q, k, v and dout once.
 
+//
+// Twice the waves of the other kernels: one half (the state waves) carries R, makes dq and the sums a and b, the
+// other (the key waves) dk, dv, the in-block part of dg and dg itself.  A wave of each half owns the same 16 tokens.
+// With one wave doing both, 2 waves per SIMD were all that the registers left, and they waited 57 % of the time
+// (32 x 3136 tokens, 8 heads of 64 x 64, bfloat16: 380 us, so 344).
+
+// The gradient's workgroup: a block's tokens as in B, twice the waves.
+template <typename B>
+struct Pairs {
+  static constexpr int kWaves = B::kWaves;
+  static constexpr int kC = B::kC;
+  static constexpr int kThreads = 2 * B::kThreads;
+};
+
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) void linattn_grad_kernel(LinArgs a) {
+struct GradLds {
+  using B = BlockOf<T, DK, DV>;
+  using S = State<T, DK, DV>;
+  // S and R as operands: side by side where LDS has room for both, else one after the other
+  static constexpr int kState = S::kPlanes * S::kPlane;
+  static constexpr bool kBoth = (2 * B::kC * (DK + DV) + 2 * kState) * sizeof(T) + 8192 <= 160 * 1024;
+  __align__(16) T qs[B::kC * DK];
+  __align__(16) T ks[B::kC * DK];
+  __align__(16) T vs[B::kC * DV];
+  __align__(16) T os[B::kC * DV];
+  __align__(16) T ss[(kBoth ? 2 : 1) * kState];
+  __align__(16) Decays<B::kC> decays[2];
+  float rows[B::kWaves][B::kC], into[B::kWaves][B::kC], after[B::kWaves][B::kC];
+  float across[2][B::kWaves];  // written before the barrier that the wave with the last block's has to pass
+  __device__ __forceinline__ T* rs() { return kBoth ? ss + kState : ss; }
+};
+
+// q, k, v and dout of a block on their way to LDS.
+template <typename T, int DK, int DV>
+struct GradTiles {
+  using G = Pairs<BlockOf<T, DK, DV>>;
+  Stream<T, DK, G> q, k;
+  Stream<T, DV, G> v, o;
+  const Where& w;
+  int dk, dv;
+  __device__ __forceinline__ GradTiles(const LinArgs& a, const Where& where)
+      : q(a.q, where.b, where.h / a.share, 0), k(a.k, where.b, where.h / a.share, 0), v(a.v, where.b, where.h, 0),
+        o(a.dout, where.b, where.h, 0), w(where), dk(a.dk), dv(a.dvd) {}
+  __device__ __forceinline__ void skip(int blocks) {
+    q.skip(blocks);
+    k.skip(blocks);
+    v.skip(blocks);
+    o.skip(blocks);
+  }
+  __device__ __forceinline__ void load(int t0) {
+    q.load(w.live - t0, dk);
+    k.load(w.live - t0, dk);
+    v.load(w.live - t0, dv);
+    o.load(w.live - t0, dv);
+  }
+  __device__ __forceinline__ void store(GradLds<T, DK, DV>& lds) const {
+    q.tile.store(lds.qs);
+    k.tile.store(lds.ks);
+    v.tile.store(lds.vs);
+    o.tile.store(lds.os);
+  }
+};
+
+// The two halves pass the same barriers: one when a block's tiles are in LDS, two around the exchange of S for R
+// (where LDS holds one of them), one when the block is done.
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, GradLds<T, DK, DV>& lds) {
   using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC;
   constexpr int DT = DK / 16, NT = DV / 16;
-  // S and R as operands: side by side where LDS has room for both, else one after the other
-  constexpr int kStateLds = S::kPlanes * S::kPlane;
-  constexpr bool kBoth = (2 * C * (DK + DV) + 2 * kStateLds) * sizeof(T) + 8192 <= 160 * 1024;
-  __shared__ __align__(16) T qs[C * DK];
-  __shared__ __align__(16) T ks[C * DK];
-  __shared__ __align__(16) T vs[C * DV];
-  __shared__ __align__(16) T os[C * DV];
-  __shared__ __align__(16) T ss[(kBoth ? 2 : 1) * kStateLds];
-  __shared__ __align__(16) Decays<C> decays[2];
-  __shared__ float rows[B::kWaves][C], into[B::kWaves][C], after[B::kWaves][C];
-  __shared__ float across[2][B::kWaves];  // written before the barrier that the wave with the last block's has to pass
-  T* const rs = kBoth ? ss + kStateLds : ss;
-  const Where w = where<B>(a, DV, blockIdx.x, gridDim.x);
-  Stream<T, DK, B> q(a.q, w.b, w.h / a.share, 0), k(a.k, w.b, w.h / a.share, 0);
-  Stream<T, DV, B> v(a.v, w.b, w.h, 0), o(a.dout, w.b, w.h, 0);
-  const float* g = a.g + w.b * a.gb + w.h * a.gh;
-  const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
-  const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
-  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
-  const int wave = wave_id(), l = threadIdx.x & 63, li = l & 15, g4 = (l >> 4) * 4;
-
+  constexpr bool kBoth = GradLds<T, DK, DV>::kBoth;
+  const int wave = wave_id();
+  const int kt = a.heads * a.dk;
+  const int64_t kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  GradTiles<T, DK, DV> tiles(a, w);
   Places<T, DK> wk;
   Places<T, DV> wv;
   S st, first;  // R; the state that enters the part of the segment
@@ -1065,48 +1158,31 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
     if (end < a.parts) st.join(a.seg_ds + part0 * (DK * DV), a.seg_dg + part0, a.parts - 1, -1, a.parts - end, DV);
   }
-  auto enter = [&](int part) {  // first: the state that enters a part
+  auto enter = [&](int part, auto ahead) {  // first: the state that enters a part
     if (a.parts > 1 && !a.chain) {
       first.load(a.seg_s + (part0 + part) * (DK * DV), DK, DV, DV);
     } else {
       first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-      if (part > 0) first.join(a.seg_s + part0 * (DK * DV), a.seg_g + part0, 0, 1, part, DV);
+      if (part > 0) first.template join<decltype(ahead)::value>(a.seg_s + part0 * (DK * DV), a.seg_g + part0, 0, 1, part, DV);
     }
   };
-  float gx = 0.0f;
-  auto skip = [&](int blocks) {
-    q.skip(blocks);
-    k.skip(blocks);
-    v.skip(blocks);
-    o.skip(blocks);
-  };
-  auto load = [&](int t0) {
-    q.load(w.live - t0, a.dk);
-    k.load(w.live - t0, a.dk);
-    v.load(w.live - t0, a.dvd);
-    o.load(w.live - t0, a.dvd);
-  };
   if (w.c0 < w.c1) {
-    enter((w.c1 - 1) / a.per_part);
-    skip(w.c1 - 1);
-    load((w.c1 - 1) * C);
-    if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), decays[(w.c1 - 1) & 1]);
-    if (w.c1 - 1 > w.c0) gx = load_g<C>(a, g, (w.c1 - 2) * C, w.live);
+    enter((w.c1 - 1) / a.per_part, std::integral_constant<int, 4>{});
+    tiles.skip(w.c1 - 1);
+    tiles.load((w.c1 - 1) * C);
   }
   for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
-    const Decays<C>& d = decays[c & 1];
+    const Decays<C>& d = lds.decays[c & 1];
     wk.here();
     wv.here();
+    const int l = lane_here(), li = l & 15, g4 = (l >> 4) * 4;
     const int64_t block = w.bh * a.blocks + c;
-    if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1) enter(c / a.per_part);
+    if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1) enter(c / a.per_part, std::integral_constant<int, 1>{});  // few registers
     S old;  // the state that enters the block
     old.load(a.states + block * (DK * DV), DK, DV, DV);
     const float since = __builtin_amdgcn_exp2f(a.block_g[block]);
-    q.tile.store(qs);
-    k.tile.store(ks);
-    v.tile.store(vs);
-    o.tile.store(os);
+    tiles.store(lds);
     {
       float y = 0.0f;  // <S, R>, both in this wave's layout
 #pragma unroll
@@ -1119,27 +1195,22 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
             y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
           }
       y = sum_rows(row_sum(y));
-      if ((threadIdx.x & 63) == 0) across[c & 1][wave] = y;
+      if ((threadIdx.x & 63) == 0) lds.across[c & 1][wave] = y;
     }
-    old.publish(wv, ss);
-    if constexpr (kBoth) st.publish(wv, rs);
+    old.publish(wv, lds.ss);
+    if constexpr (kBoth) st.publish(wv, lds.rs());
     __syncthreads();
-    if (c > w.c0) {
-      skip(-1);
-      load(t0 - C);
-      if (wave == c % B::kWaves) scan_g(gx, decays[(c - 1) & 1]);
-      if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
-    }
     const int d0 = wave * S::kDT * 16;
-    old.bilinear(wv, os, [&](int t, int jt) { return load4(at<T, DK>(qs, jt * 16, wk.perm, 0, d0 + t * 16)); },
-                 into[wave]);
+    old.bilinear(wv, lds.os,
+                 [&](int t, int jt) { return load4(at<T, DK>(lds.qs, jt * 16, wk.perm, 0, d0 + t * 16)); },
+                 lds.into[wave]);
     // dq of this wave's 16 queries: column i of every result tile
     if (t0 + wave * 16 < w.live) {
       const int i0 = wave * 16, i = i0 + li;
       const float gh = d.hi[i], gl = d.lo[i];
       Frag<T> of[DV / 32];
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<DV>(wv, os, i0, kk * 32);
+      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<DV>(wv, lds.os, i0, kk * 32);
       f32x4 acc[DT];
       const float e0 = d.from0[i] * a.scale;
 #pragma unroll
@@ -1149,7 +1220,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
         for (int pl = 0; pl < S::kPlanes; ++pl)
 #pragma unroll
           for (int kk = 0; kk < DV / 32; ++kk)
-            acc[dt] = mma(frag_row<DV>(wv, ss + pl * S::kPlane, dt * 16, kk * 32), of[kk], acc[dt]);
+            acc[dt] = mma(frag_row<DV>(wv, lds.ss + pl * S::kPlane, dt * 16, kk * 32), of[kk], acc[dt]);
         acc[dt] *= e0;
       }
 #pragma unroll
@@ -1162,7 +1233,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
           if (j0 <= i0) {
             f32x4 dp = zero4();
 #pragma unroll
-            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<DV>(wv, vs, j0, kk * 32), of[kk], dp);
+            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<DV>(wv, lds.vs, j0, kk * 32), of[kk], dp);
             if (j0 < i0) {
               const f32x4 e = load4(d.toE + j0 + g4);
               const float from = d.between(gh, gl, j0 + 15) * a.scale;
@@ -1182,156 +1253,202 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
         pack_parts(p, pf);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
-          const Frag<T> x = frag_col<DK>(wk, ks, jj * 32, dt * 16);
+          const Frag<T> x = frag_col<DK>(wk, lds.ks, jj * 32, dt * 16);
 #pragma unroll
           for (int i = 0; i < kParts<T>; ++i) acc[dt] = mma(x, pf[i], acc[dt]);
         }
       }
-      if (t0 + i < w.live) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-          if (dt * 16 + g4 < a.dk) {
-            const uint32_t at = static_cast<uint32_t>(i * kt + dt * 16 + g4);
-            if (a.share == 1)
-              store_acc(static_cast<T*>(a.dq) + (kbase + t0 * kt) + at, acc[dt]);
-            else
-              store_acc(static_cast<float*>(a.dq) + (kbase + t0 * kt) + at, acc[dt]);
-          }
-      }
+      const uint32_t at = static_cast<uint32_t>(i) * kt + g4;
+      if (a.share == 1)
+        store_tiles(static_cast<T*>(a.dq) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, t0 + i < w.live, acc);
+      else
+        store_tiles(static_cast<float*>(a.dq) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, t0 + i < w.live, acc);
     }
     if constexpr (!kBoth) {
       __syncthreads();
-      st.publish(wv, rs);
+      st.publish(wv, lds.rs());
       __syncthreads();
     }
-    st.bilinear(wv, vs, [&](int t, int jt) { return load4(at<T, DK>(ks, jt * 16, wk.perm, 0, d0 + t * 16)); },
-                after[wave]);
+    if (c > w.c0) {
+      tiles.skip(-1);
+      tiles.load(t0 - C);
+    }
+    st.bilinear(wv, lds.vs,
+                [&](int t, int jt) { return load4(at<T, DK>(lds.ks, jt * 16, wk.perm, 0, d0 + t * 16)); },
+                lds.after[wave]);
+    st.decay(d.from0[C - 1]);
+#pragma unroll
+    for (int kk = C / 32 - 1; kk >= 0; --kk) {
+      if (t0 + kk * 32 >= w.live) continue;
+      const Cols<T, DV, (S::kDT > 1 && sizeof(T) == 2)> xa(wv, lds.os, kk * 32);
+      float m[8];
+      eight(d.from0 + kk * 32, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[e] *= a.scale;
+      st.add(wk, lds.qs, kk * 32, xa, m);
+    }
+    __syncthreads();
+  }
+  if (a.ds0 && w.seg == 0) st.store(a.ds0 + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
+}
+
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, GradLds<T, DK, DV>& lds) {
+  using B = BlockOf<T, DK, DV>;
+  using S = State<T, DK, DV>;
+  constexpr int C = B::kC;
+  constexpr int DT = DK / 16, NT = DV / 16;
+  constexpr bool kBoth = GradLds<T, DK, DV>::kBoth;
+  const int wave = wave_id() - B::kWaves;
+  const float* g = a.g + w.b * a.gb + w.h * a.gh;
+  const int kt = a.heads * a.dk;
+  const int64_t kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int vt = a.heads * a.dvd;
+  const int64_t vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
+  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
+  GradTiles<T, DK, DV> tiles(a, w);
+  Places<T, DK> wk;
+  Places<T, DV> wv;
+  float gx = 0.0f;
+  if (w.c0 < w.c1) {
+    tiles.skip(w.c1 - 1);
+    tiles.load((w.c1 - 1) * C);
+    if (wave == 0) scan_g(load_g<C>(a, g, (w.c1 - 1) * C, w.live), lds.decays[(w.c1 - 1) & 1]);
+    if (w.c1 - 1 > w.c0) gx = load_g<C>(a, g, (w.c1 - 2) * C, w.live);
+  }
+  for (int c = w.c1 - 1; c >= w.c0; --c) {
+    const int t0 = c * C;
+    const Decays<C>& d = lds.decays[c & 1];
+    wk.here();
+    wv.here();
+    const int l = lane_here(), li = l & 15, g4 = (l >> 4) * 4;
+    tiles.store(lds);
+    __syncthreads();
+    if (c > w.c0) {
+      if (wave == c % B::kWaves) scan_g(gx, lds.decays[(c - 1) & 1]);
+      if (c - 1 > w.c0) gx = load_g<C>(a, g, t0 - 2 * C, w.live);
+    }
     // dk and dv of this wave's 16 keys: column j of every result tile
     const int j0 = wave * 16, j = j0 + li;
     const float gh = d.hi[j], gl = d.lo[j], toC = d.toC[j];
     Frag<T> kf[DK / 32], vf[DV / 32];
 #pragma unroll
-    for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<DK>(wk, ks, j0, kk * 32);
+    for (int kk = 0; kk < DK / 32; ++kk) kf[kk] = frag_row<DK>(wk, lds.ks, j0, kk * 32);
 #pragma unroll
-    for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<DV>(wv, vs, j0, kk * 32);
+    for (int kk = 0; kk < DV / 32; ++kk) vf[kk] = frag_row<DV>(wv, lds.vs, j0, kk * 32);
     f32x4 ak[DT], av[NT];
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      ak[dt] = zero4();
-#pragma unroll
-      for (int pl = 0; pl < S::kPlanes; ++pl)
-#pragma unroll
-        for (int kk = 0; kk < DV / 32; ++kk)
-          ak[dt] = mma(frag_row<DV>(wv, rs + pl * S::kPlane, dt * 16, kk * 32), vf[kk], ak[dt]);
-      ak[dt] *= toC;
-    }
+    for (int dt = 0; dt < DT; ++dt) ak[dt] = zero4();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) av[nt] = zero4();
-#pragma unroll
-    for (int kk = 0; kk < DK / 32; ++kk) {
-#pragma unroll
-      for (int pl = 0; pl < S::kPlanes; ++pl)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          av[nt] = mma(frag_col_row<DV>(wv, rs + pl * S::kPlane, kk * 32, nt * 16), kf[kk], av[nt]);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) av[nt] *= toC;
-    st.decay(d.from0[C - 1]);
     // Queries from the last 32 down.  Beside the products, M_ij summed over the queries from t on (in
     // this lane's column; `later`: the tiles done) and then over the keys before t.
     float later = 0.0f;
 #pragma unroll
     for (int kk = C / 32 - 1; kk >= 0; --kk) {
+      if (kk < wave / 2) break;
       if (t0 + kk * 32 >= w.live) {  // no tokens; the table of rows has to be whole
-        if (kk >= wave / 2 && l < 32 && kk * 32 + l >= j0) rows[wave][kk * 32 + l] = 0.0f;
+        if (l < 32 && kk * 32 + l >= j0) lds.rows[wave][kk * 32 + l] = 0.0f;
         continue;
       }
-      const Cols<T, DV> xa(wv, os, kk * 32);
-      if (kk >= wave / 2) {
-        float p[8], x[8];
+      float p[8], x[8];
 #pragma unroll
-        for (int t = 1; t >= 0; --t) {
-          const int i0 = kk * 32 + t * 16;
-          if (i0 >= j0) {
-            f32x4 sc = zero4(), dp = zero4();
+      for (int t = 1; t >= 0; --t) {
+        const int i0 = kk * 32 + t * 16;
+        if (i0 >= j0) {
+          f32x4 sc = zero4(), dp = zero4();
 #pragma unroll
-            for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<DK>(wk, qs, i0, n * 32), kf[n], sc);
+          for (int n = 0; n < DK / 32; ++n) sc = mma(frag_row<DK>(wk, lds.qs, i0, n * 32), kf[n], sc);
 #pragma unroll
-            for (int n = 0; n < DV / 32; ++n) dp = mma(frag_row<DV>(wv, os, i0, n * 32), vf[n], dp);
-            float u[4];
-            if (i0 > j0) {  // through the last token before the 16 queries
-              const f32x4 e = load4(d.fromF + i0 + g4);
-              const float to = __builtin_amdgcn_exp2f((d.hi[i0 - 1] - gh) + (d.lo[i0 - 1] - gl)) * a.scale;
+          for (int n = 0; n < DV / 32; ++n) dp = mma(frag_row<DV>(wv, lds.os, i0, n * 32), vf[n], dp);
+          float u[4];
+          if (i0 > j0) {  // through the last token before the 16 queries
+            const f32x4 e = load4(d.fromF + i0 + g4);
+            const float to = __builtin_amdgcn_exp2f((d.hi[i0 - 1] - gh) + (d.lo[i0 - 1] - gl)) * a.scale;
 #pragma unroll
-              for (int r = 3; r >= 0; --r) {
-                const float f = e[r] * to;
-                p[t * 4 + r] = sc[r] * f;
-                x[t * 4 + r] = dp[r] * f;
-                u[r] = sc[r] * x[t * 4 + r] + (r < 3 ? u[r + 1] : 0.0f);
-              }
-            } else {
-#pragma unroll
-              for (int r = 3; r >= 0; --r) {
-                const int i = i0 + g4 + r;
-                const float f = __builtin_amdgcn_exp2f((d.hi[i] - gh) + (d.lo[i] - gl)) * a.scale;
-                p[t * 4 + r] = i >= j ? sc[r] * f : 0.0f;
-                x[t * 4 + r] = i >= j ? dp[r] * f : 0.0f;
-                u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
-              }
-            }
-            float tiles[4];  // this lane's rows of the tile, and the other lanes' of the column
-            rows_of(u[0], tiles);
-            const float below = sum_after(tiles, g4 / 4) + later;
-            later += (tiles[0] + tiles[1]) + (tiles[2] + tiles[3]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int i = i0 + g4 + r;
-              const float m = row_sum(j < i ? u[r] + below : 0.0f);
-              if (li == 0) rows[wave][i] = m;
+            for (int r = 3; r >= 0; --r) {
+              const float f = e[r] * to;
+              p[t * 4 + r] = sc[r] * f;
+              x[t * 4 + r] = dp[r] * f;
+              u[r] = sc[r] * x[t * 4 + r] + (r < 3 ? u[r + 1] : 0.0f);
             }
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[t * 4 + r] = x[t * 4 + r] = 0.0f;
+            for (int r = 3; r >= 0; --r) {
+              const int i = i0 + g4 + r;
+              const float f = __builtin_amdgcn_exp2f((d.hi[i] - gh) + (d.lo[i] - gl)) * a.scale;
+              p[t * 4 + r] = i >= j ? sc[r] * f : 0.0f;
+              x[t * 4 + r] = i >= j ? dp[r] * f : 0.0f;
+              u[r] = (i > j ? sc[r] * x[t * 4 + r] : 0.0f) + (r < 3 ? u[r + 1] : 0.0f);
+            }
           }
-        }
-        Frag<T> pf[kParts<T>], xf[kParts<T>];
-        pack_parts(p, pf);
-        pack_parts(x, xf);
+          float quads[4];  // this lane's rows of the tile, and the other lanes' of the column
+          rows_of(u[0], quads);
+          const float below = sum_after(quads, g4 / 4) + later;
+          later += (quads[0] + quads[1]) + (quads[2] + quads[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Frag<T> f = xa[nt];
+          for (int r = 0; r < 4; ++r) {
+            const int i = i0 + g4 + r;
+            const float m = row_sum(j < i ? u[r] + below : 0.0f);
+            if (li == 0) lds.rows[wave][i] = m;
+          }
+        } else {
 #pragma unroll
-          for (int i = 0; i < kParts<T>; ++i) av[nt] = mma(f, pf[i], av[nt]);
-        }
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const Frag<T> f = frag_col<DK>(wk, qs, kk * 32, dt * 16);
-#pragma unroll
-          for (int i = 0; i < kParts<T>; ++i) ak[dt] = mma(f, xf[i], ak[dt]);
+          for (int r = 0; r < 4; ++r) p[t * 4 + r] = x[t * 4 + r] = 0.0f;
         }
       }
-      float m[8];
-      eight(d.from0 + kk * 32, m);
+      Frag<T> pf[kParts<T>], xf[kParts<T>];
+      pack_parts(p, pf);
+      pack_parts(x, xf);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[e] *= a.scale;
-      st.add(wk, qs, kk * 32, xa, m);
+      for (int nt = 0; nt < NT; ++nt) {
+        const Frag<T> f = frag_col<DV>(wv, lds.os, kk * 32, nt * 16);
+#pragma unroll
+        for (int i = 0; i < kParts<T>; ++i) av[nt] = mma(f, pf[i], av[nt]);
+      }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        const Frag<T> f = frag_col<DK>(wk, lds.qs, kk * 32, dt * 16);
+#pragma unroll
+        for (int i = 0; i < kParts<T>; ++i) ak[dt] = mma(f, xf[i], ak[dt]);
+      }
     }
-    if (t0 + j < w.live) {
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-        if (dt * 16 + g4 < a.dk) {
-          const uint32_t at = static_cast<uint32_t>(j * kt + dt * 16 + g4);
-          if (a.share == 1)
-            store_acc(static_cast<T*>(a.dk_out) + (kbase + t0 * kt) + at, ak[dt]);
-          else
-            store_acc(static_cast<float*>(a.dk_out) + (kbase + t0 * kt) + at, ak[dt]);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (nt * 16 + g4 < a.dvd)
-          store_acc(static_cast<T*>(a.dv_out) + (vbase + t0 * vt) + static_cast<uint32_t>(j * vt + nt * 16 + g4), av[nt]);
+    if (c > w.c0) {
+      tiles.skip(-1);
+      tiles.load(t0 - C);
     }
+    if constexpr (!kBoth) {
+      __syncthreads();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      f32x4 s = zero4();
+#pragma unroll
+      for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+        for (int kk = 0; kk < DV / 32; ++kk)
+          s = mma(frag_row<DV>(wv, lds.rs() + pl * S::kPlane, dt * 16, kk * 32), vf[kk], s);
+      ak[dt] += s * toC;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 s = zero4();
+#pragma unroll
+      for (int pl = 0; pl < S::kPlanes; ++pl)
+#pragma unroll
+        for (int kk = 0; kk < DK / 32; ++kk)
+          s = mma(frag_col_row<DV>(wv, lds.rs() + pl * S::kPlane, kk * 32, nt * 16), kf[kk], s);
+      av[nt] += s * toC;
+    }
+    const bool there = t0 + j < w.live;
+    const uint32_t at = static_cast<uint32_t>(j) * kt + g4;
+    if (a.share == 1)
+      store_tiles(static_cast<T*>(a.dk_out) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, there, ak);
+    else
+      store_tiles(static_cast<float*>(a.dk_out) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, there, ak);
+    store_tiles(static_cast<T*>(a.dv_out) + (vbase + static_cast<int64_t>(t0) * vt), static_cast<uint32_t>(j) * vt + g4,
+                a.dvd, there, av);
     __syncthreads();
     if (wave == c % B::kWaves) {
       // lane t: token t0 + t.  The other waves write these arrays again only past the next barrier.
@@ -1340,15 +1457,15 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
       if (mine) {
 #pragma unroll
         for (int i = 0; i < B::kWaves; ++i) {
-          from += into[i][l];
-          before += after[i][l];
+          from += lds.into[i][l];
+          before += lds.after[i][l];
         }
         from *= a.scale * d.from0[l];
         before *= d.toC[l];
 #pragma unroll
-        for (int i = 0; i < B::kWaves; ++i) y += across[c & 1][i];
+        for (int i = 0; i < B::kWaves; ++i) y += lds.across[c & 1][i];
         y *= d.from0[C - 1];
-        for (int i = 0; i <= l / 16; ++i) y += rows[i][l];
+        for (int i = 0; i <= l / 16; ++i) y += lds.rows[i][l];
       }
       float r[4];
       rows_of(row_sum(from), r);
@@ -1358,18 +1475,34 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(2) voi
       if (mine) dg[static_cast<int64_t>(t0 + l) * a.heads] = from + before + y;
     }
   }
+}
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__((Pairs<BlockOf<T, DK, DV>>::kThreads)) __attribute__((amdgpu_waves_per_eu(
+    grad_waves_for(sizeof(T), DK, DV)))) void linattn_grad_kernel(LinArgs a) {
+  using B = BlockOf<T, DK, DV>;
+  using G = Pairs<B>;
+  constexpr int C = B::kC;
+  __shared__ GradLds<T, DK, DV> lds;
+  const Where w = where<B>(a, DV, blockIdx.x, gridDim.x);
+  if (wave_id() < B::kWaves)
+    grad_states<T, DK, DV>(a, w, lds);
+  else
+    grad_keys<T, DK, DV>(a, w, lds);
+  const int64_t kt = static_cast<int64_t>(a.heads) * a.dk, kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
+  const int64_t vt = static_cast<int64_t>(a.heads) * a.dvd, vbase = (w.b * a.seqlen * a.heads + w.h) * a.dvd;
   if (a.share == 1) {
-    zero_rest<B>(a, w, static_cast<T*>(a.dq) + kbase, kt, a.dk);
-    zero_rest<B>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
+    zero_rest<G>(a, w, static_cast<T*>(a.dq) + kbase, kt, a.dk);
+    zero_rest<G>(a, w, static_cast<T*>(a.dk_out) + kbase, kt, a.dk);
   } else {
-    zero_rest<B>(a, w, static_cast<float*>(a.dq) + kbase, kt, a.dk);
-    zero_rest<B>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
+    zero_rest<G>(a, w, static_cast<float*>(a.dq) + kbase, kt, a.dk);
+    zero_rest<G>(a, w, static_cast<float*>(a.dk_out) + kbase, kt, a.dk);
   }
-  zero_rest<B>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
+  zero_rest<G>(a, w, static_cast<T*>(a.dv_out) + vbase, vt, a.dvd);
+  float* dg = a.dg + w.b * a.seqlen * a.heads + w.h;
   const int t_end = w.end * C < a.seqlen ? w.end * C : a.seqlen;
-  for (int64_t t = (w.live > w.c0 * C ? w.live : w.c0 * C) + static_cast<int>(threadIdx.x); t < t_end; t += B::kThreads)
+  for (int64_t t = (w.live > w.c0 * C ? w.live : w.c0 * C) + static_cast<int>(threadIdx.x); t < t_end; t += G::kThreads)
     dg[t * a.heads] = 0.0f;
-  if (a.ds0 && w.seg == 0) st.store(a.ds0 + w.bh * a.dk * a.dvd, a.dk, a.dvd, a.dvd);
 }
 
 // dq and dk of a shared head: the sum over the heads that read it, rounded once.  `in` is [tokens]
@@ -1697,7 +1830,7 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
       } else {
         hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false, true>), walks(a), block, 0, stream, a);
       }
-      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), walks(a), block, 0, stream, a);
+      hipLaunchKernelGGL((linattn_grad_kernel<T, DK, DV>), walks(a), dim3(2 * block.x), 0, stream, a);
     }
   });
   const int64_t tokens = a.batch * a.seqlen;
