@@ -400,15 +400,17 @@ struct Buffer {
   __amdgpu_buffer_rsrc_t r;
   __device__ __forceinline__ explicit Buffer(const void* base)
       : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(kNowhere), kRaw)) {}
-  // at + more, of which kNowhere looks at the first
+  // At at + more (less than 64 KB).  Stores have the sum in the address and not `more` in the instruction's scalar
+  // offset: the compiler then takes a 16-byte store's registers as free at once, and a few lanes' values written to
+  // them by the next instruction were stored instead (float32 outputs of the forward, when stores had to queue).
   __device__ __forceinline__ u32x4 load16(uint32_t at, int more = 0) const {
     return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), more, 0);
   }
   __device__ __forceinline__ void store(const float*, f32x4 v, uint32_t at, int more) const {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, static_cast<int>(at), more, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, static_cast<int>(at + more), 0, 0);
   }
   __device__ __forceinline__ void store(const uint16_t*, f32x4 v, uint32_t at, int more) const {
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, r, static_cast<int>(at), more, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, r, static_cast<int>(at + more), 0, 0);
   }
 };
 

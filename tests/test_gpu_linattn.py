@@ -331,6 +331,32 @@ def test_same_bits():
         assert all(torch.equal(g[k], g2[k]) for k in g)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(32, 64), (64, 64), (64, 128)])
+def test_equal_rows_under_load(dk, dv, dtype):
+    """All rows of a batch that fills the chip, and holds the stores up, get the bits of the first, and the first
+    what the formula says.  A 16-byte store whose registers the next instruction took again went wrong only here."""
+    import selective_state_space_41_amd as V
+    B, T, H, Hk = 48, 1500, 4, 1
+    p = make(26, 1, T, H, Hk, dk, dv, dtype)
+    t = {k: dev(p, k).expand(B, -1, -1, -1).contiguous() for k in ("q", "k", "v", "dout")}
+    t["g"] = dev(p, "g").expand(B, -1, -1).contiguous()
+    print(f"[linattn] equal rows {dk} x {dv} {dtype}", flush=True)
+    out, sT = V.linattn_fwd(t["q"], t["k"], t["v"], t["g"], scale=p["scale"])
+    g = V.linattn_bwd(t["q"], t["k"], t["v"], t["g"], t["dout"], scale=p["scale"])
+    torch.cuda.synchronize()
+    g.update(out=out, final_state=sT)
+    for key, y in g.items():
+        assert y is None or torch.equal(y, y[:1].expand_as(y)), key
+    (r_out, r_sT), (m_out, m_sT) = oracle_fwd(p, None, None)
+    check("out", out[:1], r_out, m_out, ACT[dtype])
+    check("final_state", sT[:1], r_sT, m_sT, WIDE[dtype])
+    r, m = oracle_bwd(p, None, None, None)
+    for key in ("dq", "dk", "dv"):
+        check(key, g[key][:1], r[key], m[key], ACT[dtype])
+    check("dlog_decay", g["dlog_decay"][:1], r["dg"], m["dg"], WIDE[dtype])
+
+
 def test_captured_graph():
     """Forward, step and gradient captured in a graph and replayed between eager work: every replay
     gives the eager results."""
