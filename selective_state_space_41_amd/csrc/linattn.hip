@@ -557,6 +557,10 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
                __uint_as_float(w.y & 0xffff0000u)};
 }
 
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
+  return __builtin_fmaf(a[3], b[3], __builtin_fmaf(a[2], b[2], __builtin_fmaf(a[1], b[1], a[0] * b[0])));
+}
+
 // The state, transposed in the accumulators: wave w holds columns d of its own tiles (tile index
 // w * DT + t), rows n = 16 nt + 4 g + r.
 template <typename T, int DK, int DV>
@@ -621,25 +625,63 @@ struct State {
   // into LDS as an operand, [d][n]; bfloat16 with what the rounding left in a second plane
   static constexpr int kPlane = DK * DV;
   static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
-  __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p) const {
+  // What the second rounding left (8 bits more, all that there are), as operands of rows d, n in frag_col's order.
+  struct Third {
+    bf16x8 f[kPlanes == 2 ? kDT : 1][DV / 32];
+  };
+  __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p, Third* third = nullptr) const {
     if (!mine()) return;
 #pragma unroll
-    for (int t = 0; t < kDT; ++t)
+    for (int t = 0; t < kDT; ++t) {
+      uint32_t left[2 * kNT];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         T* to = at<T, DV>(p, (wave_id() * kDT + t) * 16, wv.perm, 0, nt * 16);
         store_acc(to, s[t][nt]);
         if constexpr (kPlanes == 2) {
-          f32x4 rest;
+          uint32_t second[2];
 #pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const uint32_t h = pack2(s[t][nt][r], s[t][nt][r + 1]);
-            rest[r] = s[t][nt][r] - __uint_as_float(h << 16);
-            rest[r + 1] = s[t][nt][r + 1] - __uint_as_float(h & 0xffff0000u);
+          for (int r = 0; r < 2; ++r) {
+            const float x = s[t][nt][2 * r], y = s[t][nt][2 * r + 1];
+            const uint32_t h = pack2(x, y);
+            const float u = x - __uint_as_float(h << 16), v = y - __uint_as_float(h & 0xffff0000u);
+            second[r] = pack2(u, v);
+            if (third)
+              left[2 * nt + r] = pack2(u - __uint_as_float(second[r] << 16), v - __uint_as_float(second[r] & 0xffff0000u));
           }
-          store_acc(to + kPlane, rest);
+          *reinterpret_cast<uint2*>(to + kPlane) = make_uint2(second[0], second[1]);
         }
       }
+      if constexpr (kPlanes == 2) {
+        if (third) {
+#pragma unroll
+          for (int kk = 0; kk < DV / 32; ++kk) __builtin_memcpy(&third->f[t][kk], left + 4 * kk, 16);
+        }
+      }
+    }
+  }
+  // The sum over this wave's d of y_j[d] (third x_j)[d] for the block's 64 tokens, in lane j; x, y: [token][n], [d].
+  __device__ __forceinline__ static float bilinear(const Third& third, const Places<T, DK>& wk, const Places<T, DV>& wv,
+                                                   const T* x, const T* y) {
+    static_assert(kPlanes == 2 && B::kWaves == 4);
+    if (!mine()) return 0.0f;
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+      for (int t = 0; t < kDT; ++t) {
+        f32x4 acc = zero4();
+#pragma unroll
+        for (int kk = 0; kk < DV / 32; ++kk) acc = mma(third.f[t][kk], frag_row_perm<DV>(wv, x, jt * 16, kk * 32), acc);
+        part[jt] += dot4(acc, load4(at<const T, DK>(y, jt * 16, wk.perm, 0, (wave_id() * kDT + t) * 16)));
+      }
+    // over the 4 rows of lanes, tile jt's sum to row jt
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    auto sum = [](u32x2 v) { return __uint_as_float(v[0]) + __uint_as_float(v[1]); };
+    auto bits = [](float v) { return __float_as_uint(v); };
+    const float even = sum(__builtin_amdgcn_permlane32_swap(bits(part[0]), bits(part[2]), false, false));
+    const float odd = sum(__builtin_amdgcn_permlane32_swap(bits(part[1]), bits(part[3]), false, false));
+    return sum(__builtin_amdgcn_permlane16_swap(bits(even), bits(odd), false, false));
   }
   __device__ __forceinline__ void decay(float e) {
 #pragma unroll
@@ -668,48 +710,6 @@ struct State {
 #pragma unroll
         for (int i = 0; i < kPieces<T>; ++i) s[t][nt] = mma(x, piece[i], s[t][nt]);
       }
-    }
-  }
-  // sum over this wave's d of y_j[d] (S x_j)[d], to float32's precision: the state goes into the product
-  // from its registers, in as many bfloat16 pieces as it has bits.  x: [token][n]; y4(t, jt): this lane's
-  // 4 channels 16 d_tile + 4 g .. of token 16 jt + (lane & 15).  out[j] for the block's tokens.
-  template <typename Y>
-  __device__ __forceinline__ void bilinear(const Places<T, DV>& wv, const T* x, Y&& y4, float* out) const {
-    float part[B::kWaves];
-#pragma unroll
-    for (int jt = 0; jt < B::kWaves; ++jt) part[jt] = 0.0f;
-    if (mine()) {
-#pragma unroll
-      for (int t = 0; t < kDT; ++t) {
-        f32x4 acc[B::kWaves];
-#pragma unroll
-        for (int jt = 0; jt < B::kWaves; ++jt) acc[jt] = zero4();
-#pragma unroll
-        for (int kk = 0; kk < DV / 32; ++kk) {
-          float m[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m[e] = s[t][2 * kk + (e >> 2)][e & 3];
-          Frag<T> piece[kPieces<T>];
-          split(m, piece);
-#pragma unroll
-          for (int jt = 0; jt < B::kWaves; ++jt) {
-            const Frag<T> xb = frag_row_perm<DV>(wv, x, jt * 16, kk * 32);
-#pragma unroll
-            for (int i = 0; i < kPieces<T>; ++i) acc[jt] = mma(piece[i], xb, acc[jt]);
-          }
-        }
-#pragma unroll
-        for (int jt = 0; jt < B::kWaves; ++jt) {
-          const f32x4 y = y4(t, jt);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) part[jt] = __builtin_fmaf(acc[jt][r], y[r], part[jt]);
-        }
-      }
-    }
-#pragma unroll
-    for (int jt = 0; jt < B::kWaves; ++jt) {
-      const float v = sum_rows(part[jt]);
-      if ((threadIdx.x & 63) < 16) out[jt * 16 + (threadIdx.x & 15)] = v;
     }
   }
 };
@@ -1077,7 +1077,10 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
 // Twice the waves of the other kernels: one half (the state waves) carries R, makes dq and the sums a and b, the
 // other (the key waves) dk, dv, the in-block part of dg and dg itself.  A wave of each half owns the same 16 tokens.
 // With one wave doing both, 2 waves per SIMD were all that the registers left, and they waited 57 % of the time
-// (32 x 3136 tokens, 8 heads of 64 x 64, bfloat16: 380 us, so 344).
+// (32 x 3136 tokens, 8 heads of 64 x 64, bfloat16: 380 us, so 344).  a and b are dot products with the first terms
+// of dq and dk, which the accumulators hold (337 us; 344 with the states multiplied once more in all of their bits);
+// for bfloat16 those have 16 bits of S and R, and the state waves add what the last 8 make (with 16 bits alone, 311
+// us, dg was off by 1.6e-6 of its norm, with all by 1.5e-7).
 
 // The gradient's workgroup: a block's tokens as in B, twice the waves.
 template <typename B>
@@ -1100,7 +1103,8 @@ struct GradLds {
   __align__(16) T os[B::kC * DV];
   __align__(16) T ss[(kBoth ? 2 : 1) * kState];
   __align__(16) Decays<B::kC> decays[2];
-  float rows[B::kWaves][B::kC], into[B::kWaves][B::kC], after[B::kWaves][B::kC];
+  float rows[B::kWaves][B::kC], into[B::kC], after[B::kC];
+  float thirds[S::kPlanes == 2 ? 2 : 1][B::kWaves][B::kC];  // into's and after's parts from the states' last bits
   float across[2][B::kWaves];  // written before the barrier that the wave with the last block's has to pass
   __device__ __forceinline__ T* rs() { return kBoth ? ss + kState : ss; }
 };
@@ -1199,13 +1203,15 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
       y = sum_rows(row_sum(y));
       if ((threadIdx.x & 63) == 0) lds.across[c & 1][wave] = y;
     }
-    old.publish(wv, lds.ss);
-    if constexpr (kBoth) st.publish(wv, lds.rs());
+    constexpr bool kThirds = S::kPlanes == 2;
+    typename S::Third third[2];
+    old.publish(wv, lds.ss, kThirds ? &third[0] : nullptr);
+    if constexpr (kBoth) st.publish(wv, lds.rs(), kThirds ? &third[1] : nullptr);
     __syncthreads();
-    const int d0 = wave * S::kDT * 16;
-    old.bilinear(wv, lds.os,
-                 [&](int t, int jt) { return load4(at<T, DK>(lds.qs, jt * 16, wk.perm, 0, d0 + t * 16)); },
-                 lds.into[wave]);
+    if constexpr (kThirds) {
+      lds.thirds[0][wave][l] = S::bilinear(third[0], wk, wv, lds.os, lds.qs);
+      if constexpr (kBoth) lds.thirds[1][wave][l] = S::bilinear(third[1], wk, wv, lds.vs, lds.ks);
+    }
     // dq of this wave's 16 queries: column i of every result tile
     if (t0 + wave * 16 < w.live) {
       const int i0 = wave * 16, i = i0 + li;
@@ -1215,6 +1221,7 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
       for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<DV>(wv, lds.os, i0, kk * 32);
       f32x4 acc[DT];
       const float e0 = d.from0[i] * a.scale;
+      float into = 0.0f;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         acc[dt] = zero4();
@@ -1223,8 +1230,11 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
 #pragma unroll
           for (int kk = 0; kk < DV / 32; ++kk)
             acc[dt] = mma(frag_row<DV>(wv, lds.ss + pl * S::kPlane, dt * 16, kk * 32), of[kk], acc[dt]);
+        into += dot4(acc[dt], load4(at<T, DK>(lds.qs, i0, wk.perm, 0, dt * 16)));
         acc[dt] *= e0;
       }
+      into = sum_rows(into);
+      if (l < 16) lds.into[i] = into;
 #pragma unroll
       for (int jj = 0; jj < C / 32; ++jj) {
         if (jj > wave / 2) break;
@@ -1268,16 +1278,14 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
     }
     if constexpr (!kBoth) {
       __syncthreads();
-      st.publish(wv, lds.rs());
+      st.publish(wv, lds.rs(), kThirds ? &third[1] : nullptr);
       __syncthreads();
+      if constexpr (kThirds) lds.thirds[1][wave][l] = S::bilinear(third[1], wk, wv, lds.vs, lds.ks);
     }
     if (c > w.c0) {
       tiles.skip(-1);
       tiles.load(t0 - C);
     }
-    st.bilinear(wv, lds.vs,
-                [&](int t, int jt) { return load4(at<T, DK>(lds.ks, jt * 16, wk.perm, 0, d0 + t * 16)); },
-                lds.after[wave]);
     st.decay(d.from0[C - 1]);
 #pragma unroll
     for (int kk = C / 32 - 1; kk >= 0; --kk) {
@@ -1423,6 +1431,7 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
       __syncthreads();
       __syncthreads();
     }
+    float after = 0.0f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
       f32x4 s = zero4();
@@ -1431,8 +1440,11 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
 #pragma unroll
         for (int kk = 0; kk < DV / 32; ++kk)
           s = mma(frag_row<DV>(wv, lds.rs() + pl * S::kPlane, dt * 16, kk * 32), vf[kk], s);
+      after += dot4(s, load4(at<T, DK>(lds.ks, j0, wk.perm, 0, dt * 16)));
       ak[dt] += s * toC;
     }
+    after = sum_rows(after);
+    if (l < 16) lds.after[j] = after;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 s = zero4();
@@ -1457,10 +1469,14 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
       const bool mine = l < C && t0 + l < w.live;
       float from = 0.0f, before = 0.0f, y = 0.0f;
       if (mine) {
+        from = lds.into[l];
+        before = lds.after[l];
+        if constexpr (S::kPlanes == 2) {
 #pragma unroll
-        for (int i = 0; i < B::kWaves; ++i) {
-          from += lds.into[i][l];
-          before += lds.after[i][l];
+          for (int i = 0; i < B::kWaves; ++i) {
+            from += lds.thirds[0][i][l];
+            before += lds.thirds[1][i][l];
+          }
         }
         from *= a.scale * d.from0[l];
         before *= d.toC[l];
