@@ -62,7 +62,9 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("linattn_grad_kernelItLi64ELi64E", 4),
     ("linattn_step_kernel", 6),
 ]
-SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64)]  # bytes per lane
+# Bytes per lane.  linattn_grad: eight registers of its key waves, spilled once a block; with 2 waves per SIMD and no
+# scratch it takes 380 us instead of 337 (32 x 3136 tokens, 8 heads).
+SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E", 32)]
 
 
 def kernel_resources(report):
