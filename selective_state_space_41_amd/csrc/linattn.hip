@@ -774,6 +774,7 @@ __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p
 // ---------------------------------------------------------------------------------------------
 // A segment's own state from a zero start: forward (k, v) or, BACK, the state's gradient (q, dout)
 // from a zero end.  KEEP also writes the state before each block.
+// Bound by HBM with the state's update beside it: 8 x 6085 tokens, 6 heads of 128 x 64, 2 key heads, bfloat16: 31 us.
 
 template <typename T, int DK, int DV, bool BACK, bool KEEP, int C = BlockOf<T, DK, DV>::kC>
 __device__ __forceinline__ void segment_walk(const LinArgs& a, uint32_t id, uint32_t n_ids, T* ys, T* xs,
@@ -853,7 +854,8 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) voi
 }
 
 // The gradient's two passes, which do not depend on each other, in one launch: the first half of the
-// workgroups walks from the end.
+// workgroups walks from the end.  Bound by HBM: 32 x 3136 tokens, 8 heads of 64 x 64, bfloat16, read 411 MB and
+// write 206 MB of states in 121 us, 5.1 TB/s.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_passes_kernel(LinArgs a) {
   constexpr int C = BlockOf<T, DK, DV>::kC;
@@ -869,6 +871,7 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) voi
 
 // In place: each segment's own state becomes the state that enters it (BACK: the gradient at its
 // end).  A thread owns 4 elements of one (sequence, head) and has 8 segments on their way at a time.
+// Latency bound: 10 segments of 48 states of 128 x 64, 8 us.
 template <bool BACK>
 __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) {
   const int per = DK * a.ld / 4;
@@ -909,6 +912,11 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
 
 // ---------------------------------------------------------------------------------------------
 // forward
+//
+// A wave owns 16 queries of a block and a part of the state's rows.  Keys and values come one block ahead through
+// registers; a deeper prefetch or both of them in LDS twice would cost a workgroup per CU.  Bound by the chain of
+// dependent products of a block and by LDS: 128 x 197 tokens, 6 heads of 64 x 64, bfloat16: 26.8 us, 3.4 TB/s;
+// 8 x 6085, 6 heads of 128 x 64: 68 us after the segments' 31 and the prefix's 8; float32 1 x 197: 9 us after 5.
 
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
@@ -1081,6 +1089,9 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
 // of dq and dk, which the accumulators hold (337 us; 344 with the states multiplied once more in all of their bits);
 // for bfloat16 those have 16 bits of S and R, and the state waves add what the last 8 make (with 16 bits alone, 311
 // us, dg was off by 1.6e-6 of its norm, with all by 1.5e-7).
+// What bounds it now is instruction issue: of its cycles vector instructions take 58 %, LDS 36 %, the matrix cores 24 %.
+// Float32, 2 x 1001 tokens, 8 heads of 32 x 128: 35 us, bound by a block's chain of float32 products, whose rate is
+// an eighteenth of bfloat16's.
 
 // The gradient's workgroup: a block's tokens as in B, twice the waves.
 template <typename B>
@@ -1524,7 +1535,8 @@ __global__ __launch_bounds__((Pairs<BlockOf<T, DK, DV>>::kThreads)) __attribute_
 }
 
 // dq and dk of a shared head: the sum over the heads that read it, rounded once.  `in` is [tokens]
-// [heads][dim] float32, `out` [tokens][heads / share][dim]; a thread takes 4 channels.
+// [heads][dim] float32, `out` [tokens][heads / share][dim]; a thread takes 4 channels.  2002 tokens, 8 heads of 32
+// on 2: 4.8 us for 5 MB, mostly the launch.
 template <typename T>
 __global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restrict__ in_q, T* __restrict__ out_q,
                                                             const float* __restrict__ in_k, T* __restrict__ out_k,
@@ -1543,7 +1555,7 @@ __global__ __launch_bounds__(256) void linattn_share_kernel(const float* __restr
 }
 
 // The gradient of a decay that all tokens of a head share: kDecayParts partial sums of dg, then
-// their sum, each in a fixed order; few tokens in one go.
+// their sum, each in a fixed order; few tokens in one go (2002 tokens, 8 heads: 4 us, one launch less).
 constexpr int kDecayParts = 64;
 constexpr int64_t kDecayTokens = 4096;  // up to here one launch sums them
 __global__ __launch_bounds__(256) void linattn_decay_kernel(const float* __restrict__ in, float* __restrict__ out,
@@ -1580,7 +1592,8 @@ struct StepArgs {
 
 // One workgroup per (sequence, head, 64 columns): 16 lanes hold 4 columns each, 16 rows at a time, all ROWS /
 // 16 of them on their way at once.  The state is read once and written once in 16-byte accesses, which is all
-// the time there is to it; the products are float32.
+// the time there is to it; the products are float32.  256 sequences, 12 heads of 64 x 64: 18 us a call for 101 MB,
+// 5.5 TB/s (a part of the states is still in the 256 MB cache).
 template <typename T, int ROWS>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6))) void linattn_step_kernel(StepArgs a) {
   constexpr int kN = ROWS / 16;
@@ -1685,8 +1698,8 @@ int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
 // / whole: 8 x 6085 tokens, 6 heads of 128 x 64, bfloat16: 101 (10 segments) / over 500; 1 x 6085, 6 of 64 x 64:
 // 32 (32 segments, halves of the channels) / 282; 1 x 197, 6 of 64 x 64: bfloat16 11.4 (halves) / 14.2, float32 13.0
 // (halves, 4 segments) / 26.8; 128 x 197, 6 of 64 x 64: 24.6 (whole) / 50 in 2 segments, 30 in halves.
-// The gradient needs all channels of a token together and is only cut into segments: 32 x 3136, 8 of 64 x 64:
-// 475 (2 segments) / 649; 1 x 197, 6 of 64 x 64: 24 (4 segments) / 43.
+// The gradient needs all channels of a token together and is only cut into segments: 32 x 3136, 8 of 64 x 64, bfloat16:
+// 460 (2 segments) / 520 whole; 2 x 1001, 8 of 32 x 128, float32: 49 / 239 (passes and walk).
 Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
   Plan best{};
   double least = 0.0;

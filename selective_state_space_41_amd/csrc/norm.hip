@@ -6,7 +6,8 @@
 // store, so x and the residual are read once and nothing but the outputs is written.  The sum of
 // squares, the scale's maximum and the gradient's dot product are float32 butterflies over the
 // row's lanes.  Bound by HBM: the arithmetic is about 6 (forward) or 12 (gradient) operations for
-// 8 or more bytes.
+// 8 or more bytes.  Measured: 48680 x 768 bfloat16 with residual to 8 bits, 262 MB in 60 us, 4.4 TB/s;
+// gradient of 25216 x 384 bfloat16 with a float32 residual, 155 MB in 28 us, and 4 us for dw's partial rows.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -23,7 +24,9 @@ constexpr float kFp8Max = 448.0f;         // largest finite e4m3 value
 constexpr float kMinScale = 1.17549435e-38f;  // a smaller scale would have no finite reciprocal
 constexpr int kGroupLanes = 16;           // a group of 128 channels: 16 lanes' runs of 8
 constexpr int kMaxDim = 16 * 64 * 4 * 8;  // 16 waves, 4 runs of 8 per lane
-constexpr int kFwdBlocks = 1 << 20;       // forward: a workgroup per rows; only past this do they go round
+// Forward: a workgroup per rows, 60 us on 48680 x 768 (a fixed grid that goes round over the rows: 68); only past this many
+// do they go round.
+constexpr int kFwdBlocks = 1 << 20;
 // Gradient: workgroups that go round over the rows, each with a partial row of the weight's gradient (2048 of
 // them measured 50 us instead of 38 on 25216 x 384).
 constexpr int kBwdBlocks = 1024;

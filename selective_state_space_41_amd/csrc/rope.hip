@@ -4,7 +4,8 @@
 // Bound by HBM: every element is read and written once.  A thread owns one unit of channels of one
 // token (V channels of each half, or V channels in neighbouring pairs), computes the unit's sines
 // and cosines once and applies them to its share of the token's query and key heads; the trigonometry
-// is thus paid once per token and pair, not per head.
+// is thus paid once per token and pair, not per head.  Measured: 128 x 197 tokens, 6 + 6 heads of 64, bfloat16,
+// 77 MB in 16.2 us (partly from the 256 MB cache); 12544 tokens, 12 + 4 heads of 128, float32, 205 MB in 43 us, 4.8 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -153,7 +154,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   if (a.k.heads) rope_heads<T, V, INTERLEAVED>(a.k, b, t, share, a.shares, at, half, c, s);
 }
 
-// Threads wanted before a token's heads stay with one thread: about 8 waves on every SIMD.
+// Threads wanted before a token's heads stay with one thread: about 8 waves on every SIMD.  Measured on those two
+// shapes, us: 128 K threads 17.4 and 43.6, 300 K 18.0 and 40.5, 512 K 17.6 and 42.8, 2 M 19.2 and 62.
 constexpr int64_t kWantThreads = 256 * 4 * 8 * 64;
 
 template <typename T, int V, bool INTERLEAVED>
@@ -172,11 +174,12 @@ vmscan_status launch_rope(RopeArgs a, hipStream_t stream) {
 }
 
 bool runs_aligned(const RopeTensor& x, int64_t n) {
-  return aligned_to(x.in, 16) && aligned_to(x.out, 16) && x.ib % n == 0 && x.it % n == 0 && x.ih % n == 0 && x.ob % n == 0 && x.ot % n == 0 && x.oh % n == 0;
+  return aligned_to(x.in, 16) && aligned_to(x.out, 16) && x.ib % n == 0 && x.it % n == 0 && x.ih % n == 0 &&
+         x.ob % n == 0 && x.ot % n == 0 && x.oh % n == 0;
 }
 
 // The unit of channels: 16 bytes when every run of that size starts on a 16-byte boundary and the rotated
-// channels and the rest are whole runs, else one pair.
+// channels and the rest are whole runs, else one pair (the 205 MB of float32 above: 43 us, 58 in 32-byte units).
 template <typename T>
 vmscan_status run_rope(const RopeArgs& a, int interleaved, hipStream_t stream) {
   constexpr int kRun = 16 / sizeof(T);
