@@ -238,6 +238,20 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, want) and torch.equal(state[-1], one[0]) and torch.equal(state[0], one[1])
 
 
+def test_largest_token_stride():
+    """Float32 tokens 2^24 - 4 elements apart: a block's offsets reach 4.2e9 bytes, the most that is accepted."""
+    T, stride = 67, 2 ** 24 - 4
+    p = make(27, 1, T, 1, 1, 32, 64, "f32")
+    big = torch.empty(stride * (T - 1) + 256, dtype=torch.float32, device="cuda")
+    t = {}
+    for i, key in enumerate(("q", "k", "v", "dout")):
+        x = dev(p, key)
+        t[key] = big[64 * i:].as_strided(x.shape, (0, stride, 0, 1))
+        t[key].copy_(x)
+    print("[linattn] largest token stride", flush=True)
+    run_both("largest stride", p, **t)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("H,Hk,dk,dv,decay", [(1, 1, 8, 8, "token"), (6, 2, 64, 64, "head"), (2, 1, 128, 128, "token"),
                                               (3, 3, 24, 72, "token"), (4, 4, 16, 128, "head")])
