@@ -62,9 +62,9 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("linattn_grad_kernelItLi64ELi64E", 4),
     ("linattn_step_kernel", 6),
 ]
-# Bytes per lane.  linattn_grad: eight registers of its key waves, spilled once a block; with 2 waves per SIMD and no
-# scratch it takes 380 us instead of 337 (32 x 3136 tokens, 8 heads).
-SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E", 32)]
+# Bytes per lane.  linattn_grad: twelve registers of its key waves, spilled once a block; with 2 waves per SIMD and no
+# scratch the call takes 476 us instead of 424 (32 x 3136 tokens, 8 heads).
+SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E", 48)]
 
 
 def kernel_resources(report):

@@ -24,13 +24,11 @@
 // wave reads, go from global memory straight to operands.  The float32 path has the same structure with
 // the 16 x 16 x 4 float32 instruction, eight per product, and plain LDS reads.
 //
-// Rounding for bfloat16 activations.  Accumulators and carried states are float32.  Where the state, the
-// scores or their gradients enter a product whose result is rounded to bfloat16 (o, dq, dk, dv), they
-// are two bfloat16 numbers, the rounded value and what the rounding left (16 bits): with one alone o's
-// error was 1.5 times its own rounding's.  Where the result stays float32 (the states, their gradients,
-// the decays' gradient), the operand that is not a plain activation is three bfloat16 numbers, which
-// hold all of its 24 bits: with two the decays' gradient was off by 2.6e-6 of its largest value, with
-// three by under 5e-7.
+// Rounding for bfloat16 activations.  Everything is float32 until an output's one rounding.  An operand that is
+// not a plain activation (the state and its gradient, the scores and theirs, weighted keys and queries) enters the bfloat16
+// products as three bfloat16 numbers, which hold all of its 24 bits.  With two (16 bits, up to 2^-18 of a term) an
+// output whose terms cancel to 2^-12 of themselves was off by 1 % instead of its rounding's 0.2 %, and the decays'
+// gradient by 2.6e-6 of its largest value instead of under 5e-7.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -118,8 +116,15 @@ struct Places {
     }
   }
   // Called at the top of a loop: the places with their constants are then made in the loop, where they are
-  // used, and do not take its registers (the constants' many combinations would).
-  __device__ __forceinline__ void here() { asm volatile("" : "+v"(row), "+v"(perm), "+v"(col), "+v"(col_row)); }
+  // used, and do not take its registers (the constants' many combinations would).  Only for those that it uses: each
+  // takes a register all the way.
+  template <bool ROW = true, bool PERM = true, bool COL = true, bool COL_ROW = true>
+  __device__ __forceinline__ void here() {
+    if constexpr (ROW) asm volatile("" : "+v"(row));
+    if constexpr (PERM) asm volatile("" : "+v"(perm));
+    if constexpr (COL) asm volatile("" : "+v"(col));
+    if constexpr (COL_ROW) asm volatile("" : "+v"(col_row));
+  }
 };
 // base with `r` more rows and `col` more elements; the tile's rows start at row0, a multiple of 16.
 template <typename T, int D>
@@ -158,6 +163,19 @@ __device__ __forceinline__ Frag32 frag_row_perm(const Places<float, D>& w, const
   __builtin_memcpy(f.v, __builtin_assume_aligned(at<const float, D>(tile, row0, w.perm, 0, col), 16), 16);
   __builtin_memcpy(f.v + 4, __builtin_assume_aligned(at<const float, D>(tile, row0, w.perm, 0, col + 16), 16), 16);
   return f;
+}
+
+// An operand in that order back into a row-major tile, to be read by its columns.
+template <int D>
+__device__ __forceinline__ void put_row_perm(const Places<uint16_t, D>& w, uint16_t* tile, int row0, int col, const bf16x8& f) {
+  const uint4 u = __builtin_bit_cast(uint4, f);
+  *reinterpret_cast<uint2*>(at<uint16_t, D>(tile, row0, w.perm, 0, col)) = make_uint2(u.x, u.y);
+  *reinterpret_cast<uint2*>(at<uint16_t, D>(tile, row0, w.perm, 0, col + 16)) = make_uint2(u.z, u.w);
+}
+template <int D>
+__device__ __forceinline__ void put_row_perm(const Places<float, D>& w, float* tile, int row0, int col, const Frag32& f) {
+  __builtin_memcpy(__builtin_assume_aligned(at<float, D>(tile, row0, w.perm, 0, col), 16), f.v, 16);
+  __builtin_memcpy(__builtin_assume_aligned(at<float, D>(tile, row0, w.perm, 0, col + 16), 16), f.v + 4, 16);
 }
 
 // Operand whose contracted index runs down the LDS column: lane (i, g) holds column col + i, rows
@@ -253,23 +271,6 @@ __device__ __forceinline__ void split(const float (&x)[8], bf16x8 (&f)[3]) {
 __device__ __forceinline__ void split(const float (&x)[8], Frag32 (&f)[1]) { __builtin_memcpy(f[0].v, x, sizeof(x)); }
 template <typename T>
 constexpr int kPieces = sizeof(T) == 2 ? 3 : 1;
-
-// Eight scores (two result tiles, rows 16 t + 4 g + r) as an operand in frag_col's order, in two parts: the
-// rounded ones and what the rounding left.  One part alone would add as much error to a bfloat16 output as its
-// own rounding does, and all of a token's channels would have the same one.
-__device__ __forceinline__ void pack_parts(const float (&x)[8], bf16x8 (&f)[2]) {
-  uint32_t h[4], r[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    h[e] = pack2(x[2 * e], x[2 * e + 1]);
-    r[e] = pack2(x[2 * e] - __uint_as_float(h[e] << 16), x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
-  }
-  f[0] = __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
-  f[1] = __builtin_bit_cast(bf16x8, make_uint4(r[0], r[1], r[2], r[3]));
-}
-__device__ __forceinline__ void pack_parts(const float (&x)[8], Frag32 (&f)[1]) { split(x, f); }
-template <typename T>
-constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
 
 // Sums and scans over the 16 lanes of a row with lane-rotating adds, over the 4 rows (g) of a wave
 // with row swaps: no LDS round trips.
@@ -370,6 +371,11 @@ struct Block {
 };
 template <typename T, int DK, int DV>
 using BlockOf = Block<waves_of(sizeof(T), DK, DV)>;
+
+// Whether the gradient's walk reads the state that enters a part of a segment again for each block instead of keeping it:
+// where R alone takes 64 registers (float32: 128) of a wave.  Call, us, read again / kept: bfloat16 4 x 2048 tokens, 8 heads of
+// 128 x 128 174 / 202, float32 4 x 1024 183 / 270; heads of 64 x 64 have registers for both.
+constexpr bool rereads(int dk, int dv) { return dk == 128 && dv == 128; }
 
 // Waves per SIMD that a kernel's registers must leave room for, where LDS does too: bfloat16 heads; the others need
 // their registers.
@@ -579,12 +585,13 @@ struct State {
   __device__ __forceinline__ static uint32_t place_of(int ld) {  // of [0][0], in bytes
     return (static_cast<uint32_t>(d_of(0)) * ld + n_of(0)) * 4;
   }
-  __device__ __forceinline__ void load(const float* p, int dk, int dv, int ld) {
+  // tiles nt0 .. nt1 - 1 of each row of them
+  __device__ __forceinline__ void load(const float* p, int dk, int dv, int ld, int nt0 = 0, int nt1 = kNT) {
     const Buffer from(p);
 #pragma unroll
     for (int t = 0; t < kDT; ++t)
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int nt = nt0; nt < nt1; ++nt)
         s[t][nt] = __builtin_bit_cast(
             f32x4, from.load16(p && d_of(t) < dk && n_of(nt) < dv ? place_of(ld) : kNowhere, (t * 16 * ld + nt * 16) * 4));
   }
@@ -622,66 +629,39 @@ struct State {
         }
     }
   }
-  // into LDS as an operand, [d][n]; bfloat16 with what the rounding left in a second plane
+  // into LDS as an operand, [d][n]: for bfloat16 three planes, each the rounded rest of those before.  Planes
+  // FROM .. TO - 1, one after the other from p.
   static constexpr int kPlane = DK * DV;
-  static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;
-  // What the second rounding left (8 bits more, all that there are), as operands of rows d, n in frag_col's order.
-  struct Third {
-    bf16x8 f[kPlanes == 2 ? kDT : 1][DV / 32];
-  };
-  __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p, Third* third = nullptr) const {
+  static constexpr int kPlanes = kPieces<T>;
+  template <int FROM = 0, int TO = kPlanes>
+  __device__ __forceinline__ void publish(const Places<T, DV>& wv, T* p) const {
     if (!mine()) return;
 #pragma unroll
-    for (int t = 0; t < kDT; ++t) {
-      uint32_t left[2 * kNT];
+    for (int t = 0; t < kDT; ++t)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         T* to = at<T, DV>(p, (wave_id() * kDT + t) * 16, wv.perm, 0, nt * 16);
-        store_acc(to, s[t][nt]);
-        if constexpr (kPlanes == 2) {
-          uint32_t second[2];
+        if constexpr (kPlanes == 1) {
+          store_acc(to, s[t][nt]);
+        } else {
+          f32x4 rest = s[t][nt];
+          if constexpr (FROM > 0) asm volatile("" : "+v"(rest));  // the rests are made again, not kept since the planes before
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float x = s[t][nt][2 * r], y = s[t][nt][2 * r + 1];
-            const uint32_t h = pack2(x, y);
-            const float u = x - __uint_as_float(h << 16), v = y - __uint_as_float(h & 0xffff0000u);
-            second[r] = pack2(u, v);
-            if (third)
-              left[2 * nt + r] = pack2(u - __uint_as_float(second[r] << 16), v - __uint_as_float(second[r] & 0xffff0000u));
+          for (int pl = 0; pl < TO; ++pl) {
+            const uint32_t lo = pack2(rest[0], rest[1]), hi = pack2(rest[2], rest[3]);
+            if (pl >= FROM) *reinterpret_cast<uint2*>(to + (pl - FROM) * kPlane) = make_uint2(lo, hi);
+            rest[0] -= __uint_as_float(lo << 16), rest[1] -= __uint_as_float(lo & 0xffff0000u);
+            rest[2] -= __uint_as_float(hi << 16), rest[3] -= __uint_as_float(hi & 0xffff0000u);
           }
-          *reinterpret_cast<uint2*>(to + kPlane) = make_uint2(second[0], second[1]);
         }
       }
-      if constexpr (kPlanes == 2) {
-        if (third) {
-#pragma unroll
-          for (int kk = 0; kk < DV / 32; ++kk) __builtin_memcpy(&third->f[t][kk], left + 4 * kk, 16);
-        }
-      }
-    }
   }
-  // The sum over this wave's d of y_j[d] (third x_j)[d] for the block's 64 tokens, in lane j; x, y: [token][n], [d].
-  __device__ __forceinline__ static float bilinear(const Third& third, const Places<T, DK>& wk, const Places<T, DV>& wv,
-                                                   const T* x, const T* y) {
-    static_assert(kPlanes == 2 && B::kWaves == 4);
-    if (!mine()) return 0.0f;
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // Rows d of this wave's tile t as operands, n in frag_col's order, 32 from n0.
+  __device__ __forceinline__ void rows(int t, int n0, Frag<T> (&piece)[kPieces<T>]) const {
+    float x[8];
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-      for (int t = 0; t < kDT; ++t) {
-        f32x4 acc = zero4();
-#pragma unroll
-        for (int kk = 0; kk < DV / 32; ++kk) acc = mma(third.f[t][kk], frag_row_perm<DV>(wv, x, jt * 16, kk * 32), acc);
-        part[jt] += dot4(acc, load4(at<const T, DK>(y, jt * 16, wk.perm, 0, (wave_id() * kDT + t) * 16)));
-      }
-    // over the 4 rows of lanes, tile jt's sum to row jt
-    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-    auto sum = [](u32x2 v) { return __uint_as_float(v[0]) + __uint_as_float(v[1]); };
-    auto bits = [](float v) { return __float_as_uint(v); };
-    const float even = sum(__builtin_amdgcn_permlane32_swap(bits(part[0]), bits(part[2]), false, false));
-    const float odd = sum(__builtin_amdgcn_permlane32_swap(bits(part[1]), bits(part[3]), false, false));
-    return sum(__builtin_amdgcn_permlane16_swap(bits(even), bits(odd), false, false));
+    for (int r = 0; r < 4; ++r) x[r] = s[t][n0 / 16][r], x[4 + r] = s[t][n0 / 16 + 1][r];
+    split(x, piece);
   }
   __device__ __forceinline__ void decay(float e) {
 #pragma unroll
@@ -1035,13 +1015,13 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
             for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
           }
         }
-        Frag<T> pf[kParts<T>];
-        pack_parts(p, pf);
+        Frag<T> pf[kPieces<T>];
+        split(p, pf);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const Frag<T> x = xa[nt];
 #pragma unroll
-          for (int i = 0; i < kParts<T>; ++i) acc[nt] = mma(x, pf[i], acc[nt]);
+          for (int i = 0; i < kPieces<T>; ++i) acc[nt] = mma(x, pf[i], acc[nt]);
         }
       }
       float m[8];
@@ -1083,15 +1063,17 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
 
 //
 // Twice the waves of the other kernels: one half (the state waves) carries R, makes dq and the sums a and b, the
-// other (the key waves) dk, dv, the in-block part of dg and dg itself.  A wave of each half owns the same 16 tokens.
-// With one wave doing both, 2 waves per SIMD were all that the registers left, and they waited 57 % of the time
-// (32 x 3136 tokens, 8 heads of 64 x 64, bfloat16: 380 us, so 344).  a and b are dot products with the first terms
-// of dq and dk, which the accumulators hold (337 us; 344 with the states multiplied once more in all of their bits);
-// for bfloat16 those have 16 bits of S and R, and the state waves add what the last 8 make (with 16 bits alone, 311
-// us, dg was off by 1.6e-6 of its norm, with all by 1.5e-7).
-// What bounds it now is instruction issue: of its cycles vector instructions take 58 %, LDS 36 %, the matrix cores 24 %.
+// other (the key waves) dk, dv, the in-block part of dg and dg itself.  A key wave owns 16 tokens, a state wave the
+// rows d of S and R that it holds.  With one wave doing both, 2 waves per SIMD were all that the registers left, and they waited
+// 57 % of the time.  a and b are dot products with the first terms of dq and dk, which the accumulators hold.
+//
+// Six planes of states (S and R in three bfloat16 pieces each) do not fit LDS beside the tiles of 64 x 64 heads for two
+// workgroups on a CU.  So only R is published.  S never leaves its registers: a state wave multiplies its rows with all of the
+// block's dO, which leaves its channels of every query's dq, and X, which that needs whole, comes from the key waves, which
+// make it for dk, through LDS.  (With S's and R's last planes in one place, exchanged within a block, the call took 519 us
+// instead of 424: 32 x 3136 tokens, 8 heads of 64 x 64.)  What bounds it is instruction issue.
 // Float32, 2 x 1001 tokens, 8 heads of 32 x 128: 35 us, bound by a block's chain of float32 products, whose rate is
-// an eighteenth of bfloat16's.
+// a ninth of bfloat16's.
 
 // The gradient's workgroup: a block's tokens as in B, twice the waves.
 template <typename B>
@@ -1105,19 +1087,23 @@ template <typename T, int DK, int DV>
 struct GradLds {
   using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
-  // S and R as operands: side by side where LDS has room for both, else one after the other
-  static constexpr int kState = S::kPlanes * S::kPlane;
-  static constexpr bool kBoth = (2 * B::kC * (DK + DV) + 2 * kState) * sizeof(T) + 8192 <= 160 * 1024;
+  static constexpr int kSmall = 6 * 1024;  // the tables below
+  // R's planes: all of them, or for bfloat16 heads of 128 x 128 two, and the third when they have been read
+  static constexpr int kPlanes =
+      S::kPlanes == 3 && (2 * B::kC * (DK + DV) + 3 * S::kPlane + 3 * 3 * 1024) * sizeof(T) + kSmall > 160 * 1024 ? 2 : S::kPlanes;
+  // X: blocks of 32 keys and 32 queries [key][query], those with a query at or after a key
+  static constexpr int kHalves = B::kC / 32;
+  static constexpr int kX = kHalves * (kHalves + 1) / 2 * 1024;
   __align__(16) T qs[B::kC * DK];
   __align__(16) T ks[B::kC * DK];
   __align__(16) T vs[B::kC * DV];
   __align__(16) T os[B::kC * DV];
-  __align__(16) T ss[(kBoth ? 2 : 1) * kState];
+  __align__(16) T rs[kPlanes * S::kPlane];
+  __align__(16) T xs[kPieces<T> * kX];
   __align__(16) Decays<B::kC> decays[2];
-  float rows[B::kWaves][B::kC], into[B::kC], after[B::kC];
-  float thirds[S::kPlanes == 2 ? 2 : 1][B::kWaves][B::kC];  // into's and after's parts from the states' last bits
-  float across[2][B::kWaves];  // written before the barrier that the wave with the last block's has to pass
-  __device__ __forceinline__ T* rs() { return kBoth ? ss + kState : ss; }
+  float rows[B::kWaves][B::kC], into[B::kWaves][B::kC], after[B::kC];
+  float across[B::kWaves];
+  __device__ __forceinline__ T* x(int keys, int queries, int piece) { return xs + piece * kX + (keys + queries) * 1024; }
 };
 
 // q, k, v and dout of a block on their way to LDS.
@@ -1151,36 +1137,51 @@ struct GradTiles {
   }
 };
 
-// The two halves pass the same barriers: one when a block's tiles are in LDS, two around the exchange of S for R
-// (where LDS holds one of them), one when the block is done.
+// The two halves pass the same barriers: one when a block's tiles and R's planes are in LDS, one when X is, one when the
+// block is done; where LDS holds two of R's three planes, two more around the exchange for the third.
 template <typename T, int DK, int DV>
 __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, GradLds<T, DK, DV>& lds) {
   using B = BlockOf<T, DK, DV>;
   using S = State<T, DK, DV>;
   constexpr int C = B::kC;
-  constexpr int DT = DK / 16, NT = DV / 16;
-  constexpr bool kBoth = GradLds<T, DK, DV>::kBoth;
+  constexpr int NT = DV / 16, kTiles = C / 16;
+  constexpr int kPlanes = GradLds<T, DK, DV>::kPlanes;
   const int wave = wave_id();
   const int kt = a.heads * a.dk;
   const int64_t kbase = (w.b * a.seqlen * a.heads + w.h) * a.dk;
   GradTiles<T, DK, DV> tiles(a, w);
   Places<T, DK> wk;
   Places<T, DV> wv;
-  S st, first;  // R; the state that enters the part of the segment
+  Places<T, 32> wx;
+  S st;  // R
+  // The state that enters the part of the segment: kept, or read again for each block (never with a chain, which would have
+  // to sum it up each time).
+  constexpr bool kReload = rereads(DK, DV);
+  S first;
+  const float* first_at = nullptr;
+  int first_dk = DK, first_dv = DV;
   const int end = (w.seg + 1) * a.subs < a.parts ? (w.seg + 1) * a.subs : a.parts;
   const int64_t part0 = w.bh * a.parts;
-  if (a.parts > 1 && !a.chain) {
+  const bool summed = a.parts > 1 && (kReload || !a.chain);  // by the prefix kernels
+  if (summed) {
     st.load(a.seg_ds + (part0 + end - 1) * (DK * DV), DK, DV, DV);
   } else {
     st.load(a.dsT ? a.dsT + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-    if (end < a.parts) st.join(a.seg_ds + part0 * (DK * DV), a.seg_dg + part0, a.parts - 1, -1, a.parts - end, DV);
+    if constexpr (!kReload) {
+      if (end < a.parts) st.join(a.seg_ds + part0 * (DK * DV), a.seg_dg + part0, a.parts - 1, -1, a.parts - end, DV);
+    }
   }
-  auto enter = [&](int part, auto ahead) {  // first: the state that enters a part
-    if (a.parts > 1 && !a.chain) {
-      first.load(a.seg_s + (part0 + part) * (DK * DV), DK, DV, DV);
+  auto enter = [&](int part, auto ahead) {
+    if (summed) {
+      first_at = a.seg_s + (part0 + part) * (DK * DV);
     } else {
-      first.load(a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr, a.dk, a.dvd, a.dvd);
-      if (part > 0) first.template join<decltype(ahead)::value>(a.seg_s + part0 * (DK * DV), a.seg_g + part0, 0, 1, part, DV);
+      first_at = a.s0 ? a.s0 + w.bh * a.dk * a.dvd : nullptr;
+      first_dk = a.dk, first_dv = a.dvd;
+    }
+    if constexpr (!kReload) {
+      first.load(first_at, first_dk, first_dv, first_dv);
+      if (!summed && part > 0)
+        first.template join<decltype(ahead)::value>(a.seg_s + part0 * (DK * DV), a.seg_g + part0, 0, 1, part, DV);
     }
   };
   if (w.c0 < w.c1) {
@@ -1191,122 +1192,144 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
   for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
     const Decays<C>& d = lds.decays[c & 1];
-    wk.here();
-    wv.here();
+    wk.template here<false, true, true, false>();
+    wv.template here<false, true, true, false>();
+    wx.template here<false, false, true, false>();
     const int l = lane_here(), li = l & 15, g4 = (l >> 4) * 4;
     const int64_t block = w.bh * a.blocks + c;
     if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1) enter(c / a.per_part, std::integral_constant<int, 1>{});  // few registers
-    S old;  // the state that enters the block
-    old.load(a.states + block * (DK * DV), DK, DV, DV);
+    // The state that enters the block, put together 32 value channels at a time where they are used, kAhead of them on
+    // their way.
+    S old;
+    constexpr int kAhead = kReload ? 1 : DV / 32;
+    const float* kept = a.states + block * (DK * DV);
+#pragma unroll
+    for (int kk = 0; kk < kAhead; ++kk) {
+      old.load(kept, DK, DV, DV, 2 * kk, 2 * kk + 2);
+      if constexpr (kReload) first.load(first_at, first_dk, first_dv, first_dv, 2 * kk, 2 * kk + 2);
+    }
     const float since = __builtin_amdgcn_exp2f(a.block_g[block]);
-    tiles.store(lds);
-    {
-      float y = 0.0f;  // <S, R>, both in this wave's layout
+    float y = 0.0f;  // <S, R>, both in this wave's layout
+    auto whole = [&](int kk) {
 #pragma unroll
       for (int t = 0; t < S::kDT; ++t)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 2 * kk; nt < 2 * kk + 2; ++nt)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             old.s[t][nt][r] = __builtin_fmaf(first.s[t][nt][r], since, old.s[t][nt][r]);
             y = __builtin_fmaf(old.s[t][nt][r], st.s[t][nt][r], y);
           }
-      y = sum_rows(row_sum(y));
-      if ((threadIdx.x & 63) == 0) lds.across[c & 1][wave] = y;
-    }
-    constexpr bool kThirds = S::kPlanes == 2;
-    typename S::Third third[2];
-    old.publish(wv, lds.ss, kThirds ? &third[0] : nullptr);
-    if constexpr (kBoth) st.publish(wv, lds.rs(), kThirds ? &third[1] : nullptr);
+    };
+    tiles.store(lds);
+    st.template publish<0, kPlanes>(wv, lds.rs);
     __syncthreads();
-    if constexpr (kThirds) {
-      lds.thirds[0][wave][l] = S::bilinear(third[0], wk, wv, lds.os, lds.qs);
-      if constexpr (kBoth) lds.thirds[1][wave][l] = S::bilinear(third[1], wk, wv, lds.vs, lds.ks);
+    // dq of all of the block's queries in this wave's channels: column li of tile it is query 16 it + li.  First the states'
+    // part, whose product with q is the decays' sum a.
+    f32x4 acc[S::kDT][kTiles];
+    float part[kTiles];
+#pragma unroll
+    for (int it = 0; it < kTiles; ++it) {
+      part[it] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < S::kDT; ++t) acc[t][it] = zero4();
     }
-    // dq of this wave's 16 queries: column i of every result tile
-    if (t0 + wave * 16 < w.live) {
-      const int i0 = wave * 16, i = i0 + li;
-      const float gh = d.hi[i], gl = d.lo[i];
-      Frag<T> of[DV / 32];
+    if (S::mine()) {
 #pragma unroll
-      for (int kk = 0; kk < DV / 32; ++kk) of[kk] = frag_row<DV>(wv, lds.os, i0, kk * 32);
-      f32x4 acc[DT];
-      const float e0 = d.from0[i] * a.scale;
-      float into = 0.0f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        acc[dt] = zero4();
-#pragma unroll
-        for (int pl = 0; pl < S::kPlanes; ++pl)
-#pragma unroll
-          for (int kk = 0; kk < DV / 32; ++kk)
-            acc[dt] = mma(frag_row<DV>(wv, lds.ss + pl * S::kPlane, dt * 16, kk * 32), of[kk], acc[dt]);
-        into += dot4(acc[dt], load4(at<T, DK>(lds.qs, i0, wk.perm, 0, dt * 16)));
-        acc[dt] *= e0;
-      }
-      into = sum_rows(into);
-      if (l < 16) lds.into[i] = into;
-#pragma unroll
-      for (int jj = 0; jj < C / 32; ++jj) {
-        if (jj > wave / 2) break;
-        float p[8];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int j0 = jj * 32 + t * 16;
-          if (j0 <= i0) {
-            f32x4 dp = zero4();
-#pragma unroll
-            for (int kk = 0; kk < DV / 32; ++kk) dp = mma(frag_row<DV>(wv, lds.vs, j0, kk * 32), of[kk], dp);
-            if (j0 < i0) {
-              const f32x4 e = load4(d.toE + j0 + g4);
-              const float from = d.between(gh, gl, j0 + 15) * a.scale;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) p[t * 4 + r] = dp[r] * (e[r] * from);
-            } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                p[t * 4 + r] = g4 + r <= li ? dp[r] * (d.between(gh, gl, j0 + g4 + r) * a.scale) : 0.0f;
-            }
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[t * 4 + r] = 0.0f;
-          }
+      for (int kk = 0; kk < DV / 32; ++kk) {
+        if (kk + kAhead < DV / 32) {
+          old.load(kept, DK, DV, DV, 2 * (kk + kAhead), 2 * (kk + kAhead) + 2);
+          if constexpr (kReload) first.load(first_at, first_dk, first_dv, first_dv, 2 * (kk + kAhead), 2 * (kk + kAhead) + 2);
         }
-        Frag<T> pf[kParts<T>];
-        pack_parts(p, pf);
+        whole(kk);
+        Frag<T> piece[S::kDT][kPieces<T>];
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const Frag<T> x = frag_col<DK>(wk, lds.ks, jj * 32, dt * 16);
+        for (int t = 0; t < S::kDT; ++t) old.rows(t, kk * 32, piece[t]);
 #pragma unroll
-          for (int i = 0; i < kParts<T>; ++i) acc[dt] = mma(x, pf[i], acc[dt]);
+        for (int it = 0; it < kTiles; ++it) {
+          const Frag<T> o = frag_row_perm<DV>(wv, lds.os, it * 16, kk * 32);
+#pragma unroll
+          for (int pl = 0; pl < kPieces<T>; ++pl)
+#pragma unroll
+            for (int t = 0; t < S::kDT; ++t) acc[t][it] = mma(piece[t][pl], o, acc[t][it]);
         }
       }
-      const uint32_t at = static_cast<uint32_t>(i) * kt + g4;
-      if (a.share == 1)
-        store_tiles(static_cast<T*>(a.dq) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, t0 + i < w.live, acc);
-      else
-        store_tiles(static_cast<float*>(a.dq) + (kbase + static_cast<int64_t>(t0) * kt), at, a.dk, t0 + i < w.live, acc);
+#pragma unroll
+      for (int it = 0; it < kTiles; ++it) {
+        const float e0 = d.from0[it * 16 + li] * a.scale;
+#pragma unroll
+        for (int t = 0; t < S::kDT; ++t) {
+          part[it] += dot4(acc[t][it], load4(at<T, DK>(lds.qs, it * 16, wk.perm, 0, (wave * S::kDT + t) * 16)));
+          acc[t][it] *= e0;
+        }
+      }
     }
-    if constexpr (!kBoth) {
-      __syncthreads();
-      st.publish(wv, lds.rs(), kThirds ? &third[1] : nullptr);
-      __syncthreads();
-      if constexpr (kThirds) lds.thirds[1][wave][l] = S::bilinear(third[1], wk, wv, lds.vs, lds.ks);
+    y = sum_rows(row_sum(y));
+    if (l == 0) lds.across[wave] = y;
+#pragma unroll
+    for (int it = 0; it < kTiles; ++it) {
+      const float into = sum_rows(part[it]);
+      if (l < 16) lds.into[wave][it * 16 + l] = into;
     }
     if (c > w.c0) {
       tiles.skip(-1);
       tiles.load(t0 - C);
     }
-    st.decay(d.from0[C - 1]);
+    auto next = [&]() {  // R before the block
+      st.decay(d.from0[C - 1]);
 #pragma unroll
-    for (int kk = C / 32 - 1; kk >= 0; --kk) {
-      if (t0 + kk * 32 >= w.live) continue;
-      const Cols<T, DV, (S::kDT > 1 && sizeof(T) == 2)> xa(wv, lds.os, kk * 32);
-      float m[8];
-      eight(d.from0 + kk * 32, m);
+      for (int kk = C / 32 - 1; kk >= 0; --kk) {
+        if (t0 + kk * 32 >= w.live) continue;
+        const Cols<T, DV, (S::kDT > 1 && sizeof(T) == 2)> xa(wv, lds.os, kk * 32);
+        float m[8];
+        eight(d.from0 + kk * 32, m);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[e] *= a.scale;
-      st.add(wk, lds.qs, kk * 32, xa, m);
+        for (int e = 0; e < 8; ++e) m[e] *= a.scale;
+        st.add(wk, lds.qs, kk * 32, xa, m);
+      }
+    };
+    if constexpr (kPlanes == S::kPlanes) next();
+    __syncthreads();
+    if (S::mine()) {
+      // then X's: sum_j X_ij k_j
+#pragma unroll
+      for (int jj = 0; jj < C / 32; ++jj) {
+        if (t0 + jj * 32 >= w.live) break;
+        Frag<T> kf[S::kDT];
+#pragma unroll
+        for (int t = 0; t < S::kDT; ++t) kf[t] = frag_col<DK>(wk, lds.ks, jj * 32, (wave * S::kDT + t) * 16);
+#pragma unroll
+        for (int it = jj * 2; it < kTiles; ++it) {
+          if (t0 + it * 16 >= w.live) break;
+#pragma unroll
+          for (int pl = 0; pl < kPieces<T>; ++pl) {
+            const Frag<T> x = frag_col<32>(wx, lds.x(jj, it / 2, pl), 0, it % 2 * 16);
+#pragma unroll
+            for (int t = 0; t < S::kDT; ++t) acc[t][it] = mma(kf[t], x, acc[t][it]);
+          }
+        }
+      }
+      const uint32_t at = static_cast<uint32_t>(li) * kt + g4;
+      auto put = [&](auto* out) {
+        const Buffer to(out);
+#pragma unroll
+        for (int it = 0; it < kTiles; ++it)
+#pragma unroll
+          for (int t = 0; t < S::kDT; ++t) {
+            const int ch = (wave * S::kDT + t) * 16;
+            to.store(out, acc[t][it], t0 + it * 16 + li < w.live && ch + g4 < a.dk
+                         ? (at + static_cast<uint32_t>(it * 16) * kt + ch) * static_cast<uint32_t>(sizeof(*out)) : kNowhere, 0);
+          }
+      };
+      const int64_t first_query = kbase + static_cast<int64_t>(t0) * kt;
+      if (a.share == 1) put(static_cast<T*>(a.dq) + first_query);
+      else put(static_cast<float*>(a.dq) + first_query);
+    }
+    if constexpr (kPlanes < S::kPlanes) {
+      __syncthreads();
+      st.template publish<2, 3>(wv, lds.rs);
+      __syncthreads();
+      next();
     }
     __syncthreads();
   }
@@ -1319,7 +1342,7 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
   using S = State<T, DK, DV>;
   constexpr int C = B::kC;
   constexpr int DT = DK / 16, NT = DV / 16;
-  constexpr bool kBoth = GradLds<T, DK, DV>::kBoth;
+  constexpr int kPlanes = GradLds<T, DK, DV>::kPlanes;
   const int wave = wave_id() - B::kWaves;
   const float* g = a.g + w.b * a.gb + w.h * a.gh;
   const int kt = a.heads * a.dk;
@@ -1330,6 +1353,7 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
   GradTiles<T, DK, DV> tiles(a, w);
   Places<T, DK> wk;
   Places<T, DV> wv;
+  Places<T, 32> wx;
   float gx = 0.0f;
   if (w.c0 < w.c1) {
     tiles.skip(w.c1 - 1);
@@ -1340,8 +1364,9 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
   for (int c = w.c1 - 1; c >= w.c0; --c) {
     const int t0 = c * C;
     const Decays<C>& d = lds.decays[c & 1];
-    wk.here();
-    wv.here();
+    wk.template here<true, true, true, false>();
+    wv.template here<true, false, true, true>();
+    wx.template here<false, true, false, false>();
     const int l = lane_here(), li = l & 15, g4 = (l >> 4) * 4;
     tiles.store(lds);
     __syncthreads();
@@ -1362,6 +1387,29 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
     for (int dt = 0; dt < DT; ++dt) ak[dt] = zero4();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) av[nt] = zero4();
+    float after = 0.0f;
+    auto states = [&](auto from, auto to) {  // the products with planes from .. to - 1 of R
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        f32x4 s = zero4();
+#pragma unroll
+        for (int pl = decltype(from)::value; pl < decltype(to)::value; ++pl)
+#pragma unroll
+          for (int kk = 0; kk < DV / 32; ++kk) s = mma(frag_row<DV>(wv, lds.rs + (pl - decltype(from)::value) * S::kPlane, dt * 16, kk * 32), vf[kk], s);
+        after += dot4(s, load4(at<T, DK>(lds.ks, j0, wk.perm, 0, dt * 16)));
+        ak[dt] += s * toC;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 s = zero4();
+#pragma unroll
+        for (int pl = decltype(from)::value; pl < decltype(to)::value; ++pl)
+#pragma unroll
+          for (int kk = 0; kk < DK / 32; ++kk) 
+            s = mma(frag_col_row<DV>(wv, lds.rs + (pl - decltype(from)::value) * S::kPlane, kk * 32, nt * 16), kf[kk], s);
+        av[nt] += s * toC;
+      }
+    };
     // Queries from the last 32 down.  Beside the products, M_ij summed over the queries from t on (in
     // this lane's column; `later`: the tiles done) and then over the keys before t.
     float later = 0.0f;
@@ -1418,54 +1466,37 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
           for (int r = 0; r < 4; ++r) p[t * 4 + r] = x[t * 4 + r] = 0.0f;
         }
       }
-      Frag<T> pf[kParts<T>], xf[kParts<T>];
-      pack_parts(p, pf);
-      pack_parts(x, xf);
+      Frag<T> piece[kPieces<T>];
+      split(p, piece);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const Frag<T> f = frag_col<DV>(wv, lds.os, kk * 32, nt * 16);
 #pragma unroll
-        for (int i = 0; i < kParts<T>; ++i) av[nt] = mma(f, pf[i], av[nt]);
+        for (int i = 0; i < kPieces<T>; ++i) av[nt] = mma(f, piece[i], av[nt]);
       }
+      split(x, piece);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         const Frag<T> f = frag_col<DK>(wk, lds.qs, kk * 32, dt * 16);
 #pragma unroll
-        for (int i = 0; i < kParts<T>; ++i) ak[dt] = mma(f, xf[i], ak[dt]);
+        for (int i = 0; i < kPieces<T>; ++i) ak[dt] = mma(f, piece[i], ak[dt]);
       }
+#pragma unroll
+      for (int i = 0; i < kPieces<T>; ++i) put_row_perm<32>(wx, lds.x(wave / 2, kk, i), wave % 2 * 16, 0, piece[i]);
     }
     if (c > w.c0) {
       tiles.skip(-1);
       tiles.load(t0 - C);
     }
-    if constexpr (!kBoth) {
+    __syncthreads();
+    states(std::integral_constant<int, 0>{}, std::integral_constant<int, kPlanes>{});
+    if constexpr (kPlanes < S::kPlanes) {
       __syncthreads();
       __syncthreads();
-    }
-    float after = 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      f32x4 s = zero4();
-#pragma unroll
-      for (int pl = 0; pl < S::kPlanes; ++pl)
-#pragma unroll
-        for (int kk = 0; kk < DV / 32; ++kk)
-          s = mma(frag_row<DV>(wv, lds.rs() + pl * S::kPlane, dt * 16, kk * 32), vf[kk], s);
-      after += dot4(s, load4(at<T, DK>(lds.ks, j0, wk.perm, 0, dt * 16)));
-      ak[dt] += s * toC;
+      states(std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{});
     }
     after = sum_rows(after);
     if (l < 16) lds.after[j] = after;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f32x4 s = zero4();
-#pragma unroll
-      for (int pl = 0; pl < S::kPlanes; ++pl)
-#pragma unroll
-        for (int kk = 0; kk < DK / 32; ++kk)
-          s = mma(frag_col_row<DV>(wv, lds.rs() + pl * S::kPlane, kk * 32, nt * 16), kf[kk], s);
-      av[nt] += s * toC;
-    }
     const bool there = t0 + j < w.live;
     const uint32_t at = static_cast<uint32_t>(j) * kt + g4;
     if (a.share == 1)
@@ -1480,19 +1511,13 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
       const bool mine = l < C && t0 + l < w.live;
       float from = 0.0f, before = 0.0f, y = 0.0f;
       if (mine) {
-        from = lds.into[l];
-        before = lds.after[l];
-        if constexpr (S::kPlanes == 2) {
 #pragma unroll
-          for (int i = 0; i < B::kWaves; ++i) {
-            from += lds.thirds[0][i][l];
-            before += lds.thirds[1][i][l];
-          }
-        }
+        for (int i = 0; i < B::kWaves; ++i) from += lds.into[i][l];
+        before = lds.after[l];
         from *= a.scale * d.from0[l];
         before *= d.toC[l];
 #pragma unroll
-        for (int i = 0; i < B::kWaves; ++i) y += lds.across[c & 1][i];
+        for (int i = 0; i < B::kWaves; ++i) y += lds.across[i];
         y *= d.from0[C - 1];
         for (int i = 0; i <= l / 16; ++i) y += lds.rows[i][l];
       }
@@ -1717,7 +1742,7 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
       double time = rounds * (per + 1) * block;  // a block's time to start and end
       // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
       const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_key(dk) * width * 4;
-      const bool chain = seg > 1 && mb < kChainMb;
+      const bool chain = seg > 1 && mb < kChainMb && !(back && rereads(pad_key(dk), width));
       if (seg > 1) time += kPassShare[back] * time + kPassUs[back] + (back ? 2 : 1) * (chain ? kMbUs * mb : kJoinUs + kSegmentUs * seg);
       if (best.blocks == 0 || time < least) {
         least = time;
