@@ -460,7 +460,8 @@ vmscan_status vmscan_rope_axes(const void *q, const int64_t *q_strides, void *q_
  *                   token strides below 2^24 elements.
  *   log_decay     : float32; decay_strides (batch, token, head; 0 broadcasts) or NULL for one value
  *                   per head, [heads].  -inf clears the state; values above 0 are taken as they are.
- *   initial_state, final_state : [batch, heads, dk, dv] float32 or NULL
+ *   initial_state, final_state : [batch, heads, dk, dv] float32 or NULL; they may be one buffer, whose
+ *                   states then go on in place, and must not overlap otherwise (VMSCAN_ERR_UNSUPPORTED)
  *   lengths       : [batch] int32 or NULL: row b has lengths[b] tokens (clamped to 0 .. seqlen).  What
  *                   lies past them is never read (it may be NaN), `out` is 0 there and the
  *                   final state is the one after the last token.
@@ -486,7 +487,8 @@ vmscan_status vmscan_linattn_fwd(const void *q, const int64_t *q_strides, const 
  * Outputs, dense: dq, dk_out [batch, seqlen, kheads, dk] (summed over the heads that share them) and
  * dv_out [batch, seqlen, heads, dv], activation dtype; dlog_decay float32, [batch, seqlen, heads] or,
  * when decay_strides is NULL, [heads]; dinitial_state [batch, heads, dk, dv] float32 or NULL.  Zero
- * past a row's length.  No atomics: the same inputs give the same bits.
+ * past a row's length.  No atomics: the same inputs give the same bits.  dinitial_state may be the buffer
+ * of dfinal_state or of initial_state and must not overlap them otherwise (VMSCAN_ERR_UNSUPPORTED).
  * per_head of the workspace query: 1 when decay_strides will be NULL.
  */
 size_t vmscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int kheads,

@@ -751,7 +751,8 @@ def linattn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None
     kheads, dk]; v: [batch, L, heads, dv], heads a multiple of kheads (a q/k head serves neighbouring
     heads); float32 or bfloat16, contiguous channels, other strides multiples of 16 bytes; dk and dv
     multiples of 8 up to 128.  log_decay: float32 [batch, L, heads] (any strides) or [heads].  scale
-    defaults to dk ** -0.5.  initial_state / final_state: [batch, heads, dk, dv] float32.  lengths: [batch]
+    defaults to dk ** -0.5.  initial_state / final_state: [batch, heads, dk, dv] float32; the same tensor for
+    both is updated in place (they must not overlap otherwise).  lengths: [batch]
     int32, the tokens of each row; out is 0 past them.  ``prepare`` as for ``vmscan_fwd_bidir`` (the
     callable then rewrites the same out and final_state): returns (callable, out, final_state)."""
     dt, (nb, L), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 4)

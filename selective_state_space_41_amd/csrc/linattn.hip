@@ -1943,6 +1943,15 @@ void place(LinArgs& a, const Layout& y, unsigned char* ws) {
   a.seg_dg = reinterpret_cast<float*>(ws + y.seg_dg);
 }
 
+// Whether a state output may be written where `in` lies: not at all, or exactly there.  A walk that joins the states
+// itself reads them while another one may write its output, so in place the sums are a launch of their own.
+bool states_ok(const LinArgs& a, const float* out, const float* in) {
+  if (!out || !in || out == in) return true;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(out), q = reinterpret_cast<uintptr_t>(in);
+  const uintptr_t n = static_cast<uintptr_t>(a.batch) * a.heads * a.dk * a.dvd * sizeof(float);
+  return p < q ? q - p >= n : p - q >= n;
+}
+
 vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
   if (a.batch * a.heads * 2 * p.parts * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
   if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
@@ -1974,8 +1983,10 @@ vmscan_status vmscan_linattn_fwd(const void* q, const int64_t* q_strides, const 
   const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, false, dtype, false);
   st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
   if (st != VMSCAN_OK) return st;
+  if (!states_ok(a, final_state, initial_state)) return VMSCAN_ERR_UNSUPPORTED;
   place(a, y, static_cast<unsigned char*>(workspace));
   a.out = out, a.sT = final_state;
+  if (final_state && final_state == initial_state) a.chain = false;
   return dtype == VMSCAN_F32 ? run_fwd<float>(a, y.p.width, stream)
                             : run_fwd<uint16_t>(a, y.p.width, stream);
 }
@@ -2009,9 +2020,12 @@ vmscan_status vmscan_linattn_bwd(const void* q, const int64_t* q_strides, const 
   st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
   if (st != VMSCAN_OK) return st;
   if (kheads != heads && batch * seqlen * kheads * (dk / 4) / 256 >= (int64_t{1} << 31) - 1) return VMSCAN_ERR_SHAPE;
+  if (!states_ok(a, dinitial_state, dfinal_state) || !states_ok(a, dinitial_state, initial_state))
+    return VMSCAN_ERR_UNSUPPORTED;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   place(a, y, ws);
   a.dsT = dfinal_state, a.ds0 = dinitial_state, a.dv_out = dv_out;
+  if (dinitial_state && (dinitial_state == dfinal_state || dinitial_state == initial_state)) a.chain = false;
   return dtype == VMSCAN_F32 ? run_bwd<float>(a, y, ws, dq, dk_out, dlog_decay, per_head, stream)
                              : run_bwd<uint16_t>(a, y, ws, dq, dk_out, dlog_decay, per_head, stream);
 }
