@@ -470,6 +470,13 @@ vmscan_status vmscan_rope_axes(const void *q, const int64_t *q_strides, void *q_
  * VMSCAN_ERR_UNSUPPORTED).  A NaN or infinity in a token's v can reach earlier outputs of the same
  * 64 tokens.
  */
+/* How a call of vmscan_linattn_fwd (gradient 0) or _bwd (1) is cut up, which is the library's choice by sizes:
+ * cut[0] tokens of a block, [1] value channels of a workgroup, [2] segments of a sequence, each walked by a
+ * workgroup, [3] parts of a segment in the gradient's passes, [4] how the states of segments or parts are joined. */
+enum { VMSCAN_JOIN_NONE = 0, VMSCAN_JOIN_WALK = 1, VMSCAN_JOIN_LAUNCH = 2 };
+vmscan_status vmscan_linattn_plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv,
+                                  vmscan_dtype dtype, int gradient, int32_t *cut);
+
 size_t vmscan_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int dk, int dv,
                                           vmscan_dtype dtype);
 vmscan_status vmscan_linattn_fwd(const void *q, const int64_t *q_strides, const void *k,

@@ -93,6 +93,8 @@ def _load():
     lib.vmscan_rope_axes.argtypes = ([_c_void_p] * 9 + [_i64, _c_void_p, _c_void_p, _i64, _i64] + [ctypes.c_int] * 8 +
                                      [_c_void_p])
     sizes = [_i64, _i64] + [ctypes.c_int] * 4
+    lib.vmscan_linattn_plan.restype = ctypes.c_int
+    lib.vmscan_linattn_plan.argtypes = [_i64, _i64] + [ctypes.c_int] * 5 + [_c_void_p]
     lib.vmscan_linattn_fwd_workspace_bytes.restype = ctypes.c_size_t
     lib.vmscan_linattn_fwd_workspace_bytes.argtypes = [_i64, _i64] + [ctypes.c_int] * 4
     lib.vmscan_linattn_fwd.restype = ctypes.c_int
@@ -741,6 +743,17 @@ def _linattn_args(q, k, v, log_decay, ndim):
     else:
         raise ValueError(f"log_decay has shape {tuple(log_decay.shape)}, expected {(H,)} or {lead + (H,)}")
     return dt, lead, H, Hk, dk, dv, qs, ks, vs, gs
+
+
+def linattn_plan(batch, seqlen, heads, dk, dv, dtype=torch.bfloat16, gradient=False):
+    """How ``linattn_fwd`` (or, with ``gradient``, ``linattn_bwd``) cuts up a call (vmscan_linattn_plan): a dict with the
+    tokens of a block, the value channels of a workgroup (width), segments of a sequence, parts of a segment and how their
+    states are joined (None, "walk" or "launch")."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    cut = (ctypes.c_int32 * 5)()
+    _check(load().vmscan_linattn_plan(batch, seqlen, heads, dk, dv, _DTYPES[dtype], int(bool(gradient)), cut))
+    return dict(block=cut[0], width=cut[1], segments=cut[2], parts=cut[3], join=(None, "walk", "launch")[cut[4]])
 
 
 def linattn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None, out=None, final_state=None,

@@ -54,21 +54,39 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("bwd_ckpt_kernel", 6),
     ("adj_state_kernel", 6),
     ("lane_scan_kernel", 2),
-    # linear attention, bfloat16 heads up to 64 x 64: what LDS leaves room for (planning counts on it)
-    ("linattn_fwd_kernelItLi64ELi64E", 3),
-    ("linattn_fwd_kernelItLi128ELi64E", 2),
     ("linattn_segment_kernelItLi64ELi64E", 4),
     ("linattn_passes_kernelItLi64ELi64E", 4),
-    ("linattn_grad_kernelItLi64ELi64E", 4),
     ("linattn_step_kernel", 6),
 ]
+# Linear attention: workgroups per CU that the cuts of a call are planned with (kWalks of csrc/linattn.hip), by kernel, type
+# and padded key channels, for 32, 64 and 128 value channels of a workgroup; 0: no such kernel.
+WALKS_PER_CU = {
+    "fwd": {"t": {32: (4, 3, 2), 64: (4, 3, 2), 128: (2, 2, 0)}, "f": {32: (4, 2, 1), 64: (3, 2, 0), 128: (2, 1, 0)}},
+    "grad": {"t": {32: (0, 2, 1), 64: (0, 2, 1), 128: (0, 1, 1)}, "f": {32: (0, 1, 1), 64: (0, 1, 1), 128: (0, 1, 1)}},
+}
+LDS_PER_CU = 160 * 1024
+
+
+def walk_floors():
+    """[(kernel name fragment, workgroups per CU, waves per SIMD that makes)] of WALKS_PER_CU."""
+    out = []
+    for kernel, types in WALKS_PER_CU.items():
+        for t, keys in types.items():
+            for dk, per_cu in keys.items():
+                for dv, n in zip((32, 64, 128), per_cu):
+                    waves = 4 if kernel == "fwd" else 4 if (t, dk, dv) == ("f", 128, 128) else 8  # of a workgroup
+                    if n:
+                        out.append((f"linattn_{kernel}_kernelI{t}Li{dk}ELi{dv}E", n, n * waves // 4))
+    return out
+
+
 # Bytes per lane.  linattn_grad: twelve registers of its key waves, spilled once a block; with 2 waves per SIMD and no
 # scratch the call takes 476 us instead of 424 (32 x 3136 tokens, 8 heads).
 SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E", 48)]
 
 
 def kernel_resources(report):
-    """Per-kernel {VGPRs, AGPRs, ScratchSize, Occupancy} from -Rpass-analysis=kernel-resource-usage."""
+    """Per-kernel {VGPRs, AGPRs, ScratchSize, Occupancy, LDS} from -Rpass-analysis=kernel-resource-usage."""
     res, cur = {}, None
     for line in report.splitlines():
         m = re.search(r"remark: Function Name: (\S+)", line)
@@ -76,7 +94,8 @@ def kernel_resources(report):
             cur = m.group(1)
             res[cur] = {}
             continue
-        m = re.search(r"remark:\s+(VGPRs|AGPRs|ScratchSize \[bytes/lane\]|Occupancy \[waves/SIMD\]): (\d+)", line)
+        m = re.search(r"remark:\s+(VGPRs|AGPRs|ScratchSize \[bytes/lane\]|Occupancy \[waves/SIMD\]|"
+                      r"LDS Size \[bytes/block\]): (\d+)", line)
         if m and cur:
             res[cur][m.group(1).split()[0]] = int(m.group(2))
     return res
@@ -90,6 +109,13 @@ def check_resources(res):
             if frag in name and r.get("Occupancy", 0) < floor:
                 bad.append(f"{name}: {r.get('Occupancy')} waves per SIMD (VGPRs {r.get('VGPRs')}, AGPRs "
                            f"{r.get('AGPRs')}), needs {floor}")
+        for frag, per_cu, floor in walk_floors():
+            if frag not in name:
+                continue
+            if r.get("Occupancy", 0) < floor:
+                bad.append(f"{name}: {r.get('Occupancy')} waves per SIMD, {per_cu} workgroups per CU need {floor}")
+            if r.get("LDS", 0) * per_cu > LDS_PER_CU:
+                bad.append(f"{name}: {r.get('LDS')} bytes of LDS, planned with {per_cu} workgroups per CU")
         allowed = next((b for frag, b in SCRATCH_ALLOWED if frag in name), 0)
         if any(frag in name for frag, _ in OCCUPANCY_FLOORS) and r.get("ScratchSize", 0) > allowed:
             bad.append(f"{name}: {r.get('ScratchSize')} bytes of scratch per lane, at most {allowed}")
@@ -113,6 +139,7 @@ def build(verbose=False):
     if not any(frag in name for name in res for frag, _ in OCCUPANCY_FLOORS):
         raise RuntimeError("build: the compiler printed no kernel resource report")
     bad = check_resources(res)
+    bad += [f"{frag}: planned with, and not built" for frag, _, _ in walk_floors() if not any(frag in n for n in res)]
     if bad:
         raise RuntimeError("build: kernels below their occupancy floor:\n  " + "\n  ".join(bad))
     os.replace(tmp, LIB)

@@ -1683,10 +1683,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6))) void l
 
 constexpr int kMaxHeadDim = 128;
 constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // a block's offsets fit 32 bits in bytes
-// Estimates of plan(), us: a block by [gradient][float32][channels 32, 64, 128]; the segments' pass as a share
-// of the walk and its launches by [gradient]; the join, by a launch and per segment, or per MB read.
-constexpr double kBlockUs[2][2][3] = {{{2.2, 2.9, 4.6}, {4.2, 5.5, 9.0}}, {{0.0, 8.0, 13.0}, {0.0, 14.0, 24.0}}};
-constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {3.0, 5.0}, kJoinUs = 3.0, kSegmentUs = 0.2, kMbUs = 0.1;
+// Estimates of plan(), us: the segments' pass as a share of the walk and its launches by [gradient]; the join, by a
+// launch and per segment, or per MB read.
+constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {7.0, 5.0}, kJoinUs = 3.0, kSegmentUs = 0.2, kMbUs = 0.1;
 // Measured, us, joined by the walks / by a launch: 12 MB 14.2 / 18.0 (1 x 1000 tokens, 6 heads of 64 x 64, 16
 // segments), 49 MB 29.1 / 31.9 (1 x 6085, 32 segments), 77 MB 106 / 101 (8 x 6085, 6 of 128 x 64, 10 segments).
 constexpr double kChainMb = 64.0;
@@ -1704,27 +1703,45 @@ struct Plan {
   int subs, parts;
   bool chain;
 };
-// Workgroups that run at a time: 256 CUs times what registers and LDS leave room for.
-int64_t slots_for(vmscan_dtype dtype, int dk, int width, bool back) {
-  const int wide = (pad_key(dk) == 128) + (width == 128);
+// A walk's workgroups by [gradient][float32][padded key channels 32, 64, 128][value channels of a workgroup 32, 64, 128]:
+// how many of them a CU holds at a time, which is what the compiler's report of registers and LDS leaves room for (the build
+// checks the report against this table), and the time of a block, us, where one has a CU for itself and where all places are
+// taken (16 blocks of 64 tokens, 32 for float32 128 x 128; the gradient with its passes).  {}: no such kernel.  The gradient
+// needs all value channels; in the forward 128 of them in one workgroup lose to two halves (us for 128: bfloat16 128 x 128
+// 10.2 and 8.0, float32 64 x 128 12.1 and 11.6, 128 x 128 45 and 25).
+struct Walk {
   int per_cu;
-  if (back)
-    per_cu = wide == 0 ? 2 : 1;
-  else if (dtype == VMSCAN_F32)
-    per_cu = wide == 0 ? 4 : 2;
-  else
-    per_cu = wide == 0 ? 3 : wide == 1 ? 2 : 1;
-  return 256 * per_cu;
+  double alone, full;
+};
+constexpr Walk kWalks[2][2][3][3] = {
+    {{{{4, 2.5, 5.1}, {3, 3.1, 5.2}, {2, 4.6, 6.7}}, {{4, 3.0, 6.3}, {3, 4.0, 7.1}, {2, 5.5, 8.1}}, {{2, 4.1, 5.6}, {2, 6.0, 8.0}, {}}},
+     {{{4, 4.0, 9.6}, {2, 5.1, 9.0}, {1, 8.7, 8.7}}, {{3, 5.8, 11.2}, {2, 7.7, 11.6}, {}}, {{2, 9.6, 13.0}, {1, 12.6, 12.6}, {}}}},
+    {{{{}, {2, 7.5, 10.5}, {1, 10.4, 10.4}}, {{}, {2, 9.2, 14.8}, {1, 13.8, 13.8}}, {{}, {1, 14.1, 14.1}, {1, 30.4, 30.4}}},
+     {{{}, {1, 13.1, 13.1}, {1, 21.4, 21.4}}, {{}, {1, 16.9, 16.9}, {1, 26.2, 26.2}}, {{}, {1, 31.1, 31.1}, {1, 35.7, 35.7}}}}};
+constexpr int size_class(int channels) { return channels == 32 ? 0 : channels == 64 ? 1 : 2; }
+template <typename T, int DK, int DV, bool BACK>
+constexpr bool kHasWalk = kWalks[BACK][sizeof(T) == 4][size_class(DK)][size_class(DV)].per_cu > 0;
+// A block's time in `n` workgroups: whole rounds of them over the chip, and a last one that leaves places free.
+double block_time(const Walk& w, int64_t n) {
+  const int64_t places = 256 * w.per_cu, rest = n % places;
+  double us = static_cast<double>(n / places) * w.full;
+  if (rest) {
+    const int64_t on_cu = (rest + 255) / 256;
+    us += w.per_cu > 1 ? w.alone + (w.full - w.alone) * static_cast<double>(on_cu - 1) / (w.per_cu - 1) : w.full;
+  }
+  return us;
 }
 // How a call is cut up.  The forward's value channels are independent, so several workgroups can share them (each
 // repeats the scores), and a sequence can be cut into segments (a pass over the keys and values more, and
 // a prefix over the segments).  Of all cuts the one with the least estimated time is taken: rounds of workgroups
-// times blocks, a block's time as measured where one workgroup has a CU for itself.  Measured, us, cut as taken
-// / whole: 8 x 6085 tokens, 6 heads of 128 x 64, bfloat16: 101 (10 segments) / over 500; 1 x 6085, 6 of 64 x 64:
-// 32 (32 segments, halves of the channels) / 282; 1 x 197, 6 of 64 x 64: bfloat16 11.4 (halves) / 14.2, float32 13.0
-// (halves, 4 segments) / 26.8; 128 x 197, 6 of 64 x 64: 24.6 (whole) / 50 in 2 segments, 30 in halves.
-// The gradient needs all channels of a token together and is only cut into segments: 32 x 3136, 8 of 64 x 64, bfloat16:
-// 460 (2 segments) / 520 whole; 2 x 1001, 8 of 32 x 128, float32: 49 / 239 (passes and walk).
+// times blocks, a block's time as kWalks has it.  Calls measured, us, cut as taken / otherwise: bfloat16, 8 x 6085 tokens, 6
+// heads of 128 x 64: 107 (10 segments) / 500 whole, 113 in 16; 1 x 6085, 6 of 64 x 64: 30 (20, halves of the channels) / 317
+// whole, 31 in 32; 1 x 197, 6 of 64 x 64: 16 (whole, halves) / 17 not halved, 20 in 4; 128 x 197, 6 of 64 x 64: 30 (whole) / 45
+// in 2, 36 in halves.  Float32 64 x 64: 8 x 6085, 6 heads: 151 (10) / 166 (8, halves); 16 x 3136, 12: 280 (5) / 326 (2, halves);
+// 1 x 197, 6: 20 (4, halves) / 24 whole.
+// The gradient needs all channels of a token together and is only cut into segments: bfloat16 64 x 64, 32 x 3136, 8 heads:
+// 408 (2) / 481 whole; 2 x 3136, 8: 54 (13) / 62 (25); float32, 32 x 3136, 8 of 64 x 64: 830 (whole) / 913 in 2; 2 x 1001, 8 of 32
+// x 128: 52 (16) / 329 whole.
 Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype, bool back) {
   Plan best{};
   double least = 0.0;
@@ -1733,13 +1750,13 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
     const int C = 16 * waves_of(f32 ? 4 : 2, pad_key(dk), width);
     const int blocks = static_cast<int>((seqlen + C - 1) / C);
     const int slices = (dv + width - 1) / width;
-    const int64_t walks = batch * heads * slices, slots = slots_for(dtype, dk, width, back);
-    const double block = kBlockUs[back][f32][width == 32 ? 0 : width == 64 ? 1 : 2];
+    const int64_t walks = batch * heads * slices;
+    const Walk walk = kWalks[back][f32][size_class(pad_key(dk))][size_class(width)];
+    if (walk.per_cu == 0) continue;
     for (int seg = 1; seg <= blocks && seg <= kMaxSegments; ++seg) {
       const int per = (blocks + seg - 1) / seg;
       if ((blocks + per - 1) / per != seg) continue;
-      const double rounds = static_cast<double>((walks * seg + slots - 1) / slots);
-      double time = rounds * (per + 1) * block;  // a block's time to start and end
+      double time = (per + 1) * block_time(walk, walks * seg);  // a block's time to start and end
       // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
       const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_key(dk) * width * 4;
       const bool chain = seg > 1 && mb < kChainMb && !(back && rereads(pad_key(dk), width));
@@ -1857,11 +1874,13 @@ template <typename T>
 vmscan_status run_fwd(const LinArgs& a, int width, hipStream_t stream) {
   with_dims(a.dk, width, [&](auto dk, auto dv) {
     constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-    if (a.segments > 1)
-      hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false, false>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads),
-                         0, stream, a);
-    launch_prefix<false>(a, DK, stream);
-    hipLaunchKernelGGL((linattn_fwd_kernel<T, DK, DV>), walks(a), dim3(BlockOf<T, DK, DV>::kThreads), 0, stream, a);
+    if constexpr (kHasWalk<T, DK, DV, false>) {
+      const dim3 block(BlockOf<T, DK, DV>::kThreads);
+      if (a.segments > 1)
+        hipLaunchKernelGGL((linattn_segment_kernel<T, DK, DV, false, false>), walks(a), block, 0, stream, a);
+      launch_prefix<false>(a, DK, stream);
+      hipLaunchKernelGGL((linattn_fwd_kernel<T, DK, DV>), walks(a), block, 0, stream, a);
+    }
   });
   return launched();
 }
@@ -1877,7 +1896,7 @@ vmscan_status run_bwd(LinArgs a, const Layout& y, unsigned char* ws, void* dq, v
   b.segments = a.parts, b.per_segment = a.per_part;
   with_dims(a.dk, y.p.width, [&](auto k, auto v) {
     constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
-    if constexpr (DV >= 64) {
+    if constexpr (kHasWalk<T, DK, DV, true>) {
       const dim3 block(BlockOf<T, DK, DV>::kThreads);
       if (a.segments > 1) {
         hipLaunchKernelGGL((linattn_passes_kernel<T, DK, DV>), dim3(2 * walks(b).x), block, 0, stream, b);
@@ -1961,6 +1980,18 @@ vmscan_status need_workspace(const void* ws, size_t have, size_t need, const Lin
 }  // namespace
 
 extern "C" {
+
+vmscan_status vmscan_linattn_plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype dtype,
+                                  int gradient, int32_t* cut) {
+  if (!cut) return VMSCAN_ERR_NULL;
+  if (!sizes_ok(batch, seqlen, heads, heads, dk, dv)) return VMSCAN_ERR_SHAPE;
+  if (!options_ok(heads, heads, dk, dv, dtype) || (gradient != 0 && gradient != 1)) return VMSCAN_ERR_UNSUPPORTED;
+  const Plan p = plan(batch, seqlen, heads, dk, dv, dtype, gradient != 0);
+  cut[0] = 16 * waves_of(dtype == VMSCAN_F32 ? 4 : 2, pad_key(dk), p.width);
+  cut[1] = p.width, cut[2] = p.segments, cut[3] = p.subs;
+  cut[4] = p.parts == 1 ? VMSCAN_JOIN_NONE : p.chain ? VMSCAN_JOIN_WALK : VMSCAN_JOIN_LAUNCH;
+  return VMSCAN_OK;
+}
 
 size_t vmscan_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int dk, int dv,
                                           vmscan_dtype dtype) {
