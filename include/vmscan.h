@@ -424,6 +424,13 @@ vmscan_status vmscan_rmsnorm_bwd(const void *dy, const void *r, const float *wei
                                  void *dresidual, float *dweight, int64_t rows, int64_t dim,
                                  vmscan_dtype dtype, vmscan_dtype residual_dtype, void *workspace,
                                  size_t workspace_bytes, hipStream_t stream);
+/* The same for an r whose rows are r_stride >= dim elements apart: the forward's x, when that was so
+ * and had no residual. */
+vmscan_status vmscan_rmsnorm_bwd_ex(const void *dy, const void *r, int64_t r_stride, const float *weight,
+                                    const float *rstd, const void *dresidual_out, void *dx,
+                                    void *dresidual, float *dweight, int64_t rows, int64_t dim,
+                                    vmscan_dtype dtype, vmscan_dtype residual_dtype, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Rotary positions with several axes (rows and columns of an image; time, rows and columns of a

@@ -86,9 +86,11 @@ def _load():
                                        [ctypes.c_int] * 4 + [_c_void_p])
     lib.vmscan_rmsnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.vmscan_rmsnorm_bwd_workspace_bytes.argtypes = [_i64, _i64]
+    bwd_args = [_c_void_p] * 6 + [_i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p]
     lib.vmscan_rmsnorm_bwd.restype = ctypes.c_int
-    lib.vmscan_rmsnorm_bwd.argtypes = ([_c_void_p] * 8 + [_i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p,
-                                                         ctypes.c_size_t, _c_void_p])
+    lib.vmscan_rmsnorm_bwd.argtypes = [_c_void_p] * 2 + bwd_args
+    lib.vmscan_rmsnorm_bwd_ex.restype = ctypes.c_int
+    lib.vmscan_rmsnorm_bwd_ex.argtypes = [_c_void_p] * 2 + [_i64] + bwd_args
     lib.vmscan_rope_axes.restype = ctypes.c_int
     lib.vmscan_rope_axes.argtypes = ([_c_void_p] * 9 + [_i64, _c_void_p, _c_void_p, _i64, _i64] + [ctypes.c_int] * 8 +
                                      [_c_void_p])
@@ -589,6 +591,15 @@ def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+def _row_stride(t, name):
+    """The row stride of a contiguous [..., dim] tensor, or of a [rows, dim] one whose rows are apart."""
+    if t.is_contiguous():
+        return t.shape[-1]
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t.stride(0)
+    raise ValueError(f"{name} must be contiguous, or [rows, dim] with contiguous channels and rows that do not overlap")
+
+
 def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=None, residual_out=None, stream=None):
     """Residual addition and root-mean-square norm (vmscan_rmsnorm_fwd): r = x + residual, y = r *
     rsqrt(mean(r^2) + eps) * weight.  Returns (y, scale, residual_out, rstd).
@@ -604,12 +615,7 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
     dev, shape = x.device, tuple(x.shape)
     dim, lead = shape[-1], shape[:-1]
     rows = x.numel() // dim if dim else 0
-    if x.is_contiguous():
-        row_stride = dim
-    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= dim:
-        row_stride = x.stride(0)
-    else:
-        raise ValueError("x must be contiguous, or [rows, dim] with contiguous channels and rows that do not overlap")
+    row_stride = _row_stride(x, "x")
     _need(weight, "weight", (dim,), torch.float32, dev)
     rdt = dt
     if residual is not None:
@@ -646,13 +652,15 @@ def rmsnorm_bwd(dy, r, weight, rstd, dresidual_out=None, workspace=None, stream=
     """Gradient of ``rmsnorm_fwd`` (vmscan_rmsnorm_bwd); returns a dict with dx (dy's dtype), dresidual
     (r's dtype; dx itself when the two are the same) and dweight [dim] float32.
 
-    dy: [..., dim] gradient of y; r: the forward's residual_out; rstd: the forward's; dresidual_out: the
-    gradient that reaches residual_out on its other way, or None."""
+    dy: [..., dim] contiguous gradient of y; r: the forward's residual_out (without a residual its x, rows apart
+    or not); rstd: the forward's; dresidual_out: the gradient that reaches residual_out on its other way, or None."""
     dt = _is_act(dy, "dy", dy.dim() if isinstance(dy, torch.Tensor) else 0)
     dev, shape, dim = dy.device, dy.shape, dy.shape[-1]
     rdt = _is_act(r, "r", dy.dim())
     _need(dy, "dy", shape, dy.dtype, dev)
-    _need(r, "r", shape, r.dtype, dev)
+    if r.shape != shape or r.device != dev:
+        raise ValueError(f"r is {tuple(r.shape)} on {r.device}, expected {tuple(shape)} on {dev}")
+    r_stride = _row_stride(r, "r")
     _need(weight, "weight", (dim,), torch.float32, dev)
     _need(rstd, "rstd", shape[:-1], torch.float32, dev)
     if dresidual_out is not None:
@@ -662,10 +670,10 @@ def rmsnorm_bwd(dy, r, weight, rstd, dresidual_out=None, workspace=None, stream=
     given = workspace
     workspace = _workspace(workspace, lib.vmscan_rmsnorm_bwd_workspace_bytes(rows, dim), dev)
     dx, dw = torch.empty_like(dy), torch.empty(dim, dtype=torch.float32, device=dev)
-    dres = torch.empty_like(r) if r.dtype != dy.dtype else None
+    dres = torch.empty(shape, dtype=r.dtype, device=dev) if r.dtype != dy.dtype else None
     _made(stream, dx, dw, dres, workspace if given is None else None)
-    _enqueue(lib.vmscan_rmsnorm_bwd,
-             (dy.data_ptr(), r.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _p(dresidual_out), dx.data_ptr(),
+    _enqueue(lib.vmscan_rmsnorm_bwd_ex,
+             (dy.data_ptr(), r.data_ptr(), r_stride, weight.data_ptr(), rstd.data_ptr(), _p(dresidual_out), dx.data_ptr(),
               _p(dres), dw.data_ptr(), rows, dim, dt, rdt, _p(workspace), _nbytes(workspace), _on(stream, dev)), dev)
     return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
 

@@ -46,7 +46,7 @@ struct NormBwdArgs {
   const float *w, *rstd;
   void *dx, *dres_out;
   float* part;
-  int64_t rows;
+  int64_t rows, r_stride;
   int dim;
 };
 
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void rmsnorm_bwd_kernel(NormB
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = (e * kLanes + lane) * 8;
-      load_upto8(static_cast<const R*>(a.r) + at + c, n - c, r[e]);
+      load_upto8(static_cast<const R*>(a.r) + row * a.r_stride + c, n - c, r[e]);
       load_upto8(static_cast<const T*>(a.dy) + at + c, n - c, g[e]);
       if (a.dres) load_upto8(static_cast<const R*>(a.dres) + at + c, n - c, d[e]);
     }
@@ -436,8 +436,17 @@ vmscan_status vmscan_rmsnorm_bwd(const void* dy, const void* r, const float* wei
                                  const void* dresidual_out, void* dx, void* dresidual, float* dweight, int64_t rows,
                                  int64_t dim, vmscan_dtype dtype, vmscan_dtype residual_dtype, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream) {
+  return vmscan_rmsnorm_bwd_ex(dy, r, dim, weight, rstd, dresidual_out, dx, dresidual, dweight, rows, dim, dtype,
+                               residual_dtype, workspace, workspace_bytes, stream);
+}
+
+vmscan_status vmscan_rmsnorm_bwd_ex(const void* dy, const void* r, int64_t r_stride, const float* weight,
+                                    const float* rstd, const void* dresidual_out, void* dx, void* dresidual,
+                                    float* dweight, int64_t rows, int64_t dim, vmscan_dtype dtype,
+                                    vmscan_dtype residual_dtype, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream) {
   if (!dy || !r || !weight || !rstd || !dx || !dweight) return VMSCAN_ERR_NULL;
-  if (!norm_shape_ok(rows, dim)) return VMSCAN_ERR_SHAPE;
+  if (!norm_shape_ok(rows, dim) || r_stride < dim || r_stride > (int64_t{1} << 40)) return VMSCAN_ERR_SHAPE;
   // with one type for both, dx is the residual's gradient too
   if (!dtypes_ok(dtype, residual_dtype) || (dresidual && dtype == residual_dtype)) return VMSCAN_ERR_UNSUPPORTED;
   const void* ptrs[] = {dy, r, weight, rstd, dresidual_out, dx, dresidual, dweight, workspace};
@@ -446,7 +455,7 @@ vmscan_status vmscan_rmsnorm_bwd(const void* dy, const void* r, const float* wei
   if (!workspace || workspace_bytes < vmscan_rmsnorm_bwd_workspace_bytes(rows, dim)) return VMSCAN_ERR_WORKSPACE;
   const unsigned blocks = blocks_for(rows, dim, kBwdBlocks);
   float* part = static_cast<float*>(workspace);
-  const NormBwdArgs a{dy, r, dresidual_out, weight, rstd, dx, dresidual, part, rows, static_cast<int>(dim)};
+  const NormBwdArgs a{dy, r, dresidual_out, weight, rstd, dx, dresidual, part, rows, r_stride, static_cast<int>(dim)};
   if (dtype == VMSCAN_F32)
     launch_bwd<float, float>(a, blocks, stream);
   else if (residual_dtype == VMSCAN_F32)
