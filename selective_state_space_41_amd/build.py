@@ -86,9 +86,9 @@ SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E"
                    # the other walks of the gradient whose state does not fit beside the block's results
                    ("linattn_grad_kernelItLi128ELi128E", 260), ("linattn_grad_kernelIfLi128ELi128E", 36),
                    ("linattn_grad_kernelIfLi128ELi64E", 104),
-                   # rows over 8192 channels: 16 waves of 128 registers, which hold half of the gradient's five tensors
-                   ("rmsnorm_bwd_kernelIffLi64ELi16ELi4E", 396), ("rmsnorm_bwd_kernelItfLi64ELi16ELi4E", 440),
-                   ("rmsnorm_bwd_kernelIttLi64ELi16ELi4E", 408)]
+                   # rows over 8192 channels: 16 waves of 128 registers
+                   ("rmsnorm_bwd_kernelIffLi64ELi16ELi4E", 228), ("rmsnorm_bwd_kernelItfLi64ELi16ELi4E", 208),
+                   ("rmsnorm_bwd_kernelIttLi64ELi16ELi4E", 204)]
 # Kernels whose scratch is checked beside those with a floor.
 SCRATCH_CHECKED = ("linattn_", "rmsnorm_", "rope_kernel")
 

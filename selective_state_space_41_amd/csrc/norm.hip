@@ -3,7 +3,8 @@
 //
 // A row belongs to LPR lanes of one wave (short rows share a wave) or to all W waves of a
 // workgroup; a lane keeps its E runs of 8 consecutive elements in registers from the load to the
-// store, so x and the residual are read once and nothing but the outputs is written.  The sum of
+// store, so x and the residual are read once and nothing but the outputs is written (but for the gradient of rows over
+// 8192 channels, which spills some 50 registers of a lane).  The sum of
 // squares, the scale's maximum and the gradient's dot product are float32 butterflies over the
 // row's lanes.  Bound by HBM: the arithmetic is about 6 (forward) or 12 (gradient) operations for
 // 8 or more bytes.  Measured: 48680 x 768 bfloat16 with residual to 8 bits, 262 MB in 60 us, 4.4 TB/s;
@@ -238,11 +239,15 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void rmsnorm_bwd_kernel(NormB
   const int lane = W > 1 ? threadIdx.x : threadIdx.x % LPR;
   const int sub = W > 1 ? 0 : threadIdx.x / LPR;
   const int dim = a.dim;
-  float w[E][8], dw[E][8];
+  // 16 waves have 128 registers each, which r, dy and the weight's gradient nearly fill: they read the weight again for each
+  // row, and the gradient of the residual where it is added.  4000 x 16384, us, so / all kept, in scratch: bfloat16 with a
+  // float32 residual 616 / 922, float32 518 / 823; a second read of the whole row instead 774 and 736.
+  constexpr bool kKeep = W * E < 64;
+  float w[kKeep ? E : 1][8], dw[E][8];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = (e * kLanes + lane) * 8;
-    load_upto8(a.w + c, dim - c, w[e]);
+    if constexpr (kKeep) load_upto8(a.w + c, dim - c, w[e]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[e][k] = 0.0f;
   }
@@ -251,36 +256,50 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void rmsnorm_bwd_kernel(NormB
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < a.rows;
        row0 += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
     const int64_t row = row0 + sub;
+    int here = lane;
+    if constexpr (!kKeep) asm volatile("" : "+v"(here));  // places are made where they are used, not kept for all rows
     const bool live = row < a.rows;
     const int n = live ? dim : 0;
     const int64_t at = row * dim;
     const float rstd = live ? a.rstd[row] : 0.0f;
-    float r[E][8], g[E][8], d[E][8];
+    float r[E][8], g[E][8], d[kKeep ? E : 1][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = (e * kLanes + lane) * 8;
+      const int c = (e * kLanes + here) * 8;
       load_upto8(static_cast<const R*>(a.r) + row * a.r_stride + c, n - c, r[e]);
       load_upto8(static_cast<const T*>(a.dy) + at + c, n - c, g[e]);
-      if (a.dres) load_upto8(static_cast<const R*>(a.dres) + at + c, n - c, d[e]);
+      if constexpr (kKeep)
+        if (a.dres) load_upto8(static_cast<const R*>(a.dres) + at + c, n - c, d[e]);
     }
     float dot = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+    for (int e = 0; e < E; ++e) {
+      float (&we)[8] = w[kKeep ? e : 0];
+      if constexpr (!kKeep) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_upto8(a.w + (e * kLanes + here) * 8, dim - (e * kLanes + here) * 8, we);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         r[e][k] *= rstd;
         dw[e][k] = __builtin_fmaf(g[e][k], r[e][k], dw[e][k]);
-        g[e][k] *= w[e][k];
+        g[e][k] *= we[k];
         dot = __builtin_fmaf(r[e][k], g[e][k], dot);
       }
+    }
     dot = over_row<Add, LPR, W>(dot, slots[turn]) * inv_dim;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = (e * kLanes + lane) * 8;
+      const int c = (e * kLanes + here) * 8;
+      float (&de)[8] = d[kKeep ? e : 0];
+      if constexpr (!kKeep) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (a.dres) load_upto8(static_cast<const R*>(a.dres) + at + c, n - c, de);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float v = rstd * __builtin_fmaf(-r[e][k], dot, g[e][k]);
-        g[e][k] = a.dres ? v + d[e][k] : v;
+        g[e][k] = a.dres ? v + de[k] : v;
       }
       store_upto8(static_cast<T*>(a.dx) + at + c, n - c, g[e]);
       if constexpr (kSplit)

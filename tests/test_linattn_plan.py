@@ -37,6 +37,7 @@ def _report(name, occ, lds, scratch=0):
     ("linattn_fwd_kernelItLi128ELi64E", 2, 90000, 0, 1), ("linattn_grad_kernelItLi64ELi64E", 4, 81168, 48, 0),
     ("linattn_grad_kernelItLi64ELi64E", 2, 81168, 0, 1), ("linattn_grad_kernelIfLi64ELi64E", 2, 99600, 0, 0),
     ("linattn_fwd_kernelItLi32ELi32E", 4, 17408, 8, 1), ("linattn_prefix_kernelILb1E", 8, 0, 16, 1),
+    ("rmsnorm_bwd_kernelItfLi64ELi16ELi4E", 4, 128, 440, 1), ("rmsnorm_bwd_kernelItfLi64ELi16ELi4E", 4, 128, 208, 0),
     ("rmsnorm_fwd_kernelIffLb0ELi64ELi1ELi4E", 4, 0, 4, 1), ("rope_kernelIfLi4ELb0E", 8, 0, 4, 1)])
 def test_guard(name, occ, lds, scratch, bad):
     assert len(build.check_resources(_report(name, occ, lds, scratch))) == bad
