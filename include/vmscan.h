@@ -474,8 +474,9 @@ vmscan_status vmscan_rope_axes(const void *q, const int64_t *q_strides, void *q_
  *                   final state is the one after the last token.
  *   out           : [batch, seqlen, heads, dv]   activation dtype, dense
  * heads must be a multiple of kheads; dk and dv multiples of 8 up to 128 (else
- * VMSCAN_ERR_UNSUPPORTED).  A NaN or infinity in a token's v can reach earlier outputs of the same
- * 64 tokens.
+ * VMSCAN_ERR_UNSUPPORTED).  The masked scores are multiplied, as zeros, within a block (64 tokens; see
+ * vmscan_linattn_plan), so a NaN or infinity in a token's v can reach the outputs of earlier tokens of its
+ * block, but no others before it; one in its q, k or decay reaches no earlier output.
  */
 /* How a call of vmscan_linattn_fwd (gradient 0) or _bwd (1) is cut up, which is the library's choice by sizes:
  * cut[0] tokens of a block, [1] value channels of a workgroup, [2] segments of a sequence, each walked by a
@@ -502,7 +503,9 @@ vmscan_status vmscan_linattn_fwd(const void *q, const int64_t *q_strides, const 
  * dv_out [batch, seqlen, heads, dv], activation dtype; dlog_decay float32, [batch, seqlen, heads] or,
  * when decay_strides is NULL, [heads]; dinitial_state [batch, heads, dk, dv] float32 or NULL.  Zero
  * past a row's length.  No atomics: the same inputs give the same bits.  dinitial_state may be the buffer
- * of dfinal_state or of initial_state and must not overlap them otherwise (VMSCAN_ERR_UNSUPPORTED).
+ * of dfinal_state or of initial_state and must not overlap them otherwise (VMSCAN_ERR_UNSUPPORTED).  A NaN
+ * or infinity in a token's k can reach dq of earlier tokens of its block, one in its q or dout dk and dv of
+ * later ones, and those of other blocks where the formula has it.
  * per_head of the workspace query: 1 when decay_strides will be NULL.
  */
 size_t vmscan_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int kheads,
