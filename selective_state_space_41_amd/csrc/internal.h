@@ -19,6 +19,9 @@ inline vmscan_status launched() {
   return e == hipSuccess ? VMSCAN_OK : launch_failed(e);
 }
 
+// A launch holds less than 2^32 threads along x: this many workgroups of 256.
+constexpr int64_t kMaxBlocks256 = (int64_t{1} << 24) - 1;
+
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Eight consecutive activations as float32.  The rows of odd-length tensors start at any element:

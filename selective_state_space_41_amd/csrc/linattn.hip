@@ -1971,8 +1971,9 @@ bool states_ok(const LinArgs& a, const float* out, const float* in) {
   return p < q ? q - p >= n : p - q >= n;
 }
 
-vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p) {
-  if (a.batch * a.heads * 2 * p.parts * p.slices >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
+vmscan_status need_workspace(const void* ws, size_t have, size_t need, const LinArgs& a, const Plan& p, bool back) {
+  // workgroups of the largest launch: the forward's walk, the gradient's two passes (its walk has twice the threads)
+  if (a.batch * a.heads * (back ? 2 * p.parts : p.segments) * p.slices > kMaxBlocks256) return VMSCAN_ERR_SHAPE;
   if (!aligned_to(ws, 16)) return VMSCAN_ERR_ALIGN;
   return need && (!ws || have < need) ? VMSCAN_ERR_WORKSPACE : VMSCAN_OK;
 }
@@ -2012,7 +2013,7 @@ vmscan_status vmscan_linattn_fwd(const void* q, const int64_t* q_strides, const 
   if (st != VMSCAN_OK) return st;
   if (!aligned_to(out, 16) || !aligned_to(final_state, 16)) return VMSCAN_ERR_ALIGN;
   const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, false, dtype, false);
-  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p, false);
   if (st != VMSCAN_OK) return st;
   if (!states_ok(a, final_state, initial_state)) return VMSCAN_ERR_UNSUPPORTED;
   place(a, y, static_cast<unsigned char*>(workspace));
@@ -2048,9 +2049,9 @@ vmscan_status vmscan_linattn_bwd(const void* q, const int64_t* q_strides, const 
   if (!aligned_to(dlog_decay, 4)) return VMSCAN_ERR_ALIGN;
   const bool per_head = decay_strides == nullptr;
   const Layout y = layout(batch, seqlen, heads, kheads, dk, dv, per_head, dtype, true);
-  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p);
+  st = need_workspace(workspace, workspace_bytes, y.total, a, y.p, true);
   if (st != VMSCAN_OK) return st;
-  if (kheads != heads && batch * seqlen * kheads * (dk / 4) / 256 >= (int64_t{1} << 31) - 1) return VMSCAN_ERR_SHAPE;
+  if (kheads != heads && batch * seqlen * kheads * (dk / 4) / 256 >= kMaxBlocks256) return VMSCAN_ERR_SHAPE;
   if (!states_ok(a, dinitial_state, dfinal_state) || !states_ok(a, dinitial_state, initial_state))
     return VMSCAN_ERR_UNSUPPORTED;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -2068,7 +2069,7 @@ vmscan_status vmscan_linattn_step(const void* q, const int64_t* q_strides, const
                                   vmscan_dtype dtype, hipStream_t stream) {
   if (!q || !q_strides || !k || !k_strides || !v || !v_strides || !log_decay || !state || !out) return VMSCAN_ERR_NULL;
   if (!sizes_ok(batch, 1, heads, kheads, dk, dv) || pool < 1 || pool >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
-  if (!slots && pool != batch) return VMSCAN_ERR_SHAPE;
+  if ((!slots && pool != batch) || batch * heads > kMaxBlocks256) return VMSCAN_ERR_SHAPE;
   if (!options_ok(heads, kheads, dk, dv, dtype)) return VMSCAN_ERR_UNSUPPORTED;
   const void* ptrs[] = {q, k, v};
   for (const void* p : ptrs)

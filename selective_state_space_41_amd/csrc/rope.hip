@@ -30,7 +30,7 @@ struct RopeArgs {
   const float *pos, *inv_freq;
   const int* axis;
   int64_t pos_stride;  // between batches; 0: one grid for all
-  int64_t tokens;      // batch * seqlen
+  int64_t first, tokens;  // of batch * seqlen, the launch's first one and how far it goes
   int64_t seqlen;
   int dim, rot, axes;
   int units, pass_units;  // units of rotated channels; of channels that only pass through
@@ -129,9 +129,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   constexpr int kPairs = INTERLEAVED ? V / 2 : V;  // pairs per unit
   const int per_token = (a.units + a.pass_units) * a.shares;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t token = id / per_token;
+  const int64_t in_launch = id / per_token, token = a.first + in_launch;
   if (token >= a.tokens) return;
-  const int rest = static_cast<int>(id - token * per_token);
+  const int rest = static_cast<int>(id - in_launch * per_token);
   const int share = rest / (a.units + a.pass_units), unit = rest % (a.units + a.pass_units);
   const int64_t b = token / a.seqlen, t = token - b * a.seqlen;
   if (unit >= a.units) {
@@ -167,10 +167,15 @@ vmscan_status launch_rope(RopeArgs a, hipStream_t stream) {
   a.shares = 1;
   while (a.shares < heads && a.tokens * per * a.shares < kWantThreads) a.shares *= 2;
   if (a.shares > heads) a.shares = heads;
-  const int64_t blocks = (a.tokens * per * a.shares + 255) / 256;
-  if (blocks >= (int64_t{1} << 31)) return VMSCAN_ERR_SHAPE;
-  hipLaunchKernelGGL((rope_kernel<T, V, INTERLEAVED>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a);
-  return launched();
+  const int64_t tokens = a.tokens, most = kMaxBlocks256 * 256 / (per * a.shares);  // tokens of a launch
+  for (a.first = 0; a.first < tokens; a.first += most) {
+    a.tokens = tokens - a.first < most ? tokens : a.first + most;
+    const int64_t blocks = ((a.tokens - a.first) * per * a.shares + 255) / 256;
+    hipLaunchKernelGGL((rope_kernel<T, V, INTERLEAVED>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a);
+    const vmscan_status st = launched();
+    if (st != VMSCAN_OK) return st;
+  }
+  return VMSCAN_OK;
 }
 
 bool runs_aligned(const RopeTensor& x, int64_t n) {
@@ -204,7 +209,8 @@ vmscan_status vmscan_rope_axes(const void* q, const int64_t* q_strides, void* q_
   if (batch < 1 || seqlen < 1 || heads < 1 || kheads < 0 || dim < 2 || rot < 2 || rot > dim || rot % 2 != 0 ||
       axes < 1 || positions_stride < 0)
     return VMSCAN_ERR_SHAPE;
-  if (seqlen >= (int64_t{1} << 31) || batch >= (int64_t{1} << 31) || heads > 65536 || kheads > 65536 || dim > 65536)
+  if (seqlen >= (int64_t{1} << 31) || batch >= (int64_t{1} << 31) || heads > 65536 || kheads > 65536 || dim > 65536 ||
+      batch * seqlen >= (int64_t{1} << 40))
     return VMSCAN_ERR_SHAPE;
   if ((dtype != VMSCAN_F32 && dtype != VMSCAN_BF16) || (interleaved != 0 && interleaved != 1) ||
       (inverse != 0 && inverse != 1))
