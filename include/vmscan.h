@@ -442,7 +442,8 @@ vmscan_status vmscan_rmsnorm_bwd_ex(const void *dy, const void *r, int64_t r_str
  *   q, q_out   : [batch, seqlen, heads, dim]  activation dtype; *_strides: batch, token and head
  *   k, k_out   : [batch, seqlen, kheads, dim]  stride in elements, channels contiguous.  kheads = 0:
  *                no k (its four arguments are not looked at).  An output may be its own input (same
- *                strides); otherwise they must not overlap.  Pointers: aligned to one element.
+ *                strides); otherwise they must not overlap.  Pointers: aligned to one element.  An
+ *                output whose own elements overlap (a stride of 0, say) is refused (VMSCAN_ERR_SHAPE).
  *   positions  : [seqlen, axes] float32 per batch, positions_stride elements apart (0: shared)
  *   inv_freq   : [rot / 2] float32
  *   axis       : [rot / 2] int32; a pair whose axis is not in 0 .. axes - 1 is not turned

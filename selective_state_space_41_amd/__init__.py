@@ -686,7 +686,7 @@ def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False,
     axis: [pairs] int32 give pair p the angle positions[..., axis[p]] * inv_freq[p].  The pairs are the
     channels (p, p + pairs), or (2p, 2p + 1) when ``interleaved``; channels from 2 * pairs on pass
     through.  ``inverse`` turns back: the gradient of the forward turn.  Outputs are contiguous unless
-    given; an output may be its own input."""
+    given; an output may be its own input, unless that is expanded (its elements overlap)."""
     dt = _is_act(q, "q", 4)
     dev, (nb, L, H, dim) = q.device, q.shape
     qs = _strided(q, "q", q.shape, q.dtype, dev)

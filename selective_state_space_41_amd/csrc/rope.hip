@@ -10,6 +10,7 @@
 
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "internal.h"
 #include "vmscan.h"
@@ -194,6 +195,23 @@ vmscan_status run_rope(const RopeArgs& a, int interleaved, hipStream_t stream) {
   return wide ? launch_rope<T, kRun, false>(a, stream) : launch_rope<T, 1, false>(a, stream);
 }
 
+// Whether no two elements of [batch][token][head][dim] with these strides are one: every stride covers what lies
+// inside it.
+bool distinct(const int64_t* strides, int64_t batch, int64_t seqlen, int64_t heads, int64_t dim) {
+  int64_t st[3] = {0, 0, 0}, n[3] = {batch, seqlen, heads};
+  for (int i = 0; i < 3; ++i) st[i] = strides[i] < 0 ? -strides[i] : strides[i];
+  for (int i = 0; i < 2; ++i)  // by stride
+    for (int j = 0; j + 1 < 3 - i; ++j)
+      if (st[j] > st[j + 1]) std::swap(st[j], st[j + 1]), std::swap(n[j], n[j + 1]);
+  int64_t inside = dim;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1) {
+      if (st[i] < inside) return false;
+      inside += st[i] * (n[i] - 1);
+    }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -220,6 +238,9 @@ vmscan_status vmscan_rope_axes(const void* q, const int64_t* q_strides, void* q_
   for (const void* p : heads_at)
     if (!aligned_to(p, elem)) return VMSCAN_ERR_ALIGN;
   if (!aligned_to(positions, 4) || !aligned_to(inv_freq, 4) || !aligned_to(axis, 4)) return VMSCAN_ERR_ALIGN;
+  if (!distinct(q_out_strides, batch, seqlen, heads, dim) ||
+      (kheads && !distinct(k_out_strides, batch, seqlen, kheads, dim)))
+    return VMSCAN_ERR_SHAPE;
   RopeArgs a{};
   a.q = RopeTensor{q, q_out, q_strides[0], q_strides[1], q_strides[2], q_out_strides[0], q_out_strides[1],
                    q_out_strides[2], heads};
