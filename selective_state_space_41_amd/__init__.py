@@ -507,6 +507,9 @@ def fwd_bidir_chunk_len(batch, dim, seqlen, d_state=D_STATE):
 
 # ------------------------------------------------------------------------------------------------
 # Operators of a linear-attention block: norm with residual, rotary positions, decayed attention.
+#
+# ``stream``: the stream that a call works on, the current one by default.  Ordering it after what makes the inputs, and
+# the current one after it, is the caller's; memory that the call allocates is safe on both.
 
 _DTYPES = {torch.float32: VMSCAN_F32, torch.bfloat16: VMSCAN_BF16}
 _FP8 = torch.float8_e4m3fn
@@ -553,13 +556,17 @@ def _strided(t, name, shape, dtype, device):
     return _pack2(a if n != 1 else 0, b if m != 1 else 0)
 
 
-def _made(stream, *tensors):
-    """Tensors that a call allocated itself and uses on ``stream``: if that is not the stream they
-    were allocated on, the allocator must not reuse them before that stream is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on_stream(stream, fn, *args):
+    """The call on another stream: what it allocates is that stream's memory (a block of the current one's could still
+    be written by work that waits there), and stays reserved while the current one uses it."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    for t in got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,):
+        for x in t.values() if isinstance(t, dict) else (t,):
+            if isinstance(x, torch.Tensor):
+                x.record_stream(here)
+    return got
 
 
 def _enqueue(fn, args, dev, prepare=False, keep=None):
@@ -581,9 +588,7 @@ def _enqueue(fn, args, dev, prepare=False, keep=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
+def _current(dev):
     return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -609,6 +614,8 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
     out_dtype None: y in x's dtype, scale None; torch.float8_e4m3fn: y holds 8-bit codes and scale
     [..., 1] float32 (group 0, one per row) or [..., ceil(dim / 128)] (group 128): y * scale is the
     norm.  ``residual_out`` may be ``residual`` (in place).  rstd [...] float32 is for ``rmsnorm_bwd``."""
+    if stream is not None:
+        return _on_stream(stream, rmsnorm_fwd, x, weight, residual, eps, out_dtype, group, y, residual_out)
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor with a channel dimension")
     dt = _is_act(x, "x", x.dim())
@@ -623,7 +630,6 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
         _need(residual, "residual", shape, residual.dtype, dev)
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-            _made(stream, residual_out)
         else:
             _need(residual_out, "residual_out", shape, residual.dtype, dev)
     elif residual_out is not None:
@@ -634,17 +640,15 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, y=N
     ydt = _FP8 if fp8 else x.dtype
     if y is None:
         y = torch.empty(shape, dtype=ydt, device=dev) if fp8 or row_stride != dim else torch.empty_like(x)
-        _made(stream, y)
     else:
         _need(y, "y", shape, ydt, dev)
     scale = None
     if fp8:
         scale = torch.empty(lead + (-(-dim // group) if group else 1,), dtype=torch.float32, device=dev)
     rstd = torch.empty(lead, dtype=torch.float32, device=dev)
-    _made(stream, scale, rstd)
     _enqueue(load().vmscan_rmsnorm_fwd,
              (x.data_ptr(), row_stride, _p(residual), weight.data_ptr(), y.data_ptr(), _p(scale), _p(residual_out),
-              rstd.data_ptr(), rows, dim, eps, dt, rdt, int(fp8), int(group), _on(stream, dev)), dev)
+              rstd.data_ptr(), rows, dim, eps, dt, rdt, int(fp8), int(group), _current(dev)), dev)
     return y, scale, residual_out if residual is not None else x, rstd
 
 
@@ -654,6 +658,8 @@ def rmsnorm_bwd(dy, r, weight, rstd, dresidual_out=None, workspace=None, stream=
 
     dy: [..., dim] contiguous gradient of y; r: the forward's residual_out (without a residual its x, rows apart
     or not); rstd: the forward's; dresidual_out: the gradient that reaches residual_out on its other way, or None."""
+    if stream is not None:
+        return _on_stream(stream, rmsnorm_bwd, dy, r, weight, rstd, dresidual_out, workspace)
     dt = _is_act(dy, "dy", dy.dim() if isinstance(dy, torch.Tensor) else 0)
     dev, shape, dim = dy.device, dy.shape, dy.shape[-1]
     rdt = _is_act(r, "r", dy.dim())
@@ -667,14 +673,12 @@ def rmsnorm_bwd(dy, r, weight, rstd, dresidual_out=None, workspace=None, stream=
         _need(dresidual_out, "dresidual_out", shape, r.dtype, dev)
     rows = dy.numel() // dim if dim else 0
     lib = load()
-    given = workspace
     workspace = _workspace(workspace, lib.vmscan_rmsnorm_bwd_workspace_bytes(rows, dim), dev)
     dx, dw = torch.empty_like(dy), torch.empty(dim, dtype=torch.float32, device=dev)
     dres = torch.empty(shape, dtype=r.dtype, device=dev) if r.dtype != dy.dtype else None
-    _made(stream, dx, dw, dres, workspace if given is None else None)
     _enqueue(lib.vmscan_rmsnorm_bwd_ex,
              (dy.data_ptr(), r.data_ptr(), r_stride, weight.data_ptr(), rstd.data_ptr(), _p(dresidual_out), dx.data_ptr(),
-              _p(dres), dw.data_ptr(), rows, dim, dt, rdt, _p(workspace), _nbytes(workspace), _on(stream, dev)), dev)
+              _p(dres), dw.data_ptr(), rows, dim, dt, rdt, _p(workspace), _nbytes(workspace), _current(dev)), dev)
     return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
 
 
@@ -687,6 +691,8 @@ def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False,
     channels (p, p + pairs), or (2p, 2p + 1) when ``interleaved``; channels from 2 * pairs on pass
     through.  ``inverse`` turns back: the gradient of the forward turn.  Outputs are contiguous unless
     given; an output may be its own input, unless that is expanded (its elements overlap)."""
+    if stream is not None:
+        return _on_stream(stream, rope_axes, q, k, positions, inv_freq, axis, interleaved, inverse, q_out, k_out)
     dt = _is_act(q, "q", 4)
     dev, (nb, L, H, dim) = q.device, q.shape
     qs = _strided(q, "q", q.shape, q.dtype, dev)
@@ -701,7 +707,6 @@ def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False,
     _need(positions, "positions", (L, axes) if positions.dim() == 2 else (nb, L, axes), torch.float32, dev)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _made(stream, q_out)
     qos = _strided(q_out, "q_out", q.shape, q.dtype, dev)
     Hk, ks, kos = 0, None, None
     if k is not None:
@@ -713,14 +718,13 @@ def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False,
         ks = _strided(k, "k", (nb, L, Hk, dim), q.dtype, dev)
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-            _made(stream, k_out)
         kos = _strided(k_out, "k_out", k.shape, q.dtype, dev)
     elif k_out is not None:
         raise ValueError("k_out needs a k")
     _enqueue(load().vmscan_rope_axes,
              (q.data_ptr(), qs, q_out.data_ptr(), qos, _p(k), ks, _p(k_out), kos, positions.data_ptr(),
               L * axes if positions.dim() == 3 else 0, inv_freq.data_ptr(), axis.data_ptr(), nb, L, H, Hk, dim,
-              2 * pairs, axes, int(bool(interleaved)), int(bool(inverse)), dt, _on(stream, dev)), dev)
+              2 * pairs, axes, int(bool(interleaved)), int(bool(inverse)), dt, _current(dev)), dev)
     return q_out, k_out
 
 
@@ -776,6 +780,9 @@ def linattn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None
     both is updated in place (they must not overlap otherwise).  lengths: [batch]
     int32, the tokens of each row; out is 0 past them.  ``prepare`` as for ``vmscan_fwd_bidir`` (the
     callable then rewrites the same out and final_state): returns (callable, out, final_state)."""
+    if stream is not None:
+        return _on_stream(stream, linattn_fwd, q, k, v, log_decay, scale, initial_state, lengths, out, final_state,
+                          workspace, None, prepare)
     dt, (nb, L), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 4)
     dev = q.device
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
@@ -785,20 +792,15 @@ def linattn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None
         _need(lengths, "lengths", (nb,), torch.int32, dev)
     if out is None:
         out = torch.empty(nb, L, H, dv, dtype=q.dtype, device=dev)
-        _made(stream, out)
     else:
         _need(out, "out", (nb, L, H, dv), q.dtype, dev)
     if final_state is None:
         final_state = torch.empty(nb, H, dk, dv, dtype=torch.float32, device=dev)
-        _made(stream, final_state)
     lib = load()
-    given = workspace
     workspace = _workspace(workspace, lib.vmscan_linattn_fwd_workspace_bytes(nb, L, H, dk, dv, dt), dev)
-    if given is None:
-        _made(stream, workspace)
     args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, _p(initial_state),
             _p(lengths), out.data_ptr(), final_state.data_ptr(), nb, L, H, Hk, dk, dv,
-            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _on(stream, dev))
+            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _current(dev))
     run = _enqueue(lib.vmscan_linattn_fwd, args, dev, prepare,
                    (q, k, v, log_decay, initial_state, lengths, out, final_state, workspace))
     return (run, out, final_state) if prepare else (out, final_state)
@@ -810,6 +812,9 @@ def linattn_bwd(q, k, v, log_decay, dout, scale=None, initial_state=None, length
     [batch, heads, dk, dv] (vmscan_linattn_bwd); returns a dict with dq, dk, dv, dlog_decay (of log_decay's
     shape) and dinitial_state (None without an initial_state).  Deterministic.  ``prepare`` as for
     ``vmscan_bwd_bidir_v2``."""
+    if stream is not None:
+        return _on_stream(stream, linattn_bwd, q, k, v, log_decay, dout, scale, initial_state, lengths, dfinal_state,
+                          workspace, None, prepare)
     dt, (nb, L), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 4)
     dev = q.device
     os_ = _strided(dout, "dout", (nb, L, H, dv), q.dtype, dev)
@@ -823,14 +828,12 @@ def linattn_bwd(q, k, v, log_decay, dout, scale=None, initial_state=None, length
     g = dict(dq=act(nb, L, Hk, dk), dk=act(nb, L, Hk, dk), dv=act(nb, L, H, dv), dlog_decay=f32(*log_decay.shape),
              dinitial_state=f32(nb, H, dk, dv) if initial_state is not None else None)
     lib = load()
-    given = workspace
     workspace = _workspace(workspace, lib.vmscan_linattn_bwd_workspace_bytes(nb, L, H, Hk, dk, dv, int(gs is None), dt),
                            dev)
-    _made(stream, *g.values(), workspace if given is None else None)
     args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, _p(initial_state),
             _p(lengths), dout.data_ptr(), os_, _p(dfinal_state), g["dq"].data_ptr(), g["dk"].data_ptr(),
             g["dv"].data_ptr(), g["dlog_decay"].data_ptr(), _p(g["dinitial_state"]), nb, L, H, Hk, dk, dv,
-            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _on(stream, dev))
+            float(dk ** -0.5 if scale is None else scale), dt, _p(workspace), _nbytes(workspace), _current(dev))
     run = _enqueue(lib.vmscan_linattn_bwd, args, dev, prepare,
                    (q, k, v, log_decay, initial_state, lengths, dout, dfinal_state, g, workspace))
     return (run, g) if prepare else g
@@ -844,6 +847,8 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, st
     [pool, heads, dk, dv] float32; slots: [batch] int32, the state of each sequence (all different; one
     outside 0 .. pool - 1 skips the row, whose out is 0), or None with pool = batch.  ``prepare`` as for
     ``linattn_fwd``: returns (callable, out)."""
+    if stream is not None:
+        return _on_stream(stream, linattn_step, q, k, v, log_decay, state, scale, slots, out, None, prepare)
     dt, (nb,), H, Hk, dk, dv, qs, ks, vs, gs = _linattn_args(q, k, v, log_decay, 3)
     dev = q.device
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
@@ -856,11 +861,10 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, st
         raise ValueError(f"without slots the pool holds one state per sequence: {pool} for {nb}")
     if out is None:
         out = torch.empty(nb, H, dv, dtype=q.dtype, device=dev)
-        _made(stream, out)
     else:
         _need(out, "out", (nb, H, dv), q.dtype, dev)
     args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, log_decay.data_ptr(), gs, state.data_ptr(),
             _p(slots), out.data_ptr(), nb, pool, H, Hk, dk, dv, float(dk ** -0.5 if scale is None else scale), dt,
-            _on(stream, dev))
+            _current(dev))
     run = _enqueue(load().vmscan_linattn_step, args, dev, prepare, (q, k, v, log_decay, state, slots, out))
     return (run, out) if prepare else out
