@@ -74,7 +74,7 @@ __device__ __forceinline__ f32x4 mma(const Frag32& a, const Frag32& b, f32x4 c) 
 
 // LDS tiles are [rows][D] without padding; the 16-byte runs of a row lie in an order that depends on the
 // row, so that the products' accesses meet no bank twice (the padded tiles that this replaced lost 40 % of
-// their LDS cycles to conflicts).  256 bytes are served at a time, one word from each of 64 banks: 16 rows of
+// their LDS cycles to conflicts; the 8-byte writes of states and scores still lose 16 to 18 % in the kernels that have them).  256 bytes are served at a time, one word from each of 64 banks: 16 rows of
 // one run (row operands), and 8 rows of two neighbouring runs, rows 0 .. 7 or 0 .. 3 and 8 .. 11 (column
 // operands).  256 / row bytes rows (at least 1) lie side by side; row r's run c is at place c ^ m, m from the
 // bits k of r above those: all k differ in m, and the k of such 8 rows differ in m / 2.  (Float32 columns are
@@ -754,7 +754,8 @@ __device__ __forceinline__ void zero_rest(const LinArgs& a, const Where& w, O* p
 // ---------------------------------------------------------------------------------------------
 // A segment's own state from a zero start: forward (k, v) or, BACK, the state's gradient (q, dout)
 // from a zero end.  KEEP also writes the state before each block.
-// Bound by HBM with the state's update beside it: 8 x 6085 tokens, 6 heads of 128 x 64, 2 key heads, bfloat16: 31 us.
+// Bound by a block's chain (its loads, its decays, then the state's update), not by HBM: 8 x 6085 tokens (three quarters of them
+// live), 6 heads of 128 x 64, 2 key heads, bfloat16: 31 us, 60 MB at 1.9 TB/s.
 
 template <typename T, int DK, int DV, bool BACK, bool KEEP, int C = BlockOf<T, DK, DV>::kC>
 __device__ __forceinline__ void segment_walk(const LinArgs& a, uint32_t id, uint32_t n_ids, T* ys, T* xs,
@@ -834,8 +835,8 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) voi
 }
 
 // The gradient's two passes, which do not depend on each other, in one launch: the first half of the
-// workgroups walks from the end.  Bound by HBM: 32 x 3136 tokens, 8 heads of 64 x 64, bfloat16, read 411 MB and
-// write 206 MB of states in 121 us, 5.1 TB/s.
+// workgroups walks from the end, and only the parts that a later segment's walk needs.  Bound by HBM: 32 x 3136 tokens, 8
+// heads of 64 x 64, bfloat16, read 309 MB (k and v, half of q and dout) and write 232 MB (206 of them states) in 123 us, 4.4 TB/s.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(4) void linattn_passes_kernel(LinArgs a) {
   constexpr int C = BlockOf<T, DK, DV>::kC;
@@ -895,8 +896,9 @@ __global__ __launch_bounds__(256) void linattn_prefix_kernel(LinArgs a, int DK) 
 //
 // A wave owns 16 queries of a block and a part of the state's rows.  Keys and values come one block ahead through
 // registers; a deeper prefetch or both of them in LDS twice would cost a workgroup per CU.  Bound by the chain of
-// dependent products of a block and by LDS: 128 x 197 tokens, 6 heads of 64 x 64, bfloat16: 26.8 us, 3.4 TB/s;
-// 8 x 6085, 6 heads of 128 x 64: 68 us after the segments' 31 and the prefix's 8; float32 1 x 197: 9 us after 5.
+// dependent products of a block and by LDS: 128 x 197 tokens, 6 heads of 64 x 64, bfloat16: 29.8 us, 3.0 TB/s (vector
+// instructions 44 % of the cycles, LDS 25 %, the matrix cores 20 %); 8 x 6085, 6 heads of 128 x 64: 77 us, 1.5 TB/s, after the
+// segments' 31 and the prefix's 8; float32 1 x 197: 9 us after 5.
 
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) void linattn_fwd_kernel(LinArgs a) {
@@ -1071,8 +1073,9 @@ __global__ __launch_bounds__((BlockOf<T, DK, DV>::kThreads)) VMSCAN_WAVES(3) voi
 // workgroups on a CU.  So only R is published.  S never leaves its registers: a state wave multiplies its rows with all of the
 // block's dO, which leaves its channels of every query's dq, and X, which that needs whole, comes from the key waves, which
 // make it for dk, through LDS.  (With S's and R's last planes in one place, exchanged within a block, the call took 519 us
-// instead of 424: 32 x 3136 tokens, 8 heads of 64 x 64.)  What bounds it is instruction issue.
-// Float32, 2 x 1001 tokens, 8 heads of 32 x 128: 35 us, bound by a block's chain of float32 products, whose rate is
+// instead of 424: 32 x 3136 tokens, 8 heads of 64 x 64.)  That walk takes 332 us (318 to 347) and is bound by instruction issue:
+// of its cycles vector instructions take 51 %, LDS 31 %, the matrix cores 22 %.
+// Float32, 2 x 1001 tokens, 8 heads of 32 x 128: 36 us, bound by a block's chain of float32 products, whose rate is
 // a ninth of bfloat16's.
 
 // The gradient's workgroup: a block's tokens as in B, twice the waves.
@@ -1686,8 +1689,8 @@ constexpr int64_t kMaxTokenStride = int64_t{1} << 24;  // a block's offsets fit 
 // Estimates of plan(), us: the segments' pass as a share of the walk and its launches by [gradient]; the join, by a
 // launch and per segment, or per MB read.
 constexpr double kPassShare[2] = {0.4, 0.15}, kPassUs[2] = {7.0, 5.0}, kJoinUs = 3.0, kSegmentUs = 0.2, kMbUs = 0.1;
-// Measured, us, joined by the walks / by a launch: 12 MB 14.2 / 18.0 (1 x 1000 tokens, 6 heads of 64 x 64, 16
-// segments), 49 MB 29.1 / 31.9 (1 x 6085, 32 segments), 77 MB 106 / 101 (8 x 6085, 6 of 128 x 64, 10 segments).
+// Calls measured, us, joined by the walks / by a launch: 12 MB 17 / 20 (1 x 1000 tokens, 6 heads of 64 x 64, 16
+// segments), 29 MB 38 / 40 (4 x 2048, 16 heads, 8 segments), 77 MB 108 / 104 (8 x 6085, 6 of 128 x 64, 10 segments).
 constexpr double kChainMb = 64.0;
 constexpr int64_t kPassWalks = 1024;    // workgroups wanted in each of the gradient's passes ..
 constexpr int kMaxParts = 12;           // .. as long as no more than so many parts have to be joined

@@ -7,7 +7,7 @@
 // 8192 channels, which spills some 50 registers of a lane).  The sum of
 // squares, the scale's maximum and the gradient's dot product are float32 butterflies over the
 // row's lanes.  Bound by HBM: the arithmetic is about 6 (forward) or 12 (gradient) operations for
-// 8 or more bytes.  Measured: 48680 x 768 bfloat16 with residual to 8 bits, 262 MB in 60 us, 4.4 TB/s;
+// 8 or more bytes.  Measured: 48680 x 768 bfloat16 with residual to 8 bits, 262 MB in 62 us, 4.2 TB/s;
 // gradient of 25216 x 384 bfloat16 with a float32 residual, 155 MB in 28 us, and 4 us for dw's partial rows.
 #include <hip/hip_runtime.h>
 
