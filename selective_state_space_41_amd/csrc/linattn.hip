@@ -1759,7 +1759,9 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
     for (int seg = 1; seg <= blocks && seg <= kMaxSegments; ++seg) {
       const int per = (blocks + seg - 1) / seg;
       if ((blocks + per - 1) / per != seg) continue;
-      double time = (per + 1) * block_time(walk, walks * seg);  // a block's time to start and end
+      // Each round takes a block's time more to start and end; the gradient's, which is latency, even on a full CU.
+      const double block = block_time(walk, walks * seg);
+      double time = per * block + (back ? static_cast<double>((walks * seg + 256 * walk.per_cu - 1) / (256 * walk.per_cu)) * walk.alone : block);
       // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
       const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_key(dk) * width * 4;
       const bool chain = seg > 1 && mb < kChainMb && !(back && rereads(pad_key(dk), width));
