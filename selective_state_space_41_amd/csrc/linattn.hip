@@ -74,7 +74,8 @@ __device__ __forceinline__ f32x4 mma(const Frag32& a, const Frag32& b, f32x4 c) 
 
 // LDS tiles are [rows][D] without padding; the 16-byte runs of a row lie in an order that depends on the
 // row, so that the products' accesses meet no bank twice (the padded tiles that this replaced lost 40 % of
-// their LDS cycles to conflicts; the 8-byte writes of states and scores still lose 16 to 18 % in the kernels that have them).  256 bytes are served at a time, one word from each of 64 banks: 16 rows of
+// their LDS cycles to conflicts; the 8-byte writes of states and scores still lose 16 to 18 % in the kernels that
+// have them).  256 bytes are served at a time, one word from each of 64 banks: 16 rows of
 // one run (row operands), and 8 rows of two neighbouring runs, rows 0 .. 7 or 0 .. 3 and 8 .. 11 (column
 // operands).  256 / row bytes rows (at least 1) lie side by side; row r's run c is at place c ^ m, m from the
 // bits k of r above those: all k differ in m, and the k of such 8 rows differ in m / 2.  (Float32 columns are
@@ -1092,11 +1093,12 @@ struct GradLds {
   using S = State<T, DK, DV>;
   static constexpr int kSmall = 6 * 1024;  // the tables below
   // R's planes: all of them, or for bfloat16 heads of 128 x 128 two, and the third when they have been read
-  static constexpr int kPlanes =
-      S::kPlanes == 3 && (2 * B::kC * (DK + DV) + 3 * S::kPlane + 3 * 3 * 1024) * sizeof(T) + kSmall > 160 * 1024 ? 2 : S::kPlanes;
-  // X: blocks of 32 keys and 32 queries [key][query], those with a query at or after a key
+  // (X: blocks of 32 keys and 32 queries [key][query], those with a query at or after a key)
   static constexpr int kHalves = B::kC / 32;
   static constexpr int kX = kHalves * (kHalves + 1) / 2 * 1024;
+  static constexpr size_t kAll =
+      (2 * B::kC * (DK + DV) + S::kPlanes * S::kPlane + kPieces<T> * kX) * sizeof(T) + kSmall;
+  static constexpr int kPlanes = S::kPlanes == 3 && kAll > 160 * 1024 ? 2 : S::kPlanes;
   __align__(16) T qs[B::kC * DK];
   __align__(16) T ks[B::kC * DK];
   __align__(16) T vs[B::kC * DV];
@@ -1200,7 +1202,8 @@ __device__ __forceinline__ void grad_states(const LinArgs& a, const Where& w, Gr
     wx.template here<false, false, true, false>();
     const int l = lane_here(), li = l & 15, g4 = (l >> 4) * 4;
     const int64_t block = w.bh * a.blocks + c;
-    if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1) enter(c / a.per_part, std::integral_constant<int, 1>{});  // few registers
+    if (a.subs > 1 && (c + 1) % a.per_part == 0 && c + 1 < w.c1)
+      enter(c / a.per_part, std::integral_constant<int, 1>{});  // few registers
     // The state that enters the block, put together 32 value channels at a time where they are used, kAhead of them on
     // their way.
     S old;
@@ -1398,7 +1401,8 @@ __device__ __forceinline__ void grad_keys(const LinArgs& a, const Where& w, Grad
 #pragma unroll
         for (int pl = decltype(from)::value; pl < decltype(to)::value; ++pl)
 #pragma unroll
-          for (int kk = 0; kk < DV / 32; ++kk) s = mma(frag_row<DV>(wv, lds.rs + (pl - decltype(from)::value) * S::kPlane, dt * 16, kk * 32), vf[kk], s);
+          for (int kk = 0; kk < DV / 32; ++kk)
+            s = mma(frag_row<DV>(wv, lds.rs + (pl - decltype(from)::value) * S::kPlane, dt * 16, kk * 32), vf[kk], s);
         after += dot4(s, load4(at<T, DK>(lds.ks, j0, wk.perm, 0, dt * 16)));
         ak[dt] += s * toC;
       }
@@ -1717,8 +1721,12 @@ struct Walk {
   double alone, full;
 };
 constexpr Walk kWalks[2][2][3][3] = {
-    {{{{4, 2.5, 5.1}, {3, 3.1, 5.2}, {2, 4.6, 6.7}}, {{4, 3.0, 6.3}, {3, 4.0, 7.1}, {2, 5.5, 8.1}}, {{2, 4.1, 5.6}, {2, 6.0, 8.0}, {}}},
-     {{{4, 4.0, 9.6}, {2, 5.1, 9.0}, {1, 8.7, 8.7}}, {{3, 5.8, 11.2}, {2, 7.7, 11.6}, {}}, {{2, 9.6, 13.0}, {1, 12.6, 12.6}, {}}}},
+    {{{{4, 2.5, 5.1}, {3, 3.1, 5.2}, {2, 4.6, 6.7}},
+      {{4, 3.0, 6.3}, {3, 4.0, 7.1}, {2, 5.5, 8.1}},
+      {{2, 4.1, 5.6}, {2, 6.0, 8.0}, {}}},
+     {{{4, 4.0, 9.6}, {2, 5.1, 9.0}, {1, 8.7, 8.7}},
+      {{3, 5.8, 11.2}, {2, 7.7, 11.6}, {}},
+      {{2, 9.6, 13.0}, {1, 12.6, 12.6}, {}}}},
     {{{{}, {2, 7.5, 10.5}, {1, 10.4, 10.4}}, {{}, {2, 9.2, 14.8}, {1, 13.8, 13.8}}, {{}, {1, 14.1, 14.1}, {1, 30.4, 30.4}}},
      {{{}, {1, 13.1, 13.1}, {1, 21.4, 21.4}}, {{}, {1, 16.9, 16.9}, {1, 26.2, 26.2}}, {{}, {1, 31.1, 31.1}, {1, 35.7, 35.7}}}}};
 constexpr int size_class(int channels) { return channels == 32 ? 0 : channels == 64 ? 1 : 2; }
@@ -1761,7 +1769,8 @@ Plan plan(int64_t batch, int64_t seqlen, int heads, int dk, int dv, vmscan_dtype
       if ((blocks + per - 1) / per != seg) continue;
       // Each round takes a block's time more to start and end; the gradient's, which is latency, even on a full CU.
       const double block = block_time(walk, walks * seg);
-      double time = per * block + (back ? static_cast<double>((walks * seg + 256 * walk.per_cu - 1) / (256 * walk.per_cu)) * walk.alone : block);
+      const double rounds = static_cast<double>((walks * seg + 256 * walk.per_cu - 1) / (256 * walk.per_cu));
+      double time = per * block + (back ? rounds * walk.alone : block);
       // Joining the segments' states: each walk reads those before it, or one more launch makes the sums.
       const double mb = 0.5e-6 * walks * seg * (seg - 1) * pad_key(dk) * width * 4;
       const bool chain = seg > 1 && mb < kChainMb && !(back && rereads(pad_key(dk), width));
