@@ -540,6 +540,138 @@ vmscan_status vmscan_linattn_step(const void *q, const int64_t *q_strides, const
                                   int64_t pool, int heads, int kheads, int dk, int dv, float scale,
                                   vmscan_dtype dtype, hipStream_t stream);
 
+/*
+ * The operators below are those of a gated recurrence block over image tokens, for training that keeps its
+ * activations in 8 bits: the 8-bit form itself, the group norm with its activation and the gated linear
+ * recurrence.  Activations are token-major, [batch, seqlen, dim] (channels last); *_strides are batch and token
+ * stride in elements, channels contiguous, and such inputs may start at any element.  Outputs are dense.
+ * Ownership, errors, streams and the workspace follow the conventions above (no wait status word).
+ */
+
+/*
+ * Activations in 8 bits: OCP e4m3 codes and a float32 scale for each 128 channels of a row (the last group may
+ * be short): x ~ code * scale, scale = max|x| / 448 over the group (1 where that is 0; at least the smallest normal
+ * float32), the code the value nearest to x / scale: the 8-bit form of vmscan_rmsnorm_fwd with group 128.  A NaN or
+ * an infinity makes its group's values NaN.
+ *   x     : [rows, dim] activation dtype; pack: rows x_stride >= dim elements apart; unpack: dense
+ *   codes : [rows, dim] bytes
+ *   scale : [rows, ceil(dim / 128)] float32
+ * 1 <= dim <= 2^30; rows * ceil(dim / 128) below 2^28 - 16 (VMSCAN_ERR_SHAPE).  No workspace.
+ */
+vmscan_status vmscan_act8_pack(const void *x, int64_t x_stride, void *codes, float *scale,
+                               int64_t rows, int64_t dim, vmscan_dtype dtype, hipStream_t stream);
+vmscan_status vmscan_act8_unpack(const void *codes, const float *scale, void *x, int64_t rows,
+                                 int64_t dim, vmscan_dtype dtype, hipStream_t stream);
+
+/*
+ * Group norm with an optional activation.  Over the tokens and the dim / groups neighbouring channels of each
+ * group of a batch row:
+ *   mean, var = E[x], E[(x - mean)^2];   rstd = 1 / sqrt(var + eps)
+ *   u = (x - mean) * rstd * weight + bias;   y = act ? u * sigmoid(u) : u
+ *   x          : [batch, seqlen, dim] activation dtype, x_strides
+ *   weight, bias : [dim] float32
+ *   lengths    : [batch] int32 or NULL: row b has lengths[b] tokens (clamped to 0 .. seqlen).  What lies past
+ *                them is never read, y is 0 there; a row without tokens has mean 0 and var 0.
+ *   y          : [batch, seqlen, dim] activation dtype
+ *   mean, rstd : [batch, groups] float32, for the gradient
+ *   keep_codes, keep_scale : NULL, or x's 8-bit form (as vmscan_act8_pack; zeros past a row's length)
+ * dim <= 4096 and a multiple of groups, batch < 65536 (else VMSCAN_ERR_SHAPE).  y must not alias x.  `keep` of the
+ * workspace query: 1 when the 8-bit form will be kept.
+ */
+size_t vmscan_groupnorm_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
+                                            int64_t groups, int keep);
+vmscan_status vmscan_groupnorm_fwd(const void *x, const int64_t *x_strides, const float *weight,
+                                   const float *bias, const int32_t *lengths, void *y, float *mean,
+                                   float *rstd, void *keep_codes, float *keep_scale, int64_t batch,
+                                   int64_t seqlen, int64_t dim, int64_t groups, float eps, int act,
+                                   vmscan_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/*
+ * Gradient of vmscan_groupnorm_fwd.  With n = (x - mean) * rstd, u = n * weight + bias and
+ * g = dy * (act ? sigmoid(u) (1 + u (1 - sigmoid(u))) : 1):
+ *   dx = rstd * (weight g - E[weight g] - n E[weight g n])  (E over the group),  dweight = sum g n,  dbias = sum g
+ *   dy            : [batch, seqlen, dim] activation dtype, dy_strides
+ *   x, x_strides  : as in the forward; or NULL, and codes, codes_scale the 8-bit form that it kept
+ *   mean, rstd    : the forward's
+ *   dx            : [batch, seqlen, dim] activation dtype, 0 past a row's length
+ *   dweight, dbias : [dim] float32, summed in a fixed order
+ */
+size_t vmscan_groupnorm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
+                                            int64_t groups);
+vmscan_status vmscan_groupnorm_bwd(const void *dy, const int64_t *dy_strides, const void *x,
+                                   const int64_t *x_strides, const void *codes,
+                                   const float *codes_scale, const float *weight, const float *bias,
+                                   const float *mean, const float *rstd, const int32_t *lengths,
+                                   void *dx, float *dweight, float *dbias, int64_t batch,
+                                   int64_t seqlen, int64_t dim, int64_t groups, int act,
+                                   vmscan_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/*
+ * Gated linear recurrence with one state per channel.  Per (batch b, channel d), in float32:
+ *   a_t = exp(A sigmoid(r_t)),  A = -exp(A_log[d]);   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+ * from h_{-1} = initial_state (NULL: 0), over t = 0 .. n - 1, or with reverse = 1 from t = n - 1 down to 0.
+ *   x, r, i    : [batch, seqlen, dim] activation dtype; the scan input and its two gates before their
+ *                sigmoids; token strides below 2^24 elements
+ *   A_log      : [dim] float32
+ *   initial_state, final_state : [batch, dim] float32 or NULL; they may be one buffer, whose states then go on
+ *                in place, and must not overlap otherwise (VMSCAN_ERR_UNSUPPORTED)
+ *   lengths    : [batch] int32 or NULL: n = lengths[b] (clamped to 0 .. seqlen).  What lies past them is never
+ *                read, `out` is 0 there and the final state is the one after the last token of the walk.
+ *   out        : [batch, seqlen, dim] activation dtype: h
+ *   keep_codes, keep_scale : NULL, or the 8-bit form (as vmscan_act8_pack) of what the gradient needs:
+ *                [4, batch, seqlen, dim] and [4, batch, seqlen, ceil(dim / 128)], planes x, r, i and h (before
+ *                its rounding to `out`), zeros past a row's length
+ * A NaN or infinity reaches the later states of its own channel only.
+ */
+size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+vmscan_status vmscan_gated_scan_fwd(const void *x, const int64_t *x_strides, const void *r,
+                                    const int64_t *r_strides, const void *i,
+                                    const int64_t *i_strides, const float *A_log,
+                                    const float *initial_state, const int32_t *lengths, int reverse,
+                                    void *out, float *final_state, void *keep_codes,
+                                    float *keep_scale, int64_t batch, int64_t seqlen, int64_t dim,
+                                    vmscan_dtype dtype, void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/*
+ * Gradients of vmscan_gated_scan_fwd.  x, r, i (and their strides) as there and h [batch, seqlen, dim] its `out`;
+ * or these seven NULL, and codes, codes_scale what it kept in 8 bits.  And
+ *   dout           : [batch, seqlen, dim] activation dtype, dout_strides
+ *   dfinal_state   : [batch, dim] float32 or NULL (0)
+ * Outputs: dx, dr, di [batch, seqlen, dim] activation dtype, 0 past a row's length; dA_log [dim] float32;
+ * dinitial_state [batch, dim] float32 or NULL; it may be the buffer of dfinal_state, and must not overlap that
+ * one otherwise, nor initial_state (VMSCAN_ERR_UNSUPPORTED).  At a_t = 1, where sqrt(1 - a^2) has no slope, the
+ * gradient of r is its limit.  No atomics: the same inputs give the same bits.
+ */
+size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+vmscan_status vmscan_gated_scan_bwd(const void *x, const int64_t *x_strides, const void *r,
+                                    const int64_t *r_strides, const void *i,
+                                    const int64_t *i_strides, const void *h, const void *codes,
+                                    const float *codes_scale, const float *A_log,
+                                    const float *initial_state, const int32_t *lengths, int reverse,
+                                    const void *dout, const int64_t *dout_strides,
+                                    const float *dfinal_state, void *dx, void *dr, void *di,
+                                    float *dA_log, float *dinitial_state, int64_t batch,
+                                    int64_t seqlen, int64_t dim, vmscan_dtype dtype,
+                                    void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of each of `batch` sequences: the recurrence once, the states updated in place.
+ *   x, r, i : [batch, dim] activation dtype, rows *_stride elements apart
+ *   state   : [pool, dim] float32
+ *   slots   : [batch] int32: the state of each sequence, all different; a row whose slot is not in
+ *             0 .. pool - 1 has no state: its out is 0.  NULL: row b has state b, pool = batch.
+ *   out     : [batch, dim] activation dtype, dense
+ * No workspace.
+ */
+vmscan_status vmscan_gated_scan_step(const void *x, int64_t x_stride, const void *r,
+                                     int64_t r_stride, const void *i, int64_t i_stride,
+                                     const float *A_log, float *state, const int32_t *slots,
+                                     void *out, int64_t batch, int64_t pool, int64_t dim,
+                                     vmscan_dtype dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

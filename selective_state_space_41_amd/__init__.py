@@ -107,6 +107,32 @@ def _load():
     lib.vmscan_linattn_bwd.restype = ctypes.c_int
     lib.vmscan_linattn_bwd.argtypes = ([_c_void_p] * 18 + sizes + [ctypes.c_float, ctypes.c_int, _c_void_p,
                                                                    ctypes.c_size_t, _c_void_p])
+    lib.vmscan_act8_pack.restype = lib.vmscan_act8_unpack.restype = ctypes.c_int
+    lib.vmscan_act8_pack.argtypes = [_c_void_p, _i64, _c_void_p, _c_void_p, _i64, _i64, ctypes.c_int, _c_void_p]
+    lib.vmscan_act8_unpack.argtypes = [_c_void_p] * 3 + [_i64, _i64, ctypes.c_int, _c_void_p]
+    lib.vmscan_groupnorm_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_groupnorm_fwd_workspace_bytes.argtypes = [_i64] * 4 + [ctypes.c_int]
+    lib.vmscan_groupnorm_fwd.restype = ctypes.c_int
+    lib.vmscan_groupnorm_fwd.argtypes = ([_c_void_p] * 10 + [_i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                                                         _c_void_p, ctypes.c_size_t, _c_void_p])
+    lib.vmscan_groupnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_groupnorm_bwd_workspace_bytes.argtypes = [_i64] * 4
+    lib.vmscan_groupnorm_bwd.restype = ctypes.c_int
+    lib.vmscan_groupnorm_bwd.argtypes = ([_c_void_p] * 14 + [_i64] * 4 + [ctypes.c_int, ctypes.c_int, _c_void_p,
+                                                                         ctypes.c_size_t, _c_void_p])
+    lib.vmscan_gated_scan_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_gated_scan_fwd_workspace_bytes.argtypes = [_i64] * 3
+    lib.vmscan_gated_scan_fwd.restype = ctypes.c_int
+    lib.vmscan_gated_scan_fwd.argtypes = ([_c_void_p] * 9 + [ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 +
+                                          [ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p])
+    lib.vmscan_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.vmscan_gated_scan_bwd_workspace_bytes.argtypes = [_i64] * 3
+    lib.vmscan_gated_scan_bwd.restype = ctypes.c_int
+    lib.vmscan_gated_scan_bwd.argtypes = ([_c_void_p] * 12 + [ctypes.c_int] + [_c_void_p] * 8 + [_i64] * 3 +
+                                          [ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p])
+    lib.vmscan_gated_scan_step.restype = ctypes.c_int
+    lib.vmscan_gated_scan_step.argtypes = ([_c_void_p, _i64] * 3 + [_c_void_p] * 4 + [_i64] * 3 +
+                                           [ctypes.c_int, _c_void_p])
     lib.vmscan_linattn_step.restype = ctypes.c_int
     lib.vmscan_linattn_step.argtypes = [_c_void_p] * 11 + sizes + [ctypes.c_float, ctypes.c_int, _c_void_p]
     return lib
@@ -563,7 +589,7 @@ def _on_stream(stream, fn, *args):
     with torch.cuda.stream(stream):
         got = fn(*args)
     for t in got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,):
-        for x in t.values() if isinstance(t, dict) else (t,):
+        for x in t.values() if isinstance(t, dict) else t if isinstance(t, tuple) else (t,):
             if isinstance(x, torch.Tensor):
                 x.record_stream(here)
     return got
@@ -867,4 +893,292 @@ def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, st
             _p(slots), out.data_ptr(), nb, pool, H, Hk, dk, dv, float(dk ** -0.5 if scale is None else scale), dt,
             _current(dev))
     run = _enqueue(load().vmscan_linattn_step, args, dev, prepare, (q, k, v, log_decay, state, slots, out))
+    return (run, out) if prepare else out
+
+
+# ------------------------------------------------------------------------------------------------
+# Operators of a gated recurrence block: group norm with activation, gated linear recurrence, activations in 8 bits.
+# Streams as for the operators above.
+
+ACT8_GROUP = 128  # channels that share a scale
+
+
+def _groups(dim):
+    return -(-dim // ACT8_GROUP)
+
+
+def _codes(codes, scale, shape, dev, name):
+    """Checks an 8-bit form of activations of ``shape``; None stands for any."""
+    if not isinstance(codes, torch.Tensor) or not isinstance(scale, torch.Tensor):
+        raise TypeError(f"{name} must be (codes, scale) tensors")
+    shape = tuple(codes.shape) if shape is None else shape
+    dev = codes.device if dev is None else dev
+    if codes.dim() < 1 or not codes.is_cuda:
+        raise ValueError(f"{name}'s codes must be on a GPU and have a channel dimension")
+    _need(codes, f"{name}'s codes", shape, _FP8, dev)
+    _need(scale, f"{name}'s scale", shape[:-1] + (_groups(shape[-1]),), torch.float32, dev)
+
+
+def _new_codes(shape, dev):
+    return (torch.empty(shape, dtype=_FP8, device=dev),
+            torch.empty(shape[:-1] + (_groups(shape[-1]),), dtype=torch.float32, device=dev))
+
+
+def act8_pack(x, stream=None):
+    """Activations in 8 bits (vmscan_act8_pack): returns (codes, scale), e4m3 codes in x's shape and a float32 scale for
+    each 128 channels, [..., ceil(dim / 128)]; codes * scale is x to 2^-4 of each value.
+
+    x: [..., dim] float32 or bfloat16, contiguous or [rows, dim] with rows apart."""
+    if stream is not None:
+        return _on_stream(stream, act8_pack, x)
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with a channel dimension")
+    dt, shape = _is_act(x, "x", x.dim()), tuple(x.shape)
+    row_stride = _row_stride(x, "x")
+    codes, scale = _new_codes(shape, x.device)
+    _enqueue(load().vmscan_act8_pack,
+             (x.data_ptr(), row_stride, codes.data_ptr(), scale.data_ptr(), x.numel() // shape[-1] if shape[-1] else 0,
+              shape[-1], dt, _current(x.device)), x.device)
+    return codes, scale
+
+
+def act8_unpack(codes, scale, dtype=torch.bfloat16, out=None, stream=None):
+    """The activations that ``act8_pack`` (or an operator's ``keep``) left in 8 bits (vmscan_act8_unpack)."""
+    if stream is not None:
+        return _on_stream(stream, act8_unpack, codes, scale, dtype, out)
+    _codes(codes, scale, None, None, "the 8-bit form")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    shape, dev = tuple(codes.shape), codes.device
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", shape, dtype, dev)
+    _enqueue(load().vmscan_act8_unpack,
+             (codes.data_ptr(), scale.data_ptr(), out.data_ptr(), codes.numel() // shape[-1] if shape[-1] else 0, shape[-1],
+              _DTYPES[dtype], _current(dev)), dev)
+    return out
+
+
+def _tokens(t, name):
+    """[batch, ..., dim] as [batch, tokens, dim] without a copy."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() == 3:
+        return t
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [batch, tokens, dim] or [batch, ..., dim], got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or [batch, tokens, dim] with contiguous channels")
+    return t.view(t.shape[0], -1, t.shape[-1])
+
+
+def groupnorm_fwd(x, weight, bias, groups, eps=1e-5, act=True, lengths=None, keep=False, y=None, workspace=None,
+                  stream=None, prepare=False):
+    """Group norm of channels-last tokens with an optional SiLU (vmscan_groupnorm_fwd); returns (y, mean, rstd, kept).
+
+    x: [batch, L, dim] float32 or bfloat16, any strides with contiguous channels, or contiguous [batch, ..., dim];
+    weight, bias: [dim] float32; groups: of dim / groups neighbouring channels, each normalised over a batch row's
+    tokens; lengths: [batch] int32, the tokens of each row (y is 0 past them).  mean, rstd: [batch, groups] float32, for
+    ``groupnorm_bwd``.  kept: with ``keep`` x in 8 bits, (codes, scale) as from ``act8_pack``, else None.
+    ``prepare`` as for ``vmscan_fwd_bidir``: returns (callable, y, mean, rstd, kept)."""
+    if stream is not None:
+        return _on_stream(stream, groupnorm_fwd, x, weight, bias, groups, eps, act, lengths, keep, y, workspace, None, prepare)
+    given, x = x, _tokens(x, "x")
+    dt = _is_act(x, "x", 3)
+    dev, shape = x.device, tuple(x.shape)
+    nb, L, dim = shape
+    xs = _strided(x, "x", shape, x.dtype, dev)
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    _need(bias, "bias", (dim,), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    if groups < 1 or dim % groups:
+        raise ValueError(f"{dim} channels cannot be {groups} groups")
+    if y is None:
+        y = torch.empty(given.shape, dtype=x.dtype, device=dev)
+    else:
+        _need(y, "y", given.shape, x.dtype, dev)
+    mean, rstd = torch.empty(2, nb, groups, dtype=torch.float32, device=dev).unbind(0)
+    kept = _new_codes(tuple(given.shape), dev) if keep else None
+    codes, scale = kept if keep else (None, None)
+    lib = load()
+    workspace = _workspace(workspace, lib.vmscan_groupnorm_fwd_workspace_bytes(nb, L, dim, groups, int(bool(keep))), dev)
+    args = (x.data_ptr(), xs, weight.data_ptr(), bias.data_ptr(), _p(lengths), y.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), _p(codes), _p(scale), nb, L, dim, groups, eps, int(bool(act)), dt, _p(workspace),
+            _nbytes(workspace), _current(dev))
+    run = _enqueue(lib.vmscan_groupnorm_fwd, args, dev, prepare,
+                   (x, weight, bias, lengths, y, mean, rstd, kept, workspace))
+    return (run, y, mean, rstd, kept) if prepare else (y, mean, rstd, kept)
+
+
+def groupnorm_bwd(dy, x, weight, bias, mean, rstd, act=True, lengths=None, workspace=None, stream=None, prepare=False):
+    """Gradient of ``groupnorm_fwd`` (vmscan_groupnorm_bwd); returns a dict with dx (dy's dtype), dweight and dbias [dim]
+    float32.
+
+    dy: [batch, L, dim] (strides as x's) or contiguous [batch, ..., dim]; x: the forward's input, or the (codes, scale)
+    that it kept in 8 bits; mean, rstd: the forward's.  ``prepare`` as for ``vmscan_bwd_bidir_v2``."""
+    if stream is not None:
+        return _on_stream(stream, groupnorm_bwd, dy, x, weight, bias, mean, rstd, act, lengths, workspace, None, prepare)
+    given, dy = dy, _tokens(dy, "dy")
+    dt = _is_act(dy, "dy", 3)
+    dev, shape = dy.device, tuple(dy.shape)
+    nb, L, dim = shape
+    dys = _strided(dy, "dy", shape, dy.dtype, dev)
+    codes = scale = xs = None
+    if isinstance(x, tuple):
+        codes, scale = x
+        x = None
+        _codes(codes, scale, tuple(given.shape), dev, "x")
+    else:
+        x = _tokens(x, "x")
+        xs = _strided(x, "x", shape, dy.dtype, dev)
+    _need(weight, "weight", (dim,), torch.float32, dev)
+    _need(bias, "bias", (dim,), torch.float32, dev)
+    if not isinstance(mean, torch.Tensor) or mean.dim() != 2:
+        raise ValueError("mean must be [batch, groups]")
+    groups = mean.shape[1]
+    _need(mean, "mean", (nb, groups), torch.float32, dev)
+    _need(rstd, "rstd", (nb, groups), torch.float32, dev)
+    if groups < 1 or dim % groups:
+        raise ValueError(f"{dim} channels cannot be {groups} groups")
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    dx = torch.empty(given.shape, dtype=dy.dtype, device=dev)
+    dw, db = torch.empty(2, dim, dtype=torch.float32, device=dev).unbind(0)
+    lib = load()
+    workspace = _workspace(workspace, lib.vmscan_groupnorm_bwd_workspace_bytes(nb, L, dim, groups), dev)
+    args = (dy.data_ptr(), dys, _p(x), xs, _p(codes), _p(scale), weight.data_ptr(), bias.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), _p(lengths), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), nb, L, dim, groups, int(bool(act)),
+            dt, _p(workspace), _nbytes(workspace), _current(dev))
+    g = dict(dx=dx, dweight=dw, dbias=db)
+    run = _enqueue(lib.vmscan_groupnorm_bwd, args, dev, prepare,
+                   (dy, x, codes, scale, weight, bias, mean, rstd, lengths, g, workspace))
+    return (run, g) if prepare else g
+
+
+def gated_scan_fwd(x, r, i, A_log, initial_state=None, lengths=None, reverse=False, keep=False, out=None, final_state=None,
+                   workspace=None, stream=None, prepare=False):
+    """Gated linear recurrence with one state per channel (vmscan_gated_scan_fwd); returns (out, final_state, kept).
+
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with a_t = exp(-exp(A_log) sigmoid(r_t)); out is h.  x, r, i:
+    [batch, L, dim] float32 or bfloat16, any strides with contiguous channels; A_log: [dim] float32.  initial_state /
+    final_state: [batch, dim] float32; the same tensor for both is updated in place.  lengths: [batch] int32, the
+    tokens of each row; out is 0 past them.  ``reverse`` walks from a row's last token to its first.  kept: with ``keep``
+    x, r, i and h in 8 bits for ``gated_scan_bwd``, (codes [4, batch, L, dim], scale), else None.  ``prepare`` as
+    for ``vmscan_fwd_bidir``: returns (callable, out, final_state, kept)."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_fwd, x, r, i, A_log, initial_state, lengths, reverse, keep, out, final_state,
+                          workspace, None, prepare)
+    dt = _is_act(x, "x", 3)
+    dev, shape, adt = x.device, tuple(x.shape), x.dtype
+    nb, L, dim = shape
+    xs, rs, is_ = (_strided(t, name, shape, adt, dev) for name, t in (("x", x), ("r", r), ("i", i)))
+    _need(A_log, "A_log", (dim,), torch.float32, dev)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _need(t, name, (nb, dim), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=adt, device=dev)
+    else:
+        _need(out, "out", shape, adt, dev)
+    if final_state is None:
+        final_state = torch.empty(nb, dim, dtype=torch.float32, device=dev)
+    kept = _new_codes((4,) + shape, dev) if keep else None
+    codes, scale = kept if keep else (None, None)
+    lib = load()
+    workspace = _workspace(workspace, lib.vmscan_gated_scan_fwd_workspace_bytes(nb, L, dim), dev)
+    args = (x.data_ptr(), xs, r.data_ptr(), rs, i.data_ptr(), is_, A_log.data_ptr(), _p(initial_state), _p(lengths),
+            int(bool(reverse)), out.data_ptr(), final_state.data_ptr(), _p(codes), _p(scale), nb, L, dim, dt, _p(workspace),
+            _nbytes(workspace), _current(dev))
+    run = _enqueue(lib.vmscan_gated_scan_fwd, args, dev, prepare,
+                   (x, r, i, A_log, initial_state, lengths, out, final_state, kept, workspace))
+    return (run, out, final_state, kept) if prepare else (out, final_state, kept)
+
+
+def gated_scan_bwd(kept, A_log, dout, initial_state=None, lengths=None, reverse=False, dfinal_state=None, workspace=None,
+                   stream=None, prepare=False):
+    """Gradients of ``gated_scan_fwd`` (vmscan_gated_scan_bwd); returns a dict with dx, dr, di (dout's dtype), dA_log [dim]
+    and dinitial_state [batch, dim] float32 (None without an initial_state).  Deterministic.
+
+    kept: (x, r, i, h), the forward's inputs and its out, or the (codes, scale) that it kept in 8 bits; dout: [batch, L,
+    dim], any strides with contiguous channels; dfinal_state: [batch, dim] float32 or None; the others as in the forward.
+    ``prepare`` as for ``vmscan_bwd_bidir_v2``."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_bwd, kept, A_log, dout, initial_state, lengths, reverse, dfinal_state,
+                          workspace, None, prepare)
+    dt = _is_act(dout, "dout", 3)
+    dev, shape, adt = dout.device, tuple(dout.shape), dout.dtype
+    nb, L, dim = shape
+    dos = _strided(dout, "dout", shape, adt, dev)
+    x = r = i = h = codes = scale = xs = rs = is_ = None
+    if not isinstance(kept, (tuple, list)) or len(kept) not in (2, 4):
+        raise TypeError("kept must be (x, r, i, h), or the (codes, scale) that the forward kept")
+    if len(kept) == 2:
+        codes, scale = kept
+        _codes(codes, scale, (4,) + shape, dev, "kept")
+    else:
+        x, r, i, h = kept
+        xs, rs, is_ = (_strided(t, name, shape, adt, dev) for name, t in (("x", x), ("r", r), ("i", i)))
+        _need(h, "h", shape, adt, dev)
+    _need(A_log, "A_log", (dim,), torch.float32, dev)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _need(t, name, (nb, dim), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (nb,), torch.int32, dev)
+    f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=dev)
+    act = lambda: torch.empty(shape, dtype=adt, device=dev)
+    g = dict(dx=act(), dr=act(), di=act(), dA_log=f32(dim), dinitial_state=f32(nb, dim) if initial_state is not None else None)
+    lib = load()
+    workspace = _workspace(workspace, lib.vmscan_gated_scan_bwd_workspace_bytes(nb, L, dim), dev)
+    args = (_p(x), xs, _p(r), rs, _p(i), is_, _p(h), _p(codes), _p(scale), A_log.data_ptr(), _p(initial_state), _p(lengths),
+            int(bool(reverse)), dout.data_ptr(), dos, _p(dfinal_state), g["dx"].data_ptr(), g["dr"].data_ptr(),
+            g["di"].data_ptr(), g["dA_log"].data_ptr(), _p(g["dinitial_state"]), nb, L, dim, dt, _p(workspace),
+            _nbytes(workspace), _current(dev))
+    run = _enqueue(lib.vmscan_gated_scan_bwd, args, dev, prepare,
+                   (x, r, i, h, codes, scale, A_log, initial_state, lengths, dout, dfinal_state, g, workspace))
+    return (run, g) if prepare else g
+
+
+def gated_scan_step(x, r, i, A_log, state, slots=None, out=None, stream=None, prepare=False):
+    """One token of each of ``batch`` sequences (vmscan_gated_scan_step): updates ``state`` in place and returns out
+    [batch, dim].
+
+    x, r, i: [batch, dim], rows apart or not; state: [pool, dim] float32; slots: [batch] int32, the state of each
+    sequence (all different; one outside 0 .. pool - 1 skips the row, whose out is 0), or None with pool = batch.
+    ``prepare`` as for ``gated_scan_fwd``: returns (callable, out)."""
+    if stream is not None:
+        return _on_stream(stream, gated_scan_step, x, r, i, A_log, state, slots, out, None, prepare)
+    dt = _is_act(x, "x", 2)
+    dev, shape, adt = x.device, tuple(x.shape), x.dtype
+    nb, dim = shape
+    strides = []
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape or t.dtype != adt or t.device != dev:
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {adt} on {dev}")
+        s = t.stride()
+        if s[1] != 1 and dim != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+        strides.append(s[0] if nb != 1 else 0)
+    _need(A_log, "A_log", (dim,), torch.float32, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be [pool, dim]")
+    pool = state.shape[0]
+    _need(state, "state", (pool, dim), torch.float32, dev)
+    if slots is not None:
+        _need(slots, "slots", (nb,), torch.int32, dev)
+    elif pool != nb:
+        raise ValueError(f"without slots the pool holds one state per sequence: {pool} for {nb}")
+    if out is None:
+        out = torch.empty(shape, dtype=adt, device=dev)
+    else:
+        _need(out, "out", shape, adt, dev)
+    args = (x.data_ptr(), strides[0], r.data_ptr(), strides[1], i.data_ptr(), strides[2], A_log.data_ptr(),
+            state.data_ptr(), _p(slots), out.data_ptr(), nb, pool, dim, dt, _current(dev))
+    run = _enqueue(load().vmscan_gated_scan_step, args, dev, prepare, (x, r, i, A_log, state, slots, out))
     return (run, out) if prepare else out

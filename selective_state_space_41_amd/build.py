@@ -16,7 +16,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libvmscan.so")
-SOURCES = ("vmscan.hip", "linattn.hip", "norm.hip", "rope.hip")  # in csrc/
+SOURCES = ("vmscan.hip", "linattn.hip", "norm.hip", "rope.hip", "act8.hip", "groupnorm.hip", "gated_scan.hip")  # in csrc/
 PROBE = os.path.join(PKG, "vmscan_probe")
 
 # Packed fp32 VALU forms are kept out of every gfx950 code object.
@@ -90,7 +90,7 @@ SCRATCH_ALLOWED = [("bwd_scan_kernelIf", 64), ("linattn_grad_kernelItLi64ELi64E"
                    ("rmsnorm_bwd_kernelIffLi64ELi16ELi4E", 228), ("rmsnorm_bwd_kernelItfLi64ELi16ELi4E", 208),
                    ("rmsnorm_bwd_kernelIttLi64ELi16ELi4E", 204)]
 # Kernels whose scratch is checked beside those with a floor.
-SCRATCH_CHECKED = ("linattn_", "rmsnorm_", "rope_kernel")
+SCRATCH_CHECKED = ("linattn_", "rmsnorm_", "rope_kernel", "act8_", "groupnorm_", "gated_scan_")
 
 
 def kernel_resources(report):
