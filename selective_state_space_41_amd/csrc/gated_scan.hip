@@ -1,14 +1,21 @@
 // Gated linear recurrence with one state per channel: forward, gradient and single tokens.  What is computed is
 // stated in include/vmscan.h.
 //
-// A workgroup owns 2 * CL neighbouring channels of one sequence, two to a lane, and walks the sequence in blocks of
-// R runs of S tokens.  A run's S tokens stay in registers: their (decay, input) pairs are joined to one pair, the R
-// pairs of a block meet in LDS, and every run then walks its tokens from the state that enters it.  Inputs are read
-// once and the outputs written once.  Where there are too few sequences and channels for the chip a sequence is cut
-// into segments, whose own pairs a first launch makes.
+// A workgroup owns 128 neighbouring channels, two to a lane, of a chunk of R * S tokens; a wave owns a run of S of
+// them, whose (decay, input) pairs stay in its registers.  The pairs of a run are joined to one pair, the R pairs of a
+// chunk meet in LDS and become the chunk's pair, which is published for the chunks after it; the state that enters
+// the chunk comes from those before it in the same way, and every run then walks its tokens from the state that
+// enters it.  So inputs are read once and outputs written once however long the sequence is.
+//
+// Between chunks: a chunk waits for the published pairs of the chunks before it in its group of 4 R and for
+// the state that the last chunk of the group before published.  The order of the joins is fixed, whatever arrives
+// first.  Workgroups take their chunks in the order in which they start (a counter), chunks of all sequences by their
+// place, so a chunk only waits for chunks that running workgroups hold: every wait ends.  A published value is one
+// 64-bit word that is written at once; a first launch sets all of them to a value that no result has.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "vmscan.h"
@@ -31,26 +38,49 @@ struct ScanArgs {
   uint8_t* keep;
   float* keep_scale;
   float *end, *dA_log;           // the state at the end (gradient: of the one at the start)
-  float2* pairs;                 // per sequence and segment: channels' pairs
-  float* part;                   // gradient: per sequence and segment, channels' sums for A_log
+  uint32_t* status;              // the wait status word and, behind it, the counter of started workgroups
+  uint64_t* pairs;               // per chain and chunk: 128 channels' pairs
+  uint64_t* states;              // per chain and group of chunks: the states after it
+  float* part;                   // gradient: per sequence and chunk, channels' sums for A_log
   int64_t x_batch, x_token, r_batch, r_token, i_batch, i_token, dout_batch, dout_token;
   int64_t batch, seqlen, plane;  // plane: tokens of a plane of the 8-bit copies
   int dim, groups, tiles;
-  int segments, seg_len;
+  int chains, chunks;            // chains: sequences' tiles of 128 channels; chunks of a sequence
   int reverse;
 };
+
+constexpr int kTile = 128;          // channels of a workgroup
+// Chunks whose pairs are joined one by one, four by each of a workgroup's R waves.
+__host__ __device__ constexpr int groups_of(int chunks, int R) { return (chunks + 4 * R - 1) / (4 * R); }
+constexpr uint64_t kNothing = ~uint64_t{0};
+constexpr int kPatience = 1 << 22;  // polls of a wait that should have ended long ago
 
 // Two neighbouring channels.
 struct Two {
   float a, b;
 };
+// As loaded: a bfloat16 or 8-bit pair stays one register until it is used.
+struct RawB {
+  uint32_t w;
+};
+struct Raw8 {
+  uint32_t w;
+};
+__device__ __forceinline__ Two values(RawB r) { return {__uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u)}; }
+__device__ __forceinline__ Two values(Two r) { return r; }
+__device__ __forceinline__ Two values(Raw8 r) {
+  const auto v = __builtin_amdgcn_cvt_pk_f32_fp8(r.w, false);
+  return {v[0], v[1]};
+}
 // `p` is the row's place of this lane's first channel; ODD: the second may be missing (d1 = 0 reads the first again).
 template <bool ODD>
-__device__ __forceinline__ Two load2(const uint16_t* p, int d1) {
-  if constexpr (ODD) return {bf16_to_f32(p[0]), bf16_to_f32(p[d1])};
+__device__ __forceinline__ RawB load2(const uint16_t* p, int d1) {
   uint32_t w;
-  __builtin_memcpy(&w, p, 4);
-  return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+  if constexpr (ODD)
+    w = p[0] | static_cast<uint32_t>(p[d1]) << 16;
+  else
+    __builtin_memcpy(&w, p, 4);
+  return {w};
 }
 template <bool ODD>
 __device__ __forceinline__ Two load2(const float* p, int d1) {
@@ -60,24 +90,23 @@ __device__ __forceinline__ Two load2(const float* p, int d1) {
   return {v.x, v.y};
 }
 template <bool ODD>
-__device__ __forceinline__ Two load2(const uint8_t* p, int d1) {
-  uint32_t w;
-  if constexpr (ODD) {
-    w = p[0] | static_cast<uint32_t>(p[d1]) << 8;
-  } else {
-    uint16_t h;
-    __builtin_memcpy(&h, p, 2);
-    w = h;
-  }
-  const auto v = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-  return {v[0], v[1]};
+__device__ __forceinline__ Raw8 load2(const uint8_t* p, int d1) {
+  if constexpr (ODD) return {p[0] | static_cast<uint32_t>(p[d1]) << 8};
+  uint16_t h;
+  __builtin_memcpy(&h, p, 2);
+  return {h};
 }
+template <typename T, bool ODD>
+using Raw = decltype(load2<ODD>(static_cast<const T*>(nullptr), 0));
+// n: channels that exist, 1 at least.
 template <bool ODD>
 __device__ __forceinline__ void store2(uint16_t* p, int n, Two v) {
   if (ODD && n == 1) {
     store1(p, v.a);
-  } else if (n > 0) {
-    const uint32_t w = static_cast<uint32_t>(f32_to_bf16(v.a)) | static_cast<uint32_t>(f32_to_bf16(v.b)) << 16;
+  } else {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 w = __builtin_convertvector((f32x2{v.a, v.b}), bf16x2);  // nearest even, both at once
     __builtin_memcpy(p, &w, 4);
   }
 }
@@ -85,7 +114,7 @@ template <bool ODD>
 __device__ __forceinline__ void store2(float* p, int n, Two v) {
   if (ODD && n == 1) {
     *p = v.a;
-  } else if (n > 0) {
+  } else {
     const float2 w = make_float2(v.a, v.b);
     __builtin_memcpy(p, &w, 8);
   }
@@ -105,63 +134,101 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// A token's decay from rate = e^A_log and the gate's sigmoid: a = e^-y and w = 1 - a^2 for y = rate * sigmoid(r) >= 0.
-// Below v = 2 y = 1/4 the difference is the series of 1 - e^-v (the next term is under 2^-24 of it); above, one
-// fused multiply-add.
-struct Decay {
-  float a, w, y;
+// 1 / (1 + 2^t)
+__device__ __forceinline__ float sigmoid_of(float t) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t)); }
+
+// A channel's rate e^A_log, as the factor of the decay's exponent and of v below.
+struct Rate {
+  float e, v;  // -rate log2(e), 2 rate
 };
-__device__ __forceinline__ Decay decay_of(float rate, float p) {
-  Decay d;
-  d.y = rate * p;
-  d.a = __builtin_amdgcn_exp2f(d.y * -kLog2e);
-  const float v = d.y + d.y;
-  float s = __builtin_fmaf(v, -1.0f / 720.0f, 1.0f / 120.0f);
-  s = __builtin_fmaf(v, s, -1.0f / 24.0f);
-  s = __builtin_fmaf(v, s, 1.0f / 6.0f);
-  s = __builtin_fmaf(v, s, -0.5f);
+__device__ __forceinline__ Rate rate_of(const float* A_log, int c) {
+  const float r = __builtin_amdgcn_exp2f(A_log[c] * kLog2e);
+  return {r * -kLog2e, r + r};
+}
+__device__ __forceinline__ float decay_of(Rate rate, float p) { return __builtin_amdgcn_exp2f(rate.e * p); }
+
+// w = 1 - a^2 = 1 - e^-v for v = 2 rate sigmoid(r) >= 0 and a = e^(-v/2).  Below v = 1/4 by v times a polynomial for
+// (1 - e^-v) / v, interpolated at Chebyshev points with the value 1 at 0 (within 0.2 * 2^-24 of it; the first four
+// terms of the series would leave 23); above, one fused multiply-add.
+__device__ __forceinline__ float gain_of(float a, float v) {
+  float s = __builtin_fmaf(v, 0x1.f6c6ecp-8f, -0x1.547fd4p-5f);
+  s = __builtin_fmaf(v, s, 0x1.5552aep-3f);
+  s = __builtin_fmaf(v, s, -0x1.fffffep-2f);
   s = __builtin_fmaf(v, s, 1.0f);
-  d.w = v < 0.25f ? v * s : __builtin_fmaf(-d.a, d.a, 1.0f);
-  return d;
+  s *= v;
+  asm volatile("" : "+v"(s));  // both are computed: the compiler would branch around the polynomial
+  return v < 0.25f ? s : __builtin_fmaf(-a, a, 1.0f);
 }
 
 template <typename T>
 constexpr bool kTail = sizeof(T) == 4;
 
-__device__ __forceinline__ int64_t tokens_of(const ScanArgs& a, int64_t b) {
-  if (!a.lengths) return a.seqlen;
-  const int64_t n = a.lengths[b];
-  return n < 0 ? 0 : n > a.seqlen ? a.seqlen : n;
+__device__ __forceinline__ int tokens_of(const ScanArgs& a, int64_t b) {
+  const int all = static_cast<int>(a.seqlen);
+  if (!a.lengths) return all;
+  const int n = a.lengths[b];
+  return n < 0 ? 0 : n > all ? all : n;
 }
 
-// What a workgroup and a lane work on.  Tokens are counted along the walk; `back` walks turn the count around within
+// What a workgroup and a wave work on.  Tokens are counted along the walk; `back` walks turn the count around within
 // the row's n tokens, and what lies past them keeps its place.
-template <int CL, bool ODD>
+template <int R, int S, bool ODD>
 struct Where {
-  int64_t b, n;
-  int seg, tile, run, c, cc, d1, have;  // c: first channel, cc: one that exists, have: channels that exist
+  int64_t b;
+  int n, mine, left, rest;  // the sequence's tokens, the wave's first; live and written ones from there on (any sign)
+  int chain, chunk, run, tile, lane;
+  int c, cc, d1, have;      // first channel, one that exists, 1 if the next exists too, channels that exist
   bool back;
-  __device__ __forceinline__ Where(const ScanArgs& a, bool turn) {
-    const int64_t u = blockIdx.x;
-    tile = static_cast<int>(u % a.tiles);
-    const int64_t s = u / a.tiles;
-    seg = static_cast<int>(s % a.segments);
-    b = s / a.segments;
-    n = tokens_of(a, b);
-    run = threadIdx.x / CL;
-    c = (tile * CL + threadIdx.x % CL) * 2;
+  __device__ __forceinline__ Where(const ScanArgs& a, uint32_t unit, bool turn) {
+    chunk = __builtin_amdgcn_readfirstlane(unit / static_cast<uint32_t>(a.chains));
+    chain = static_cast<int>(unit - static_cast<uint32_t>(chunk) * static_cast<uint32_t>(a.chains));
+    const int row = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(chain) / static_cast<uint32_t>(a.tiles));
+    tile = chain - row * a.tiles;
+    b = row;
+    n = __builtin_amdgcn_readfirstlane(tokens_of(a, b));
+    run = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    lane = threadIdx.x % 64;
+    mine = chunk * (R * S) + run * S;
+    left = n - mine;
+    rest = static_cast<int>(a.seqlen) - mine;
+    c = tile * kTile + lane * 2;
     have = a.dim - c;
     const int top = ODD ? a.dim - 1 : a.dim - 2;
     cc = c < top ? c : top;
     d1 = !ODD || cc + 1 < a.dim ? 1 : 0;
     back = (a.reverse != 0) != turn;
   }
-  // The place of the walk's token t < n; of any other, t itself.
-  __device__ __forceinline__ int64_t at(int64_t t) const { return back && t < n ? n - 1 - t : t; }
-  __device__ __forceinline__ int64_t in(int64_t t) const { return at(t < n ? t : n - 1); }  // n > 0
+  __device__ __forceinline__ int begin() const { return chunk * (R * S); }
+  // The chunk that holds the walk's last token (the first one of a row without tokens).
+  __device__ __forceinline__ bool last() const { return begin() + R * S >= n; }
+  // The place of the wave's token k, live or not.
+  __device__ __forceinline__ int at(int k) const { return back && k < left ? n - 1 - mine - k : mine + k; }
 };
 
-__device__ __forceinline__ float rate_of(const float* A_log, int c) { return __builtin_amdgcn_exp2f(A_log[c] * kLog2e); }
+// A lane's channels in a uniform row: a scalar base and a 32-bit offset.
+template <typename T>
+__device__ __forceinline__ T* in_row(T* row, int c) {
+  using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+  using Global = Byte __attribute__((address_space(1)));
+  Global* base = (Global*)reinterpret_cast<Byte*>(row);
+  asm("" : "+s"(base));  // the sum is the load's or store's own, not a 64-bit addition in every lane
+  return reinterpret_cast<T*>((Byte*)(base + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
+}
+
+// The rows of the wave's live tokens, one after another along the walk.
+template <typename T>
+struct Rows {
+  T* row;
+  int64_t step;
+  template <typename W>
+  __device__ __forceinline__ Rows(T* tokens, int64_t token, const W& w, int from = 0)
+      : row(tokens + (w.back ? w.n - 1 - w.mine - from : w.mine + from) * token), step(w.back ? -token : token) {}
+  __device__ __forceinline__ T* next(int c) {
+    T* p = in_row(row, c);
+    row += step;
+    return p;
+  }
+};
 
 // (decay, input) pairs after one another: h -> A h + H.
 struct Pairs {
@@ -171,381 +238,448 @@ __device__ __forceinline__ void then(Pairs& p, float a0, float h0, float a1, flo
   p.H0 = __builtin_fmaf(a0, p.H0, h0), p.A0 *= a0;
   p.H1 = __builtin_fmaf(a1, p.H1, h1), p.A1 *= a1;
 }
-
-// The state that enters this thread's run, from the one that enters the block (c0, c1), which becomes the one after it.
-template <int CL, int R>
-__device__ __forceinline__ Two enter(const float4 (&part)[R][CL], int run, float& c0, float& c1) {
-  Two in{c0, c1};
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    if (j == run) in = {c0, c1};
-    const float4 q = part[j][threadIdx.x % CL];
-    c0 = __builtin_fmaf(q.x, c0, q.y);
-    c1 = __builtin_fmaf(q.z, c1, q.w);
-  }
-  return in;
+__device__ __forceinline__ Two through(const Pairs& p, Two h) {
+  return {__builtin_fmaf(p.A0, h.a, p.H0), __builtin_fmaf(p.A1, h.b, p.H1)};
 }
 
-// The state that enters a segment: the given one through the pairs of the segments before.  Of several segments each
-// takes the given one from its copy in the last segment's place, so that the state at the end may be written over it.
-template <typename W>
-__device__ __forceinline__ Two enter_segment(const ScanArgs& a, const W& w, const float* first) {
-  Two h{0.0f, 0.0f};
-  if (a.segments > 1) {
-    const float2* p = a.pairs + (w.b * a.segments + a.segments - 1) * a.dim + w.cc;
-    h = {p[0].y, p[w.d1].y};
-  } else if (first) {
-    h = {first[w.b * a.dim + w.cc], first[w.b * a.dim + w.cc + w.d1]};
+// Published words.  A NaN is published as the usual one, so that no result is kNothing.
+__device__ __forceinline__ uint32_t word_of(float v) { return v == v ? __float_as_uint(v) : 0x7fc00000u; }
+__device__ __forceinline__ void publish(uint64_t* at, float lo, float hi) {
+  __hip_atomic_store(at, static_cast<uint64_t>(word_of(hi)) << 32 | word_of(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t* at) {
+  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 await(const uint64_t* at, uint64_t v, uint32_t* status) {
+  for (int i = 0; v == kNothing && i < kPatience; ++i) {
+    __builtin_amdgcn_s_sleep(1);
+    v = peek(at);
   }
-  for (int s = 0; s < w.seg; ++s) {
-    const float2* p = a.pairs + (w.b * a.segments + s) * a.dim + w.cc;
-    const float2 p0 = p[0], p1 = p[w.d1];
-    h.a = __builtin_fmaf(p0.x, h.a, p0.y);
-    h.b = __builtin_fmaf(p1.x, h.b, p1.y);
+  if (v == kNothing) *status = 1;
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
+// What a workgroup's waves share.
+template <int R>
+struct Shared {
+  float4 part[R][64];    // the runs' pairs
+  float4 before[R][64];  // the pairs of the chunks before, four by four
+  float2 base[64];       // the state before those
+};
+
+// The workgroup's unit of work, of chains times chunks: where chunks wait for others, by the order of their start.
+__device__ __forceinline__ uint32_t unit_of(const ScanArgs& a) {
+  __shared__ uint32_t ticket;
+  if (a.chunks == 1) return blockIdx.x;
+  if (threadIdx.x == 0) ticket = __hip_atomic_fetch_add(a.status + 1, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(ticket);
+}
+
+// The state that enters this wave's run, from its pair p.  `first` is the state at the sequence's start; `after` gets the
+// state after the sequence's last token.  Each wave joins four of the chunks before, and all of them the waves' pairs.
+template <int R, int S, bool ODD>
+__device__ __forceinline__ Two enter(const ScanArgs& a, const Where<R, S, ODD>& w, const Pairs& p, Shared<R>& s,
+                                     const float* first, float* after) {
+  constexpr int kEach = 4, kGroupChunks = kEach * R;
+  const int lane = w.lane, group = w.chunk / kGroupChunks, begin = group * kGroupChunks;
+  uint64_t* mine = a.pairs + (static_cast<int64_t>(w.chain) * a.chunks + w.chunk) * kTile + lane;
+  uint64_t* state = a.states + (static_cast<int64_t>(w.chain) * groups_of(a.chunks, R) + group) * 64 + lane;
+  const bool last = w.last();
+  // what the chunks before have published by now; the others are waited for below
+  const int from = begin + w.run * kEach, many = w.chunk - from < kEach ? w.chunk - from : kEach;
+  const uint64_t* theirs = mine - static_cast<int64_t>(w.chunk - from) * kTile;
+  uint64_t v[kEach][2], base = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (k < many) v[k][0] = peek(theirs + k * kTile), v[k][1] = peek(theirs + k * kTile + 64);
+  if (w.run == R - 1 && group > 0) base = peek(state - 64);
+  s.part[w.run][lane] = make_float4(p.A0, p.H0, p.A1, p.H1);
+  __syncthreads();
+  Pairs all{1.0f, 0.0f, 1.0f, 0.0f};
+  if (w.run == 0) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float4 q = s.part[j][lane];
+      then(all, q.x, q.y, q.z, q.w);
+    }
+    if (group == 0) {
+      Two h{0.0f, 0.0f};
+      if (w.chunk == 0 && first) h = {first[w.b * a.dim + w.cc], first[w.b * a.dim + w.cc + w.d1]};
+      s.base[lane] = make_float2(h.a, h.b);
+      if (w.chunk == 0) {  // the state after it, whatever enters: no other chunk reads the state at the start
+        const Two end = through(all, h);
+        all = {0.0f, end.a, 0.0f, end.b};
+      }
+    }
+    if (!last) {
+      publish(mine, all.A0, all.H0);
+      publish(mine + 64, all.A1, all.H1);
+    }
+  }
+  Pairs q{1.0f, 0.0f, 1.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (k < many) {
+      const float2 p0 = await(theirs + k * kTile, v[k][0], a.status), p1 = await(theirs + k * kTile + 64, v[k][1], a.status);
+      then(q, p0.x, p0.y, p1.x, p1.y);
+    }
+  if (many > 0) s.before[w.run][lane] = make_float4(q.A0, q.H0, q.A1, q.H1);
+  if (w.run == R - 1 && group > 0) s.base[lane] = await(state - 64, base, a.status);
+  __syncthreads();
+  const float2 b = s.base[lane];
+  Two h{b.x, b.y};
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (begin + j * kEach < w.chunk) {
+      const float4 t = s.before[j][lane];
+      h = {__builtin_fmaf(t.x, h.a, t.y), __builtin_fmaf(t.z, h.b, t.w)};
+    }
+  if (w.run == 0) {
+    const Two end = through(all, h);
+    if (!last && w.chunk == begin + kGroupChunks - 1) publish(state, end.a, end.b);
+    if (last && after) {
+      if (w.have > 0) after[w.b * a.dim + w.c] = end.a;
+      if (w.have > 1) after[w.b * a.dim + w.c + 1] = end.b;
+    }
+  }
+  for (int j = 0; j < w.run; ++j) {
+    const float4 t = s.part[j][lane];
+    h = {__builtin_fmaf(t.x, h.a, t.y), __builtin_fmaf(t.z, h.b, t.w)};
   }
   return h;
 }
 
-template <typename W>
-__device__ __forceinline__ void put(float* to, const ScanArgs& a, const W& w, float v0, float v1) {
-  if (w.have > 0) to[w.b * a.dim + w.c] = v0;
-  if (w.have > 1) to[w.b * a.dim + w.c + 1] = v1;
-}
-
-// A token's (a, beta, sigmoid(i) x) of both channels -> (a, b).
-template <typename T>
-__device__ __forceinline__ void forward_of(Two x, Two r, Two i, Two rate, bool live, Two& a, Two& b) {
-  const Decay d0 = decay_of(rate.a, sigmoid<kTail<T>>(r.a)), d1 = decay_of(rate.b, sigmoid<kTail<T>>(r.b));
-  const float q0 = sigmoid<kTail<T>>(i.a), q1 = sigmoid<kTail<T>>(i.b);
-  a = live ? Two{d0.a, d1.a} : Two{1.0f, 1.0f};
-  b = live ? Two{__builtin_amdgcn_sqrtf(d0.w) * q0 * x.a, __builtin_amdgcn_sqrtf(d1.w) * q1 * x.b} : Two{0.0f, 0.0f};
-}
-
-// The 8-bit copy of a token's 128 channels, two to a lane of the wave.
-template <bool ODD>
-__device__ __forceinline__ void keep2(const ScanArgs& a, int plane, int64_t row, int c, int have, Two v) {
-  float top = Max::of(have > 0 ? __builtin_fabsf(v.a) : 0.0f, have > 1 ? __builtin_fabsf(v.b) : 0.0f);
-  top = over_lanes<Max, 64>(top);
-  const float s = scale_of(top), inv = 1.0f / s;
-  const uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(v.a * inv, v.b * inv, 0, false);
-  const int64_t at = plane * a.plane + row;
-  uint8_t* p = a.keep + at * a.dim + c;
-  if (have > 1) {
-    const uint16_t h = static_cast<uint16_t>(w);
-    __builtin_memcpy(p, &h, 2);
-  } else if (ODD && have == 1) {
-    *p = static_cast<uint8_t>(w);
+// The 8-bit copies of four tokens' 128 channels, two to a lane.  The four largest magnitudes are found together: each
+// exchange of half the lanes leaves one register for two, so that a row of 16 lanes ends up with one token (as
+// unsigned numbers, whose order is that of the magnitudes and in which a NaN is the largest).  `rows` gives the
+// token's row of the plane's codes, `place` its number in the plane.
+template <bool ODD, typename ROW, typename PLACE>
+__device__ __forceinline__ void keep4(float* scales, int groups, int c, int have, int lane, int many, const Two (&v)[4],
+                                      ROW&& row, PLACE&& place) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const auto larger = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  const auto bits = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
+  uint32_t m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = larger(bits(v[k].a), ODD && have < 2 ? 0u : bits(v[k].b));
+    if (have <= 0) m[k] = 0;
   }
-  if (threadIdx.x % 64 == 0) a.keep_scale[at * a.groups + c / kGroup] = s;
+  u32x2 r = __builtin_amdgcn_permlane32_swap(m[0], m[1], false, false);
+  const uint32_t m01 = larger(r[0], r[1]);
+  r = __builtin_amdgcn_permlane32_swap(m[2], m[3], false, false);
+  const uint32_t m23 = larger(r[0], r[1]);
+  r = __builtin_amdgcn_permlane16_swap(m01, m23, false, false);  // rows of 16 lanes: tokens 0, 2, 1, 3
+  uint32_t t = larger(r[0], r[1]);
+  t = larger(t, __float_as_uint(dpp<0xb1>(__uint_as_float(t))));
+  t = larger(t, __float_as_uint(dpp<0x4e>(__uint_as_float(t))));
+  t = larger(t, __float_as_uint(dpp<0x141>(__uint_as_float(t))));
+  t = larger(t, __float_as_uint(dpp<0x140>(__uint_as_float(t))));
+  // as scale_of and its reciprocal, by products (one unit in the last place)
+  const float top = __uint_as_float(t), q = top * (1.0f / kFp8Max);
+  const float s = top == 0.0f ? 1.0f : q < kMinScale ? kMinScale : q, inv = __builtin_amdgcn_rcpf(s);
+  constexpr int kRow[4] = {0, 32, 16, 48};
+  float f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), kRow[k]));
+  if (have > 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= many) break;
+      const uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(v[k].a * f[k], v[k].b * f[k], 0, false);
+      uint8_t* p = in_row(row(k), c);
+      if (ODD && have == 1) {
+        *p = static_cast<uint8_t>(w);
+      } else {
+        const uint16_t h = static_cast<uint16_t>(w);
+        __builtin_memcpy(p, &h, 2);
+      }
+    }
+  }
+  const int token = ((lane >> 5) & 1) | ((lane >> 3) & 2);
+  if (lane % 16 == 0 && token < many) scales[place(token) * groups] = s;
 }
 
-template <typename T, int CL, int R, int S, bool ODD, bool KEEP>
-__global__ __launch_bounds__(CL * R) void gated_scan_fwd_kernel(ScanArgs a) {
-  static_assert(!KEEP || CL == 64, "a scale's 128 channels are one wave's");
-  __shared__ float4 part[2][R][CL];
-  const Where<CL, ODD> w(a, false);
-  const Two rate{rate_of(a.A_log, w.cc), rate_of(a.A_log, w.cc + w.d1)};
-  Two carry = enter_segment(a, w, a.first);
-  const int64_t begin = static_cast<int64_t>(w.seg) * a.seg_len;
-  const int64_t end = begin + a.seg_len < a.seqlen ? begin + a.seg_len : a.seqlen;
-  const T* x = static_cast<const T*>(a.x) + w.b * a.x_batch + w.cc;
-  const T* r = static_cast<const T*>(a.r) + w.b * a.r_batch + w.cc;
-  const T* i = static_cast<const T*>(a.i) + w.b * a.i_batch + w.cc;
-  T* out = static_cast<T*>(a.out) + w.b * a.seqlen * a.dim + w.c;
-  int turn = 0;
-  for (int64_t t0 = begin; t0 < end; t0 += R * S, turn ^= 1) {
-    const int64_t mine = t0 + w.run * S;
-    Two av[S], bv[S];
-    Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
-    if (t0 < w.n) {
-      Two xv[S], rv[S], iv[S];
+// Before the chunk's entering state is known: a run's decays and inputs, joined to a pair, and its 8-bit copies.  FULL:
+// all S tokens are live.
+template <bool FULL, typename T, int R, int S, bool ODD, bool KEEP>
+__device__ __forceinline__ Pairs take_run(const ScanArgs& a, const Where<R, S, ODD>& w, Two (&av)[S], Two (&bv)[S]) {
+  const Rate rate0 = rate_of(a.A_log, w.cc), rate1 = rate_of(a.A_log, w.cc + w.d1);
+  Rows<const T> x(static_cast<const T*>(a.x) + w.b * a.x_batch, a.x_token, w);
+  Rows<const T> r(static_cast<const T*>(a.r) + w.b * a.r_batch, a.r_token, w);
+  Rows<const T> i(static_cast<const T*>(a.i) + w.b * a.i_batch, a.i_token, w);
+  Raw<T, ODD> xv[S], rv[S], iv[S];
 #pragma unroll
-      for (int k = 0; k < S; ++k) {
-        const int64_t t = w.in(mine + k);
-        xv[k] = load2<ODD>(x + t * a.x_token, w.d1);
-        rv[k] = load2<ODD>(r + t * a.r_token, w.d1);
-        iv[k] = load2<ODD>(i + t * a.i_token, w.d1);
-      }
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        const bool live = mine + k < w.n;
-        forward_of<T>(xv[k], rv[k], iv[k], rate, live, av[k], bv[k]);
-        then(p, av[k].a, bv[k].a, av[k].b, bv[k].b);
-        if constexpr (KEEP)
-          if (mine + k < end) {
-            const int64_t row = w.b * a.seqlen + w.at(mine + k);
-            const Two zero{0.0f, 0.0f};
-            keep2<ODD>(a, 0, row, w.c, w.have, live ? xv[k] : zero);
-            keep2<ODD>(a, 1, row, w.c, w.have, live ? rv[k] : zero);
-            keep2<ODD>(a, 2, row, w.c, w.have, live ? iv[k] : zero);
-          }
-      }
+  for (int k = 0; k < S; ++k) {
+    if (FULL || k < w.left) {
+      xv[k] = load2<ODD>(x.next(w.cc), w.d1);
+      rv[k] = load2<ODD>(r.next(w.cc), w.d1);
+      iv[k] = load2<ODD>(i.next(w.cc), w.d1);
     } else {
-#pragma unroll
-      for (int k = 0; k < S; ++k) av[k] = {1.0f, 1.0f}, bv[k] = {0.0f, 0.0f};
-      if constexpr (KEEP)
-        for (int k = 0; k < S; ++k)
-          if (mine + k < end)
-            for (int plane = 0; plane < 3; ++plane)
-              keep2<ODD>(a, plane, w.b * a.seqlen + mine + k, w.c, w.have, Two{0.0f, 0.0f});
+      xv[k] = rv[k] = iv[k] = {};
     }
-    part[turn][w.run][threadIdx.x % CL] = make_float4(p.A0, p.H0, p.A1, p.H1);
-    __syncthreads();
-    Two h = enter<CL, R>(part[turn], w.run, carry.a, carry.b);
+  }
+  if constexpr (KEEP) {
+    const int64_t row0 = w.b * a.seqlen;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      h = {__builtin_fmaf(av[k].a, h.a, bv[k].a), __builtin_fmaf(av[k].b, h.b, bv[k].b)};
-      const int64_t t = mine + k;
-      if (t < end) {
-        const Two y = t < w.n ? h : Two{0.0f, 0.0f};
-        store2<ODD>(out + w.at(t) * a.dim, w.have, y);
-        if constexpr (KEEP) keep2<ODD>(a, 3, w.b * a.seqlen + w.at(t), w.c, w.have, y);
+    for (int k = 0; k < S; k += 4) {
+      if (!FULL && k >= w.rest) break;
+#pragma unroll
+      for (int plane = 0; plane < 3; ++plane) {
+        const auto& v = plane == 0 ? xv : plane == 1 ? rv : iv;
+        const int64_t first = plane * a.plane + row0;
+        keep4<ODD>(
+            a.keep_scale + first * a.groups + w.tile, a.groups, w.c, w.have, w.lane, FULL ? 4 : w.rest - k,
+            {values(v[k]), values(v[k + 1]), values(v[k + 2]), values(v[k + 3])},
+            [&](int j) { return a.keep + (first + w.at(k + j)) * a.dim; }, [&](int j) { return static_cast<int64_t>(w.at(k + j)); });
+        __builtin_amdgcn_sched_barrier(0);  // one after another: registers
       }
     }
   }
-  if (a.end && w.seg == a.segments - 1 && w.run == 0) put(a.end, a, w, carry.a, carry.b);
-}
-
-// The last segment's pair, which nothing follows, holds the state given at the start.
-template <typename W>
-__device__ __forceinline__ void copy_first(const ScanArgs& a, const W& w, const float* first) {
-  if (w.run != 0) return;
-  float2* p = a.pairs + (w.b * a.segments + w.seg) * a.dim + w.c;
-  const float* f = first + w.b * a.dim + w.c;
-  if (w.have > 0) p[0] = make_float2(0.0f, first ? f[0] : 0.0f);
-  if (w.have > 1) p[1] = make_float2(0.0f, first ? f[1] : 0.0f);
-}
-
-// The pairs of the segments but the last.  A run takes a contiguous share of the segment, and
-// the shares are joined at the end.
-template <typename T, int CL, int R, bool ODD>
-__global__ __launch_bounds__(CL * R) void gated_scan_pairs_kernel(ScanArgs a) {
-  __shared__ float4 part[R][CL];
-  const Where<CL, ODD> w(a, false);
-  if (w.seg == a.segments - 1) {
-    copy_first(a, w, a.first);
-    return;
-  }
-  const Two rate{rate_of(a.A_log, w.cc), rate_of(a.A_log, w.cc + w.d1)};
-  const int64_t begin = static_cast<int64_t>(w.seg) * a.seg_len;
-  const int share = (a.seg_len + R - 1) / R;
-  const int64_t from = begin + w.run * share;
-  int64_t to = from + share;
-  if (to > begin + a.seg_len) to = begin + a.seg_len;
-  if (to > w.n) to = w.n;
-  const T* x = static_cast<const T*>(a.x) + w.b * a.x_batch + w.cc;
-  const T* r = static_cast<const T*>(a.r) + w.b * a.r_batch + w.cc;
-  const T* i = static_cast<const T*>(a.i) + w.b * a.i_batch + w.cc;
   Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
-#pragma unroll 8
-  for (int64_t t = from; t < to; ++t) {
-    const int64_t at = w.at(t);
-    Two av, bv;
-    forward_of<T>(load2<ODD>(x + at * a.x_token, w.d1), load2<ODD>(r + at * a.r_token, w.d1),
-                  load2<ODD>(i + at * a.i_token, w.d1), rate, true, av, bv);
-    then(p, av.a, bv.a, av.b, bv.b);
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    if (FULL || k < w.left) {
+      const Two x = values(xv[k]), r = values(rv[k]), i = values(iv[k]);
+      const float p0 = sigmoid<kTail<T>>(r.a), p1 = sigmoid<kTail<T>>(r.b);
+      av[k] = {decay_of(rate0, p0), decay_of(rate1, p1)};
+      bv[k] = {__builtin_amdgcn_sqrtf(gain_of(av[k].a, rate0.v * p0)) * sigmoid<kTail<T>>(i.a) * x.a,
+               __builtin_amdgcn_sqrtf(gain_of(av[k].b, rate1.v * p1)) * sigmoid<kTail<T>>(i.b) * x.b};
+      then(p, av[k].a, bv[k].a, av[k].b, bv[k].b);
+    } else {
+      av[k] = {1.0f, 1.0f}, bv[k] = {0.0f, 0.0f};
+    }
   }
-  part[w.run][threadIdx.x % CL] = make_float4(p.A0, p.H0, p.A1, p.H1);
-  __syncthreads();
-  if (w.run != 0) return;
-  for (int j = 1; j < R; ++j) {
-    const float4 q = part[j][threadIdx.x % CL];
-    then(p, q.x, q.y, q.z, q.w);
-  }
-  float2* to_pairs = a.pairs + (w.b * a.segments + w.seg) * a.dim + w.c;
-  if (w.have > 0) to_pairs[0] = make_float2(p.A0, p.H0);
-  if (w.have > 1) to_pairs[1] = make_float2(p.A1, p.H1);
+  return p;
 }
 
-// The gradient's reads of one token.
-template <typename T, bool ODD, bool CODES>
-struct Reads {
-  const T *x, *r, *i, *h, *d;
-  template <typename W>
-  __device__ __forceinline__ Reads(const ScanArgs& a, const W& w) {
-    x = static_cast<const T*>(a.x) + w.b * a.x_batch + w.cc;
-    r = static_cast<const T*>(a.r) + w.b * a.r_batch + w.cc;
-    i = static_cast<const T*>(a.i) + w.b * a.i_batch + w.cc;
-    h = static_cast<const T*>(a.h) + w.b * a.seqlen * a.dim + w.cc;
-    d = static_cast<const T*>(a.dout) + w.b * a.dout_batch + w.cc;
+// A run's states from the one that enters it.
+template <bool FULL, typename T, int R, int S, bool ODD, bool KEEP>
+__device__ __forceinline__ void walk_run(const ScanArgs& a, const Where<R, S, ODD>& w, const Two (&av)[S], const Two (&bv)[S],
+                                         Two h) {
+  const int64_t row0 = w.b * a.seqlen;
+  T* out = static_cast<T*>(a.out) + row0 * a.dim;
+  Rows<T> rows(out, a.dim, w);
+  if (!KEEP && w.have <= 0) return;  // 8-bit copies take all lanes
+#pragma unroll
+  for (int k = 0; k < S; k += 4) {
+    Two y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h = {__builtin_fmaf(av[k + j].a, h.a, bv[k + j].a), __builtin_fmaf(av[k + j].b, h.b, bv[k + j].b)};
+      y[j] = FULL || k + j < w.left ? h : Two{0.0f, 0.0f};
+      if (FULL || k + j < w.rest) {
+        T* to = FULL ? rows.next(w.c) : in_row(out + static_cast<int64_t>(w.at(k + j)) * a.dim, w.c);
+        if (!KEEP || w.have > 0) store2<ODD>(to, w.have, y[j]);
+      }
+    }
+    if constexpr (KEEP) {
+      const int64_t first = 3 * a.plane + row0;
+      if (FULL || k < w.rest)
+        keep4<ODD>(
+            a.keep_scale + first * a.groups + w.tile, a.groups, w.c, w.have, w.lane, FULL ? 4 : w.rest - k, y,
+            [&](int j) { return a.keep + (first + w.at(k + j)) * a.dim; }, [&](int j) { return static_cast<int64_t>(w.at(k + j)); });
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  template <typename W>
-  __device__ __forceinline__ Two code(const ScanArgs& a, const W& w, int plane, int64_t t) const {
-    const int64_t at = plane * a.plane + w.b * a.seqlen + t;
-    const float s = a.codes_scale[at * a.groups + w.cc / kGroup];
-    const Two v = load2<ODD>(a.codes + at * a.dim + w.cc, w.d1);
-    return {v.a * s, v.b * s};
-  }
-  template <typename W>
-  __device__ __forceinline__ Two rv(const ScanArgs& a, const W& w, int64_t t) const {
-    if constexpr (CODES) return code(a, w, 1, t);
-    return load2<ODD>(r + t * a.r_token, w.d1);
-  }
-  template <typename W>
-  __device__ __forceinline__ Two xv(const ScanArgs& a, const W& w, int64_t t) const {
-    if constexpr (CODES) return code(a, w, 0, t);
-    return load2<ODD>(x + t * a.x_token, w.d1);
-  }
-  template <typename W>
-  __device__ __forceinline__ Two iv(const ScanArgs& a, const W& w, int64_t t) const {
-    if constexpr (CODES) return code(a, w, 2, t);
-    return load2<ODD>(i + t * a.i_token, w.d1);
-  }
-  // the state before the walk-back's token t: the next one's output, or the state at the start
-  template <typename W>
-  __device__ __forceinline__ Two before(const ScanArgs& a, const W& w, int64_t t, Two first) const {
-    if (t + 1 >= w.n) return first;
-    const int64_t at = w.at(t + 1);
-    if constexpr (CODES) return code(a, w, 3, at);
-    return load2<ODD>(h + at * a.dim, w.d1);
-  }
-  __device__ __forceinline__ Two dv(const ScanArgs& a, int d1, int64_t t) const { return load2<ODD>(d + t * a.dout_token, d1); }
-};
+}
 
-// One channel of a token of the gradient: G is the gradient of its state.
+template <typename T, int R, int S, bool ODD, bool KEEP>
+__global__ __launch_bounds__(64 * R, 4) void gated_scan_fwd_kernel(ScanArgs a) {
+  static_assert(S % 4 == 0, "8-bit copies are made four tokens at a time");
+  __shared__ Shared<R> shared;
+  const Where<R, S, ODD> w(a, unit_of(a), false);
+  Two av[S], bv[S], h{0.0f, 0.0f};
+  const Pairs p = w.left >= S ? take_run<true, T, R, S, ODD, KEEP>(a, w, av, bv) : take_run<false, T, R, S, ODD, KEEP>(a, w, av, bv);
+  if (w.chunk == 0 || w.begin() < w.n) h = enter<R, S, ODD>(a, w, p, shared, a.first, a.end);
+  if (w.left >= S)
+    walk_run<true, T, R, S, ODD, KEEP>(a, w, av, bv, h);
+  else
+    walk_run<false, T, R, S, ODD, KEEP>(a, w, av, bv, h);
+}
+
+// A uniform load through the scalar cache, of what no kernel that runs writes.
+__device__ __forceinline__ float scalar_load(const float* p) {
+  return *reinterpret_cast<const float __attribute__((address_space(4)))*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// One channel of a token of the gradient: G is the gradient of its state, p and q the gates' sigmoids, a its decay.
 struct TokenGrad {
-  float dx, dr, di, dA;
+  float dx, dr, di, dA, c;  // dr and dA: half of dA; c: what reaches the state before
 };
-template <bool TAIL>
-__device__ __forceinline__ TokenGrad gradient_of(float G, const Decay& d, float p, float x, float i, float before) {
-  const float q = sigmoid<TAIL>(i);
+__device__ __forceinline__ TokenGrad gradient_of(float G, Rate rate, float p, float a, float x, float q, float before) {
+  const float v = rate.v * p, w = gain_of(a, v);
   // Below the normal numbers w counts as 2^-126: beta, under 2^-63, is then off by less than that, and its limit 0 is met.
-  const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(d.w, 1.17549435e-38f));
-  const float beta = d.w * rs;
-  const float gb = G * beta;
+  const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(w, 1.17549435e-38f));
+  const float gb = G * (w * rs), u = q * x;
   TokenGrad g;
+  g.c = a * G;
   g.dx = gb * q;
-  g.di = g.dx * x * (1.0f - q);
-  // d/d(log a), times log a = -y; log a / beta has the limit 0 at a = 1
-  g.dA = G * d.a * d.y * __builtin_fmaf(q * x * d.a, rs, -before);
-  // log a / beta = -y rs
-  g.dr = g.dA * (1.0f - p);
+  g.di = gb * u * (1.0f - q);
+  // d/d(log a), times log a = -v / 2; log a / beta = -v rs / 2 has the limit 0 at a = 1
+  g.dA = g.c * v * __builtin_fmaf(u * a, rs, -before);
+  g.dr = g.dA * __builtin_fmaf(p, -0.5f, 0.5f);
   return g;
 }
 
-template <typename T, int CL, int R, int S, bool ODD, bool CODES>
-__global__ __launch_bounds__(CL * R) void gated_scan_bwd_kernel(ScanArgs a) {
-  __shared__ float4 part[2][R][CL];
-  const Where<CL, ODD> w(a, true);
-  const Two rate{rate_of(a.A_log, w.cc), rate_of(a.A_log, w.cc + w.d1)};
-  Two carry = enter_segment(a, w, a.last);
-  Two first{0.0f, 0.0f};
-  if (a.first) first = {a.first[w.b * a.dim + w.cc], a.first[w.b * a.dim + w.cc + w.d1]};
-  const int64_t begin = static_cast<int64_t>(w.seg) * a.seg_len;
-  const int64_t end = begin + a.seg_len < a.seqlen ? begin + a.seg_len : a.seqlen;
-  const Reads<T, ODD, CODES> reads(a, w);
-  const int64_t row0 = w.b * a.seqlen;
-  T* dx = static_cast<T*>(a.dx) + row0 * a.dim + w.c;
-  T* dr = static_cast<T*>(a.dr) + row0 * a.dim + w.c;
-  T* di = static_cast<T*>(a.di) + row0 * a.dim + w.c;
-  Two dA{0.0f, 0.0f};
-  int turn = 0;
-  for (int64_t t0 = begin; t0 < end; t0 += R * S, turn ^= 1) {
-    const int64_t mine = t0 + w.run * S;
-    Two pv[S], dv[S], xv[S], iv[S], hv[S];
-    Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
-    if (t0 < w.n) {
-      Two rv[S];
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        const int64_t t = w.in(mine + k);
-        rv[k] = reads.rv(a, w, t);
-        dv[k] = reads.dv(a, w.d1, t);
-        xv[k] = reads.xv(a, w, t);
-        iv[k] = reads.iv(a, w, t);
-        hv[k] = reads.before(a, w, mine + k, first);
-      }
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        pv[k] = {sigmoid<kTail<T>>(rv[k].a), sigmoid<kTail<T>>(rv[k].b)};
-        const Decay d0 = decay_of(rate.a, pv[k].a), d1 = decay_of(rate.b, pv[k].b);
-        if (mine + k < w.n) then(p, d0.a, d0.a * dv[k].a, d1.a, d1.a * dv[k].b);
-      }
+// What the gradient reads of a wave's tokens.
+template <typename T, int S, bool ODD, bool CODES>
+struct Taken {
+  using In = Raw<typename std::conditional<CODES, uint8_t, T>::type, ODD>;
+  In x[S], r[S], i[S], h[S];
+  Raw<T, ODD> d[S];
+  Two p[S];                       // sigmoid(r)
+  float scale[CODES ? 4 : 1][S];  // of the 8-bit forms, uniform
+  __device__ __forceinline__ Two of(int plane, In raw, int k) const {
+    const Two v = values(raw);
+    if constexpr (CODES) return Two{v.a * scale[plane][k], v.b * scale[plane][k]};
+    return v;
+  }
+  __device__ __forceinline__ Two gate(int plane, In raw, int k) const {
+    const Two v = values(raw);
+    if constexpr (CODES) {  // the scale and log2(e) in one factor
+      const float f = scale[plane][k] * -kLog2e;
+      return {sigmoid_of(v.a * f), sigmoid_of(v.b * f)};
     }
-    part[turn][w.run][threadIdx.x % CL] = make_float4(p.A0, p.H0, p.A1, p.H1);
-    __syncthreads();
-    Two c = enter<CL, R>(part[turn], w.run, carry.a, carry.b);
+    return {sigmoid<kTail<T>>(v.a), sigmoid<kTail<T>>(v.b)};
+  }
+};
+
+template <bool FULL, typename T, int R, int S, bool ODD, bool CODES>
+__device__ __forceinline__ Pairs take_back(const ScanArgs& a, const Where<R, S, ODD>& w, Rate rate0, Rate rate1,
+                                           Taken<T, S, ODD, CODES>& v) {
+  const int64_t row0 = w.b * a.seqlen;
+  Rows<const T> d(static_cast<const T*>(a.dout) + w.b * a.dout_batch, a.dout_token, w);
+  // the state before a token is the output of the walk-back's next one; the very last's is the state given
+  if constexpr (CODES) {
+    const auto codes = [&](int plane, int from) { return Rows<const uint8_t>(a.codes + (plane * a.plane + row0) * a.dim, a.dim, w, from); };
+    const auto scales = [&](int plane, int from) {
+      return Rows<const float>(a.codes_scale + (plane * a.plane + row0) * a.groups + w.tile, a.groups, w, from);
+    };
+    Rows<const uint8_t> x = codes(0, 0), r = codes(1, 0), i = codes(2, 0), h = codes(3, 1);
+    Rows<const float> sx = scales(0, 0), sr = scales(1, 0), si = scales(2, 0), sh = scales(3, 1);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      const int64_t t = mine + k;
-      if (t >= end) break;
-      Two gx{0.0f, 0.0f}, gr{0.0f, 0.0f}, gi{0.0f, 0.0f};
-      if (t < w.n) {
-        const Decay d0 = decay_of(rate.a, pv[k].a), d1 = decay_of(rate.b, pv[k].b);
-        const float G0 = dv[k].a + c.a, G1 = dv[k].b + c.b;
-        const TokenGrad g0 = gradient_of<kTail<T>>(G0, d0, pv[k].a, xv[k].a, iv[k].a, hv[k].a);
-        const TokenGrad g1 = gradient_of<kTail<T>>(G1, d1, pv[k].b, xv[k].b, iv[k].b, hv[k].b);
-        gx = {g0.dx, g1.dx}, gr = {g0.dr, g1.dr}, gi = {g0.di, g1.di};
-        dA.a += g0.dA, dA.b += g1.dA;
-        c = {d0.a * G0, d1.a * G1};
+      if (FULL || k < w.left) {
+        v.r[k] = load2<ODD>(r.next(w.cc), w.d1), v.scale[1][k] = scalar_load(sr.next(0));
+        v.d[k] = load2<ODD>(d.next(w.cc), w.d1);
+        v.x[k] = load2<ODD>(x.next(w.cc), w.d1), v.scale[0][k] = scalar_load(sx.next(0));
+        v.i[k] = load2<ODD>(i.next(w.cc), w.d1), v.scale[2][k] = scalar_load(si.next(0));
+        if (k < S - 1 ? FULL || k + 1 < w.left : k + 1 < w.left)
+          v.h[k] = load2<ODD>(h.next(w.cc), w.d1), v.scale[3][k] = scalar_load(sh.next(0));
       }
-      const int64_t at = w.at(t) * a.dim;
-      store2<ODD>(dx + at, w.have, gx);
-      store2<ODD>(dr + at, w.have, gr);
-      store2<ODD>(di + at, w.have, gi);
+    }
+  } else {
+    Rows<const T> x(static_cast<const T*>(a.x) + w.b * a.x_batch, a.x_token, w);
+    Rows<const T> r(static_cast<const T*>(a.r) + w.b * a.r_batch, a.r_token, w);
+    Rows<const T> i(static_cast<const T*>(a.i) + w.b * a.i_batch, a.i_token, w);
+    Rows<const T> h(static_cast<const T*>(a.h) + row0 * a.dim, a.dim, w, 1);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (FULL || k < w.left) {
+        v.r[k] = load2<ODD>(r.next(w.cc), w.d1);
+        v.d[k] = load2<ODD>(d.next(w.cc), w.d1);
+        v.x[k] = load2<ODD>(x.next(w.cc), w.d1);
+        v.i[k] = load2<ODD>(i.next(w.cc), w.d1);
+        if (k < S - 1 ? FULL || k + 1 < w.left : k + 1 < w.left) v.h[k] = load2<ODD>(h.next(w.cc), w.d1);
+      }
     }
   }
-  if (a.end && w.seg == a.segments - 1 && w.run == 0) put(a.end, a, w, carry.a, carry.b);
-  // this segment's share of A_log's gradient, its runs in a fixed order
+  Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    if (FULL || k < w.left) {
+      const Two d = values(v.d[k]);
+      v.p[k] = v.gate(1, v.r[k], k);
+      const float a0 = decay_of(rate0, v.p[k].a), a1 = decay_of(rate1, v.p[k].b);
+      then(p, a0, a0 * d.a, a1, a1 * d.b);
+    }
+  }
+  return p;
+}
+
+// A run's gradients from c, the gradient that the walk-back brings; returns the run's sums for A_log.
+template <bool FULL, typename T, int R, int S, bool ODD, bool CODES>
+__device__ __forceinline__ Two walk_back(const ScanArgs& a, const Where<R, S, ODD>& w, Rate rate0, Rate rate1,
+                                         const Taken<T, S, ODD, CODES>& v, Two c) {
+  const int64_t row0 = w.b * a.seqlen;
+  T *dx = static_cast<T*>(a.dx) + row0 * a.dim, *dr = static_cast<T*>(a.dr) + row0 * a.dim,
+    *di = static_cast<T*>(a.di) + row0 * a.dim;
+  Rows<T> px(dx, a.dim, w), pr(dr, a.dim, w), pi(di, a.dim, w);
+  Two dA{0.0f, 0.0f}, first{0.0f, 0.0f};
+  if (w.have <= 0) return dA;
+  if (w.left <= S && a.first) first = {a.first[w.b * a.dim + w.cc], a.first[w.b * a.dim + w.cc + w.d1]};
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    Two gx{0.0f, 0.0f}, gr{0.0f, 0.0f}, gi{0.0f, 0.0f};
+    if (FULL || k < w.left) {
+      const Two d = values(v.d[k]), x = v.of(0, v.x[k], k), q = v.gate(2, v.i[k], k), p = v.p[k];
+      const Two h = (FULL && k < S - 1) || k + 1 < w.left ? v.of(3, v.h[k], k) : first;
+      const TokenGrad g0 = gradient_of(d.a + c.a, rate0, p.a, decay_of(rate0, p.a), x.a, q.a, h.a);
+      const TokenGrad g1 = gradient_of(d.b + c.b, rate1, p.b, decay_of(rate1, p.b), x.b, q.b, h.b);
+      gx = {g0.dx, g1.dx}, gr = {g0.dr, g1.dr}, gi = {g0.di, g1.di};
+      dA.a += g0.dA, dA.b += g1.dA;
+      c = {g0.c, g1.c};
+    }
+    if (FULL) {
+      store2<ODD>(px.next(w.c), w.have, gx);
+      store2<ODD>(pr.next(w.c), w.have, gr);
+      store2<ODD>(pi.next(w.c), w.have, gi);
+    } else if (k < w.rest) {
+      const int64_t at = static_cast<int64_t>(w.at(k)) * a.dim;
+      store2<ODD>(in_row(dx + at, w.c), w.have, gx);
+      store2<ODD>(in_row(dr + at, w.c), w.have, gr);
+      store2<ODD>(in_row(di + at, w.c), w.have, gi);
+    }
+  }
+  return {0.5f * dA.a, 0.5f * dA.b};
+}
+
+template <typename T, int R, int S, bool ODD, bool CODES>
+__global__ __launch_bounds__(64 * R, 4) void gated_scan_bwd_kernel(ScanArgs a) {
+  __shared__ Shared<R> shared;
+  const Where<R, S, ODD> w(a, unit_of(a), true);
+  const Rate rate0 = rate_of(a.A_log, w.cc), rate1 = rate_of(a.A_log, w.cc + w.d1);
+  Taken<T, S, ODD, CODES> v;
+  const Pairs p = w.left >= S ? take_back<true, T, R, S, ODD, CODES>(a, w, rate0, rate1, v)
+                              : take_back<false, T, R, S, ODD, CODES>(a, w, rate0, rate1, v);
+  Two c{0.0f, 0.0f};
+  if (w.chunk == 0 || w.begin() < w.n) c = enter<R, S, ODD>(a, w, p, shared, a.last, a.end);
+  Two dA = w.left >= S ? walk_back<true, T, R, S, ODD, CODES>(a, w, rate0, rate1, v, c)
+                       : walk_back<false, T, R, S, ODD, CODES>(a, w, rate0, rate1, v, c);
+  // this chunk's share of A_log's gradient, its runs in a fixed order
   __syncthreads();
-  part[0][w.run][threadIdx.x % CL] = make_float4(dA.a, dA.b, 0.0f, 0.0f);
+  shared.part[w.run][w.lane] = make_float4(dA.a, dA.b, 0.0f, 0.0f);
   __syncthreads();
   if (w.run != 0) return;
-  for (int j = 1; j < R; ++j) dA.a += part[0][j][threadIdx.x].x, dA.b += part[0][j][threadIdx.x].y;
-  float* to = a.part + (w.b * a.segments + w.seg) * a.dim + w.c;
+  for (int j = 1; j < R; ++j) dA.a += shared.part[j][w.lane].x, dA.b += shared.part[j][w.lane].y;
+  float* to = a.part + (w.b * a.chunks + w.chunk) * a.dim + w.c;
   if (w.have > 0) to[0] = dA.a;
   if (w.have > 1) to[1] = dA.b;
 }
 
-template <typename T, int CL, int R, bool ODD, bool CODES>
-__global__ __launch_bounds__(CL * R) void gated_scan_bwd_pairs_kernel(ScanArgs a) {
-  __shared__ float4 part[R][CL];
-  const Where<CL, ODD> w(a, true);
-  if (w.seg == a.segments - 1) {
-    copy_first(a, w, a.last);
-    return;
-  }
-  const Two rate{rate_of(a.A_log, w.cc), rate_of(a.A_log, w.cc + w.d1)};
-  const int64_t begin = static_cast<int64_t>(w.seg) * a.seg_len;
-  const int share = (a.seg_len + R - 1) / R;
-  const int64_t from = begin + w.run * share;
-  int64_t to = from + share;
-  if (to > begin + a.seg_len) to = begin + a.seg_len;
-  if (to > w.n) to = w.n;
-  const Reads<T, ODD, CODES> reads(a, w);
-  Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
-#pragma unroll 8
-  for (int64_t t = from; t < to; ++t) {
-    const int64_t at = w.at(t);
-    const Two r = reads.rv(a, w, at), d = reads.dv(a, w.d1, at);
-    const Decay d0 = decay_of(rate.a, sigmoid<kTail<T>>(r.a)), d1 = decay_of(rate.b, sigmoid<kTail<T>>(r.b));
-    then(p, d0.a, d0.a * d.a, d1.a, d1.a * d.b);
-  }
-  part[w.run][threadIdx.x % CL] = make_float4(p.A0, p.H0, p.A1, p.H1);
-  __syncthreads();
-  if (w.run != 0) return;
-  for (int j = 1; j < R; ++j) {
-    const float4 q = part[j][threadIdx.x % CL];
-    then(p, q.x, q.y, q.z, q.w);
-  }
-  float2* to_pairs = a.pairs + (w.b * a.segments + w.seg) * a.dim + w.c;
-  if (w.have > 0) to_pairs[0] = make_float2(p.A0, p.H0);
-  if (w.have > 1) to_pairs[1] = make_float2(p.A1, p.H1);
+// Sets the published words to kNothing and the two words before them to 0.
+__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint32_t* status, uint64_t* words, int64_t n) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 2;
+  if (i == 0) status[0] = status[1] = 0;
+  if (i < n) *reinterpret_cast<ulonglong2*>(words + i) = make_ulonglong2(kNothing, kNothing);
 }
 
-// dA_log: 32 channels of a workgroup, 8 shares of the partial rows, joined in LDS in a fixed order.
-__global__ __launch_bounds__(256) void gated_scan_rate_kernel(const float* __restrict__ part, float* __restrict__ to,
-                                                              int64_t rows, int dim) {
-  __shared__ float s[8][32];
+// dA_log: 32 channels of a workgroup, 32 shares of the partial rows, joined in LDS in a fixed order.
+__global__ __launch_bounds__(1024) void gated_scan_rate_kernel(const float* __restrict__ part, float* __restrict__ to,
+                                                               int64_t rows, int dim) {
+  __shared__ float s[32][32];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), share = threadIdx.x >> 5;
   float t = 0.0f;
-  if (c < dim)
-#pragma unroll 4
-    for (int64_t i = share; i < rows; i += 8) t += part[i * dim + c];
+  if (c < dim) {
+#pragma unroll 8
+    for (int64_t i = share; i < rows; i += 32) t += part[i * dim + c];
+  }
   s[share][threadIdx.x & 31] = t;
   __syncthreads();
   if (share == 0 && c < dim) {
-    for (int i = 1; i < 8; ++i) t += s[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) t += s[i][threadIdx.x];
     to[c] = t;
   }
 }
@@ -574,25 +708,17 @@ __global__ __launch_bounds__(64) void gated_scan_step_kernel(StepArgs a) {
   const float x = load1(static_cast<const T*>(a.x) + b * a.x_batch + c);
   const float p = sigmoid<kTail<T>>(load1(static_cast<const T*>(a.r) + b * a.r_batch + c));
   const float q = sigmoid<kTail<T>>(load1(static_cast<const T*>(a.i) + b * a.i_batch + c));
-  const Decay d = decay_of(rate_of(a.A_log, c), p);
+  const Rate rate = rate_of(a.A_log, c);
+  const float decay = decay_of(rate, p);
   float* h = a.state + slot * a.dim + c;
-  const float v = __builtin_fmaf(d.a, *h, __builtin_amdgcn_sqrtf(d.w) * q * x);
+  const float v = __builtin_fmaf(decay, *h, __builtin_amdgcn_sqrtf(gain_of(decay, rate.v * p)) * q * x);
   *h = v;
   store1(out, v);
 }
 
-// How a call is cut: tiles of channels, and segments where the sequences' tiles are too few for the chip.
-constexpr int kRuns = 8, kTokens = 16, kGradTokens = 8;
-void cut(ScanArgs& a, int channels, int tokens) {
-  a.tiles = (a.dim + channels - 1) / channels;
-  const int block = kRuns * tokens;
-  const int64_t blocks = (a.seqlen + block - 1) / block, walks = a.batch * a.tiles;
-  int64_t segments = (1024 + walks - 1) / walks;
-  if (segments > (blocks + 1) / 2) segments = (blocks + 1) / 2;
-  if (segments < 1) segments = 1;
-  a.seg_len = static_cast<int>((blocks + segments - 1) / segments * block);
-  a.segments = static_cast<int>((a.seqlen + a.seg_len - 1) / a.seg_len);
-}
+// Waves of a workgroup and tokens of a wave's run.
+constexpr int kRuns = 8;
+constexpr int kTokens = 16, kGradTokens = 8;
 
 bool shape_ok(int64_t batch, int64_t seqlen, int64_t dim) {
   return batch >= 1 && seqlen >= 1 && dim >= 1 && batch < (int64_t{1} << 24) && seqlen < (int64_t{1} << 30) &&
@@ -603,13 +729,47 @@ bool strides_ok(const int64_t* s) { return s[0] >= 0 && s[1] >= 0 && s[0] <= (in
 
 bool dtype_ok(vmscan_dtype d) { return d == VMSCAN_F32 || d == VMSCAN_BF16; }
 
-ScanArgs sizes(int64_t batch, int64_t seqlen, int64_t dim, int channels, int tokens) {
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+// A call's sizes and where its workspace's parts begin: the status words, the published words, the gradient's rows.
+struct Plan {
   ScanArgs a{};
-  a.batch = batch, a.seqlen = seqlen, a.dim = static_cast<int>(dim), a.plane = batch * seqlen;
-  a.groups = static_cast<int>((dim + kGroup - 1) / kGroup);
-  cut(a, channels, tokens);
-  return a;
-}
+  bool ok = false;
+  int64_t words = 0;
+  size_t bytes = 0, part_at = 0;
+  Plan(int64_t batch, int64_t seqlen, int64_t dim, vmscan_dtype dtype, bool gradient) {
+    if (!shape_ok(batch, seqlen, dim) || !dtype_ok(dtype)) return;
+    const int tokens = gradient ? kGradTokens : kTokens;
+    a.batch = batch, a.seqlen = seqlen, a.dim = static_cast<int>(dim), a.plane = batch * seqlen;
+    a.groups = a.tiles = static_cast<int>((dim + kTile - 1) / kTile);
+    static_assert(kGroup == kTile, "a tile's channels share a scale");
+    const int64_t chains = batch * a.tiles, chunks = (seqlen + kRuns * tokens - 1) / (kRuns * tokens);
+    if (chains * chunks >= (int64_t{1} << 23)) return;  // a launch holds less than 2^32 threads
+    a.chains = static_cast<int>(chains), a.chunks = static_cast<int>(chunks);
+    if (chunks > 1) {
+      words = chains * (chunks * kTile + groups_of(static_cast<int>(chunks), kRuns) * 64);
+      bytes = 16 + static_cast<size_t>(words) * sizeof(uint64_t);
+    }
+    if (gradient) {
+      part_at = bytes;
+      bytes += static_cast<size_t>(batch) * chunks * dim * sizeof(float);
+    }
+    ok = true;
+  }
+  void place(void* workspace) {
+    char* p = static_cast<char*>(workspace);
+    a.status = reinterpret_cast<uint32_t*>(p);
+    a.pairs = reinterpret_cast<uint64_t*>(p + 16);
+    a.states = a.pairs + static_cast<int64_t>(a.chains) * a.chunks * kTile;
+    a.part = reinterpret_cast<float*>(p + part_at);
+  }
+  void clear(hipStream_t stream) const {
+    if (words)
+      hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((words + 511) / 512)), dim3(256), 0, stream,
+                         a.status, a.pairs, words);
+  }
+  dim3 grid() const { return dim3(static_cast<unsigned>(a.chains * a.chunks)); }
+};
 
 // States may be updated in place (one buffer) and must not overlap otherwise.
 bool states_ok(const ScanArgs& a, const float* to, const float* from, bool same) {
@@ -619,39 +779,29 @@ bool states_ok(const ScanArgs& a, const float* to, const float* from, bool same)
   return t == f ? same : t + n <= f || f + n <= t;
 }
 
-size_t pairs_bytes(const ScanArgs& a) {
-  return a.segments > 1 ? static_cast<size_t>(a.batch) * a.segments * a.dim * sizeof(float2) : 0;
-}
-size_t part_bytes(const ScanArgs& a) { return static_cast<size_t>(a.batch) * a.segments * a.dim * sizeof(float); }
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
-
 template <typename T, bool ODD>
-void launch_fwd(const ScanArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.batch * a.segments * a.tiles)), block(64 * kRuns);
-  if (a.segments > 1) hipLaunchKernelGGL((gated_scan_pairs_kernel<T, 64, kRuns, ODD>), grid, block, 0, stream, a);
-  if (a.keep)
-    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, 64, kRuns, kTokens, ODD, true>), grid, block, 0, stream, a);
+void launch_fwd(const Plan& p, hipStream_t stream) {
+  p.clear(stream);
+  if (p.a.keep)
+    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, ODD, true>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
   else
-    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, 64, kRuns, kTokens, ODD, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, ODD, false>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
 }
 
 template <typename T, bool ODD, bool CODES>
-void launch_bwd(const ScanArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.batch * a.segments * a.tiles)), block(64 * kRuns);
-  if (a.segments > 1)
-    hipLaunchKernelGGL((gated_scan_bwd_pairs_kernel<T, 64, kRuns, ODD, CODES>), grid, block, 0, stream, a);
-  hipLaunchKernelGGL((gated_scan_bwd_kernel<T, 64, kRuns, kGradTokens, ODD, CODES>), grid, block, 0, stream, a);
-  hipLaunchKernelGGL(gated_scan_rate_kernel, dim3(static_cast<unsigned>((a.dim + 31) / 32)), dim3(256), 0, stream, a.part,
-                     a.dA_log, a.batch * a.segments, a.dim);
+void launch_bwd(const Plan& p, hipStream_t stream) {
+  p.clear(stream);
+  hipLaunchKernelGGL((gated_scan_bwd_kernel<T, kRuns, kGradTokens, ODD, CODES>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
+  hipLaunchKernelGGL(gated_scan_rate_kernel, dim3(static_cast<unsigned>((p.a.dim + 31) / 32)), dim3(1024), 0, stream, p.a.part,
+                     p.a.dA_log, p.a.batch * p.a.chunks, p.a.dim);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
-  if (!shape_ok(batch, seqlen, dim)) return 0;
-  return pairs_bytes(sizes(batch, seqlen, dim, 2 * 64, kTokens));
+size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, vmscan_dtype dtype) {
+  return Plan(batch, seqlen, dim, dtype, false).bytes;
 }
 
 vmscan_status vmscan_gated_scan_fwd(const void* x, const int64_t* x_strides, const void* r, const int64_t* r_strides,
@@ -673,27 +823,26 @@ vmscan_status vmscan_gated_scan_fwd(const void* x, const int64_t* x_strides, con
                         static_cast<const void*>(keep_scale)})
     if (!aligned_to(p, 4)) return VMSCAN_ERR_ALIGN;
   if (!aligned_to(out, 16) || !aligned_to(workspace, 16) || !aligned_to(keep_codes, 16)) return VMSCAN_ERR_ALIGN;
-  ScanArgs a = sizes(batch, seqlen, dim, 2 * 64, kTokens);
-  if (batch * a.segments * a.tiles >= (int64_t{1} << 23)) return VMSCAN_ERR_SHAPE;
+  Plan plan(batch, seqlen, dim, dtype, false);
+  if (!plan.ok) return VMSCAN_ERR_SHAPE;
+  ScanArgs& a = plan.a;
   if (!states_ok(a, final_state, initial_state, true)) return VMSCAN_ERR_UNSUPPORTED;
-  if (pairs_bytes(a) && (!workspace || workspace_bytes < pairs_bytes(a))) return VMSCAN_ERR_WORKSPACE;
+  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return VMSCAN_ERR_WORKSPACE;
+  plan.place(workspace);
   a.x = x, a.r = r, a.i = i, a.A_log = A_log, a.first = initial_state, a.lengths = lengths, a.out = out;
   a.end = final_state, a.keep = static_cast<uint8_t*>(keep_codes), a.keep_scale = keep_scale, a.reverse = reverse;
-  a.pairs = static_cast<float2*>(workspace);
   a.x_batch = x_strides[0], a.x_token = x_strides[1], a.r_batch = r_strides[0], a.r_token = r_strides[1];
   a.i_batch = i_strides[0], a.i_token = i_strides[1];
   const bool odd = a.dim % 2 != 0;
   if (dtype == VMSCAN_F32)
-    odd ? launch_fwd<float, true>(a, stream) : launch_fwd<float, false>(a, stream);
+    odd ? launch_fwd<float, true>(plan, stream) : launch_fwd<float, false>(plan, stream);
   else
-    odd ? launch_fwd<uint16_t, true>(a, stream) : launch_fwd<uint16_t, false>(a, stream);
+    odd ? launch_fwd<uint16_t, true>(plan, stream) : launch_fwd<uint16_t, false>(plan, stream);
   return launched();
 }
 
-size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
-  if (!shape_ok(batch, seqlen, dim)) return 0;
-  const ScanArgs a = sizes(batch, seqlen, dim, 2 * 64, kGradTokens);
-  return round16(pairs_bytes(a)) + part_bytes(a);
+size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, vmscan_dtype dtype) {
+  return Plan(batch, seqlen, dim, dtype, true).bytes;
 }
 
 vmscan_status vmscan_gated_scan_bwd(const void* x, const int64_t* x_strides, const void* r, const int64_t* r_strides,
@@ -721,16 +870,16 @@ vmscan_status vmscan_gated_scan_bwd(const void* x, const int64_t* x_strides, con
   for (const void* p : {static_cast<const void*>(dx), static_cast<const void*>(dr), static_cast<const void*>(di),
                         static_cast<const void*>(workspace)})
     if (!aligned_to(p, 16)) return VMSCAN_ERR_ALIGN;
-  ScanArgs a = sizes(batch, seqlen, dim, 2 * 64, kGradTokens);
-  if (batch * a.segments * a.tiles >= (int64_t{1} << 23)) return VMSCAN_ERR_SHAPE;
+  Plan plan(batch, seqlen, dim, dtype, true);
+  if (!plan.ok) return VMSCAN_ERR_SHAPE;
+  ScanArgs& a = plan.a;
   if (!states_ok(a, dinitial_state, dfinal_state, true) || !states_ok(a, dinitial_state, initial_state, false))
     return VMSCAN_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < vmscan_gated_scan_bwd_workspace_bytes(batch, seqlen, dim)) return VMSCAN_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < plan.bytes) return VMSCAN_ERR_WORKSPACE;
+  plan.place(workspace);
   a.x = x, a.r = r, a.i = i, a.h = h, a.codes = static_cast<const uint8_t*>(codes), a.codes_scale = codes_scale;
   a.A_log = A_log, a.first = initial_state, a.last = dfinal_state, a.lengths = lengths, a.reverse = reverse;
   a.dout = dout, a.dx = dx, a.dr = dr, a.di = di, a.dA_log = dA_log, a.end = dinitial_state;
-  a.pairs = static_cast<float2*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round16(pairs_bytes(a)));
   if (!codes) {
     a.x_batch = x_strides[0], a.x_token = x_strides[1], a.r_batch = r_strides[0], a.r_token = r_strides[1];
     a.i_batch = i_strides[0], a.i_token = i_strides[1];
@@ -739,14 +888,14 @@ vmscan_status vmscan_gated_scan_bwd(const void* x, const int64_t* x_strides, con
   const bool odd = a.dim % 2 != 0;
   if (dtype == VMSCAN_F32) {
     if (codes)
-      odd ? launch_bwd<float, true, true>(a, stream) : launch_bwd<float, false, true>(a, stream);
+      odd ? launch_bwd<float, true, true>(plan, stream) : launch_bwd<float, false, true>(plan, stream);
     else
-      odd ? launch_bwd<float, true, false>(a, stream) : launch_bwd<float, false, false>(a, stream);
+      odd ? launch_bwd<float, true, false>(plan, stream) : launch_bwd<float, false, false>(plan, stream);
   } else {
     if (codes)
-      odd ? launch_bwd<uint16_t, true, true>(a, stream) : launch_bwd<uint16_t, false, true>(a, stream);
+      odd ? launch_bwd<uint16_t, true, true>(plan, stream) : launch_bwd<uint16_t, false, true>(plan, stream);
     else
-      odd ? launch_bwd<uint16_t, true, false>(a, stream) : launch_bwd<uint16_t, false, false>(a, stream);
+      odd ? launch_bwd<uint16_t, true, false>(plan, stream) : launch_bwd<uint16_t, false, false>(plan, stream);
   }
   return launched();
 }
