@@ -625,8 +625,7 @@ vmscan_status vmscan_groupnorm_bwd(const void *dy, const int64_t *dy_strides, co
  *                its rounding to `out`), zeros past a row's length
  * A NaN or infinity reaches the later states of its own channel only.
  */
-size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
-                                            vmscan_dtype dtype);
+size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 vmscan_status vmscan_gated_scan_fwd(const void *x, const int64_t *x_strides, const void *r,
                                     const int64_t *r_strides, const void *i,
                                     const int64_t *i_strides, const float *A_log,
@@ -646,8 +645,7 @@ vmscan_status vmscan_gated_scan_fwd(const void *x, const int64_t *x_strides, con
  * one otherwise, nor initial_state (VMSCAN_ERR_UNSUPPORTED).  At a_t = 1, where sqrt(1 - a^2) has no slope, the
  * gradient of r is its limit.  No atomics: the same inputs give the same bits.
  */
-size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
-                                            vmscan_dtype dtype);
+size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 vmscan_status vmscan_gated_scan_bwd(const void *x, const int64_t *x_strides, const void *r,
                                     const int64_t *r_strides, const void *i,
                                     const int64_t *i_strides, const void *h, const void *codes,

@@ -121,12 +121,12 @@ def _load():
     lib.vmscan_groupnorm_bwd.argtypes = ([_c_void_p] * 14 + [_i64] * 4 + [ctypes.c_int, ctypes.c_int, _c_void_p,
                                                                          ctypes.c_size_t, _c_void_p])
     lib.vmscan_gated_scan_fwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.vmscan_gated_scan_fwd_workspace_bytes.argtypes = [_i64] * 3 + [ctypes.c_int]
+    lib.vmscan_gated_scan_fwd_workspace_bytes.argtypes = [_i64] * 3
     lib.vmscan_gated_scan_fwd.restype = ctypes.c_int
     lib.vmscan_gated_scan_fwd.argtypes = ([_c_void_p] * 9 + [ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 +
                                           [ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p])
     lib.vmscan_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.vmscan_gated_scan_bwd_workspace_bytes.argtypes = [_i64] * 3 + [ctypes.c_int]
+    lib.vmscan_gated_scan_bwd_workspace_bytes.argtypes = [_i64] * 3
     lib.vmscan_gated_scan_bwd.restype = ctypes.c_int
     lib.vmscan_gated_scan_bwd.argtypes = ([_c_void_p] * 12 + [ctypes.c_int] + [_c_void_p] * 8 + [_i64] * 3 +
                                           [ctypes.c_int, _c_void_p, ctypes.c_size_t, _c_void_p])
@@ -1089,7 +1089,7 @@ def gated_scan_fwd(x, r, i, A_log, initial_state=None, lengths=None, reverse=Fal
     kept = _new_codes((4,) + shape, dev) if keep else None
     codes, scale = kept if keep else (None, None)
     lib = load()
-    workspace = _workspace(workspace, lib.vmscan_gated_scan_fwd_workspace_bytes(nb, L, dim, dt), dev)
+    workspace = _workspace(workspace, lib.vmscan_gated_scan_fwd_workspace_bytes(nb, L, dim), dev)
     args = (x.data_ptr(), xs, r.data_ptr(), rs, i.data_ptr(), is_, A_log.data_ptr(), _p(initial_state), _p(lengths),
             int(bool(reverse)), out.data_ptr(), final_state.data_ptr(), _p(codes), _p(scale), nb, L, dim, dt, _p(workspace),
             _nbytes(workspace), _current(dev))
@@ -1133,7 +1133,7 @@ def gated_scan_bwd(kept, A_log, dout, initial_state=None, lengths=None, reverse=
     act = lambda: torch.empty(shape, dtype=adt, device=dev)
     g = dict(dx=act(), dr=act(), di=act(), dA_log=f32(dim), dinitial_state=f32(nb, dim) if initial_state is not None else None)
     lib = load()
-    workspace = _workspace(workspace, lib.vmscan_gated_scan_bwd_workspace_bytes(nb, L, dim, dt), dev)
+    workspace = _workspace(workspace, lib.vmscan_gated_scan_bwd_workspace_bytes(nb, L, dim), dev)
     args = (_p(x), xs, _p(r), rs, _p(i), is_, _p(h), _p(codes), _p(scale), A_log.data_ptr(), _p(initial_state), _p(lengths),
             int(bool(reverse)), dout.data_ptr(), dos, _p(dfinal_state), g["dx"].data_ptr(), g["dr"].data_ptr(),
             g["di"].data_ptr(), g["dA_log"].data_ptr(), _p(g["dinitial_state"]), nb, L, dim, dt, _p(workspace),

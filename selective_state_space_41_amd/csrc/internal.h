@@ -51,6 +51,25 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
     v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
   }
 }
+// Loads of what a call reads for the last time, and stores of what is not read soon: both leave the caches to the rest
+// (large inputs that a second pass or the next kernel's reads would otherwise push out).  At element alignment.
+template <typename V, int ALIGN>
+struct Streamed {
+  typedef V type __attribute__((aligned(ALIGN)));
+};
+template <typename V, typename T>
+__device__ __forceinline__ V load_once(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const typename Streamed<V, sizeof(T)>::type*>(p));
+}
+template <typename V, typename T>
+__device__ __forceinline__ void store_away(T* p, V v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<typename Streamed<V, sizeof(T)>::type*>(p));
+}
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
@@ -108,7 +127,6 @@ __device__ __forceinline__ float dpp(float v) {
 }
 template <typename OP, int LANES>
 __device__ __forceinline__ float over_lanes(float v) {
-  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
   v = OP::of(v, dpp<0xb1>(v));   // lane ^ 1
   v = OP::of(v, dpp<0x4e>(v));   // lane ^ 2
   v = OP::of(v, dpp<0x141>(v));  // mirrored in 8
