@@ -59,6 +59,12 @@ constexpr int kPatience = 1 << 22;  // polls of a wait that should have ended lo
 struct Two {
   float a, b;
 };
+// How a row's channels lie in the lanes' pairs.
+enum Layout {
+  kPairs,   // an even number of channels (of those kept in 8 bits: a multiple of 4)
+  kShifted, // any number over 1: a lane whose second channel would be past the end loads the pair before
+  kSingle   // one channel
+};
 // As loaded: a bfloat16 or 8-bit pair stays one register until it is used.
 struct RawB {
   uint32_t w;
@@ -66,29 +72,45 @@ struct RawB {
 struct Raw8 {
   uint32_t w;
 };
-__device__ __forceinline__ Two values(RawB r) { return {__uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u)}; }
-__device__ __forceinline__ Two values(Two r) { return r; }
-__device__ __forceinline__ Two values(Raw8 r) {
+// `shift`: the lane's first channel (or, past the last one, what stands for it) is the second of the pair that it loaded.
+template <Layout L>
+__device__ __forceinline__ RawB shifted(RawB r, bool shift) {
+  if (L == kShifted && shift) r.w = r.w >> 16 | (r.w & 0xffff0000u);
+  return r;
+}
+template <Layout L>
+__device__ __forceinline__ Two shifted(Two r, bool shift) {
+  if (L == kShifted && shift) r.a = r.b;
+  return r;
+}
+template <Layout L>
+__device__ __forceinline__ Two values(RawB r, bool shift) {
+  r = shifted<L>(r, shift);
+  return {__uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u)};
+}
+template <Layout L>
+__device__ __forceinline__ Two values(Two r, bool shift) {
+  return shifted<L>(r, shift);
+}
+template <Layout L>
+__device__ __forceinline__ Two values(Raw8 r, bool shift) {
+  if constexpr (L == kShifted) r.w = shift ? r.w >> 8 : r.w;
   const auto v = __builtin_amdgcn_cvt_pk_f32_fp8(r.w, false);
   return {v[0], v[1]};
 }
-// `p` is the row's place of this lane's first channel; ODD: the second may be missing (d1 = 0 reads the first again).
 // ONCE: what is read is not needed again (the gradient's inputs: 32 x 3136 x 512 from 8 bits takes 164 us instead of
 // 171, 16 x 3136 x 256 in float32 102 instead of 113; the forward gains nothing).
-template <bool ODD, bool ONCE = false>
-__device__ __forceinline__ RawB load2(const uint16_t* p, int d1) {
+template <Layout L, bool ONCE = false>
+__device__ __forceinline__ RawB load2(const uint16_t* p) {
+  if constexpr (L == kSingle) return {p[0] * 0x10001u};
+  if constexpr (ONCE) return {load_once<uint32_t>(p)};
   uint32_t w;
-  if constexpr (ODD)
-    w = p[0] | static_cast<uint32_t>(p[d1]) << 16;
-  else if constexpr (ONCE)
-    w = load_once<uint32_t>(p);
-  else
-    __builtin_memcpy(&w, p, 4);
+  __builtin_memcpy(&w, p, 4);
   return {w};
 }
-template <bool ODD, bool ONCE = false>
-__device__ __forceinline__ Two load2(const float* p, int d1) {
-  if constexpr (ODD) return {p[0], p[d1]};
+template <Layout L, bool ONCE = false>
+__device__ __forceinline__ Two load2(const float* p) {
+  if constexpr (L == kSingle) return {p[0], p[0]};
   f32x2 v;
   if constexpr (ONCE)
     v = load_once<f32x2>(p);
@@ -96,17 +118,17 @@ __device__ __forceinline__ Two load2(const float* p, int d1) {
     __builtin_memcpy(&v, p, 8);
   return {v.x, v.y};
 }
-template <bool ODD, bool ONCE = true>
-__device__ __forceinline__ Raw8 load2(const uint8_t* p, int d1) {
-  if constexpr (ODD) return {p[0] | static_cast<uint32_t>(p[d1]) << 8};
+template <Layout L, bool ONCE = true>
+__device__ __forceinline__ Raw8 load2(const uint8_t* p) {
+  if constexpr (L == kSingle) return {p[0] * 0x101u};
   return {load_once<uint16_t>(p)};
 }
-template <typename T, bool ODD>
-using Raw = decltype(load2<ODD>(static_cast<const T*>(nullptr), 0));
+template <typename T, Layout L>
+using Raw = decltype(load2<L>(static_cast<const T*>(nullptr)));
 // n: channels that exist, 1 at least.
-template <bool ODD>
+template <Layout L>
 __device__ __forceinline__ void store2(uint16_t* p, int n, Two v) {
-  if (ODD && n == 1) {
+  if (L != kPairs && n == 1) {
     store1(p, v.a);
   } else {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -114,9 +136,9 @@ __device__ __forceinline__ void store2(uint16_t* p, int n, Two v) {
     __builtin_memcpy(p, &w, 4);
   }
 }
-template <bool ODD>
+template <Layout L>
 __device__ __forceinline__ void store2(float* p, int n, Two v) {
-  if (ODD && n == 1) {
+  if (L != kPairs && n == 1) {
     *p = v.a;
   } else {
     const float2 w = make_float2(v.a, v.b);
@@ -176,13 +198,14 @@ __device__ __forceinline__ int tokens_of(const ScanArgs& a, int64_t b) {
 
 // What a workgroup and a wave work on.  Tokens are counted along the walk; `back` walks turn the count around within
 // the row's n tokens, and what lies past them keeps its place.
-template <int R, int S, bool ODD>
+template <int R, int S, Layout L>
 struct Where {
   int64_t b;
   int n, mine, left, rest;  // the sequence's tokens, the wave's first; live and written ones from there on (any sign)
   int chain, chunk, run, tile, lane;
-  int c, cc, d1, have;      // first channel, one that exists, 1 if the next exists too, channels that exist
-  bool back;
+  int c, have;              // first channel, channels that exist
+  int cc, c0, c1;           // where the lane loads, and the channels that its values belong to (ones that exist)
+  bool back, shift;
   __device__ __forceinline__ Where(const ScanArgs& a, uint32_t unit, bool turn) {
     chunk = __builtin_amdgcn_readfirstlane(unit / static_cast<uint32_t>(a.chains));
     chain = static_cast<int>(unit - static_cast<uint32_t>(chunk) * static_cast<uint32_t>(a.chains));
@@ -197,9 +220,11 @@ struct Where {
     rest = static_cast<int>(a.seqlen) - mine;
     c = tile * kTile + lane * 2;
     have = a.dim - c;
-    const int top = ODD ? a.dim - 1 : a.dim - 2;
+    const int top = L == kSingle ? 0 : a.dim - 2;
     cc = c < top ? c : top;
-    d1 = !ODD || cc + 1 < a.dim ? 1 : 0;
+    shift = L == kShifted && c >= a.dim - 1;
+    c1 = L == kSingle ? 0 : cc + 1;
+    c0 = shift ? c1 : cc;
     back = (a.reverse != 0) != turn;
   }
   __device__ __forceinline__ int begin() const { return chunk * (R * S); }
@@ -214,7 +239,10 @@ template <typename T>
 __device__ __forceinline__ T* in_row(T* row, int c) {
   using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
   using Global = Byte __attribute__((address_space(1)));
-  Global* base = (Global*)reinterpret_cast<Byte*>(row);
+  const uint64_t at = reinterpret_cast<uint64_t>(row);
+  const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));  // (an int: not to be widened as one)
+  const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+  Global* base = (Global*)reinterpret_cast<Byte*>(static_cast<uint64_t>(high) << 32 | low);
   asm("" : "+s"(base));  // the sum is the load's or store's own, not a 64-bit addition in every lane
   return reinterpret_cast<T*>((Byte*)(base + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
 }
@@ -282,8 +310,8 @@ __device__ __forceinline__ uint32_t unit_of(const ScanArgs& a) {
 
 // The state that enters this wave's run, from its pair p.  `first` is the state at the sequence's start; `after` gets the
 // state after the sequence's last token.  Each wave joins four of the chunks before, and all of them the waves' pairs.
-template <int R, int S, bool ODD>
-__device__ __forceinline__ Two enter(const ScanArgs& a, const Where<R, S, ODD>& w, const Pairs& p, Shared<R>& s,
+template <int R, int S, Layout L>
+__device__ __forceinline__ Two enter(const ScanArgs& a, const Where<R, S, L>& w, const Pairs& p, Shared<R>& s,
                                      const float* first, float* after) {
   constexpr int kEach = 4, kGroupChunks = kEach * R;
   const int lane = w.lane, group = w.chunk / kGroupChunks, begin = group * kGroupChunks;
@@ -309,7 +337,7 @@ __device__ __forceinline__ Two enter(const ScanArgs& a, const Where<R, S, ODD>& 
     }
     if (group == 0) {
       Two h{0.0f, 0.0f};
-      if (w.chunk == 0 && first) h = {first[w.b * a.dim + w.cc], first[w.b * a.dim + w.cc + w.d1]};
+      if (w.chunk == 0 && first) h = {first[w.b * a.dim + w.c0], first[w.b * a.dim + w.c1]};
       s.base[lane] = make_float2(h.a, h.b);
       if (w.chunk == 0) {  // the state after it, whatever enters: no other chunk reads the state at the start
         const Two end = through(all, h);
@@ -354,87 +382,137 @@ __device__ __forceinline__ Two enter(const ScanArgs& a, const Where<R, S, ODD>& 
   return h;
 }
 
-// The 8-bit copies of four tokens' 128 channels, two to a lane.  The four largest magnitudes are found together: each
-// exchange of half the lanes leaves one register for two, so that a row of 16 lanes ends up with one token (as
-// unsigned numbers, whose order is that of the magnitudes and in which a NaN is the largest).  `rows` gives the
-// token's row of the plane's codes, `place` its number in the plane.
-template <bool ODD, typename ROW, typename PLACE>
-__device__ __forceinline__ void keep4(float* scales, int groups, int c, int have, int lane, int many, const Two (&v)[4],
-                                      ROW&& row, PLACE&& place) {
-  const auto larger = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
-  const auto bits = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
-  uint32_t m[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    m[k] = larger(bits(v[k].a), ODD && have < 2 ? 0u : bits(v[k].b));
-    if (have <= 0) m[k] = 0;
-  }
+// Two tokens' pairs of 8-bit codes in a register, the first's in its lower half, become four neighbouring channels of
+// one token (the first in even lanes, the second in odd ones): half the stores, of 4 bytes.  (The gradient's loads gain
+// nothing that way: 167 us instead of 161 on 32 x 3136 x 512.)
+__device__ __forceinline__ uint32_t trade(uint32_t w, uint32_t selector) {
+  const uint32_t other = __float_as_uint(dpp<0xb1>(__uint_as_float(w)));
+  return __builtin_amdgcn_perm(other, w, selector);
+}
+__device__ __forceinline__ uint32_t trade_selector(int lane) { return lane & 1 ? 0x03020706u : 0x05040100u; }
+// A lane's place in the rows of two tokens: four channels of its token's row, from the lower of the two.
+__device__ __forceinline__ int trade_place(int lane, int c, bool back, int dim) {
+  return (c & ~3) + (((lane & 1) != 0) != back ? dim : 0);
+}
+
+// The largest magnitudes of four tokens' 128 channels, two to a lane, as unsigned numbers, whose order is that of the
+// magnitudes and in which a NaN is the largest.  They are found together: each exchange of half the lanes leaves one
+// register for two, so that a row of 16 lanes ends up with one token: 0, 2, 1, 3.  (A lane past the last channel holds
+// channels that exist.)
+__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) { return x > y ? x : y; }
+template <typename MAX>
+__device__ __forceinline__ uint32_t by_rows(const uint32_t (&m)[4], MAX&& max) {
   u32x2 r = __builtin_amdgcn_permlane32_swap(m[0], m[1], false, false);
-  const uint32_t m01 = larger(r[0], r[1]);
+  const uint32_t m01 = max(r[0], r[1]);
   r = __builtin_amdgcn_permlane32_swap(m[2], m[3], false, false);
-  const uint32_t m23 = larger(r[0], r[1]);
-  r = __builtin_amdgcn_permlane16_swap(m01, m23, false, false);  // rows of 16 lanes: tokens 0, 2, 1, 3
-  uint32_t t = larger(r[0], r[1]);
+  const uint32_t m23 = max(r[0], r[1]);
+  r = __builtin_amdgcn_permlane16_swap(m01, m23, false, false);
+  return max(r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t in_row16(uint32_t t) {
   t = larger(t, __float_as_uint(dpp<0xb1>(__uint_as_float(t))));
   t = larger(t, __float_as_uint(dpp<0x4e>(__uint_as_float(t))));
   t = larger(t, __float_as_uint(dpp<0x141>(__uint_as_float(t))));
-  t = larger(t, __float_as_uint(dpp<0x140>(__uint_as_float(t))));
-  // as scale_of and its reciprocal, by products (one unit in the last place)
-  const float top = __uint_as_float(t), q = top * (1.0f / kFp8Max);
-  const float s = top == 0.0f ? 1.0f : q < kMinScale ? kMinScale : q, inv = __builtin_amdgcn_rcpf(s);
-  constexpr int kRow[4] = {0, 32, 16, 48};
-  float f[4];
+  return larger(t, __float_as_uint(dpp<0x140>(__uint_as_float(t))));
+}
+__device__ __forceinline__ uint32_t tops(RawB a, RawB b, RawB c, RawB d) {  // both channels at once, as 16-bit numbers
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const uint32_t m[4] = {a.w & 0x7fff7fffu, b.w & 0x7fff7fffu, c.w & 0x7fff7fffu, d.w & 0x7fff7fffu};
+  const uint32_t t = by_rows(m, [](uint32_t x, uint32_t y) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, x), __builtin_bit_cast(u16x2, y)));
+  });
+  return in_row16(larger(t & 0xffff0000u, t << 16));
+}
+__device__ __forceinline__ uint32_t tops(Two a, Two b, Two c, Two d) {
+  const auto one = [](Two v) { return larger(__float_as_uint(v.a) & 0x7fffffffu, __float_as_uint(v.b) & 0x7fffffffu); };
+  const uint32_t m[4] = {one(a), one(b), one(c), one(d)};
+  return in_row16(by_rows(m, larger));
+}
+
+// Where the 8-bit copies of a plane go, four tokens after four.
+template <Layout L>
+struct Kept {
+  uint8_t* codes;
+  float* scale;
+  template <typename W>
+  __device__ __forceinline__ Kept(const ScanArgs& a, const W& w, int plane) {
+    const int64_t first = plane * a.plane + w.b * a.seqlen;
+    codes = a.keep + first * a.dim, scale = a.keep_scale + first * a.groups + w.tile;
+  }
+  // FULL: the run's tokens k to k + 3 are live; else `many` of them are written, live or not.
+  template <bool FULL, typename W>
+  __device__ __forceinline__ void put(const ScanArgs& a, const W& w, int k, int many, uint32_t top, const Two (&v)[4]) const {
+    // as scale_of and its reciprocal, by products (one unit in the last place)
+    const float big = __uint_as_float(top), q = big * (1.0f / kFp8Max);
+    const float s = big == 0.0f ? 1.0f : q < kMinScale ? kMinScale : q, inv = __builtin_amdgcn_rcpf(s);
+    constexpr int kRow[4] = {0, 32, 16, 48};
+    float f[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), kRow[k]));
-  if (have > 0) {
+    for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), kRow[j]));
+    const int token = ((w.lane >> 5) & 1) | ((w.lane >> 3) & 2);
+    if constexpr (FULL) {
+      const int low = w.back ? w.at(k + 3) : w.at(k);
+      float* row = in_row(scale + static_cast<int64_t>(low) * a.groups, (w.back ? 3 - token : token) * a.groups);
+      if (w.lane % 16 == 0) *row = s;
+    } else {
+      if (w.lane % 16 == 0 && token < many) scale[static_cast<int64_t>(w.at(k + token)) * a.groups] = s;
+    }
+    if constexpr (FULL && L == kPairs) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= many) break;
-      const uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(v[k].a * f[k], v[k].b * f[k], 0, false);
-      uint8_t* p = in_row(row(k), c);
-      if (ODD && have == 1) {
-        *p = static_cast<uint8_t>(w);
-      } else {
-        store_away(p, static_cast<uint16_t>(w));
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t c = __builtin_amdgcn_cvt_pk_fp8_f32(v[j].a * f[j], v[j].b * f[j], 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[j + 1].a * f[j + 1], v[j + 1].b * f[j + 1], c, true);
+        c = trade(c, trade_selector(w.lane));
+        const int low = w.back ? w.at(k + j + 1) : w.at(k + j);
+        uint8_t* to = in_row(codes + static_cast<int64_t>(low) * a.dim, trade_place(w.lane, w.c, w.back, a.dim));
+        if (w.have > 0) store_away(to, c);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!FULL && j >= many) break;
+        const uint32_t c = __builtin_amdgcn_cvt_pk_fp8_f32(v[j].a * f[j], v[j].b * f[j], 0, false);
+        uint8_t* to = in_row(codes + static_cast<int64_t>(w.at(k + j)) * a.dim, w.c);
+        if (L != kPairs && w.have == 1)
+          *to = static_cast<uint8_t>(c);
+        else if (w.have > 0)
+          store_away(to, static_cast<uint16_t>(c));
       }
     }
   }
-  const int token = ((lane >> 5) & 1) | ((lane >> 3) & 2);
-  if (lane % 16 == 0 && token < many) scales[place(token) * groups] = s;
-}
+};
 
 // Before the chunk's entering state is known: a run's decays and inputs, joined to a pair, and its 8-bit copies.  FULL:
 // all S tokens are live.
-template <bool FULL, typename T, int R, int S, bool ODD, bool KEEP>
-__device__ __forceinline__ Pairs take_run(const ScanArgs& a, const Where<R, S, ODD>& w, Two (&av)[S], Two (&bv)[S]) {
-  const Rate rate0 = rate_of(a.A_log, w.cc), rate1 = rate_of(a.A_log, w.cc + w.d1);
+template <bool FULL, typename T, int R, int S, Layout L, bool KEEP>
+__device__ __forceinline__ Pairs take_run(const ScanArgs& a, const Where<R, S, L>& w, Two (&av)[S], Two (&bv)[S]) {
+  const Rate rate0 = rate_of(a.A_log, w.c0), rate1 = rate_of(a.A_log, w.c1);
   Rows<const T> x(static_cast<const T*>(a.x) + w.b * a.x_batch, a.x_token, w);
   Rows<const T> r(static_cast<const T*>(a.r) + w.b * a.r_batch, a.r_token, w);
   Rows<const T> i(static_cast<const T*>(a.i) + w.b * a.i_batch, a.i_token, w);
-  Raw<T, ODD> xv[S], rv[S], iv[S];
+  Raw<T, L> raw[3][S];
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     if (FULL || k < w.left) {
-      xv[k] = load2<ODD>(x.next(w.cc), w.d1);
-      rv[k] = load2<ODD>(r.next(w.cc), w.d1);
-      iv[k] = load2<ODD>(i.next(w.cc), w.d1);
+      raw[0][k] = load2<L>(x.next(w.cc));
+      raw[1][k] = load2<L>(r.next(w.cc));
+      raw[2][k] = load2<L>(i.next(w.cc));
     } else {
-      xv[k] = rv[k] = iv[k] = {};
+      raw[0][k] = raw[1][k] = raw[2][k] = {};
     }
   }
   if constexpr (KEEP) {
-    const int64_t row0 = w.b * a.seqlen;
 #pragma unroll
     for (int k = 0; k < S; k += 4) {
-      if (!FULL && k >= w.rest) break;
 #pragma unroll
       for (int plane = 0; plane < 3; ++plane) {
-        const auto& v = plane == 0 ? xv : plane == 1 ? rv : iv;
-        const int64_t first = plane * a.plane + row0;
-        keep4<ODD>(
-            a.keep_scale + first * a.groups + w.tile, a.groups, w.c, w.have, w.lane, FULL ? 4 : w.rest - k,
-            {values(v[k]), values(v[k + 1]), values(v[k + 2]), values(v[k + 3])},
-            [&](int j) { return a.keep + (first + w.at(k + j)) * a.dim; }, [&](int j) { return static_cast<int64_t>(w.at(k + j)); });
+        Raw<T, L>* in = raw[plane] + k;
+        if (FULL || k < w.rest)
+          Kept<L>(a, w, plane).template put<FULL>(a, w, k, w.rest - k,
+                                                  tops(shifted<L>(in[0], w.shift), shifted<L>(in[1], w.shift),
+                                                       shifted<L>(in[2], w.shift), shifted<L>(in[3], w.shift)),
+                                                  {values<L>(in[0], w.shift), values<L>(in[1], w.shift),
+                                                   values<L>(in[2], w.shift), values<L>(in[3], w.shift)});
         __builtin_amdgcn_sched_barrier(0);  // one after another: registers
       }
     }
@@ -443,7 +521,7 @@ __device__ __forceinline__ Pairs take_run(const ScanArgs& a, const Where<R, S, O
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     if (FULL || k < w.left) {
-      const Two x = values(xv[k]), r = values(rv[k]), i = values(iv[k]);
+      const Two x = values<L>(raw[0][k], w.shift), r = values<L>(raw[1][k], w.shift), i = values<L>(raw[2][k], w.shift);
       const float p0 = sigmoid<kTail<T>>(r.a), p1 = sigmoid<kTail<T>>(r.b);
       av[k] = {decay_of(rate0, p0), decay_of(rate1, p1)};
       bv[k] = {__builtin_amdgcn_sqrtf(gain_of(av[k].a, rate0.v * p0)) * sigmoid<kTail<T>>(i.a) * x.a,
@@ -457,8 +535,8 @@ __device__ __forceinline__ Pairs take_run(const ScanArgs& a, const Where<R, S, O
 }
 
 // A run's states from the one that enters it.
-template <bool FULL, typename T, int R, int S, bool ODD, bool KEEP>
-__device__ __forceinline__ void walk_run(const ScanArgs& a, const Where<R, S, ODD>& w, const Two (&av)[S], const Two (&bv)[S],
+template <bool FULL, typename T, int R, int S, Layout L, bool KEEP>
+__device__ __forceinline__ void walk_run(const ScanArgs& a, const Where<R, S, L>& w, const Two (&av)[S], const Two (&bv)[S],
                                          Two h) {
   const int64_t row0 = w.b * a.seqlen;
   T* out = static_cast<T*>(a.out) + row0 * a.dim;
@@ -473,32 +551,28 @@ __device__ __forceinline__ void walk_run(const ScanArgs& a, const Where<R, S, OD
       y[j] = FULL || k + j < w.left ? h : Two{0.0f, 0.0f};
       if (FULL || k + j < w.rest) {
         T* to = FULL ? rows.next(w.c) : in_row(out + static_cast<int64_t>(w.at(k + j)) * a.dim, w.c);
-        if (!KEEP || w.have > 0) store2<ODD>(to, w.have, y[j]);
+        if (!KEEP || w.have > 0) store2<L>(to, w.have, y[j]);
       }
     }
     if constexpr (KEEP) {
-      const int64_t first = 3 * a.plane + row0;
-      if (FULL || k < w.rest)
-        keep4<ODD>(
-            a.keep_scale + first * a.groups + w.tile, a.groups, w.c, w.have, w.lane, FULL ? 4 : w.rest - k, y,
-            [&](int j) { return a.keep + (first + w.at(k + j)) * a.dim; }, [&](int j) { return static_cast<int64_t>(w.at(k + j)); });
+      if (FULL || k < w.rest) Kept<L>(a, w, 3).template put<FULL>(a, w, k, w.rest - k, tops(y[0], y[1], y[2], y[3]), y);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
-template <typename T, int R, int S, bool ODD, bool KEEP>
+template <typename T, int R, int S, Layout L, bool KEEP>
 __global__ __launch_bounds__(64 * R, 4) void gated_scan_fwd_kernel(ScanArgs a) {
   static_assert(S % 4 == 0, "8-bit copies are made four tokens at a time");
   __shared__ Shared<R> shared;
-  const Where<R, S, ODD> w(a, unit_of(a), false);
+  const Where<R, S, L> w(a, unit_of(a), false);
   Two av[S], bv[S], h{0.0f, 0.0f};
-  const Pairs p = w.left >= S ? take_run<true, T, R, S, ODD, KEEP>(a, w, av, bv) : take_run<false, T, R, S, ODD, KEEP>(a, w, av, bv);
-  if (w.chunk == 0 || w.begin() < w.n) h = enter<R, S, ODD>(a, w, p, shared, a.first, a.end);
+  const Pairs p = w.left >= S ? take_run<true, T, R, S, L, KEEP>(a, w, av, bv) : take_run<false, T, R, S, L, KEEP>(a, w, av, bv);
+  if (w.chunk == 0 || w.begin() < w.n) h = enter<R, S, L>(a, w, p, shared, a.first, a.end);
   if (w.left >= S)
-    walk_run<true, T, R, S, ODD, KEEP>(a, w, av, bv, h);
+    walk_run<true, T, R, S, L, KEEP>(a, w, av, bv, h);
   else
-    walk_run<false, T, R, S, ODD, KEEP>(a, w, av, bv, h);
+    walk_run<false, T, R, S, L, KEEP>(a, w, av, bv, h);
 }
 
 // A uniform load through the scalar cache, of what no kernel that runs writes.
@@ -526,20 +600,20 @@ __device__ __forceinline__ TokenGrad gradient_of(float G, Rate rate, float p, fl
 }
 
 // What the gradient reads of a wave's tokens.
-template <typename T, int S, bool ODD, bool CODES>
+template <typename T, int S, Layout L, bool CODES>
 struct Taken {
-  using In = Raw<typename std::conditional<CODES, uint8_t, T>::type, ODD>;
-  In x[S], r[S], i[S], h[S];
-  Raw<T, ODD> d[S];
+  Raw<typename std::conditional<CODES, uint8_t, T>::type, L> in[4][S];  // x, r, i, h
+  Raw<T, L> d[S];
   Two p[S];                       // sigmoid(r)
   float scale[CODES ? 4 : 1][S];  // of the 8-bit forms, uniform
-  __device__ __forceinline__ Two of(int plane, In raw, int k) const {
-    const Two v = values(raw);
+  bool shift;
+  __device__ __forceinline__ Two of(int plane, int k) const {
+    const Two v = values<L>(in[plane][k], shift);
     if constexpr (CODES) return Two{v.a * scale[plane][k], v.b * scale[plane][k]};
     return v;
   }
-  __device__ __forceinline__ Two gate(int plane, In raw, int k) const {
-    const Two v = values(raw);
+  __device__ __forceinline__ Two gate(int plane, int k) const {
+    const Two v = values<L>(in[plane][k], shift);
     if constexpr (CODES) {  // the scale and log2(e) in one factor
       const float f = scale[plane][k] * -kLog2e;
       return {sigmoid_of(v.a * f), sigmoid_of(v.b * f)};
@@ -548,52 +622,51 @@ struct Taken {
   }
 };
 
-template <bool FULL, typename T, int R, int S, bool ODD, bool CODES>
-__device__ __forceinline__ Pairs take_back(const ScanArgs& a, const Where<R, S, ODD>& w, Rate rate0, Rate rate1,
-                                           Taken<T, S, ODD, CODES>& v) {
+template <bool FULL, typename T, int R, int S, Layout L, bool CODES>
+__device__ __forceinline__ Pairs take_back(const ScanArgs& a, const Where<R, S, L>& w, Rate rate0, Rate rate1,
+                                           Taken<T, S, L, CODES>& v) {
   const int64_t row0 = w.b * a.seqlen;
   Rows<const T> d(static_cast<const T*>(a.dout) + w.b * a.dout_batch, a.dout_token, w);
+  v.shift = w.shift;
   // the state before a token is the output of the walk-back's next one; the very last's is the state given
+  const auto there = [&](int plane, int k) { return (FULL && (plane < 3 || k < S - 1)) || k + (plane == 3) < w.left; };
+  const auto scales = [&](int plane) {
+    return Rows<const float>(a.codes_scale + (plane * a.plane + row0) * a.groups + w.tile, a.groups, w, plane == 3);
+  };
+  const auto codes = [&](int plane) { return Rows<const uint8_t>(a.codes + (plane * a.plane + row0) * a.dim, a.dim, w, plane == 3); };
   if constexpr (CODES) {
-    const auto codes = [&](int plane, int from) { return Rows<const uint8_t>(a.codes + (plane * a.plane + row0) * a.dim, a.dim, w, from); };
-    const auto scales = [&](int plane, int from) {
-      return Rows<const float>(a.codes_scale + (plane * a.plane + row0) * a.groups + w.tile, a.groups, w, from);
-    };
-    Rows<const uint8_t> x = codes(0, 0), r = codes(1, 0), i = codes(2, 0), h = codes(3, 1);
-    Rows<const float> sx = scales(0, 0), sr = scales(1, 0), si = scales(2, 0), sh = scales(3, 1);
+    Rows<const uint8_t> c[4] = {codes(0), codes(1), codes(2), codes(3)};
+    Rows<const float> scale[4] = {scales(0), scales(1), scales(2), scales(3)};
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (FULL || k < w.left) {
-        v.r[k] = load2<ODD, true>(r.next(w.cc), w.d1), v.scale[1][k] = scalar_load(sr.next(0));
-        v.d[k] = load2<ODD, true>(d.next(w.cc), w.d1);
-        v.x[k] = load2<ODD, true>(x.next(w.cc), w.d1), v.scale[0][k] = scalar_load(sx.next(0));
-        v.i[k] = load2<ODD, true>(i.next(w.cc), w.d1), v.scale[2][k] = scalar_load(si.next(0));
-        if (k < S - 1 ? FULL || k + 1 < w.left : k + 1 < w.left)
-          v.h[k] = load2<ODD, true>(h.next(w.cc), w.d1), v.scale[3][k] = scalar_load(sh.next(0));
-      }
+      if (FULL || k < w.left) v.d[k] = load2<L, true>(d.next(w.cc));
+#pragma unroll
+      for (int plane = 0; plane < 4; ++plane)
+        if (there(plane, k)) {
+          v.in[plane][k] = load2<L>(c[plane].next(w.cc));
+          // the scales' loads between the codes': all of them first cost 10 us of 160, all of them last 20
+          v.scale[plane][k] = scalar_load(scale[plane].next(0));
+        }
     }
   } else {
-    Rows<const T> x(static_cast<const T*>(a.x) + w.b * a.x_batch, a.x_token, w);
-    Rows<const T> r(static_cast<const T*>(a.r) + w.b * a.r_batch, a.r_token, w);
-    Rows<const T> i(static_cast<const T*>(a.i) + w.b * a.i_batch, a.i_token, w);
-    Rows<const T> h(static_cast<const T*>(a.h) + row0 * a.dim, a.dim, w, 1);
+    Rows<const T> in[4] = {Rows<const T>(static_cast<const T*>(a.x) + w.b * a.x_batch, a.x_token, w),
+                           Rows<const T>(static_cast<const T*>(a.r) + w.b * a.r_batch, a.r_token, w),
+                           Rows<const T>(static_cast<const T*>(a.i) + w.b * a.i_batch, a.i_token, w),
+                           Rows<const T>(static_cast<const T*>(a.h) + row0 * a.dim, a.dim, w, 1)};
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (FULL || k < w.left) {
-        v.r[k] = load2<ODD, true>(r.next(w.cc), w.d1);
-        v.d[k] = load2<ODD, true>(d.next(w.cc), w.d1);
-        v.x[k] = load2<ODD, true>(x.next(w.cc), w.d1);
-        v.i[k] = load2<ODD, true>(i.next(w.cc), w.d1);
-        if (k < S - 1 ? FULL || k + 1 < w.left : k + 1 < w.left) v.h[k] = load2<ODD, true>(h.next(w.cc), w.d1);
-      }
+      if (FULL || k < w.left) v.d[k] = load2<L, true>(d.next(w.cc));
+#pragma unroll
+      for (int plane = 0; plane < 4; ++plane)
+        if (there(plane, k)) v.in[plane][k] = load2<L, true>(in[plane].next(w.cc));
     }
   }
   Pairs p{1.0f, 0.0f, 1.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     if (FULL || k < w.left) {
-      const Two d = values(v.d[k]);
-      v.p[k] = v.gate(1, v.r[k], k);
+      const Two d = values<L>(v.d[k], w.shift);
+      v.p[k] = v.gate(1, k);
       const float a0 = decay_of(rate0, v.p[k].a), a1 = decay_of(rate1, v.p[k].b);
       then(p, a0, a0 * d.a, a1, a1 * d.b);
     }
@@ -602,22 +675,22 @@ __device__ __forceinline__ Pairs take_back(const ScanArgs& a, const Where<R, S, 
 }
 
 // A run's gradients from c, the gradient that the walk-back brings; returns the run's sums for A_log.
-template <bool FULL, typename T, int R, int S, bool ODD, bool CODES>
-__device__ __forceinline__ Two walk_back(const ScanArgs& a, const Where<R, S, ODD>& w, Rate rate0, Rate rate1,
-                                         const Taken<T, S, ODD, CODES>& v, Two c) {
+template <bool FULL, typename T, int R, int S, Layout L, bool CODES>
+__device__ __forceinline__ Two walk_back(const ScanArgs& a, const Where<R, S, L>& w, Rate rate0, Rate rate1,
+                                         const Taken<T, S, L, CODES>& v, Two c) {
   const int64_t row0 = w.b * a.seqlen;
   T *dx = static_cast<T*>(a.dx) + row0 * a.dim, *dr = static_cast<T*>(a.dr) + row0 * a.dim,
     *di = static_cast<T*>(a.di) + row0 * a.dim;
   Rows<T> px(dx, a.dim, w), pr(dr, a.dim, w), pi(di, a.dim, w);
   Two dA{0.0f, 0.0f}, first{0.0f, 0.0f};
   if (w.have <= 0) return dA;
-  if (w.left <= S && a.first) first = {a.first[w.b * a.dim + w.cc], a.first[w.b * a.dim + w.cc + w.d1]};
+  if (w.left <= S && a.first) first = {a.first[w.b * a.dim + w.c0], a.first[w.b * a.dim + w.c1]};
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     Two gx{0.0f, 0.0f}, gr{0.0f, 0.0f}, gi{0.0f, 0.0f};
     if (FULL || k < w.left) {
-      const Two d = values(v.d[k]), x = v.of(0, v.x[k], k), q = v.gate(2, v.i[k], k), p = v.p[k];
-      const Two h = (FULL && k < S - 1) || k + 1 < w.left ? v.of(3, v.h[k], k) : first;
+      const Two d = values<L>(v.d[k], w.shift), x = v.of(0, k), q = v.gate(2, k), p = v.p[k];
+      const Two h = (FULL && k < S - 1) || k + 1 < w.left ? v.of(3, k) : first;
       const TokenGrad g0 = gradient_of(d.a + c.a, rate0, p.a, decay_of(rate0, p.a), x.a, q.a, h.a);
       const TokenGrad g1 = gradient_of(d.b + c.b, rate1, p.b, decay_of(rate1, p.b), x.b, q.b, h.b);
       gx = {g0.dx, g1.dx}, gr = {g0.dr, g1.dr}, gi = {g0.di, g1.di};
@@ -625,31 +698,31 @@ __device__ __forceinline__ Two walk_back(const ScanArgs& a, const Where<R, S, OD
       c = {g0.c, g1.c};
     }
     if (FULL) {
-      store2<ODD>(px.next(w.c), w.have, gx);
-      store2<ODD>(pr.next(w.c), w.have, gr);
-      store2<ODD>(pi.next(w.c), w.have, gi);
+      store2<L>(px.next(w.c), w.have, gx);
+      store2<L>(pr.next(w.c), w.have, gr);
+      store2<L>(pi.next(w.c), w.have, gi);
     } else if (k < w.rest) {
       const int64_t at = static_cast<int64_t>(w.at(k)) * a.dim;
-      store2<ODD>(in_row(dx + at, w.c), w.have, gx);
-      store2<ODD>(in_row(dr + at, w.c), w.have, gr);
-      store2<ODD>(in_row(di + at, w.c), w.have, gi);
+      store2<L>(in_row(dx + at, w.c), w.have, gx);
+      store2<L>(in_row(dr + at, w.c), w.have, gr);
+      store2<L>(in_row(di + at, w.c), w.have, gi);
     }
   }
   return {0.5f * dA.a, 0.5f * dA.b};
 }
 
-template <typename T, int R, int S, bool ODD, bool CODES>
+template <typename T, int R, int S, Layout L, bool CODES>
 __global__ __launch_bounds__(64 * R, 4) void gated_scan_bwd_kernel(ScanArgs a) {
   __shared__ Shared<R> shared;
-  const Where<R, S, ODD> w(a, unit_of(a), true);
-  const Rate rate0 = rate_of(a.A_log, w.cc), rate1 = rate_of(a.A_log, w.cc + w.d1);
-  Taken<T, S, ODD, CODES> v;
-  const Pairs p = w.left >= S ? take_back<true, T, R, S, ODD, CODES>(a, w, rate0, rate1, v)
-                              : take_back<false, T, R, S, ODD, CODES>(a, w, rate0, rate1, v);
+  const Where<R, S, L> w(a, unit_of(a), true);
+  const Rate rate0 = rate_of(a.A_log, w.c0), rate1 = rate_of(a.A_log, w.c1);
+  Taken<T, S, L, CODES> v;
+  const Pairs p = w.left >= S ? take_back<true, T, R, S, L, CODES>(a, w, rate0, rate1, v)
+                              : take_back<false, T, R, S, L, CODES>(a, w, rate0, rate1, v);
   Two c{0.0f, 0.0f};
-  if (w.chunk == 0 || w.begin() < w.n) c = enter<R, S, ODD>(a, w, p, shared, a.last, a.end);
-  Two dA = w.left >= S ? walk_back<true, T, R, S, ODD, CODES>(a, w, rate0, rate1, v, c)
-                       : walk_back<false, T, R, S, ODD, CODES>(a, w, rate0, rate1, v, c);
+  if (w.chunk == 0 || w.begin() < w.n) c = enter<R, S, L>(a, w, p, shared, a.last, a.end);
+  Two dA = w.left >= S ? walk_back<true, T, R, S, L, CODES>(a, w, rate0, rate1, v, c)
+                       : walk_back<false, T, R, S, L, CODES>(a, w, rate0, rate1, v, c);
   // this chunk's share of A_log's gradient, its runs in a fixed order
   __syncthreads();
   shared.part[w.run][w.lane] = make_float4(dA.a, dA.b, 0.0f, 0.0f);
@@ -794,21 +867,41 @@ bool states_ok(const ScanArgs& a, const float* to, const float* from, bool same)
   return t == f ? same : t + n <= f || f + n <= t;
 }
 
-template <typename T, bool ODD>
+template <typename T, Layout L>
 void launch_fwd(const Plan& p, hipStream_t stream) {
   p.clear(stream);
   if (p.a.keep)
-    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, ODD, true>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
+    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, L, true>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
   else
-    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, ODD, false>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
+    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, kRuns, kTokens, L, false>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
 }
 
-template <typename T, bool ODD, bool CODES>
+template <typename T, Layout L, bool CODES>
 void launch_bwd(const Plan& p, hipStream_t stream) {
   p.clear(stream);
-  hipLaunchKernelGGL((gated_scan_bwd_kernel<T, kRuns, kGradTokens, ODD, CODES>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
+  hipLaunchKernelGGL((gated_scan_bwd_kernel<T, kRuns, kGradTokens, L, CODES>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
   hipLaunchKernelGGL(gated_scan_rate_kernel, dim3(static_cast<unsigned>((p.a.dim + 31) / 32)), dim3(1024), 0, stream, p.a.part,
                      p.a.dA_log, p.a.batch * p.a.chunks, static_cast<int64_t>(p.a.tiles) * kTile, p.a.dim);
+}
+
+// keep: 8-bit copies are stored four channels at once
+Layout layout_of(int dim, bool keep) { return dim == 1 ? kSingle : dim % (keep ? 4 : 2) ? kShifted : kPairs; }
+
+template <typename T>
+void dispatch_fwd(const Plan& p, hipStream_t stream) {
+  switch (layout_of(p.a.dim, p.a.keep != nullptr)) {
+    case kPairs: return launch_fwd<T, kPairs>(p, stream);
+    case kShifted: return launch_fwd<T, kShifted>(p, stream);
+    case kSingle: return launch_fwd<T, kSingle>(p, stream);
+  }
+}
+template <typename T, bool CODES>
+void dispatch_bwd(const Plan& p, hipStream_t stream) {
+  switch (layout_of(p.a.dim, false)) {
+    case kPairs: return launch_bwd<T, kPairs, CODES>(p, stream);
+    case kShifted: return launch_bwd<T, kShifted, CODES>(p, stream);
+    case kSingle: return launch_bwd<T, kSingle, CODES>(p, stream);
+  }
 }
 
 }  // namespace
@@ -848,11 +941,10 @@ vmscan_status vmscan_gated_scan_fwd(const void* x, const int64_t* x_strides, con
   a.end = final_state, a.keep = static_cast<uint8_t*>(keep_codes), a.keep_scale = keep_scale, a.reverse = reverse;
   a.x_batch = x_strides[0], a.x_token = x_strides[1], a.r_batch = r_strides[0], a.r_token = r_strides[1];
   a.i_batch = i_strides[0], a.i_token = i_strides[1];
-  const bool odd = a.dim % 2 != 0;
   if (dtype == VMSCAN_F32)
-    odd ? launch_fwd<float, true>(plan, stream) : launch_fwd<float, false>(plan, stream);
+    dispatch_fwd<float>(plan, stream);
   else
-    odd ? launch_fwd<uint16_t, true>(plan, stream) : launch_fwd<uint16_t, false>(plan, stream);
+    dispatch_fwd<uint16_t>(plan, stream);
   return launched();
 }
 
@@ -900,18 +992,10 @@ vmscan_status vmscan_gated_scan_bwd(const void* x, const int64_t* x_strides, con
     a.i_batch = i_strides[0], a.i_token = i_strides[1];
   }
   a.dout_batch = dout_strides[0], a.dout_token = dout_strides[1];
-  const bool odd = a.dim % 2 != 0;
-  if (dtype == VMSCAN_F32) {
-    if (codes)
-      odd ? launch_bwd<float, true, true>(plan, stream) : launch_bwd<float, false, true>(plan, stream);
-    else
-      odd ? launch_bwd<float, true, false>(plan, stream) : launch_bwd<float, false, false>(plan, stream);
-  } else {
-    if (codes)
-      odd ? launch_bwd<uint16_t, true, true>(plan, stream) : launch_bwd<uint16_t, false, true>(plan, stream);
-    else
-      odd ? launch_bwd<uint16_t, true, false>(plan, stream) : launch_bwd<uint16_t, false, false>(plan, stream);
-  }
+  if (dtype == VMSCAN_F32)
+    codes ? dispatch_bwd<float, true>(plan, stream) : dispatch_bwd<float, false>(plan, stream);
+  else
+    codes ? dispatch_bwd<uint16_t, true>(plan, stream) : dispatch_bwd<uint16_t, false>(plan, stream);
   return launched();
 }
 
