@@ -599,7 +599,7 @@ def _enqueue(fn, args, dev, prepare=False, keep=None):
     """The C call with the tensors' device current (a stream belongs to a device)."""
     if prepare:
         return _call(fn, args, True, keep)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         code = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -608,6 +608,9 @@ def _enqueue(fn, args, dev, prepare=False, keep=None):
         _check(code)
     return None
 
+
+# The current device's index, without torch's check that CUDA is initialised (a tensor is there).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 # The current stream's handle without making a Stream object (a tenth of the time, and these calls
 # may be as short as a few microseconds), where torch has it.
@@ -996,7 +999,7 @@ def groupnorm_fwd(x, weight, bias, groups, eps=1e-5, act=True, lengths=None, kee
     if groups < 1 or dim % groups:
         raise ValueError(f"{dim} channels cannot be {groups} groups")
     if y is None:
-        y = torch.empty(given.shape, dtype=x.dtype, device=dev)
+        y = torch.empty_like(given, memory_format=torch.contiguous_format)
     else:
         _need(y, "y", given.shape, x.dtype, dev)
     mean, rstd = torch.empty(2, nb, groups, dtype=torch.float32, device=dev).unbind(0)
@@ -1044,7 +1047,7 @@ def groupnorm_bwd(dy, x, weight, bias, mean, rstd, act=True, lengths=None, works
         raise ValueError(f"{dim} channels cannot be {groups} groups")
     if lengths is not None:
         _need(lengths, "lengths", (nb,), torch.int32, dev)
-    dx = torch.empty(given.shape, dtype=dy.dtype, device=dev)
+    dx = torch.empty_like(given, memory_format=torch.contiguous_format)
     dw, db = torch.empty(2, dim, dtype=torch.float32, device=dev).unbind(0)
     lib = load()
     workspace = _workspace(workspace, lib.vmscan_groupnorm_bwd_workspace_bytes(nb, L, dim, groups), dev)
@@ -1153,18 +1156,18 @@ def gated_scan_step(x, r, i, A_log, state, slots=None, out=None, stream=None, pr
     if stream is not None:
         return _on_stream(stream, gated_scan_step, x, r, i, A_log, state, slots, out, None, prepare)
     dt = _is_act(x, "x", 2)
-    dev, shape, adt = x.device, tuple(x.shape), x.dtype
+    dev, shape, adt = x.device, x.shape, x.dtype
     nb, dim = shape
-    strides = []
-    for name, t in (("x", x), ("r", r), ("i", i)):
+    for name, t in (("r", r), ("i", i)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.shape != shape or t.dtype != adt or t.device != dev:
-            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {adt} on {dev}")
-        s = t.stride()
-        if s[1] != 1 and dim != 1:
-            raise ValueError(f"{name} must have contiguous channels")
-        strides.append(s[0] if nb != 1 else 0)
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {tuple(shape)} {adt} on {dev}")
+    (xs, xc), (rs, rc), (is_, ic) = x.stride(), r.stride(), i.stride()
+    if dim != 1 and not xc == rc == ic == 1:
+        raise ValueError("x, r and i must have contiguous channels")
+    if nb == 1:  # a stride that says nothing
+        xs = rs = is_ = 0
     _need(A_log, "A_log", (dim,), torch.float32, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise ValueError("state must be [pool, dim]")
@@ -1175,10 +1178,10 @@ def gated_scan_step(x, r, i, A_log, state, slots=None, out=None, stream=None, pr
     elif pool != nb:
         raise ValueError(f"without slots the pool holds one state per sequence: {pool} for {nb}")
     if out is None:
-        out = torch.empty(shape, dtype=adt, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _need(out, "out", shape, adt, dev)
-    args = (x.data_ptr(), strides[0], r.data_ptr(), strides[1], i.data_ptr(), strides[2], A_log.data_ptr(),
-            state.data_ptr(), _p(slots), out.data_ptr(), nb, pool, dim, dt, _current(dev))
+    args = (x.data_ptr(), xs, r.data_ptr(), rs, i.data_ptr(), is_, A_log.data_ptr(), state.data_ptr(), _p(slots),
+            out.data_ptr(), nb, pool, dim, dt, _current(dev))
     run = _enqueue(load().vmscan_gated_scan_step, args, dev, prepare, (x, r, i, A_log, state, slots, out))
     return (run, out) if prepare else out
