@@ -658,7 +658,7 @@ __global__ __launch_bounds__(512) void groupnorm_sums_kernel(GnArgs a) {
     for (int k = 0; k < 8; ++k)
       if (k < l.n) {
         l1[l.row * a.dim + l.c + k] = s1[k];
-        l2[l.row * a.dim + l.c + k] = s2[k] * rstds[(l.c + k) / a.width];
+        l2[l.row * a.dim + l.c + k] = n ? s2[k] * rstds[(l.c + k) / a.width] : 0.0f;  // (infinite where eps is 0)
       }
   }
   __syncthreads();
@@ -802,7 +802,7 @@ __global__ __launch_bounds__(512, W8 ? 4 : 2) void groupnorm_slab_bwd_kernel(GnA
     const int at = l.row * a.slab + l.c - slab * a.slab;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < l.n) l1[at + e] = s1[e], l2[at + e] = s2[e] * a.rstd[b * a.groups + (l.c + e) / a.width];
+      if (e < l.n) l1[at + e] = s1[e], l2[at + e] = n ? s2[e] * a.rstd[b * a.groups + (l.c + e) / a.width] : 0.0f;
   }
   __syncthreads();
   join_rows(a, l1, l2, m2 + a.slab / a.width, slab * a.slab, here, a.chan + b * 2 * a.dim,
