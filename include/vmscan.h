@@ -545,7 +545,8 @@ vmscan_status vmscan_linattn_step(const void *q, const int64_t *q_strides, const
  * activations in 8 bits: the 8-bit form itself, the group norm with its activation and the gated linear
  * recurrence.  Activations are token-major, [batch, seqlen, dim] (channels last); *_strides are batch and token
  * stride in elements, channels contiguous, and such inputs may start at any element.  Outputs are dense.
- * Ownership, errors, streams and the workspace follow the conventions above (no wait status word).
+ * Ownership, errors, streams and the workspace follow the conventions above; only the recurrence over a sequence of
+ * several chunks has a wait status word.
  */
 
 /*
@@ -623,7 +624,11 @@ vmscan_status vmscan_groupnorm_bwd(const void *dy, const int64_t *dy_strides, co
  *   keep_codes, keep_scale : NULL, or the 8-bit form (as vmscan_act8_pack) of what the gradient needs:
  *                [4, batch, seqlen, dim] and [4, batch, seqlen, ceil(dim / 128)], planes x, r, i and h (before
  *                its rounding to `out`), zeros past a row's length
- * A NaN or infinity reaches the later states of its own channel only.
+ * A NaN or infinity reaches the later states of its own channel only (kept in 8 bits: that token's copies of its
+ * 128 channels too), as either of the two.
+ * A sequence is walked in chunks of 128 tokens (the gradient: of 64) by workgroups of their own; a chunk waits for what
+ * those before it publish.  If there are several, the workspace's first int32 is the call's status word.
+ * ceil(dim / 128) * batch * chunks must be below 2^23, seqlen below 2^30, dim below 2^20 (else VMSCAN_ERR_SHAPE).
  */
 size_t vmscan_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 vmscan_status vmscan_gated_scan_fwd(const void *x, const int64_t *x_strides, const void *r,
@@ -664,7 +669,7 @@ vmscan_status vmscan_gated_scan_bwd(const void *x, const int64_t *x_strides, con
  *   slots   : [batch] int32: the state of each sequence, all different; a row whose slot is not in
  *             0 .. pool - 1 has no state: its out is 0.  NULL: row b has state b, pool = batch.
  *   out     : [batch, dim] activation dtype, dense
- * No workspace.
+ * batch < 65536, dim < 2^20 (else VMSCAN_ERR_SHAPE).  No workspace.
  */
 vmscan_status vmscan_gated_scan_step(const void *x, int64_t x_stride, const void *r,
                                      int64_t r_stride, const void *i, int64_t i_stride,

@@ -7,9 +7,8 @@
 // the chunk comes from those before it in the same way, and every run then walks its tokens from the state that
 // enters it.  So inputs are read once and outputs written once however long the sequence is.
 //
-// Between chunks: a chunk waits for the published pairs of the chunks before it in its group of 4 R and for
-// the state that the last chunk of the group before published.  The order of the joins is fixed, whatever arrives
-// first.  Workgroups take their chunks in the order in which they start (a counter), chunks of all sequences by their
+// Between chunks: a chunk waits for the published pairs of the chunks before it in its group of 4 R and for the state
+// that the last chunk of the group before published.  The order of the joins is fixed, whatever arrives first.  Workgroups take their chunks in the order in which they start (a counter), chunks of all sequences by their
 // place, so a chunk only waits for chunks that running workgroups hold: every wait ends.  A published value is one
 // 64-bit word that is written at once; a first launch sets all of them to a value that no result has.
 #include <hip/hip_runtime.h>
@@ -851,6 +850,8 @@ struct Plan {
     a.states = a.pairs + static_cast<int64_t>(a.chains) * a.chunks * kTile;
     a.part = reinterpret_cast<float*>(p + part_at);
   }
+  // The word that a wait sets when it gives up; a call of one chunk waits for nothing and has none.
+  const void* status() const { return words ? a.status : nullptr; }
   void clear(hipStream_t stream) const {
     if (words)
       hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((words + 511) / 512)), dim3(256), 0, stream,
@@ -945,7 +946,7 @@ vmscan_status vmscan_gated_scan_fwd(const void* x, const int64_t* x_strides, con
     dispatch_fwd<float>(plan, stream);
   else
     dispatch_fwd<uint16_t>(plan, stream);
-  return launched();
+  return finish_call(launched(), plan.status(), stream);
 }
 
 size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
@@ -996,7 +997,7 @@ vmscan_status vmscan_gated_scan_bwd(const void* x, const int64_t* x_strides, con
     codes ? dispatch_bwd<float, true>(plan, stream) : dispatch_bwd<float, false>(plan, stream);
   else
     codes ? dispatch_bwd<uint16_t, true>(plan, stream) : dispatch_bwd<uint16_t, false>(plan, stream);
-  return launched();
+  return finish_call(launched(), plan.status(), stream);
 }
 
 vmscan_status vmscan_gated_scan_step(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,

@@ -19,6 +19,25 @@ inline vmscan_status launched() {
   return e == hipSuccess ? VMSCAN_OK : launch_failed(e);
 }
 
+// The end of an entry point.  In a build with VMSCAN_CHECK_WAITS the call waits for its kernels and
+// reads the workspace's status word, so that a wait that gave up is reported
+// as VMSCAN_ERR_WAIT; otherwise the word is left for the caller to read.
+inline vmscan_status finish_call(vmscan_status st, const void* workspace, hipStream_t stream) {
+#ifdef VMSCAN_CHECK_WAITS
+  if (st != VMSCAN_OK || !workspace) return st;
+  hipError_t e = hipStreamSynchronize(stream);
+  if (e != hipSuccess) return launch_failed(e);
+  int word = 0;
+  e = hipMemcpy(&word, workspace, sizeof(word), hipMemcpyDeviceToHost);
+  if (e != hipSuccess) return launch_failed(e);
+  return word ? VMSCAN_ERR_WAIT : VMSCAN_OK;
+#else
+  (void)workspace;
+  (void)stream;
+  return st;
+#endif
+}
+
 // A launch holds less than 2^32 threads along x: this many workgroups of 256.
 constexpr int64_t kMaxBlocks256 = (int64_t{1} << 24) - 1;
 

@@ -2184,24 +2184,7 @@ namespace {
 
 using vmscan_internal::launch_failed;
 
-// The end of an entry point.  In a build with VMSCAN_CHECK_WAITS the call waits for its kernels and
-// reads the workspace's status word, so that a wait between state parts that gave up is reported
-// as VMSCAN_ERR_WAIT; otherwise the word is left for the caller to read.
-vmscan_status finish_call(vmscan_status st, const void* workspace, hipStream_t stream) {
-#ifdef VMSCAN_CHECK_WAITS
-  if (st != VMSCAN_OK || !workspace) return st;
-  hipError_t e = hipStreamSynchronize(stream);
-  if (e != hipSuccess) return launch_failed(e);
-  int word = 0;
-  e = hipMemcpy(&word, workspace, sizeof(word), hipMemcpyDeviceToHost);
-  if (e != hipSuccess) return launch_failed(e);
-  return word ? VMSCAN_ERR_WAIT : VMSCAN_OK;
-#else
-  (void)workspace;
-  (void)stream;
-  return st;
-#endif
-}
+using vmscan_internal::finish_call;
 
 enum { kStagePrepare = 1, kStageScan = 2, kStageAll = 3 };
 

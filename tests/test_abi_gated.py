@@ -156,3 +156,14 @@ def test_binding_refuses_before_the_library():
         V.act8_unpack(x, None)
     with pytest.raises(ValueError):
         V.groupnorm_fwd(x[0], x[0, 0], x[0, 0], 2)
+
+
+def test_limits_of_a_launch(lib):
+    """Tiles of channels times batch times chunks below 2^23: beyond, no workspace is named and the call refuses."""
+    assert lib.vmscan_gated_scan_fwd_workspace_bytes(1, (1 << 30) - 1, 64) == 0
+    assert lib.vmscan_gated_scan_bwd_workspace_bytes(1 << 12, 1 << 18, 64) == 0
+    assert fwd(lib, L=(1 << 30) - 1, wsb=1 << 62) == ERR_SHAPE and bwd(lib, nb=1 << 12, L=1 << 18, wsb=1 << 62) == ERR_SHAPE
+    assert lib.vmscan_gated_scan_fwd_workspace_bytes(1, (1 << 30) - 256, 64) > 1 << 30
+    assert lib.vmscan_gated_scan_fwd_workspace_bytes(64, 128, 384) == 0  # one chunk: nothing waits
+    assert lib.vmscan_gated_scan_bwd_workspace_bytes(64, 64, 384) == 64 * 384 * 4
+    assert step(lib, nb=65536) == ERR_SHAPE
