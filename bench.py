@@ -682,11 +682,17 @@ def bench_ss2d_bwd(cfg_id, steps, warmup, torch, V, with_cpu=False, d_state=None
 
 
 def bench_operators(names, steps, warmup, torch):
-    """One line per case of the linear-attention block's operators (perf/operators.py): a user's call of
-    the library, inputs rotated over three sets, with the bytes and operations the case cannot do without."""
+    """One line per case of the linear-attention block's operators (perf/operators.py) and the gated recurrence
+    block's (perf/more_operators.py): a user's call of the library, inputs rotated over three sets, with the bytes and
+    operations the case cannot do without."""
+    import perf.more_operators as M
     import perf.operators as P
-    P.own = True
-    for case in P.listed():
+    P.own = M.own = True
+    cases = [(p, case) for p in (P, M) for case in p.listed()]
+    unknown = set(names or ()) - {case["name"] for _, case in cases}
+    if unknown:
+        raise SystemExit(f"bench: no such operator case: {', '.join(sorted(unknown))}")
+    for P, case in cases:
         if names and case["name"] not in names:
             continue
         sets = [P.prepare(case, seed) for seed in range(3)]
@@ -721,7 +727,7 @@ def main():
     ap.add_argument("--lane-scan", action="store_true",
                     help="Vim workloads through the lane-scan path (associative scan over positions, no chunk pass)")
     ap.add_argument("--operators", nargs="?", const="all", metavar="NAME[,NAME]",
-                    help="time the linear-attention block's operators, all cases or the named ones")
+                    help="time the linear-attention and gated recurrence blocks' operators, all cases or the named ones")
     ap.add_argument("--d-state", type=int, default=None, choices=(16, 32),
                     help="state size of the workloads, forward or backward (default: the workload's own, 16)")
     ap.add_argument("--calibrate-copy", action="store_true",

@@ -57,6 +57,10 @@ OCCUPANCY_FLOORS = [  # (kernel name fragment, minimum waves per SIMD)
     ("linattn_segment_kernelItLi64ELi64E", 4),
     ("linattn_passes_kernelItLi64ELi64E", 4),
     ("linattn_step_kernel", 6),
+    ("gated_scan_fwd_kernel", 4),
+    ("gated_scan_bwd_kernel", 4),
+    ("groupnorm_sums_kernelItLb1", 4),
+    ("groupnorm_dx_kernelItLb1", 6),
 ]
 # Linear attention: workgroups per CU that the cuts of a call are planned with (kWalks of csrc/linattn.hip), by kernel, type
 # and padded key channels, for 32, 64 and 128 value channels of a workgroup; 0: no such kernel.
