@@ -865,12 +865,12 @@ struct Plan {
     // to memory.  32 x 3136 x 512 takes 78 us instead of 93 (gradient from 8 bits 90 for 100), a half of that 55 for 52.
     const int64_t bytes = batch * seqlen * dim * ((dtype == VMSCAN_BF16 ? 2 : 4) * (gradient && !codes ? 3 : 2) + (keep || codes));
     once = bytes > (int64_t{160} << 20);
-    // Runs: enough workgroups for the chip, each of 16 steps at least (8 x 3136 x 512 with 4: 40 us instead of 32), or of 4
-    // where that would leave most of the chip idle (6 x 1001 x 100, gradient: 23 us instead of 38).
+    // Runs: enough workgroups for the chip, each of 16 steps at least (8 x 3136 x 512 with 4: 40 us instead of 32), or of one
+    // where that would leave most of the chip idle (6 x 1001 x 100, gradient: with 16 38 us, with 4 23, with one 19).
     const int64_t steps = (seqlen + a.rows - 1) / a.rows;
     const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
     int64_t splits = least((1024 + batch - 1) / batch, (steps + 15) / 16);
-    if (splits * batch < 256) splits = least((255 + batch) / batch, (steps + 3) / 4);
+    if (splits * batch < 256) splits = least((255 + batch) / batch, steps);
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
     a.run = static_cast<int>((steps + splits - 1) / splits * a.rows);
