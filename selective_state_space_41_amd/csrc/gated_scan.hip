@@ -739,35 +739,34 @@ __global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint32_t* status,
   if (i < n) *reinterpret_cast<ulonglong2*>(words + i) = make_ulonglong2(kNothing, kNothing);
 }
 
-// dA_log: the sum of `rows` partial rows, tiles * 128 channels each: a workgroup takes 32 channels, 8 lanes of 4 and 128
-// shares of the rows, whose sums meet in LDS in a fixed order.
+// dA_log: the sum of `rows` partial rows, tiles * 128 channels each: a workgroup takes 4 * COLS channels, COLS lanes of 4 and
+// 1024 / COLS shares of the rows; a wave's shares are joined by exchanges, the waves' in LDS, in a fixed order.
+constexpr int kRateCols = 2;  // 1 to 8 within 1 us of each other
 __global__ __launch_bounds__(1024) void gated_scan_rate_kernel(const float* __restrict__ part, float* __restrict__ to,
                                                                int64_t rows, int64_t stride, int dim) {
-  __shared__ __align__(16) float4 s[128][8];
-  const int cx = threadIdx.x & 7, share = threadIdx.x >> 3;
-  const float* p = part + blockIdx.x * 32 + cx * 4;
-  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __shared__ __align__(16) float4 s[16][kRateCols];
+  const int cx = threadIdx.x % kRateCols, share = threadIdx.x / kRateCols;
+  const float* p = part + blockIdx.x * (4 * kRateCols) + cx * 4;
+  float v[4] = {};
 #pragma unroll 4
-  for (int64_t i = share; i < rows; i += 128) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i * stride);
-    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+  for (int64_t i = share; i < rows; i += 1024 / kRateCols) {
+    const float4 t = *reinterpret_cast<const float4*>(p + i * stride);
+    v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
   }
-  s[share][cx] = t;
 #pragma unroll
-  for (int m = 64; m >= 1; m >>= 1) {
-    __syncthreads();
-    if (share < m) {
-      const float4 v = s[share + m][cx];
-      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-      s[share][cx] = t;
-    }
+  for (int m = kRateCols; m < 64; m *= 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], m);
   }
-  const int c = blockIdx.x * 32 + cx * 4;
-  if (share == 0) {
-    const float v[4] = {t.x, t.y, t.z, t.w};
+  if (threadIdx.x % 64 < kRateCols) s[threadIdx.x / 64][cx] = make_float4(v[0], v[1], v[2], v[3]);
+  __syncthreads();
+  if (threadIdx.x < 4 * kRateCols) {
+    const int c = blockIdx.x * (4 * kRateCols) + threadIdx.x;
+    const float* f = reinterpret_cast<const float*>(s) + threadIdx.x;
+    float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (c + k < dim) to[c + k] = v[k];
+    for (int w = 0; w < 16; ++w) t += f[w * 4 * kRateCols];
+    if (c < dim) to[c] = t;
   }
 }
 
@@ -881,7 +880,7 @@ template <typename T, Layout L, bool CODES>
 void launch_bwd(const Plan& p, hipStream_t stream) {
   p.clear(stream);
   hipLaunchKernelGGL((gated_scan_bwd_kernel<T, kRuns, kGradTokens, L, CODES>), p.grid(), dim3(64 * kRuns), 0, stream, p.a);
-  hipLaunchKernelGGL(gated_scan_rate_kernel, dim3(static_cast<unsigned>((p.a.dim + 31) / 32)), dim3(1024), 0, stream, p.a.part,
+  hipLaunchKernelGGL(gated_scan_rate_kernel, dim3(static_cast<unsigned>((p.a.dim + 4 * kRateCols - 1) / (4 * kRateCols))), dim3(1024), 0, stream, p.a.part,
                      p.a.dA_log, p.a.batch * p.a.chunks, static_cast<int64_t>(p.a.tiles) * kTile, p.a.dim);
 }
 
