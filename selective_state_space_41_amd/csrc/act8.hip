@@ -2,7 +2,8 @@
 // computed is stated in include/vmscan.h.
 //
 // 16 neighbouring lanes own a group of 128 channels, 8 each, so that a group's largest magnitude is a butterfly of
-// four lane operations, and loads and stores are 16 or 8 bytes a lane.  Bound by HBM.
+// four lane operations, and loads and stores are 16 or 8 bytes a lane.  Bound by HBM: 25216 x 768 bfloat16 packed in 11.5
+// us (59 MB, 5.1 TB/s), 25216 x 392 unpacked in 7.6 (30 MB, 4.0 TB/s: half of it is the launch).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
