@@ -840,14 +840,15 @@ struct Plan {
   int threads = 0, tokens = 0;  // tokens: of a thread that keeps a slab; 0: runs
   bool w8 = false, once = false;
 
-  // Threads of a workgroup and rows of a step: of the counts up to `most` the one that leaves the fewest idle.
-  int threads_for(int least, int most) {
+  // Threads of a workgroup and rows of a step: of the counts from 256 to 512 the one that leaves the fewest idle, or with
+  // `many` the largest that leaves few.
+  int threads_for(bool many) {
     int best = 0;
     float share = 0.0f;
-    for (int nt = least; nt <= most; nt += 64) {
-      const int rows = nt / a.lanes;
+    for (int i = 0; i <= 4; ++i) {
+      const int nt = many ? 512 - 64 * i : 256 + 64 * i, rows = nt / a.lanes;
       const float f = static_cast<float>(rows * a.lanes) / nt;
-      if (rows && f > share + 1e-3f) best = nt, share = f;
+      if (rows && f > share + (many && best ? 0.1f : 1e-3f)) best = nt, share = f;
     }
     a.rows = best ? best / a.lanes : 0;
     return best;
@@ -867,17 +868,19 @@ struct Plan {
     tokens = 0;
     a.slab = a.dim, a.slabs = 1;
     lanes_for(a.dim, keep);
-    threads = threads_for(256, 512);
+    // (the bfloat16 gradient with 512 threads rather than 256: 32 x 3136 x 512 from 8 bits 79 us instead of 83, 8 x 12544 x 384
+    // 65 for 71; forwards and float32 are up to 10 % slower that way)
+    threads = threads_for(gradient && dtype == VMSCAN_BF16);
     // Inputs and outputs past this fill the 256 MB last-level cache: streamed loads leave it to the outputs on their way
     // to memory.  32 x 3136 x 512 takes 78 us instead of 93 (gradient from 8 bits 90 for 100), a half of that 55 for 52.
     const int64_t bytes = batch * seqlen * dim * ((dtype == VMSCAN_BF16 ? 2 : 4) * (gradient && !codes ? 3 : 2) + (keep || codes));
     once = bytes > (int64_t{160} << 20);
-    // Runs: enough workgroups for the chip, each of 16 steps at least (8 x 3136 x 512 with 4: 40 us instead of 32), or of one
-    // where that would leave most of the chip idle (6 x 1001 x 100, gradient: with 16 38 us, with 4 23, with one 19).
+    // Runs: two workgroups a CU, not one more (64 x 3136 x 192, gradient: 512 workgroups 100 us, 1024 141; 24 images of 512
+    // channels: 504 workgroups 61 us, 528 70), or one where two would have less than 16 steps each.
     const int64_t steps = (seqlen + a.rows - 1) / a.rows;
-    const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-    int64_t splits = least((1024 + batch - 1) / batch, (steps + 15) / 16);
-    if (splits * batch < 256) splits = least((255 + batch) / batch, steps);
+    int64_t splits = 512 / batch;
+    if (splits * 16 > steps) splits = 256 / batch;
+    if (splits > steps) splits = steps;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
     a.run = static_cast<int>((steps + splits - 1) / splits * a.rows);
