@@ -106,3 +106,34 @@ def test_broadcast_inputs(dim, keep):
     h = V.groupnorm_bwd(d, i, a, a, y[1], y[2])
     h2 = V.groupnorm_bwd(d.contiguous(), i.contiguous(), a, a, y[1], y[2])
     assert all(torch.equal(h[k], h2[k]) for k in h)
+
+
+def test_many_rows():
+    """More batch rows than a grid's second dimension holds: the rows of a large call are those of small ones."""
+    import selective_state_space_41_amd as V
+    B, T, dim = 70000, 3, 6
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, r, i, d = (torch.randn(B, T, dim, device="cuda", generator=gen) for _ in range(4))
+    a, w = torch.randn(dim, device="cuda", generator=gen), torch.randn(dim, device="cuda", generator=gen)
+    n = torch.randint(0, T + 1, (B,), device="cuda", generator=gen, dtype=torch.int32)
+    first = torch.randn(B, dim, device="cuda", generator=gen)
+    out, last, kept = V.gated_scan_fwd(x, r, i, a, initial_state=first, lengths=n, keep=True)
+    g = V.gated_scan_bwd((x, r, i, out), a, d, initial_state=first, lengths=n, dfinal_state=first)
+    few = slice(B - 5, B)
+    sub = lambda t: t[few].contiguous()
+    out2, last2, kept2 = V.gated_scan_fwd(sub(x), sub(r), sub(i), a, initial_state=sub(first), lengths=sub(n), keep=True)
+    g2 = V.gated_scan_bwd((sub(x), sub(r), sub(i), out2), a, sub(d), initial_state=sub(first), lengths=sub(n), dfinal_state=sub(first))
+    assert torch.equal(out[few], out2) and torch.equal(last[few], last2)
+    assert torch.equal(kept[0][:, few].view(torch.uint8), kept2[0].view(torch.uint8)) and torch.equal(kept[1][:, few], kept2[1])
+    assert all(torch.equal(g[k][few], g2[k]) for k in ("dx", "dr", "di", "dinitial_state"))
+    x, d, n = x[:65535], d[:65535], n[:65535]
+    y, mean, rstd, _ = V.groupnorm_fwd(x, w, a, 2, lengths=n)
+    h = V.groupnorm_bwd(d, x, w, a, mean, rstd, lengths=n)
+    few = slice(65530, 65535)
+    y2, mean2, rstd2, _ = V.groupnorm_fwd(sub(x), w, a, 2, lengths=sub(n))
+    h2 = V.groupnorm_bwd(sub(d), sub(x), w, a, mean2, rstd2, lengths=sub(n))
+    assert torch.equal(y[few], y2) and torch.equal(mean[few], mean2) and torch.equal(h["dx"][few], h2["dx"])
+    with pytest.raises(RuntimeError):
+        V.groupnorm_fwd(out, w, a, 2)  # 70000 rows
+    assert torch.equal(V.act8_unpack(*V.act8_pack(out), dtype=torch.float32)[few],
+                       V.act8_unpack(*V.act8_pack(out[few]), dtype=torch.float32))
