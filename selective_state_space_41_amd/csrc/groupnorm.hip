@@ -8,11 +8,11 @@
 // gradient: two sums per group and channel), the next joins a row's runs and reads the tokens again, mostly from the
 // last-level cache.
 //
-// Measured (whole calls): 32 x 3136 x 512 bfloat16 kept in 8 bits 77 us (first launch 25, second 53) for 257 MB, 51 us at
-// a copy's rate, or 360 MB with the second read; its gradient from 8 bits 82 (41 and 51).  One float32 image 197 x 384
-// in one launch of 8 us, under a call of 11.  A single pass over large rows too, runs held in registers and each waiting
-// for the others of its row, took 79 to 100 us: loads, wait and stores of a workgroup come one after the other, and two
-// workgroups a CU do not cover that.
+// Measured (whole calls): 32 x 3136 x 512 bfloat16 kept in 8 bits 75 us (first launch 25, second 50) for 257 MB, 51 us at
+// a copy's rate, or 360 MB with the second read; its gradient from 8 bits 79 (38 and 47, the second's sums from the cache
+// in part).  One float32 image 197 x 384 in one launch of 8 us, under a call of 11.  A single pass over large rows too,
+// runs held in registers and each waiting for the others of its row, took 79 to 100 us: loads, wait and stores of a
+// workgroup come one after the other, and two workgroups a CU do not cover that.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -28,7 +28,7 @@ constexpr int kMaxDim = 4096;     // 512 threads of 8 channels
 constexpr int kMaxSplits = 128;   // runs of a batch row
 constexpr int kGroupLanes = 16;   // 8-bit copies: lanes whose channels share a scale
 // Tokens that a thread loads at once: 4, and 2 in the gradient, whose registers leave room for more waves then (32 x 3136 x
-// 512 from 8 bits 82 us instead of 89; the forward takes the same time with either).
+// 512 from 8 bits 82 us instead of 89, with 1024 workgroups; the forward takes the same time with either).
 constexpr int kAhead = 4, kAheadBack = 2;
 
 struct GnArgs {
@@ -872,7 +872,7 @@ struct Plan {
     // 65 for 71; forwards and float32 are up to 10 % slower that way)
     threads = threads_for(gradient && dtype == VMSCAN_BF16);
     // Inputs and outputs past this fill the 256 MB last-level cache: streamed loads leave it to the outputs on their way
-    // to memory.  32 x 3136 x 512 takes 78 us instead of 93 (gradient from 8 bits 90 for 100), a half of that 55 for 52.
+    // to memory.  32 x 3136 x 512 takes 74 us instead of 91 (gradient from 8 bits 79 for 91), a half of that 47 for 43.
     const int64_t bytes = batch * seqlen * dim * ((dtype == VMSCAN_BF16 ? 2 : 4) * (gradient && !codes ? 3 : 2) + (keep || codes));
     once = bytes > (int64_t{160} << 20);
     // Runs: two workgroups a CU, not one more (64 x 3136 x 192, gradient: 512 workgroups 100 us, 1024 141; 24 images of 512
