@@ -552,9 +552,10 @@ vmscan_status vmscan_linattn_step(const void *q, const int64_t *q_strides, const
 /*
  * Activations in 8 bits: OCP e4m3 codes and a float32 scale for each 128 channels of a row (the last group may
  * be short): x ~ code * scale, scale = max|x| / 448 over the group (1 where that is 0; at least the smallest normal
- * float32), the code the value nearest to x / scale: the 8-bit form of vmscan_rmsnorm_fwd with group 128.  A NaN or
- * an infinity makes its group's values NaN.  (Operators that keep this form beside their output multiply by 1 / 448 and
- * 1 / scale: a scale may differ by a unit in the last place, a code where x / scale lies between two.)
+ * float32), the code the value nearest to x / scale, ties to even, both quotients in float32: the 8-bit form of
+ * vmscan_rmsnorm_fwd with group 128.  A NaN or an infinity makes its group's values NaN.  (Operators that leave this form
+ * as or beside their output multiply by 1 / scale, and those that keep it by 1 / 448: a kept scale may differ by a unit in
+ * the last place, a code where x / scale lies half-way between two.)
  *   x     : [rows, dim] activation dtype; pack: rows x_stride >= dim elements apart; unpack: dense
  *   codes : [rows, dim] bytes
  *   scale : [rows, ceil(dim / 128)] float32
