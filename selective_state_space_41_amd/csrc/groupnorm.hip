@@ -197,15 +197,19 @@ struct Steps {
 };
 
 // A thread's tokens row, row + rows, ... below n: `load(slot)` for AHEAD of them one after another, then `use(slot)` in
-// the same order.
-template <int AHEAD, typename LOAD, typename USE>
-__device__ __forceinline__ void over_tokens(int row, int rows, int n, LOAD&& load, USE&& use) {
+// the same order and, where all AHEAD were there, `turn(tokens so far)`.
+struct NoTurn {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+template <int AHEAD, typename LOAD, typename USE, typename TURN = NoTurn>
+__device__ __forceinline__ void over_tokens(int row, int rows, int n, LOAD&& load, USE&& use, TURN&& turn = {}) {
   const int turns = n / (AHEAD * rows);  // the same number for all
   for (int i = 0; i < turns; ++i) {
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) load(k);
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) use(k);
+    turn((i + 1) * AHEAD);
   }
   const int t = row + turns * AHEAD * rows;
   if (t < n) {
@@ -273,9 +277,11 @@ __device__ __forceinline__ void over_rows(int rows, int channels, float* scratch
 // Tokens that a row of the step saw of a run of `n`.
 __device__ __forceinline__ int seen(int n, int row, int rows) { return n > row ? (n - row + rows - 1) / rows : 0; }
 
-// Mean and sum of squared deviations of each group over a run.  A thread's sums are of differences to its first
-// token, so that a large mean costs nothing; sums of different threads are joined by their means (each term's
-// deviation is taken from the joint mean, nothing is subtracted from a sum of squares).
+// Mean and sum of squared deviations of each group over a run.  A thread's sums are of differences to a centre, its first
+// token at first; every four tokens the centre moves to the mean so far, and the sums are moved with it exactly, by the
+// distance between the two float32 centres.  So neither a large mean nor tokens far from the others, the first ones among
+// them, are subtracted from a sum of squares that they dominate (a centre left at a first token 100 times the others cost
+// the variance 4e-4 of itself over 784 tokens).  Sums of different threads are joined by their means in the same sense.
 template <typename T, bool W8, bool ONCE>
 __global__ __launch_bounds__(512) void groupnorm_stats_kernel(GnArgs a) {
   extern __shared__ float lds[];  // [2][rows][dim], the channels' and the groups' means, a float per thread
@@ -302,6 +308,15 @@ __global__ __launch_bounds__(512) void groupnorm_stats_kernel(GnArgs a) {
             const float d = v[e] - k0[e];
             s[e] += d;
             q[e] = __builtin_fmaf(d, d, q[e]);
+          }
+        },
+        [&](int m) {
+          const float tokens = static_cast<float>(m), inv = __builtin_amdgcn_rcpf(tokens);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float k1 = __builtin_fmaf(s[e], inv, k0[e]), by = k1 - k0[e], t = __builtin_fmaf(-tokens, by, s[e]);
+            q[e] = __builtin_fmaf(-by, s[e] + t, q[e]);
+            s[e] = t, k0[e] = k1;
           }
         });
     const int m = seen(n, l.row, rows);
