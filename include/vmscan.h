@@ -615,6 +615,7 @@ vmscan_status vmscan_groupnorm_bwd(const void *dy, const int64_t *dy_strides, co
  * Gated linear recurrence with one state per channel.  Per (batch b, channel d), in float32:
  *   a_t = exp(A sigmoid(r_t)),  A = -exp(A_log[d]);   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
  * from h_{-1} = initial_state (NULL: 0), over t = 0 .. n - 1, or with reverse = 1 from t = n - 1 down to 0.
+ * (Rates exp(A_log[d]) over 2^125, infinite ones too, count as 2^125.)
  *   x, r, i    : [batch, seqlen, dim] activation dtype; the scan input and its two gates before their
  *                sigmoids; token strides below 2^24 elements
  *   A_log      : [dim] float32

@@ -171,12 +171,15 @@ __device__ __forceinline__ float sigmoid(float x) {
 // 1 / (1 + 2^t)
 __device__ __forceinline__ float sigmoid_of(float t) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t)); }
 
-// A channel's rate e^A_log, as the factor of the decay's exponent and of v below.
+// A channel's rate e^A_log, as the factor of the decay's exponent and of v below.  A rate over 2^125 counts as that, which
+// leaves both factors finite: its decay is 0 under any gate sigmoid(r) over 2^-118 already, and an infinite rate times a zero
+// decay or gate would be a NaN.
+constexpr float kMaxRate = 0x1p125f;
 struct Rate {
   float e, v;  // -rate log2(e), 2 rate
 };
 __device__ __forceinline__ Rate rate_of(const float* A_log, int c) {
-  const float r = __builtin_amdgcn_exp2f(A_log[c] * kLog2e);
+  const float all = __builtin_amdgcn_exp2f(A_log[c] * kLog2e), r = all > kMaxRate ? kMaxRate : all;  // a NaN stays
   return {r * -kLog2e, r + r};
 }
 __device__ __forceinline__ float decay_of(Rate rate, float p) { return __builtin_amdgcn_exp2f(rate.e * p); }
