@@ -4,7 +4,7 @@ the gradients need in 8 bits.
 
     python examples/gated_recurrence_block.py            # a training step with activations whole and in 8 bits, then tokens
 
-Training goes through torch's autograd: each operator's gradient is the library's.  A block of one direction also
+Training goes through torch's autograd: each operator's (first) gradient is the library's.  A block of one direction also
 serves: a prompt leaves one float32 state per channel in a pool, and tokens are added one by one.  The projections are
 torch's matrix products.
 """
@@ -14,6 +14,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import selective_state_space_41_amd as V  # noqa: E402
@@ -30,6 +31,7 @@ class GroupNormSiLU(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         weight, bias, mean, rstd, *kept = ctx.saved_tensors
         g = V.groupnorm_bwd(dy.contiguous(), tuple(kept) if len(kept) == 2 else kept[0], weight, bias, mean, rstd,
@@ -48,6 +50,7 @@ class GatedScan(torch.autograd.Function):
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         A_log, *kept = ctx.saved_tensors
         g = V.gated_scan_bwd(tuple(kept), A_log, dh.contiguous(), lengths=ctx.lengths, reverse=ctx.reverse)

@@ -3,7 +3,7 @@ and norm, projections, rotary positions of rows and columns, linear attention wi
 
     python examples/linear_attention_block.py            # one training step, then a prompt and single tokens
 
-Training goes through torch's autograd: each operator's gradient is the library's.  Serving normalises into 8
+Training goes through torch's autograd: each operator's (first) gradient is the library's.  Serving normalises into 8
 bits for the projection, keeps one float32 state per sequence and head in a pool, and adds tokens one by one.
 The projections are torch's matrix products.
 """
@@ -13,6 +13,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import selective_state_space_41_amd as V  # noqa: E402
@@ -28,6 +29,7 @@ class NormResidual(torch.autograd.Function):
         return y, r
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr):
         r, weight, rstd = ctx.saved_tensors
         g = V.rmsnorm_bwd(dy.contiguous(), r, weight, rstd, dresidual_out=dr.contiguous())
@@ -43,6 +45,7 @@ class Rotate(torch.autograd.Function):
         return V.rope_axes(q, k, *where)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         return V.rope_axes(dq, dk, *ctx.where, inverse=True) + (None,) * len(ctx.where)
 
@@ -56,6 +59,7 @@ class LinearAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         g = V.linattn_bwd(*ctx.saved_tensors, dout.contiguous(), lengths=ctx.lengths)
         return g["dq"], g["dk"], g["dv"], g["dlog_decay"], None
