@@ -36,12 +36,8 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(int64_t unit, int groups) {
   if (groups == 1) return {unit, 0};
-  if (unit < (int64_t{1} << 32)) {  // a 32-bit division
-    const uint32_t r = static_cast<uint32_t>(unit) / static_cast<uint32_t>(groups);
-    return {r, static_cast<int>(static_cast<uint32_t>(unit) - r * static_cast<uint32_t>(groups))};
-  }
-  const int64_t r = unit / groups;
-  return {r, static_cast<int>(unit - r * groups)};
+  const uint32_t r = static_cast<uint32_t>(unit) / static_cast<uint32_t>(groups);  // units: under 2^28
+  return {r, static_cast<int>(static_cast<uint32_t>(unit) - r * static_cast<uint32_t>(groups))};
 }
 
 // v / s as far as its code shows it: the code nearest to the float32 quotient.  The product with 1 / s alone takes 4 in 10000

@@ -829,8 +829,6 @@ bool strides_ok(const int64_t* s) { return s[0] >= 0 && s[1] >= 0 && s[0] <= (in
 
 bool dtype_ok(vmscan_dtype d) { return d == VMSCAN_F32 || d == VMSCAN_BF16; }
 
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
-
 // A call's sizes and where its workspace's parts begin: the status words, the published words, the gradient's rows.
 struct Plan {
   ScanArgs a{};

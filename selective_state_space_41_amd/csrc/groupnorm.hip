@@ -917,7 +917,7 @@ struct Plan {
     }
     if (keep && channels % 128 && channels < a.dim) return false;
     lanes_for(channels, keep);
-    const int most = 64 / regs < 1 ? 1 : regs <= 4 ? 16 : regs <= 8 ? 8 : 4;
+    const int most = regs <= 4 ? 16 : regs <= 8 ? 8 : 4;
     const int widest = gradient ? 512 : 1024;
     for (int nt = 256; nt <= widest; nt *= 2) {
       a.rows = nt / a.lanes;
@@ -1011,8 +1011,8 @@ bool shape_ok(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups) {
          batch < 65536 && seqlen < (int64_t{1} << 30);
 }
 
-bool strides_ok(const int64_t* s, int64_t dim) {
-  return s[0] >= 0 && s[1] >= 0 && s[0] <= (int64_t{1} << 40) && s[1] < (int64_t{1} << 32) && dim >= 1;
+bool strides_ok(const int64_t* s) {
+  return s[0] >= 0 && s[1] >= 0 && s[0] <= (int64_t{1} << 40) && s[1] < (int64_t{1} << 32);
 }
 
 }  // namespace
@@ -1033,7 +1033,7 @@ vmscan_status vmscan_groupnorm_fwd(const void* x, const int64_t* x_strides, cons
                                    hipStream_t stream) {
   if (!x || !x_strides || !weight || !bias || !y || !mean || !rstd) return VMSCAN_ERR_NULL;
   if ((keep_codes == nullptr) != (keep_scale == nullptr)) return VMSCAN_ERR_NULL;
-  if (!shape_ok(batch, seqlen, dim, groups) || !strides_ok(x_strides, dim) || !(eps >= 0.0f)) return VMSCAN_ERR_SHAPE;
+  if (!shape_ok(batch, seqlen, dim, groups) || !strides_ok(x_strides) || !(eps >= 0.0f)) return VMSCAN_ERR_SHAPE;
   if ((dtype != VMSCAN_F32 && dtype != VMSCAN_BF16) || (act != 0 && act != 1)) return VMSCAN_ERR_UNSUPPORTED;
   const size_t e = dtype == VMSCAN_F32 ? 4 : 2;
   if (!aligned_to(x, e) || !aligned_to(y, 16) || !aligned_to(workspace, 16)) return VMSCAN_ERR_ALIGN;
@@ -1074,7 +1074,7 @@ vmscan_status vmscan_groupnorm_bwd(const void* dy, const int64_t* dy_strides, co
   if (!dy || !dy_strides || !weight || !bias || !mean || !rstd || !dx || !dweight || !dbias) return VMSCAN_ERR_NULL;
   if ((x == nullptr) == (codes == nullptr) || (x && !x_strides) || (codes == nullptr) != (codes_scale == nullptr))
     return VMSCAN_ERR_NULL;
-  if (!shape_ok(batch, seqlen, dim, groups) || !strides_ok(dy_strides, dim) || (x && !strides_ok(x_strides, dim)))
+  if (!shape_ok(batch, seqlen, dim, groups) || !strides_ok(dy_strides) || (x && !strides_ok(x_strides)))
     return VMSCAN_ERR_SHAPE;
   if ((dtype != VMSCAN_F32 && dtype != VMSCAN_BF16) || (act != 0 && act != 1)) return VMSCAN_ERR_UNSUPPORTED;
   const size_t e = dtype == VMSCAN_F32 ? 4 : 2;
