@@ -559,7 +559,7 @@ vmscan_status vmscan_linattn_step(const void *q, const int64_t *q_strides, const
  *   x     : [rows, dim] activation dtype; pack: rows x_stride >= dim elements apart; unpack: dense
  *   codes : [rows, dim] bytes
  *   scale : [rows, ceil(dim / 128)] float32
- * 1 <= dim <= 2^30; rows * ceil(dim / 128) below 2^28 - 16 (VMSCAN_ERR_SHAPE).  No workspace.
+ * 1 <= dim <= 2^30; rows * ceil(dim / 128) at most 2^28 - 16 (else VMSCAN_ERR_SHAPE).  No workspace.
  */
 vmscan_status vmscan_act8_pack(const void *x, int64_t x_stride, void *codes, float *scale,
                                int64_t rows, int64_t dim, vmscan_dtype dtype, hipStream_t stream);
@@ -651,7 +651,7 @@ vmscan_status vmscan_gated_scan_fwd(const void *x, const int64_t *x_strides, con
  * Outputs: dx, dr, di [batch, seqlen, dim] activation dtype, 0 past a row's length; dA_log [dim] float32;
  * dinitial_state [batch, dim] float32 or NULL; it may be the buffer of dfinal_state, and must not overlap that
  * one otherwise, nor initial_state (VMSCAN_ERR_UNSUPPORTED).  At a_t = 1, where sqrt(1 - a^2) has no slope, the
- * gradient of r is its limit.  No atomics: the same inputs give the same bits.
+ * gradient of r is its limit.  Sums and joins are in a fixed order: the same inputs give the same bits.
  */
 size_t vmscan_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 vmscan_status vmscan_gated_scan_bwd(const void *x, const int64_t *x_strides, const void *r,

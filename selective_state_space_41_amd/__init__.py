@@ -929,7 +929,8 @@ def _new_codes(shape, dev):
 
 def act8_pack(x, stream=None):
     """Activations in 8 bits (vmscan_act8_pack): returns (codes, scale), e4m3 codes in x's shape and a float32 scale for
-    each 128 channels, [..., ceil(dim / 128)]; codes * scale is x to 2^-4 of each value.
+    each 128 channels, [..., ceil(dim / 128)]; codes * scale is x to 2^-4 of each value, or to 2^-10 of its scale (the
+    largest magnitude of its 128 channels over 448) where that is more: values under 2^-10 of a scale become 0.
 
     x: [..., dim] float32 or bfloat16, contiguous or [rows, dim] with rows apart."""
     if stream is not None:
