@@ -625,7 +625,7 @@ struct Taken {
   }
   __device__ __forceinline__ Two gate(int plane, int k) const {
     const Two v = values<L>(in[plane][k], shift);
-    if constexpr (CODES) {  // the scale and log2(e) in one factor
+    if constexpr (CODES) {  // the scale and log2(e) in one factor: what that rounds is far under a code's 2^-4
       const float f = scale[plane][k] * -kLog2e;
       return {sigmoid_of(v.a * f), sigmoid_of(v.b * f)};
     }

@@ -5,8 +5,8 @@
 // Where a batch row's slab of whole groups fits a workgroup's registers it is read once: the workgroup keeps it from
 // the statistics to the output.  Larger rows are cut into runs of tokens, whole rows of channels, so that accesses
 // are dense whatever the groups' width: one launch leaves each run's mean and sum of squared deviations per group (the
-// gradient: two sums per group and channel), the next joins a row's runs and reads the tokens again, mostly from the
-// last-level cache.
+// gradient: two sums per group and channel), the next joins a row's runs and reads the tokens again (from memory or the
+// last-level cache: the counters do not tell).
 //
 // Measured (whole calls): 32 x 3136 x 512 bfloat16 kept in 8 bits 75 us (first launch 25, second 50) for 257 MB, 51 us at
 // a copy's rate, or 360 MB with the second read; its gradient from 8 bits 79 (38 and 47, the second's sums from the cache
@@ -74,6 +74,8 @@ struct Lane {
   }
 };
 
+// Without the tail of u * log2(e), for float32 too: u is a rounded result here, off by up to 2^-24 of itself (and of its
+// terms), which already costs e^-u as much.
 __device__ __forceinline__ float sigmoid(float u) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f));
 }
@@ -873,7 +875,6 @@ struct Plan {
     if (keep) a.lanes = (a.lanes + kGroupLanes - 1) / kGroupLanes * kGroupLanes;
   }
 
-  // regs: registers that a thread keeps for 8 channels of a token.
   Plan(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, vmscan_dtype dtype, bool gradient, bool keep, bool codes) {
     a.batch = batch, a.seqlen = seqlen, a.dim = static_cast<int>(dim), a.groups = static_cast<int>(groups);
     a.width = a.dim / a.groups;
@@ -905,6 +906,7 @@ struct Plan {
   // A slab: the fewest whole groups of 128 bytes of a token, or of all channels; with 8-bit copies a multiple of 128
   // channels.  The fewest threads that hold it.
   bool slab_fits(bool bf16, bool gradient, bool keep, bool codes) {
+    // registers that a thread keeps for 8 channels of a token
     const int regs = w8 && bf16 ? (gradient ? (codes ? 7 : 8) : 4) : (gradient ? (codes ? 11 : 16) : 8);
     const int least = bf16 ? 64 : 32;
     int channels = (least + a.width - 1) / a.width * a.width;
