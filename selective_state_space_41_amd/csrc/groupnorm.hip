@@ -30,6 +30,7 @@ constexpr int kGroupLanes = 16;   // 8-bit copies: lanes whose channels share a 
 // Tokens that a thread loads at once: 4, and 2 in the gradient, whose registers leave room for more waves then (32 x 3136 x
 // 512 from 8 bits 82 us instead of 89, with 1024 workgroups; the forward takes the same time with either).
 constexpr int kAhead = 4, kAheadBack = 2;
+constexpr int kRecentre = 8;  // tokens of a thread after which the statistics' sums move to the mean so far
 
 struct GnArgs {
   const void *x, *dy;
@@ -280,10 +281,10 @@ __device__ __forceinline__ void over_rows(int rows, int channels, float* scratch
 __device__ __forceinline__ int seen(int n, int row, int rows) { return n > row ? (n - row + rows - 1) / rows : 0; }
 
 // Mean and sum of squared deviations of each group over a run.  A thread's sums are of differences to a centre, its first
-// token at first; every four tokens the centre moves to the mean so far, and the sums are moved with it exactly, by the
+// token at first; every eight tokens the centre moves to the mean so far, and the sums are moved with it exactly, by the
 // distance between the two float32 centres.  So neither a large mean nor tokens far from the others, the first ones among
 // them, are subtracted from a sum of squares that they dominate (a centre left at a first token 100 times the others cost
-// the variance 4e-4 of itself over 784 tokens).  Sums of different threads are joined by their means in the same sense.
+// the variance 4e-4 of itself over 784 tokens; moving it costs nothing, every four tokens 2 % of the call).  Sums of different threads are joined by their means in the same sense.
 template <typename T, bool W8, bool ONCE>
 __global__ __launch_bounds__(512) void groupnorm_stats_kernel(GnArgs a) {
   extern __shared__ float lds[];  // [2][rows][dim], the channels' and the groups' means, a float per thread
@@ -313,6 +314,7 @@ __global__ __launch_bounds__(512) void groupnorm_stats_kernel(GnArgs a) {
           }
         },
         [&](int m) {
+          if (m % kRecentre) return;
           const float tokens = static_cast<float>(m), inv = __builtin_amdgcn_rcpf(tokens);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {

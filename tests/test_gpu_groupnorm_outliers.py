@@ -3,7 +3,7 @@ others, as a register token's or a border pixel's do: neither they nor a large m
 
 Rooms of test_gpu_groupnorm.py: (80 + 8 |mean| / std) U on the reciprocal deviation.  A thread adds up to 1000 squares to
 one float32 sum here; roundings to nearest that add up at random, each within U of the sum: under 2 sqrt(1000) U = 64 U of
-the variance, 32 U of its root.  The sums' recentring, once in four tokens, adds a fourth as many."""
+the variance, 32 U of its root.  The sums' recentring, once in eight tokens, adds a fourth as many at most."""
 import numpy as np
 import pytest
 import torch
