@@ -744,7 +744,7 @@ __global__ __launch_bounds__(64 * R, 4) void gated_scan_bwd_kernel(ScanArgs a) {
   *to = make_float2(dA.a, dA.b);  // channels past the last are not summed
 }
 
-// Sets the published words to kNothing and the two words before them to 0: 1.3 to 5 us.
+// Sets the published words to kNothing and the two words before them to 0: 1.3 to 7.6 us, 4.9 in the mean of the profiled calls.
 __global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint32_t* status, uint64_t* words, int64_t n) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 2;
   if (i == 0) status[0] = status[1] = 0;

@@ -31,6 +31,7 @@ constexpr int kGroupLanes = 16;   // 8-bit copies: lanes whose channels share a 
 // 512 from 8 bits 82 us instead of 89, with 1024 workgroups; the forward takes the same time with either).
 constexpr int kAhead = 4, kAheadBack = 2;
 constexpr int kRecentre = 8;  // tokens of a thread after which the statistics' sums move to the mean so far
+static_assert(kRecentre % kAhead == 0, "whole turns");
 
 struct GnArgs {
   const void *x, *dy;
@@ -284,7 +285,8 @@ __device__ __forceinline__ int seen(int n, int row, int rows) { return n > row ?
 // token at first; every eight tokens the centre moves to the mean so far, and the sums are moved with it exactly, by the
 // distance between the two float32 centres.  So neither a large mean nor tokens far from the others, the first ones among
 // them, are subtracted from a sum of squares that they dominate (a centre left at a first token 100 times the others cost
-// the variance 4e-4 of itself over 784 tokens; moving it costs nothing, every four tokens 2 % of the call).  Sums of different threads are joined by their means in the same sense.
+// the variance 4e-4 of itself over 784 tokens; moving it costs nothing, every four tokens 2 % of the call).  Sums of
+// different threads are joined by their means in the same sense.
 template <typename T, bool W8, bool ONCE>
 __global__ __launch_bounds__(512) void groupnorm_stats_kernel(GnArgs a) {
   extern __shared__ float lds[];  // [2][rows][dim], the channels' and the groups' means, a float per thread
